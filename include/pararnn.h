@@ -298,6 +298,153 @@ int pararnn_lsim(int B, int T, int nx, int m, int p, const float *A, const float
                  const float *D, float dt, const float *U, const float *x0, float *x, float *y,
                  void *workspace, size_t ws_bytes, void *stream);
 
+/* ---- operators of a selective state space block -------------------------- */
+/*
+ * Token mixers and projections of language models around an input-dependent
+ * linear recurrence: a short causal convolution, the selective scan, the norm
+ * that adds the residual, and products on 8-bit integers, each with its
+ * gradient or its form for single tokens.  All calls are asynchronous on
+ * `stream`, allocate nothing, record no memset, read no device memory on the
+ * host, and combine in a fixed order (bitwise reproducible), so they may be
+ * captured into a graph.  A sequence array is a pr_view: element (b, t, c)
+ * lies at p[b * sb + t * st + c] (strides in elements, channels adjacent), so
+ * a slice of a wider projection is read in place.  Storage is fp32 or bf16;
+ * arithmetic, states and sums are fp32 or wider and round to storage once.
+ *
+ * Ragged batches.  `lengths` (int32 device array [B], may be NULL) holds each
+ * sequence's number of steps, taken within 0..T.  Steps past it are not read
+ * (they may hold anything, NaN included), leave the states as they are, and
+ * their outputs and gradients are written as 0.
+ * Pools.  The single-token calls keep states in a pool of `nslots` rows;
+ * slots[b] (int32 device array [B]; NULL: row b) is sequence b's row.  An
+ * index outside the pool, such as -1, marks an idle row: its output is 0 and
+ * no state is touched.  Two sequences must not share a row.
+ */
+typedef struct {
+  void *p;
+  long long sb, st;
+} pr_view;
+
+/*
+ * Short causal convolution, per channel d:
+ *   a_t = bias + sum_k w[d][k] x_{t - W + 1 + k},  y_t = silu(a_t) or a_t
+ * with x_{-1}, x_{-2}, .. from state_in.  1 <= W <= 4.
+ *   w [D, W], bias [D] or NULL         storage dtype
+ *   state_in [B, W-1, D] or NULL (= 0) the W - 1 inputs before the first step, oldest first
+ *   state_out [B, W-1, D] or NULL      the last W - 1 inputs of the sequence; may be state_in
+ */
+typedef struct {
+  int dtype; /* PR_F32 or PR_BF16                       */
+  int B, T, D, W;
+  int silu;  /* nonzero: y = silu(a), else y = a        */
+} pr_conv_problem;
+int pararnn_conv(const pr_conv_problem *p, const pr_view *x, const void *w, const void *bias, const void *state_in,
+                 const int *lengths, const pr_view *y, void *state_out, void *stream);
+/*
+ * Gradients of sum <dy, y> + sum <dstate_out, state_out>.  dx, dw (fp32
+ * [D, W]), dbias (fp32 [D]), dstate_in ([B, W-1, D], storage dtype) may be
+ * NULL; the others are as in the forward call.  workspace: 256-byte aligned,
+ * pararnn_conv_workspace_bytes.
+ */
+size_t pararnn_conv_workspace_bytes(const pr_conv_problem *p);
+int pararnn_conv_adjoint(const pr_conv_problem *p, const pr_view *x, const void *w, const void *bias,
+                         const void *state_in, const int *lengths, const pr_view *dy, const void *dstate_out,
+                         const pr_view *dx, float *dw, float *dbias, void *dstate_in, void *workspace,
+                         size_t ws_bytes, void *stream);
+/* One token for each of B sequences (p->T is ignored): x, y [B, D] with row
+ * strides sb; state [nslots, W-1, D] is read and shifted in place.          */
+int pararnn_conv_step(const pr_conv_problem *p, const pr_view *x, const void *w, const void *bias, void *state,
+                      int nslots, const int *slots, const pr_view *y, void *stream);
+
+/*
+ * Selective state space scan, per channel d and state n:
+ *   delta_t = softplus(dt_t + dt_bias) (or the sum itself)
+ *   h_t[d][n] = exp(delta_t[d] A[d][n]) h_{t-1}[d][n] + delta_t[d] u_t[d] B_t[g][n]
+ *   y_t[d] = (sum_n C_t[g][n] h_t[d][n] + D[d] u_t[d]) silu(z_t[d])
+ * Channels d of group g = d / (D / G) share B and C.  1 <= N <= 64, G divides D.
+ * A should be negative (a decay); any value is computed.
+ *   u, dt, z [B, T, D] (z.p NULL: no gate), B, C [B, T, G N]   storage dtype
+ *   A [D, N], D [D] or NULL, dt_bias [D] or NULL               fp32
+ *   h0 [B, D, N] or NULL (= 0), lengths [B] or NULL
+ * fp32 arrays with N states are 16-byte aligned where N is a multiple of 4.
+ *   y       output
+ *   h_last  [B, D, N] or NULL: the state after the last step (may be h0)
+ *   states  NULL, or [B, ceil(T / 16), D, N] fp32: the state that enters
+ *           every 16th step, for the adjoint (not written from a sequence's
+ *           length on)
+ */
+#define PR_SSM_STATE_STEPS 16
+typedef struct {
+  int dtype; /* PR_F32 or PR_BF16 */
+  int B, T, D, N, G;
+  int softplus;
+} pr_ssm_problem;
+typedef struct {
+  pr_view u, dt, z, B, C;
+  const float *A, *D, *dt_bias, *h0;
+  const int *lengths;
+} pr_ssm_inputs;
+/* Gradients; any pointer may be NULL (z only with a gate). */
+typedef struct {
+  pr_view u, dt, z, B, C;
+  float *A, *D, *dt_bias, *h0;
+} pr_ssm_grads;
+size_t pararnn_ssm_workspace_bytes(const pr_ssm_problem *p, int with_adjoint);
+int pararnn_ssm_scan(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_view *y, float *h_last, float *states,
+                     void *workspace, size_t ws_bytes, void *stream);
+/* Gradients of sum <dy, y> + sum <dh_last, h_last> (dh_last may be NULL) from
+ * the states that the forward call saved on the same inputs.                */
+int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const float *states, const pr_view *dy,
+                        const float *dh_last, const pr_ssm_grads *grads, void *workspace, size_t ws_bytes,
+                        void *stream);
+/* One token for each of B sequences (p->T, h0 and lengths are ignored; row
+ * strides sb): state [nslots, D, N] fp32 is updated in place.               */
+int pararnn_ssm_step(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_view *y, float *state, int nslots,
+                     const int *slots, void *stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, per row of n:
+ *   s = x + r, rounded to storage (the stream that goes on is what is normed)
+ *   y = s / sqrt(mean(s^2) + eps) * w
+ * in the storage dtype (y) or in 8 bits (q, scale): scale = max|y| / 127,
+ * q = y / scale to the nearest, ties to even; a row of zeros has scale 0.
+ * Exactly one of y and q is given.  x, r, s, y, q: [rows, n] with row strides
+ * (in elements); r NULL: s = x; s (sum_out) NULL: not written.  w: [n] in the
+ * storage dtype or NULL (= 1); q int8, scale [rows] fp32.
+ */
+typedef struct {
+  int dtype; /* PR_F32 or PR_BF16 */
+  int n;
+  long long rows;
+  float eps; /* >= 0 */
+} pr_norm_problem;
+typedef struct {
+  void *p;
+  long long ld;
+} pr_rows;
+int pararnn_rmsnorm(const pr_norm_problem *p, const pr_rows *x, const pr_rows *r, const void *w, const pr_rows *sum_out,
+                    const pr_rows *y, const pr_rows *q, float *scale, void *stream);
+/* Gradient of sum <dy, y> + sum <dsum, s> with respect to s (the gradient of x
+ * and of r) and to w (fp32 [n]); dsum, dx and dw may be NULL.               */
+size_t pararnn_rmsnorm_workspace_bytes(const pr_norm_problem *p);
+int pararnn_rmsnorm_adjoint(const pr_norm_problem *p, const pr_rows *s, const void *w, const pr_rows *dy,
+                            const pr_rows *dsum, const pr_rows *dx, float *dw, void *workspace, size_t ws_bytes,
+                            void *stream);
+/* The same 8-bit form of rows as they are: scale = max|x| / 127, q = x / scale. */
+int pararnn_quant_rows(const pr_norm_problem *p, const pr_rows *x, const pr_rows *q, float *scale, void *stream);
+
+/*
+ * Product of 8-bit integers with a scale for each row of a (token) and of w
+ * (output channel): out[m][n] = (sum_k a[m][k] w[n][k]) sa[m] sw[n] + bias[n].
+ * The sum is exact in 32-bit integers (K < 131072).  a [M, K], w [N, K] int8
+ * with row strides; sa [M], sw [N] fp32; out [M, N] and bias [N] (or NULL)
+ * in `dtype`.  workspace: 256-byte aligned, pararnn_gemm_i8_workspace_bytes.
+ */
+size_t pararnn_gemm_i8_workspace_bytes(int M, int N, int K);
+int pararnn_gemm_i8(int dtype, int M, int N, int K, const signed char *a, long long lda, const float *sa,
+                    const signed char *w, long long ldw, const float *sw, const void *bias, void *out, long long ldo,
+                    void *workspace, size_t ws_bytes, void *stream);
+
 /*
  * Kernel timing for profiling and benchmarks (per calling thread).
  * pararnn_trace(1) clears the counters and starts bracketing, with HIP events

@@ -24,8 +24,12 @@ PR_JAC_DENSE, PR_JAC_DIAG, PR_JAC_BLOCK2, PR_JAC_ZERO = 0, 1, 2, 3
 EXPORTS = ["pararnn_workspace_bytes", "pararnn_solve", "pararnn_adjoint", "pararnn_solve_adjoint",
            "pararnn_scan_workspace_bytes", "pararnn_affine_scan", "pararnn_strerror", "pararnn_last_error", "pararnn_trace", "pararnn_trace_read",
            "pararnn_trace_kernel", "pararnn_lsim_workspace_bytes", "pararnn_lsim", "pararnn_elk_workspace_bytes",
-           "pararnn_solve_elk", "pararnn_affine_scan_noalloc"]
+           "pararnn_solve_elk", "pararnn_affine_scan_noalloc", "pararnn_conv", "pararnn_conv_workspace_bytes",
+           "pararnn_conv_adjoint", "pararnn_conv_step", "pararnn_ssm_workspace_bytes", "pararnn_ssm_scan",
+           "pararnn_ssm_adjoint", "pararnn_ssm_step", "pararnn_rmsnorm", "pararnn_rmsnorm_workspace_bytes",
+           "pararnn_rmsnorm_adjoint", "pararnn_quant_rows", "pararnn_gemm_i8_workspace_bytes", "pararnn_gemm_i8"]
 NOALLOC_SCRATCH_BYTES = 16 << 20  # PR_NOALLOC_SCRATCH_BYTES
+SSM_STATE_STEPS = 16  # PR_SSM_STATE_STEPS
 
 
 class Problem(C.Structure):
@@ -41,6 +45,38 @@ class Weights(C.Structure):
 class Grads(C.Structure):
     _fields_ = [("W_x", C.c_void_p), ("b_x", C.c_void_p), ("W_h", C.c_void_p), ("b_h", C.c_void_p),
                 ("peep", C.c_void_p)]
+
+
+class View(C.Structure):
+    """pr_view: a [B, T, channels] array with adjacent channels."""
+    _fields_ = [("p", C.c_void_p), ("sb", C.c_longlong), ("st", C.c_longlong)]
+
+
+class Rows(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("ld", C.c_longlong)]
+
+
+class ConvProblem(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("B", C.c_int), ("T", C.c_int), ("D", C.c_int), ("W", C.c_int), ("silu", C.c_int)]
+
+
+class SsmProblem(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("B", C.c_int), ("T", C.c_int), ("D", C.c_int), ("N", C.c_int), ("G", C.c_int),
+                ("softplus", C.c_int)]
+
+
+class SsmInputs(C.Structure):
+    _fields_ = [("u", View), ("dt", View), ("z", View), ("B", View), ("C", View), ("A", C.c_void_p),
+                ("D", C.c_void_p), ("dt_bias", C.c_void_p), ("h0", C.c_void_p), ("lengths", C.c_void_p)]
+
+
+class SsmGrads(C.Structure):
+    _fields_ = [("u", View), ("dt", View), ("z", View), ("B", View), ("C", View), ("A", C.c_void_p),
+                ("D", C.c_void_p), ("dt_bias", C.c_void_p), ("h0", C.c_void_p)]
+
+
+class NormProblem(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("n", C.c_int), ("rows", C.c_longlong), ("eps", C.c_float)]
 
 
 class PararnnError(RuntimeError):
@@ -92,6 +128,24 @@ def lib():
         L.pararnn_elk_workspace_bytes.restype = S
         L.pararnn_solve_elk.argtypes = [P, P, P, P, F, F, I, P, P, P, I, P, S, P]
         L.pararnn_solve_elk.restype = I
+        LL = C.c_longlong
+        for name, res, args in (
+                ("conv", I, [P, P, P, P, P, P, P, P, P]),
+                ("conv_workspace_bytes", S, [P]),
+                ("conv_adjoint", I, [P, P, P, P, P, P, P, P, P, P, P, P, P, S, P]),
+                ("conv_step", I, [P, P, P, P, P, I, P, P, P]),
+                ("ssm_workspace_bytes", S, [P, I]),
+                ("ssm_scan", I, [P, P, P, P, P, P, S, P]),
+                ("ssm_adjoint", I, [P, P, P, P, P, P, P, S, P]),
+                ("ssm_step", I, [P, P, P, P, I, P, P]),
+                ("rmsnorm", I, [P, P, P, P, P, P, P, P, P]),
+                ("rmsnorm_workspace_bytes", S, [P]),
+                ("rmsnorm_adjoint", I, [P, P, P, P, P, P, P, P, S, P]),
+                ("quant_rows", I, [P, P, P, P, P]),
+                ("gemm_i8_workspace_bytes", S, [I, I, I]),
+                ("gemm_i8", I, [I, I, I, I, P, LL, P, P, LL, P, P, P, LL, P, S, P])):
+            f = getattr(L, "pararnn_" + name)
+            f.restype, f.argtypes = res, args
         _lib = L
     return _lib
 
@@ -253,6 +307,244 @@ def lsim(A, Bm, Cm, Dm, dt: float, U, x0, x, y, workspace, check: bool = True) -
     if check and st < 0:
         raise PararnnError(st, "pararnn_lsim")
     return st
+
+
+# ---------------------------------------------------------------------------
+# operators of a selective state space block
+# ---------------------------------------------------------------------------
+def _dtype_code(dt, what):
+    import torch
+    if dt == torch.bfloat16:
+        return PR_BF16
+    if dt == torch.float32:
+        return PR_F32
+    raise ValueError(f"{what}: storage must be float32 or bfloat16, got {dt}")
+
+
+def _strides(where, name, t, shape, adjacent):
+    step = 1
+    for k in range(1, adjacent + 1):
+        if shape[-k] != 1 and t.stride(-k) != step:
+            raise ValueError(f"{where}: the last {adjacent} axes of {name} must be contiguous, got strides {t.stride()}")
+        step *= shape[-k]
+
+
+def _need(where, name, t, shape, dtype, adjacent=1):
+    """The address of tensor t after a check of its shape, type and device;
+    None passes.  adjacent: trailing axes that must be laid out densely."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{where}: {name} must be a {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} must be on the GPU")
+    _strides(where, name, t, shape, adjacent)
+    return t.data_ptr()
+
+
+def _dense(where, name, t, shape, dtype):
+    return _need(where, name, t, shape, dtype, len(shape))
+
+
+def _view(where, name, t, shape, dtype):
+    """pr_view of t [B, T, channels] or, for single tokens, [B, channels]."""
+    if t is None:
+        return View(None, 0, 0)
+    p = _need(where, name, t, shape, dtype)
+    return View(p, t.stride(0), t.stride(1) if len(shape) == 3 else 0)
+
+
+def _rows(where, name, t, shape, dtype):
+    if t is None:
+        return None
+    return C.byref(Rows(_need(where, name, t, shape, dtype), t.stride(0)))
+
+
+def _done(st, where, check=True):
+    if check and st < 0:
+        raise PararnnError(st, where)
+    return st
+
+
+def _ws(workspace):
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def conv_workspace_bytes(dtype, B: int, T: int, D: int, W: int) -> int:
+    """Workspace of conv_adjoint for sequences stored in the torch type dtype."""
+    return lib().pararnn_conv_workspace_bytes(C.byref(ConvProblem(_dtype_code(dtype, "conv"), B, T, D, W, 1)))
+
+
+def conv(x, w, bias, y, state_in=None, state_out=None, lengths=None, silu: bool = True, check: bool = True) -> int:
+    """pararnn_conv: short causal convolution of x [B, T, D] with w [D, W] into y."""
+    import torch
+    (B, T, D), W, dt, n = x.shape, w.shape[1], x.dtype, "conv"
+    pb = ConvProblem(_dtype_code(dt, n), B, T, D, W, int(silu))
+    st = lib().pararnn_conv(C.byref(pb), C.byref(_view(n, "x", x, (B, T, D), dt)), _dense(n, "w", w, (D, W), dt),
+                            _dense(n, "bias", bias, (D,), dt), _dense(n, "state_in", state_in, (B, W - 1, D), dt),
+                            _dense(n, "lengths", lengths, (B,), torch.int32),
+                            C.byref(_view(n, "y", y, (B, T, D), dt)),
+                            _dense(n, "state_out", state_out, (B, W - 1, D), dt), _stream())
+    return _done(st, "pararnn_conv", check)
+
+
+def conv_adjoint(x, w, bias, dy, dx, dw, dbias, workspace, state_in=None, dstate_out=None, dstate_in=None, lengths=None,
+                 silu: bool = True, check: bool = True) -> int:
+    """pararnn_conv_adjoint: gradients of conv; dx, dw, dbias and dstate_in may be None."""
+    import torch
+    (B, T, D), W, dt, n, f32 = x.shape, w.shape[1], x.dtype, "conv_adjoint", torch.float32
+    pb = ConvProblem(_dtype_code(dt, n), B, T, D, W, int(silu))
+    st = lib().pararnn_conv_adjoint(
+        C.byref(pb), C.byref(_view(n, "x", x, (B, T, D), dt)), _dense(n, "w", w, (D, W), dt),
+        _dense(n, "bias", bias, (D,), dt), _dense(n, "state_in", state_in, (B, W - 1, D), dt),
+        _dense(n, "lengths", lengths, (B,), torch.int32), C.byref(_view(n, "dy", dy, (B, T, D), dt)),
+        _dense(n, "dstate_out", dstate_out, (B, W - 1, D), dt), C.byref(_view(n, "dx", dx, (B, T, D), dt)),
+        _dense(n, "dw", dw, (D, W), f32), _dense(n, "dbias", dbias, (D,), f32),
+        _dense(n, "dstate_in", dstate_in, (B, W - 1, D), dt), *_ws(workspace), _stream())
+    return _done(st, "pararnn_conv_adjoint", check)
+
+
+def conv_step(x, w, bias, state, y, slots=None, silu: bool = True, check: bool = True) -> int:
+    """pararnn_conv_step: one token x [B, D] per sequence on the pool state [slots, W - 1, D]."""
+    import torch
+    (B, D), W, dt, n = x.shape, w.shape[1], x.dtype, "conv_step"
+    pb = ConvProblem(_dtype_code(dt, n), B, 1, D, W, int(silu))
+    pool = state.shape[0]
+    st = lib().pararnn_conv_step(C.byref(pb), C.byref(_view(n, "x", x, (B, D), dt)), _dense(n, "w", w, (D, W), dt),
+                                 _dense(n, "bias", bias, (D,), dt), _dense(n, "state", state, (pool, W - 1, D), dt),
+                                 pool, _dense(n, "slots", slots, (B,), torch.int32),
+                                 C.byref(_view(n, "y", y, (B, D), dt)), _stream())
+    return _done(st, "pararnn_conv_step", check)
+
+
+def ssm_workspace_bytes(dtype, B: int, T: int, D: int, N: int, G: int = 1, with_adjoint: bool = True) -> int:
+    pb = SsmProblem(_dtype_code(dtype, "ssm"), B, T, D, N, G, 1)
+    return lib().pararnn_ssm_workspace_bytes(C.byref(pb), int(with_adjoint))
+
+
+def ssm_states_shape(B: int, T: int, D: int, N: int):
+    """Shape of the fp32 states that ssm_scan saves for ssm_scan_adjoint."""
+    return B, -(-T // SSM_STATE_STEPS), D, N
+
+
+def _ssm(where, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, softplus):
+    import torch
+    st, f32 = u.dtype, torch.float32
+    shape, (ch, N) = tuple(u.shape), A.shape
+    B, T = shape[0], shape[1] if len(shape) == 3 else 1
+    width = Bm.shape[-1]
+    if width % N or not width:
+        raise ValueError(f"{where}: B has {width} columns, not a multiple of the {N} states of A")
+    bc = shape[:-1] + (width,)
+    pb = SsmProblem(_dtype_code(st, where), B, T, shape[-1], N, width // N, int(softplus))
+    return pb, SsmInputs(
+        _view(where, "u", u, shape, st), _view(where, "dt", dt, shape, st), _view(where, "z", z, shape, st),
+        _view(where, "B", Bm, bc, st), _view(where, "C", Cm, bc, st), _dense(where, "A", A, (shape[-1], N), f32),
+        _dense(where, "D", D, (ch,), f32), _dense(where, "dt_bias", dt_bias, (ch,), f32),
+        _dense(where, "h0", h0, (B, ch, N), f32), _dense(where, "lengths", lengths, (B,), torch.int32))
+
+
+def ssm_scan(u, dt, A, Bm, Cm, y, workspace, D=None, z=None, dt_bias=None, h0=None, h_last=None, states=None,
+             lengths=None, softplus: bool = True, check: bool = True) -> int:
+    """pararnn_ssm_scan: the selective scan of u [B, T, channels] into y."""
+    import torch
+    n = "ssm_scan"
+    pb, inp = _ssm(n, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, softplus)
+    st = lib().pararnn_ssm_scan(
+        C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, tuple(u.shape), u.dtype)),
+        _dense(n, "h_last", h_last, (pb.B, pb.D, pb.N), torch.float32),
+        _dense(n, "states", states, ssm_states_shape(pb.B, pb.T, pb.D, pb.N), torch.float32), *_ws(workspace),
+        _stream())
+    return _done(st, "pararnn_ssm_scan", check)
+
+
+def ssm_scan_adjoint(u, dt, A, Bm, Cm, states, dy, workspace, D=None, z=None, dt_bias=None, lengths=None, dh_last=None,
+                     du=None, ddt=None, dz=None, dB=None, dC=None, dA=None, dD=None, ddt_bias=None, dh0=None,
+                     softplus: bool = True, check: bool = True) -> int:
+    """pararnn_ssm_adjoint: gradients of ssm_scan from the states it saved; any output may be None."""
+    import torch
+    n, f32 = "ssm_scan_adjoint", torch.float32
+    pb, inp = _ssm(n, u, dt, A, Bm, Cm, D, z, dt_bias, None, lengths, softplus)
+    shape, bc, t = tuple(u.shape), tuple(Bm.shape), u.dtype
+    gr = SsmGrads(_view(n, "du", du, shape, t), _view(n, "ddt", ddt, shape, t), _view(n, "dz", dz, shape, t),
+                  _view(n, "dB", dB, bc, t), _view(n, "dC", dC, bc, t), _dense(n, "dA", dA, (pb.D, pb.N), f32),
+                  _dense(n, "dD", dD, (pb.D,), f32), _dense(n, "ddt_bias", ddt_bias, (pb.D,), f32),
+                  _dense(n, "dh0", dh0, (pb.B, pb.D, pb.N), f32))
+    st = lib().pararnn_ssm_adjoint(
+        C.byref(pb), C.byref(inp), _dense(n, "states", states, ssm_states_shape(pb.B, pb.T, pb.D, pb.N), f32),
+        C.byref(_view(n, "dy", dy, shape, t)), _dense(n, "dh_last", dh_last, (pb.B, pb.D, pb.N), f32), C.byref(gr),
+        *_ws(workspace), _stream())
+    return _done(st, "pararnn_ssm_adjoint", check)
+
+
+def ssm_step(u, dt, A, Bm, Cm, state, y, D=None, z=None, dt_bias=None, slots=None, softplus: bool = True,
+             check: bool = True) -> int:
+    """pararnn_ssm_step: one token u [B, channels] per sequence on the fp32 pool state [slots, channels, N]."""
+    import torch
+    n = "ssm_step"
+    pb, inp = _ssm(n, u, dt, A, Bm, Cm, D, z, dt_bias, None, None, softplus)
+    pool = state.shape[0]
+    st = lib().pararnn_ssm_step(C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, tuple(u.shape), u.dtype)),
+                                _dense(n, "state", state, (pool, pb.D, pb.N), torch.float32), pool,
+                                _dense(n, "slots", slots, (pb.B,), torch.int32), _stream())
+    return _done(st, "pararnn_ssm_step", check)
+
+
+def rmsnorm(x, w, y=None, residual=None, sum_out=None, q=None, scale=None, eps: float = 1e-5,
+            check: bool = True) -> int:
+    """pararnn_rmsnorm of x [rows, n] (+ residual): y, or q (int8) with scale [rows]."""
+    import torch
+    (rows, n), dt, where = x.shape, x.dtype, "rmsnorm"
+    pb = NormProblem(_dtype_code(dt, where), n, rows, eps)
+    st = lib().pararnn_rmsnorm(
+        C.byref(pb), _rows(where, "x", x, (rows, n), dt), _rows(where, "residual", residual, (rows, n), dt),
+        _dense(where, "w", w, (n,), dt), _rows(where, "sum_out", sum_out, (rows, n), dt),
+        _rows(where, "y", y, (rows, n), dt), _rows(where, "q", q, (rows, n), torch.int8),
+        _dense(where, "scale", scale, (rows,), torch.float32), _stream())
+    return _done(st, "pararnn_rmsnorm", check)
+
+
+def rmsnorm_workspace_bytes(dtype, rows: int, n: int) -> int:
+    return lib().pararnn_rmsnorm_workspace_bytes(C.byref(NormProblem(_dtype_code(dtype, "rmsnorm"), n, rows, 0.0)))
+
+
+def rmsnorm_adjoint(s, w, dy, dx, dw, workspace, dsum=None, eps: float = 1e-5, check: bool = True) -> int:
+    """pararnn_rmsnorm_adjoint at the stored sum s [rows, n]; dx and dw may be None."""
+    import torch
+    (rows, n), dt, where = s.shape, s.dtype, "rmsnorm_adjoint"
+    pb = NormProblem(_dtype_code(dt, where), n, rows, eps)
+    st = lib().pararnn_rmsnorm_adjoint(
+        C.byref(pb), _rows(where, "s", s, (rows, n), dt), _dense(where, "w", w, (n,), dt),
+        _rows(where, "dy", dy, (rows, n), dt), _rows(where, "dsum", dsum, (rows, n), dt),
+        _rows(where, "dx", dx, (rows, n), dt), _dense(where, "dw", dw, (n,), torch.float32), *_ws(workspace), _stream())
+    return _done(st, "pararnn_rmsnorm_adjoint", check)
+
+
+def quant_rows(x, q, scale, check: bool = True) -> int:
+    """pararnn_quant_rows: x [rows, n] in 8 bits, q int8 and scale [rows]."""
+    import torch
+    (rows, n), dt, where = x.shape, x.dtype, "quant_rows"
+    pb = NormProblem(_dtype_code(dt, where), n, rows, 0.0)
+    st = lib().pararnn_quant_rows(C.byref(pb), _rows(where, "x", x, (rows, n), dt),
+                                  _rows(where, "q", q, (rows, n), torch.int8),
+                                  _dense(where, "scale", scale, (rows,), torch.float32), _stream())
+    return _done(st, "pararnn_quant_rows", check)
+
+
+def gemm_i8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return lib().pararnn_gemm_i8_workspace_bytes(M, N, K)
+
+
+def gemm_i8(a, a_scale, w, w_scale, out, workspace, bias=None, check: bool = True) -> int:
+    """pararnn_gemm_i8: out [M, N] = (a w^T) a_scale w_scale + bias for int8 a [M, K] and w [N, K]."""
+    import torch
+    (M, K), N, dt, n, f32 = a.shape, w.shape[0], out.dtype, "gemm_i8", torch.float32
+    st = lib().pararnn_gemm_i8(
+        _dtype_code(dt, n), M, N, K, _need(n, "a", a, (M, K), torch.int8), a.stride(0),
+        _dense(n, "a_scale", a_scale, (M,), f32), _need(n, "w", w, (N, K), torch.int8), w.stride(0),
+        _dense(n, "w_scale", w_scale, (N,), f32), _dense(n, "bias", bias, (N,), dt),
+        _need(n, "out", out, (M, N), dt), out.stride(0), *_ws(workspace), _stream())
+    return _done(st, "pararnn_gemm_i8", check)
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,282 @@
+// Product of 8-bit integers with a scale for each row of both operands:
+//   out[m][n] = (sum_k a[m][k] w[n][k]) sa[m] sw[n] + bias[n]
+// Sums are exact in 32-bit integers on the i8 matrix instructions, so K may be
+// split over wavefronts and blocks without a change in the result.
+//
+// Few rows (M <= 64): bound by reading w once.  A block takes 16 columns, its
+// 8 wavefronts slices of K; a lane streams 64 adjacent bytes of one row of w
+// straight into the operand registers of v_mfma_i32_16x16x64_i8, the rows of
+// a (from cache) likewise, and the wavefronts' sums meet in shared memory.
+// More rows: tiles staged through shared memory, v_mfma_i32_32x32x32_i8.
+#include "pararnn.h"
+#include "ssm.h"
+
+namespace pr {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+struct Gemm8Args {
+  const int8_t *a, *w;
+  const float *sa, *sw;
+  const void *bias;
+  void *out;
+  int *part;  // K splits: [splits][M][N]
+  long long lda, ldw, ldo;
+  int M, N, K, splits, kper;  // kper: bytes of K per split
+};
+
+struct __attribute__((packed)) Bytes16 {
+  i32x4 v;
+};
+// 16 bytes of a row from k on, zeros from `ke` on.  AL: 16-byte aligned and
+// ke a multiple of 16; else any alignment, the last bytes one by one.
+template <bool AL>
+__device__ inline i32x4 load16(const int8_t *row, int k, int ke, bool on) {
+  i32x4 v = {0, 0, 0, 0};
+  if (!on || k >= ke) return v;
+  if constexpr (AL) return *reinterpret_cast<const i32x4 *>(row + k);
+  if (k + 16 <= ke) return reinterpret_cast<const Bytes16 *>(row + k)->v;
+#pragma unroll
+  for (int i = 0; i < 15; i++)
+    if (k + i < ke) v[i / 4] |= (int)((unsigned)(uint8_t)row[k + i] << (8 * (i % 4)));
+  return v;
+}
+
+template <typename T>
+__device__ inline float scaled(const Gemm8Args &g, int v, int m, int n) {
+  return fmaf((float)v, g.sa[m] * g.sw[n], g.bias ? ldf((const T *)g.bias, n) : 0.f);
+}
+
+// ---------------------------------------------------------------------------
+template <typename T, int MT, bool AL>
+__global__ __launch_bounds__(512) void k_gemm8_rows(Gemm8Args g) {
+  __shared__ i32x4 red[8][MT][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const bool non = n0 + r < g.N;
+  const int8_t *wr = g.w + (long long)(non ? n0 + r : 0) * g.ldw;
+  const int8_t *ar[MT];
+  bool mon[MT];
+#pragma unroll
+  for (int i = 0; i < MT; i++) {
+    mon[i] = i * 16 + r < g.M;
+    ar[i] = g.a + (long long)(mon[i] ? i * 16 + r : 0) * g.lda;
+  }
+  i32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; i++) acc[i] = i32x4{0, 0, 0, 0};
+  // lane (r, q) takes bytes 64 q .. 64 q + 63 of each 256: the order of k
+  // within a step is the same in both operands
+  for (int k0 = wave * 256 + q * 64; k0 - q * 64 < g.K; k0 += 8 * 256) {
+    i32x4 b[4], a[MT][4];
+#pragma unroll
+    for (int s = 0; s < 4; s++) b[s] = load16<AL>(wr, k0 + s * 16, g.K, non);
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+      for (int s = 0; s < 4; s++) a[i][s] = load16<AL>(ar[i], k0 + s * 16, g.K, mon[i]);
+#pragma unroll
+    for (int s = 0; s < 4; s++)
+#pragma unroll
+      for (int i = 0; i < MT; i++) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[s], a[i][s], acc[i], 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; i++) red[wave][i][lane] = acc[i];
+  __syncthreads();
+  // register v of a lane: column n0 + 4 (lane / 16) + v, row lane % 16 of a
+  for (int e = threadIdx.x; e < MT * 64; e += 512) {
+    const int i = e >> 6, l = e & 63, m = i * 16 + (l & 15);
+    if (m >= g.M) continue;
+    i32x4 s = red[0][i][l];
+#pragma unroll
+    for (int k = 1; k < 8; k++) s += red[k][i][l];
+#pragma unroll
+    for (int v = 0; v < 4; v++) {
+      const int n = n0 + 4 * (l >> 4) + v;
+      if (n < g.N) stf((T *)g.out + m * g.ldo, n, scaled<T>(g, s[v], m, n));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 128 x 128 tile, K step 128 bytes, 4 wavefronts of 64 x 64.  Chunk c (16
+// bytes) of tile row r sits at slot c ^ (r / 2 % 8) of its 128-byte line, so
+// that the 16 rows of a fragment read fall on all 64 banks.
+constexpr int TB = 128;
+__device__ inline int t8_off(int r, int c) { return r * TB + ((c ^ ((r >> 1) & 7)) << 4); }
+
+template <typename T, bool AL>
+__global__ __launch_bounds__(256) void k_gemm8_tile(Gemm8Args g) {
+  __shared__ __attribute__((aligned(16))) int8_t sA[2][128 * TB], sB[2][128 * TB];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+  const int tiles_n = (g.N + 127) / 128;
+  const int m0 = (int)(blockIdx.x / tiles_n) * 128, n0 = (int)(blockIdx.x % tiles_n) * 128;
+  const int kb = blockIdx.y * g.kper, ke = g.K - kb < g.kper ? g.K : kb + g.kper;
+  i32x4 va[4], vb[4];
+  auto gload = [&](int k0) {
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      const int e = tid + q * 256, r = e >> 3, k = k0 + (e & 7) * 16;
+      va[q] = load16<AL>(g.a + (long long)(m0 + r) * g.lda, k, ke, m0 + r < g.M);
+      vb[q] = load16<AL>(g.w + (long long)(n0 + r) * g.ldw, k, ke, n0 + r < g.N);
+    }
+  };
+  auto lstore = [&](int buf) {
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      const int e = tid + q * 256, r = e >> 3, c = e & 7;
+      *reinterpret_cast<i32x4 *>(&sA[buf][t8_off(r, c)]) = va[q];
+      *reinterpret_cast<i32x4 *>(&sB[buf][t8_off(r, c)]) = vb[q];
+    }
+  };
+  i32x16 acc[2][2];
+#pragma unroll
+  for (int j = 0; j < 2; j++)
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+      for (int r = 0; r < 16; r++) acc[j][i][r] = 0;
+  int buf = 0;
+  gload(kb);
+  lstore(0);
+  __syncthreads();
+  const int ar = wm * 64 + (lane & 31), br = wn * 64 + (lane & 31), h = lane >> 5;
+  for (int k0 = kb; k0 < ke; k0 += TB) {
+    const bool more = k0 + TB < ke;
+    if (more) gload(k0 + TB);
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+      i32x4 a[2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        a[i] = *reinterpret_cast<const i32x4 *>(&sA[buf][t8_off(ar + i * 32, 2 * s + h)]);
+        b[i] = *reinterpret_cast<const i32x4 *>(&sB[buf][t8_off(br + i * 32, 2 * s + h)]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; j++)
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+          acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j], a[i], acc[j][i], 0, 0, 0);
+    }
+    if (more) lstore(buf ^ 1);
+    __syncthreads();
+    buf ^= 1;
+  }
+  // a lane holds row m = lane % 32 of each 32 x 32 tile and, per 4 registers,
+  // 4 adjacent columns 8 (v / 4) + 4 (lane / 32) ..
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const int m = m0 + wm * 64 + i * 32 + (lane & 31);
+    if (m >= g.M) continue;
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+#pragma unroll
+      for (int v = 0; v < 16; v++) {
+        const int n = n0 + wn * 64 + j * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
+        if (n >= g.N) continue;
+        if (g.splits > 1) g.part[((long long)blockIdx.y * g.M + m) * g.N + n] = acc[j][i][v];
+        else stf((T *)g.out + m * g.ldo, n, scaled<T>(g, acc[j][i][v], m, n));
+      }
+  }
+}
+
+template <typename T>
+__global__ void k_gemm8_join(Gemm8Args g) {
+  const long long mn = (long long)g.M * g.N, i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= mn) return;
+  int s = 0;
+  for (int k = 0; k < g.splits; k++) s += g.part[k * mn + i];
+  const int m = (int)(i / g.N), n = (int)(i % g.N);
+  stf((T *)g.out + m * g.ldo, n, scaled<T>(g, s, m, n));
+}
+
+template <typename T, bool AL>
+hipError_t gemm8_go(const Gemm8Args &g, hipStream_t s) {
+  if (g.M <= 64) {
+    const dim3 grid((unsigned)((g.N + 15) / 16));
+    if (g.M <= 16) k_gemm8_rows<T, 1, AL><<<grid, 512, 0, s>>>(g);
+    else if (g.M <= 32) k_gemm8_rows<T, 2, AL><<<grid, 512, 0, s>>>(g);
+    else k_gemm8_rows<T, 4, AL><<<grid, 512, 0, s>>>(g);
+    return hipGetLastError();
+  }
+  const long long tiles = (long long)((g.M + 127) / 128) * ((g.N + 127) / 128);
+  k_gemm8_tile<T, AL><<<dim3((unsigned)tiles, (unsigned)g.splits), 256, 0, s>>>(g);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || g.splits == 1) return e;
+  const long long mn = (long long)g.M * g.N;
+  k_gemm8_join<T><<<dim3((unsigned)((mn + 255) / 256)), 256, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+// Splits of K where the tiles alone leave CUs idle: enough blocks for one
+// round of the device, at least four K steps each.
+static int gemm8_splits(int M, int N, int K, int *kper) {
+  const long long tiles = (long long)((M + 127) / 128) * ((N + 127) / 128);
+  const int steps = (K + TB - 1) / TB;
+  int s = M <= 64 ? 1 : (int)(256 / tiles);
+  if (s > steps / 4) s = steps / 4;
+  if (s < 1) s = 1;
+  const int per = (steps + s - 1) / s;
+  *kper = per * TB;
+  return (steps + per - 1) / per;
+}
+
+}  // namespace pr
+
+using namespace pr;
+
+namespace {
+
+#define HIPCHK(expr)                                                                        \
+  do {                                                                                      \
+    hipError_t e_ = (expr);                                                                 \
+    if (e_ != hipSuccess) return fail(PR_EHIP, "%s: %s", #expr, hipGetErrorString(e_));     \
+  } while (0)
+
+int gemm8_check(int M, int N, int K) {
+  if (M < 1 || N < 1 || K < 1) return fail(PR_EINVAL, "sizes must be >= 1 (M=%d N=%d K=%d)", M, N, K);
+  if (K >= 131072) return fail(PR_EUNSUPPORTED, "K = %d: sums of 131072 products may pass 32 bits", K);
+  if ((double)M * N > 1e12 || (double)((M + 127) / 128) * ((N + 127) / 128) > 2e9)
+    return fail(PR_EUNSUPPORTED, "problem too large");
+  return PR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pararnn_gemm_i8_workspace_bytes(int M, int N, int K) {
+  clear_error();
+  if (gemm8_check(M, N, K) != PR_OK) return 0;
+  int kper;
+  const int s = gemm8_splits(M, N, K, &kper);
+  const size_t need = s > 1 ? (size_t)s * M * N * 4 : 0;
+  return need > 256 ? (need + 255) & ~(size_t)255 : 256;
+}
+
+int pararnn_gemm_i8(int dtype, int M, int N, int K, const signed char *a, long long lda, const float *sa,
+                    const signed char *w, long long ldw, const float *sw, const void *bias, void *out, long long ldo,
+                    void *workspace, size_t ws_bytes, void *stream) {
+  clear_error();
+  if (dtype != PR_F32 && dtype != PR_BF16) return fail(PR_EINVAL, "unknown dtype %d", dtype);
+  const int rc = gemm8_check(M, N, K);
+  if (rc != PR_OK) return rc;
+  if (!a || !sa || !w || !sw || !out) return fail(PR_EINVAL, "a, sa, w, sw and out are required");
+  if (lda < K || ldw < K || ldo < N)
+    return fail(PR_EINVAL, "row strides %lld, %lld, %lld are below K = %d, K, N = %d", lda, ldw, ldo, K, N);
+  const size_t need = pararnn_gemm_i8_workspace_bytes(M, N, K);
+  if (!workspace || ws_bytes < need) return fail(PR_EWORKSPACE, "workspace %zu bytes < %zu", ws_bytes, need);
+  if (((uintptr_t)workspace & 255) != 0) return fail(PR_EINVAL, "workspace must be 256-byte aligned");
+  Gemm8Args g{};
+  g.a = (const int8_t *)a; g.w = (const int8_t *)w; g.sa = sa; g.sw = sw; g.bias = bias; g.out = out;
+  g.part = (int *)workspace; g.lda = lda; g.ldw = ldw; g.ldo = ldo; g.M = M; g.N = N; g.K = K;
+  g.splits = gemm8_splits(M, N, K, &g.kper);
+  const bool al = K % 16 == 0 && lda % 16 == 0 && ldw % 16 == 0 && (((uintptr_t)a | (uintptr_t)w) & 15) == 0;
+  hipStream_t s = (hipStream_t)stream;
+  if (dtype == PR_BF16) HIPCHK((al ? gemm8_go<uint16_t, true>(g, s) : gemm8_go<uint16_t, false>(g, s)));
+  else HIPCHK((al ? gemm8_go<float, true>(g, s) : gemm8_go<float, false>(g, s)));
+  return PR_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,399 @@
+// Selective state space scan: the C entry points, the kernels that join the
+// time segments and the partial sums, and the single-token step.
+#include <string>
+
+#include "pararnn.h"
+#include "ssm.h"
+
+namespace pr {
+
+// ---------------------------------------------------------------------------
+// joining the segments
+// ---------------------------------------------------------------------------
+// agg[b][s] (end state of segment s from zero) becomes the state that enters
+// segment s; a segment's decay is exp(A sum of delta).  REV: the same from
+// the last segment back, for the adjoint's carry.  One thread per (b, d, n).
+template <bool REV>
+__global__ void k_ssm_join(const float *__restrict__ A, const float *__restrict__ first,
+                           const float *__restrict__ sumd, float *__restrict__ agg, int B, int D, int N, int S) {
+  const long long dn = (long long)D * N, i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= B * dn) return;
+  const long long b = i / dn, e = i % dn;
+  const int d = (int)(e / N);
+  const float A2 = A[e] * 1.4426950408889634f;
+  float carry = first ? first[i] : 0.f;
+  const float *sd = sumd + b * S * D + d;
+  float *ag = agg + b * S * dn + e;
+  constexpr int U = 8;  // segments whose loads are in flight together
+  for (int s0 = 0; s0 < S; s0 += U) {
+    float v[U], m[U];
+#pragma unroll
+    for (int q = 0; q < U; q++) {
+      const int s = REV ? S - 1 - s0 - q : s0 + q;
+      const bool in = s0 + q < S;
+      v[q] = in ? ag[s * dn] : 0.f;
+      m[q] = in ? sd[(long long)s * D] : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < U; q++) {
+      const int s = REV ? S - 1 - s0 - q : s0 + q;
+      if (s0 + q < S) {
+        ag[s * dn] = carry;
+        carry = fmaf(__builtin_amdgcn_exp2f(m[q] * A2), carry, v[q]);
+      }
+    }
+  }
+}
+
+// dB and dC of each (b, t, group, n): the sum over the group's channel blocks
+template <typename T>
+__global__ void k_ssm_bc_sum(const float *__restrict__ part, int nblk, int B, int T_, int G, int N, int NP,
+                             const int *__restrict__ lengths, View dB, View dC) {
+  const long long rows = (long long)B * T_ * G, cols = 2LL * NP;
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= rows * cols) return;
+  const int n2 = (int)(i % cols), n = n2 % NP;
+  if (n >= N) return;
+  const long long row = i / cols;
+  const int g = (int)(row % G);
+  const long long bt = row / G;
+  const int t = (int)(bt % T_), b = (int)(bt / T_);
+  const View &v = n2 < NP ? dB : dC;
+  if (!v.p) return;
+  float s = 0.f;
+  if (t < seq_len(lengths, b, T_)) {
+#pragma unroll 8
+    for (int k = 0; k < nblk; k++) s += part[k * rows * cols + i];
+  }
+  stf((T *)v.p, b * v.sb + t * v.st + (long long)g * N + n, s);
+}
+
+// 64 columns by 4 slices of the partials per block
+__global__ void k_part_sum(const float *__restrict__ part, int P, long long stride, long long cols,
+                           float *__restrict__ out) {
+  __shared__ double sh[4][64];
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  const long long j = (long long)blockIdx.x * 64 + x;
+  double s = 0;
+  if (j < cols) {
+#pragma unroll 4
+    for (int p = y; p < P; p += 4) s += (double)part[p * stride + j];
+  }
+  sh[y][x] = s;
+  __syncthreads();
+  if (y == 0 && j < cols) out[j] = (float)((sh[0][x] + sh[1][x]) + (sh[2][x] + sh[3][x]));
+}
+
+hipError_t launch_part_sum(const float *part, int P, long long stride, long long cols, float *out, hipStream_t s) {
+  if (cols < 1) return hipSuccess;
+  k_part_sum<<<dim3((unsigned)((cols + 63) / 64)), 256, 0, s>>>(part, P, stride, cols, out);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// one token
+// ---------------------------------------------------------------------------
+struct SsmStepArgs {
+  const void *u, *dt, *z, *Bm, *Cm;
+  void *y;
+  long long su, sdt, sz, sB, sC, sy;  // row strides
+  const float *A, *Dk, *bias;
+  float *state;
+  const int *slots;
+  int B, D, N, G, nslots, softplus;
+};
+
+// LG lanes (a power of two) per channel, 4 states each; the state is read and
+// written once, 16 bytes a lane where N is a multiple of 4.
+template <typename T, int LG>
+__global__ __launch_bounds__(256) void k_ssm_step(SsmStepArgs a) {
+  const int lane = threadIdx.x % LG;
+  const int d = (int)(blockIdx.x * (256 / LG) + threadIdx.x / LG), b = blockIdx.y;
+  const bool on = d < a.D;
+  const int slot = a.slots ? a.slots[b] : b;
+  const bool live = slot >= 0 && slot < a.nslots;
+  const int dd = on ? d : 0;
+  float acc = 0.f, u = 0.f, zz = 0.f;
+  if (live && on) {
+    u = ldf((const T *)a.u, b * a.su + dd);
+    float v = ldf((const T *)a.dt, b * a.sdt + dd) + (a.bias ? a.bias[dd] : 0.f);
+    if (a.z) zz = ldf((const T *)a.z, b * a.sz + dd);
+    if (a.softplus) v = softplus_f(v);
+    const float x = v * u;
+    const int g = dd / (a.D / a.G), n0 = lane * 4;
+    const T *bp = (const T *)a.Bm + b * a.sB + (long long)g * a.N;
+    const T *cp = (const T *)a.Cm + b * a.sC + (long long)g * a.N;
+    const float *ap = a.A + (long long)dd * a.N;
+    float *hp = a.state + ((long long)slot * a.D + dd) * a.N;
+    float h[4], A[4];
+    const bool v4 = (a.N & 3) == 0 && n0 < a.N;
+    if (v4) {
+      const float4 h4 = *reinterpret_cast<const float4 *>(hp + n0), a4 = *reinterpret_cast<const float4 *>(ap + n0);
+      h[0] = h4.x; h[1] = h4.y; h[2] = h4.z; h[3] = h4.w;
+      A[0] = a4.x; A[1] = a4.y; A[2] = a4.z; A[3] = a4.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        h[k] = n0 + k < a.N ? hp[n0 + k] : 0.f;
+        A[k] = n0 + k < a.N ? ap[n0 + k] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const float bb = n0 + k < a.N ? ldf(bp, n0 + k) : 0.f, cc = n0 + k < a.N ? ldf(cp, n0 + k) : 0.f;
+      h[k] = fmaf(__builtin_amdgcn_exp2f(v * (A[k] * 1.4426950408889634f)), h[k], x * bb);
+      acc = fmaf(cc, h[k], acc);
+    }
+    if (v4) {
+      *reinterpret_cast<float4 *>(hp + n0) = make_float4(h[0], h[1], h[2], h[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        if (n0 + k < a.N) hp[n0 + k] = h[k];
+    }
+  }
+#pragma unroll
+  for (int o = LG / 2; o >= 1; o >>= 1) acc += __shfl_xor(acc, o, 64);
+  if (lane == 0 && on) {
+    float y = 0.f;
+    if (live) {
+      y = a.Dk ? fmaf(a.Dk[d], u, acc) : acc;
+      if (a.z) y *= zz * fsigm(zz);
+    }
+    stf((T *)a.y, b * a.sy + d, y);
+  }
+}
+
+template <typename T>
+hipError_t launch_step(const SsmStepArgs &a, hipStream_t s) {
+  const int q = (a.N + 3) / 4;
+#define PR_STEP(LG)                                                                           \
+  {                                                                                           \
+    k_ssm_step<T, LG><<<dim3((unsigned)((a.D + 256 / LG - 1) / (256 / LG)), (unsigned)a.B), 256, 0, s>>>(a); \
+    return hipGetLastError();                                                                 \
+  }
+  if (q <= 1) PR_STEP(1)
+  if (q <= 2) PR_STEP(2)
+  if (q <= 4) PR_STEP(4)
+  if (q <= 8) PR_STEP(8)
+  PR_STEP(16)
+#undef PR_STEP
+}
+
+}  // namespace pr
+
+using namespace pr;
+
+namespace {
+
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+#define HIPCHK(expr)                                                                        \
+  do {                                                                                      \
+    hipError_t e_ = (expr);                                                                 \
+    if (e_ != hipSuccess) return fail(PR_EHIP, "%s: %s", #expr, hipGetErrorString(e_));     \
+  } while (0)
+
+struct SsmPlan {
+  int cbg = 0, NP = 0, S = 1, seglen = 0, S_adj = 1, seglen_adj = 0;
+  size_t off_agg = 0, off_sumd = 0, off_part = 0, off_pA = 0, off_pD = 0, fwd_bytes = 0, adj_bytes = 0;
+};
+
+// Time segments for `blocks` blocks of `waves` wavefronts over T steps.
+void split_time(long long waves, int T, int *S, int *seglen) {
+  const long long tiles = (T + SSM_TL - 1) / SSM_TL;
+  long long s = 1;
+  if (waves < 1024) s = (2048 + waves - 1) / waves;
+  const long long most = (tiles + 3) / 4;  // at least four tiles each
+  if (s > most) s = most;
+  if (s < 1) s = 1;
+  const long long per = (tiles + s - 1) / s;
+  *seglen = (int)(per * SSM_TL);
+  *S = (int)((tiles + per - 1) / per);
+}
+
+int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
+  if (!p) return fail(PR_EINVAL, "problem is NULL");
+  if (p->dtype != PR_F32 && p->dtype != PR_BF16) return fail(PR_EINVAL, "unknown dtype %d", p->dtype);
+  if (p->B < 1 || p->T < 1 || p->D < 1 || p->N < 1 || p->G < 1)
+    return fail(PR_EINVAL, "sizes must be >= 1 (B=%d T=%d D=%d N=%d G=%d)", p->B, p->T, p->D, p->N, p->G);
+  if (p->D % p->G != 0) return fail(PR_EINVAL, "G = %d does not divide D = %d", p->G, p->D);
+  if (p->N > 64) return fail(PR_EUNSUPPORTED, "N = %d states: at most 64", p->N);
+  if (p->T > (1 << 30)) return fail(PR_EUNSUPPORTED, "T = %d: at most 2^30", p->T);
+  const SsmGeom g = ssm_geom(p->N);
+  const int dpg = p->D / p->G;
+  pl->cbg = (dpg + 63) / 64;
+  pl->NP = g.ns * g.lpc;
+  const long long blocks = (long long)p->B * p->G * pl->cbg;
+  if (blocks > (1LL << 24)) return fail(PR_EUNSUPPORTED, "problem too large: %lld channel blocks", blocks);
+  split_time(blocks * g.lpc, p->T, &pl->S, &pl->seglen);
+  split_time(blocks * g.lpc, p->T, &pl->S_adj, &pl->seglen_adj);
+  const size_t dn = (size_t)p->D * p->N, sm = pl->S > pl->S_adj ? pl->S : pl->S_adj;
+  if ((double)p->B * sm * dn * 4 > 1e13 || (double)p->B * p->T * p->G * pl->cbg * pl->NP * 8 > 1e13)
+    return fail(PR_EUNSUPPORTED, "problem too large");
+  size_t o = 0;
+  pl->off_agg = o; o = align256(o + (sm > 1 ? p->B * sm * dn * 4 : 0));
+  pl->off_sumd = o; o = align256(o + (sm > 1 ? p->B * sm * p->D * 4 : 0));
+  pl->fwd_bytes = o > 256 ? o : 256;
+  pl->off_part = o; o = align256(o + (size_t)pl->cbg * p->B * p->T * p->G * 2 * pl->NP * 4);
+  pl->off_pA = o; o = align256(o + p->B * (size_t)pl->S_adj * dn * 4);
+  pl->off_pD = o; o = align256(o + p->B * (size_t)pl->S_adj * 2 * p->D * 4);
+  pl->adj_bytes = o;
+  return PR_OK;
+}
+
+View view(const pr_view *v) {
+  View r{nullptr, 0, 0};
+  if (v) r = View{v->p, v->sb, v->st};
+  return r;
+}
+
+// vectors of four elements may be used on it
+bool vec4_ok(const View &v, int esz) {
+  return v.p == nullptr || (((uintptr_t)v.p % (4 * esz)) == 0 && v.sb % 4 == 0 && v.st % 4 == 0);
+}
+
+int ssm_fill(const pr_ssm_problem *p, const SsmPlan &pl, const pr_ssm_inputs *in, SsmArgs *a) {
+  if (!in) return fail(PR_EINVAL, "inputs are NULL");
+  if (!in->u.p || !in->dt.p || !in->B.p || !in->C.p || !in->A) return fail(PR_EINVAL, "u, dt, A, B and C are required");
+  a->u = view(&in->u); a->dt = view(&in->dt); a->z = view(&in->z); a->Bm = view(&in->B); a->Cm = view(&in->C);
+  a->A = in->A; a->Dk = in->D; a->bias = in->dt_bias; a->h0 = in->h0; a->lengths = in->lengths;
+  a->B = p->B; a->T = p->T; a->D = p->D; a->N = p->N; a->G = p->G; a->softplus = p->softplus != 0;
+  a->dpg = p->D / p->G; a->cbg = pl.cbg;
+  const int esz = p->dtype == PR_BF16 ? 2 : 4;
+  a->vec = a->dpg % 4 == 0 && vec4_ok(a->u, esz) && vec4_ok(a->dt, esz) && vec4_ok(a->z, esz);
+  a->vecn = p->N % 4 == 0 && vec4_ok(a->Bm, esz) && vec4_ok(a->Cm, esz);
+  if (p->N % 4 == 0 && (((uintptr_t)in->A | (uintptr_t)in->h0) & 15))
+    return fail(PR_EINVAL, "A and h0 must be 16-byte aligned");
+  return PR_OK;
+}
+
+int launch_ssm(int dtype, const SsmArgs &a, int what, hipStream_t s) {
+  const hipError_t e = dtype == PR_BF16 ? launch_ssm_bf16(a, what, s) : launch_ssm_f32(a, what, s);
+  if (e != hipSuccess) return fail(PR_EHIP, "selective scan kernel: %s", hipGetErrorString(e));
+  return PR_OK;
+}
+
+int check_ws(const void *ws, size_t have, size_t need) {
+  if (!ws || have < need) return fail(PR_EWORKSPACE, "workspace %zu bytes < %zu", have, need);
+  if (((uintptr_t)ws & 255) != 0) return fail(PR_EINVAL, "workspace must be 256-byte aligned");
+  return PR_OK;
+}
+
+template <bool REV>
+int join(const SsmArgs &a, const float *first, hipStream_t s) {
+  const long long n = (long long)a.B * a.D * a.N;
+  k_ssm_join<REV><<<dim3((unsigned)((n + 255) / 256)), 256, 0, s>>>(a.A, first, a.sumd, a.agg, a.B, a.D, a.N, a.S);
+  HIPCHK(hipGetLastError());
+  return PR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pararnn_ssm_workspace_bytes(const pr_ssm_problem *p, int with_adjoint) {
+  clear_error();
+  SsmPlan pl;
+  if (ssm_plan(p, &pl) != PR_OK) return 0;
+  return with_adjoint ? pl.adj_bytes : pl.fwd_bytes;
+}
+
+int pararnn_ssm_scan(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_view *y, float *h_last, float *states,
+                     void *workspace, size_t ws_bytes, void *stream) {
+  clear_error();
+  SsmPlan pl;
+  int rc = ssm_plan(p, &pl);
+  if (rc != PR_OK) return rc;
+  SsmArgs a{};
+  rc = ssm_fill(p, pl, in, &a);
+  if (rc != PR_OK) return rc;
+  if (!y || !y->p) return fail(PR_EINVAL, "y is required");
+  rc = check_ws(workspace, ws_bytes, pl.fwd_bytes);
+  if (rc != PR_OK) return rc;
+  a.y = view(y);
+  a.vec = a.vec && vec4_ok(a.y, p->dtype == PR_BF16 ? 2 : 4);
+  a.hlast = h_last; a.states = states;
+  if (p->N % 4 == 0 && (((uintptr_t)h_last | (uintptr_t)states) & 15))
+    return fail(PR_EINVAL, "h_last and states must be 16-byte aligned");
+  char *ws = (char *)workspace;
+  a.agg = (float *)(ws + pl.off_agg); a.sumd = (float *)(ws + pl.off_sumd);
+  a.S = pl.S; a.seglen = pl.seglen;
+  hipStream_t s = (hipStream_t)stream;
+  if (a.S > 1) {
+    if ((rc = launch_ssm(p->dtype, a, SSM_FWD_AGG, s)) != PR_OK) return rc;
+    if ((rc = join<false>(a, a.h0, s)) != PR_OK) return rc;
+  }
+  return launch_ssm(p->dtype, a, SSM_FWD, s);
+}
+
+int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const float *states, const pr_view *dy,
+                        const float *dh_last, const pr_ssm_grads *gr, void *workspace, size_t ws_bytes, void *stream) {
+  clear_error();
+  SsmPlan pl;
+  int rc = ssm_plan(p, &pl);
+  if (rc != PR_OK) return rc;
+  SsmArgs a{};
+  rc = ssm_fill(p, pl, in, &a);
+  if (rc != PR_OK) return rc;
+  if (!states || !dy || !dy->p || !gr) return fail(PR_EINVAL, "states, dy and the gradients' struct are required");
+  if (gr->z.p && !in->z.p) return fail(PR_EINVAL, "dz without z");
+  rc = check_ws(workspace, ws_bytes, pl.adj_bytes);
+  if (rc != PR_OK) return rc;
+  const int esz = p->dtype == PR_BF16 ? 2 : 4;
+  a.states = (float *)states; a.dhlast = dh_last; a.dh0 = gr->h0;
+  a.dy = view(dy); a.du = view(&gr->u); a.ddt = view(&gr->dt); a.dz = view(&gr->z);
+  a.dB = view(&gr->B); a.dC = view(&gr->C);
+  a.vec = a.vec && vec4_ok(a.dy, esz) && vec4_ok(a.du, esz) && vec4_ok(a.ddt, esz) && vec4_ok(a.dz, esz);
+  if (p->N % 4 == 0 && (((uintptr_t)states | (uintptr_t)dh_last | (uintptr_t)gr->h0) & 15))
+    return fail(PR_EINVAL, "states, dh_last and dh0 must be 16-byte aligned");
+  char *ws = (char *)workspace;
+  a.agg = (float *)(ws + pl.off_agg); a.sumd = (float *)(ws + pl.off_sumd);
+  a.part = (float *)(ws + pl.off_part); a.pA = (float *)(ws + pl.off_pA); a.pD = (float *)(ws + pl.off_pD);
+  a.S = pl.S_adj; a.seglen = pl.seglen_adj;
+  hipStream_t s = (hipStream_t)stream;
+  if (a.S > 1) {
+    if ((rc = launch_ssm(p->dtype, a, SSM_ADJ_AGG, s)) != PR_OK) return rc;
+    if ((rc = join<true>(a, dh_last, s)) != PR_OK) return rc;
+  }
+  if ((rc = launch_ssm(p->dtype, a, SSM_ADJ, s)) != PR_OK) return rc;
+  const int P = a.B * a.S;
+  const long long dn = (long long)a.D * a.N;
+  if (a.dB.p || a.dC.p) {
+    const long long n = (long long)a.B * a.T * a.G * 2 * pl.NP;
+    const dim3 grid((unsigned)((n + 255) / 256));
+    if (p->dtype == PR_BF16)
+      k_ssm_bc_sum<uint16_t><<<grid, 256, 0, s>>>(a.part, a.cbg, a.B, a.T, a.G, a.N, pl.NP, a.lengths, a.dB, a.dC);
+    else
+      k_ssm_bc_sum<float><<<grid, 256, 0, s>>>(a.part, a.cbg, a.B, a.T, a.G, a.N, pl.NP, a.lengths, a.dB, a.dC);
+    HIPCHK(hipGetLastError());
+  }
+  if (gr->A) HIPCHK(launch_part_sum(a.pA, P, dn, dn, gr->A, s));
+  if (gr->D) HIPCHK(launch_part_sum(a.pD, P, 2LL * a.D, a.D, gr->D, s));
+  if (gr->dt_bias) HIPCHK(launch_part_sum(a.pD + a.D, P, 2LL * a.D, a.D, gr->dt_bias, s));
+  return PR_OK;
+}
+
+int pararnn_ssm_step(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_view *y, float *state, int nslots,
+                     const int *slots, void *stream) {
+  clear_error();
+  SsmPlan pl;
+  int rc = ssm_plan(p, &pl);
+  if (rc != PR_OK) return rc;
+  if (!in) return fail(PR_EINVAL, "inputs are NULL");
+  if (!in->u.p || !in->dt.p || !in->B.p || !in->C.p || !in->A || !y || !y->p || !state)
+    return fail(PR_EINVAL, "u, dt, A, B, C, y and the states are required");
+  if (nslots < 1 || (!slots && nslots < p->B)) return fail(PR_EINVAL, "%d states for %d sequences", nslots, p->B);
+  if (p->B > 65535) return fail(PR_EUNSUPPORTED, "B = %d: at most 65535", p->B);
+  if (p->N % 4 == 0 && (((uintptr_t)state | (uintptr_t)in->A) & 15))
+    return fail(PR_EINVAL, "A and the states must be 16-byte aligned");
+  SsmStepArgs a{};
+  a.u = in->u.p; a.dt = in->dt.p; a.z = in->z.p; a.Bm = in->B.p; a.Cm = in->C.p; a.y = y->p;
+  a.su = in->u.sb; a.sdt = in->dt.sb; a.sz = in->z.sb; a.sB = in->B.sb; a.sC = in->C.sb; a.sy = y->sb;
+  a.A = in->A; a.Dk = in->D; a.bias = in->dt_bias; a.state = state; a.slots = slots;
+  a.B = p->B; a.D = p->D; a.N = p->N; a.G = p->G; a.nslots = nslots; a.softplus = p->softplus != 0;
+  HIPCHK(p->dtype == PR_BF16 ? launch_step<uint16_t>(a, (hipStream_t)stream) : launch_step<float>(a, (hipStream_t)stream));
+  return PR_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,91 @@
+// Selective state space scan: arguments shared by its kernels and the ABI
+// layer (k_ssm.hip), and the device helpers that several of them use.
+#pragma once
+
+#include "internal.h"
+
+namespace pr {
+
+// A [B, T, channels] array: element (b, t, c) at p[b * sb + t * st + c].
+struct View {
+  void *p;
+  long long sb, st;
+};
+
+constexpr int SSM_TL = 16;  // steps per tile, and between two saved states
+
+struct SsmArgs {
+  View u, dt, z, Bm, Cm, y;          // z.p may be null
+  View dy, du, ddt, dz, dB, dC;      // adjoint; outputs may be null
+  const float *A, *Dk, *bias, *h0;   // Dk, bias, h0 may be null
+  const int *lengths;                // may be null
+  float *hlast, *states;             // may be null (states is required by the adjoint)
+  const float *dhlast;               // adjoint, may be null
+  float *dh0;                        // adjoint, may be null
+  float *agg, *sumd;                 // time split: per (b, segment) aggregates [D][N], sums of delta [D]
+  float *part;                       // adjoint: dB | dC partials [block of the group][B][T][G][2 NP]
+  float *pA, *pD;                    // adjoint: [B S][D][N] and [B S][2][D] partials of dA, dD | dbias
+  int B, T, D, N, G, softplus;
+  int dpg, cbg;                      // channels per group, channel blocks per group
+  int S, seglen;                     // time segments and their steps (a multiple of SSM_TL)
+  int vec, vecn;                     // channel arrays / B and C may be read in vectors
+};
+
+// States per lane and lanes per channel of the scan kernels for N states.
+struct SsmGeom {
+  int ns, lpc;
+};
+inline SsmGeom ssm_geom(int N) {
+  if (N <= 4) return {4, 1};
+  if (N <= 8) return {4, 2};
+  if (N <= 16) return {4, 4};
+  if (N <= 32) return {8, 4};
+  return {16, 4};
+}
+
+enum { SSM_FWD = 0, SSM_FWD_AGG = 1, SSM_ADJ = 2, SSM_ADJ_AGG = 3 };
+hipError_t launch_ssm_bf16(const SsmArgs &a, int what, hipStream_t s);
+hipError_t launch_ssm_f32(const SsmArgs &a, int what, hipStream_t s);
+
+// out[j] = sum over p of part[p * stride + j], j < cols, added in order in 64 bits
+hipError_t launch_part_sum(const float *part, int P, long long stride, long long cols, float *out, hipStream_t s);
+
+// e^x with a relative error near 1e-7 for any |x| below 80: the product with
+// log2(e) is carried in two words, which a single rounding of a large
+// argument would lose.
+__device__ inline float exp_acc(float x) {
+  const float L = 1.44269502162933349609f, Ll = 1.92596299112661746887e-8f;
+  const float p = x * L;
+  float r = fmaf(x, L, -p);
+  r = fmaf(x, Ll, r);
+  const float e = __builtin_amdgcn_exp2f(p);
+  // an infinite argument gives r = NaN, where e is already the answer
+  return fabsf(x) < 128.f ? fmaf(e, r * 0.6931471805599453f, e) : e;
+}
+
+// log(1 + e) for 0 <= e <= 1 by 2 artanh(s), s = e / (2 + e) <= 1/3: the
+// series in s^2 <= 1/9 is cut where its next term is below 2e-8 of the sum.
+__device__ inline float log1p_unit(float e) {
+  const float s = e * frcp(2.f + e), q = s * s;
+  float p = 1.f / 13.f;
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  p = p * q;
+  return fmaf(2.f * s, p, 2.f * s);
+}
+
+__device__ inline float softplus_f(float v) {
+  const float l = log1p_unit(exp_acc(-fabsf(v)));
+  return (v > 0.f ? v : 0.f) + l;  // a NaN comes through l
+}
+
+// Steps of sequence b: all T, or its length, held to 0..T.
+__device__ inline int seq_len(const int *lengths, int b, int T) {
+  const int n = lengths ? lengths[b] : T;
+  return n < 0 ? 0 : n > T ? T : n;
+}
+
+}  // namespace pr
