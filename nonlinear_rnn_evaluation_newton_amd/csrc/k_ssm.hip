@@ -220,6 +220,7 @@ int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
   if (p->D % p->G != 0) return fail(PR_EINVAL, "G = %d does not divide D = %d", p->G, p->D);
   if (p->N > 64) return fail(PR_EUNSUPPORTED, "N = %d states: at most 64", p->N);
   if (p->T > (1 << 30)) return fail(PR_EUNSUPPORTED, "T = %d: at most 2^30", p->T);
+  if (p->D > (1 << 22)) return fail(PR_EUNSUPPORTED, "D = %d: at most 2^22", p->D);
   const SsmGeom g = ssm_geom(p->N);
   const int dpg = p->D / p->G;
   pl->cbg = (dpg + 63) / 64;
@@ -253,6 +254,12 @@ bool vec4_ok(const View &v, int esz) {
   return v.p == nullptr || (((uintptr_t)v.p % (4 * esz)) == 0 && v.sb % 4 == 0 && v.st % 4 == 0);
 }
 
+// offsets within 16 steps are 31-bit
+int stride_ok(const View &v) {
+  if (v.p && (v.st < 0 || v.st > (1 << 24))) return fail(PR_EUNSUPPORTED, "time stride %lld: 0 to 2^24", v.st);
+  return PR_OK;
+}
+
 int ssm_fill(const pr_ssm_problem *p, const SsmPlan &pl, const pr_ssm_inputs *in, SsmArgs *a) {
   if (!in) return fail(PR_EINVAL, "inputs are NULL");
   if (!in->u.p || !in->dt.p || !in->B.p || !in->C.p || !in->A) return fail(PR_EINVAL, "u, dt, A, B and C are required");
@@ -261,15 +268,19 @@ int ssm_fill(const pr_ssm_problem *p, const SsmPlan &pl, const pr_ssm_inputs *in
   a->B = p->B; a->T = p->T; a->D = p->D; a->N = p->N; a->G = p->G; a->softplus = p->softplus != 0;
   a->dpg = p->D / p->G; a->cbg = pl.cbg;
   const int esz = p->dtype == PR_BF16 ? 2 : 4;
-  a->vec = a->dpg % 4 == 0 && vec4_ok(a->u, esz) && vec4_ok(a->dt, esz) && vec4_ok(a->z, esz);
-  a->vecn = p->N % 4 == 0 && vec4_ok(a->Bm, esz) && vec4_ok(a->Cm, esz);
+  a->vec = a->dpg % 4 == 0 && p->N % 4 == 0 && vec4_ok(a->u, esz) && vec4_ok(a->dt, esz) && vec4_ok(a->z, esz) &&
+           vec4_ok(a->Bm, esz) && vec4_ok(a->Cm, esz);
+  int rc = PR_OK;
+  for (const View *v : {&a->u, &a->dt, &a->z, &a->Bm, &a->Cm})
+    if ((rc = stride_ok(*v)) != PR_OK) return rc;
   if (p->N % 4 == 0 && (((uintptr_t)in->A | (uintptr_t)in->h0) & 15))
     return fail(PR_EINVAL, "A and h0 must be 16-byte aligned");
   return PR_OK;
 }
 
 int launch_ssm(int dtype, const SsmArgs &a, int what, hipStream_t s) {
-  const hipError_t e = dtype == PR_BF16 ? launch_ssm_bf16(a, what, s) : launch_ssm_f32(a, what, s);
+  const hipError_t e = dtype == PR_BF16 ? (a.vec ? launch_ssm_bf16_vec(a, what, s) : launch_ssm_bf16(a, what, s))
+                                        : (a.vec ? launch_ssm_f32_vec(a, what, s) : launch_ssm_f32(a, what, s));
   if (e != hipSuccess) return fail(PR_EHIP, "selective scan kernel: %s", hipGetErrorString(e));
   return PR_OK;
 }
@@ -312,6 +323,7 @@ int pararnn_ssm_scan(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_
   rc = check_ws(workspace, ws_bytes, pl.fwd_bytes);
   if (rc != PR_OK) return rc;
   a.y = view(y);
+  if ((rc = stride_ok(a.y)) != PR_OK) return rc;
   a.vec = a.vec && vec4_ok(a.y, p->dtype == PR_BF16 ? 2 : 4);
   a.hlast = h_last; a.states = states;
   if (p->N % 4 == 0 && (((uintptr_t)h_last | (uintptr_t)states) & 15))
@@ -344,6 +356,8 @@ int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const 
   a.states = (float *)states; a.dhlast = dh_last; a.dh0 = gr->h0;
   a.dy = view(dy); a.du = view(&gr->u); a.ddt = view(&gr->dt); a.dz = view(&gr->z);
   a.dB = view(&gr->B); a.dC = view(&gr->C);
+  for (const View *v : {&a.dy, &a.du, &a.ddt, &a.dz})
+    if ((rc = stride_ok(*v)) != PR_OK) return rc;
   a.vec = a.vec && vec4_ok(a.dy, esz) && vec4_ok(a.du, esz) && vec4_ok(a.ddt, esz) && vec4_ok(a.dz, esz);
   if (p->N % 4 == 0 && (((uintptr_t)states | (uintptr_t)dh_last | (uintptr_t)gr->h0) & 15))
     return fail(PR_EINVAL, "states, dh_last and dh0 must be 16-byte aligned");

@@ -28,7 +28,7 @@ struct SsmArgs {
   int B, T, D, N, G, softplus;
   int dpg, cbg;                      // channels per group, channel blocks per group
   int S, seglen;                     // time segments and their steps (a multiple of SSM_TL)
-  int vec, vecn;                     // channel arrays / B and C may be read in vectors
+  int vec;                           // all arrays may be moved in vectors of four
 };
 
 // States per lane and lanes per channel of the scan kernels for N states.
@@ -44,8 +44,11 @@ inline SsmGeom ssm_geom(int N) {
 }
 
 enum { SSM_FWD = 0, SSM_FWD_AGG = 1, SSM_ADJ = 2, SSM_ADJ_AGG = 3 };
+// _vec: a.vec, every array may be moved in vectors of four
 hipError_t launch_ssm_bf16(const SsmArgs &a, int what, hipStream_t s);
+hipError_t launch_ssm_bf16_vec(const SsmArgs &a, int what, hipStream_t s);
 hipError_t launch_ssm_f32(const SsmArgs &a, int what, hipStream_t s);
+hipError_t launch_ssm_f32_vec(const SsmArgs &a, int what, hipStream_t s);
 
 // out[j] = sum over p of part[p * stride + j], j < cols, added in order in 64 bits
 hipError_t launch_part_sum(const float *part, int P, long long stride, long long cols, float *out, hipStream_t s);
