@@ -31,8 +31,9 @@ __global__ void k_ssm_join(const float *__restrict__ A, const float *__restrict_
     for (int q = 0; q < U; q++) {
       const int s = REV ? S - 1 - s0 - q : s0 + q;
       const bool in = s0 + q < S;
-      v[q] = in ? ag[s * dn] : 0.f;
-      m[q] = in ? sd[(long long)s * D] : 0.f;
+      // (the last one in this order has no sum: nothing follows it)
+      v[q] = in && s0 + q + 1 < S ? ag[s * dn] : 0.f;
+      m[q] = in && s0 + q + 1 < S ? sd[(long long)s * D] : 0.f;
     }
 #pragma unroll
     for (int q = 0; q < U; q++) {
@@ -195,19 +196,22 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
   } while (0)
 
 struct SsmPlan {
-  int cbg = 0, NP = 0, S = 1, seglen = 0, S_adj = 1, seglen_adj = 0;
+  int cbg = 0, NP = 0, S = 1, seglen = 0;
   size_t off_agg = 0, off_sumd = 0, off_part = 0, off_pA = 0, off_pD = 0, fwd_bytes = 0, adj_bytes = 0;
 };
 
-// Time segments for `blocks` blocks of `waves` wavefronts over T steps.
-void split_time(long long waves, int T, int *S, int *seglen) {
+// Time segments for `blocks` blocks over T steps: a block for each CU, at
+// least four tiles each; a segment's extent in any array below 2^31 bytes (16
+// steps are).
+void split_time(long long blocks, int T, long long max_tile_bytes, int *S, int *seglen) {
   const long long tiles = (T + SSM_TL - 1) / SSM_TL;
-  long long s = 1;
-  if (waves < 1024) s = (2048 + waves - 1) / waves;
-  const long long most = (tiles + 3) / 4;  // at least four tiles each
+  long long s = (256 + blocks - 1) / blocks;
+  const long long most = (tiles + 3) / 4;
   if (s > most) s = most;
   if (s < 1) s = 1;
-  const long long per = (tiles + s - 1) / s;
+  long long per = (tiles + s - 1) / s;
+  const long long fit = ((1LL << 31) - (1LL << 30)) / max_tile_bytes;
+  if (per > fit) per = fit;
   *seglen = (int)(per * SSM_TL);
   *S = (int)((tiles + per - 1) / per);
 }
@@ -224,12 +228,18 @@ int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
   const SsmGeom g = ssm_geom(p->N);
   const int dpg = p->D / p->G;
   pl->cbg = (dpg + 63) / 64;
-  pl->NP = g.ns * g.lpc;
+  pl->NP = 4 * g.ns * g.ws;
   const long long blocks = (long long)p->B * p->G * pl->cbg;
   if (blocks > (1LL << 24)) return fail(PR_EUNSUPPORTED, "problem too large: %lld channel blocks", blocks);
-  split_time(blocks * g.lpc, p->T, &pl->S, &pl->seglen);
-  split_time(blocks * g.lpc, p->T, &pl->S_adj, &pl->seglen_adj);
-  const size_t dn = (size_t)p->D * p->N, sm = pl->S > pl->S_adj ? pl->S : pl->S_adj;
+  const int esz = p->dtype == PR_BF16 ? 2 : 4;
+  // rows as slices of projections up to four times as wide as they need be
+  const long long width = p->D > (long long)p->G * p->N ? p->D : (long long)p->G * p->N;
+  long long tile = SSM_TL * 4 * width * esz;
+  if (tile < (long long)p->D * p->N * 4) tile = (long long)p->D * p->N * 4;
+  if (tile < SSM_TL * 8LL * p->G * pl->NP) tile = SSM_TL * 8LL * p->G * pl->NP;
+  if (tile > (1LL << 27)) return fail(PR_EUNSUPPORTED, "problem too large: %lld bytes in 16 steps", tile);
+  split_time(blocks, p->T, tile, &pl->S, &pl->seglen);
+  const size_t dn = (size_t)p->D * p->N, sm = pl->S;
   if ((double)p->B * sm * dn * 4 > 1e13 || (double)p->B * p->T * p->G * pl->cbg * pl->NP * 8 > 1e13)
     return fail(PR_EUNSUPPORTED, "problem too large");
   size_t o = 0;
@@ -237,15 +247,15 @@ int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
   pl->off_sumd = o; o = align256(o + (sm > 1 ? p->B * sm * p->D * 4 : 0));
   pl->fwd_bytes = o > 256 ? o : 256;
   pl->off_part = o; o = align256(o + (size_t)pl->cbg * p->B * p->T * p->G * 2 * pl->NP * 4);
-  pl->off_pA = o; o = align256(o + p->B * (size_t)pl->S_adj * dn * 4);
-  pl->off_pD = o; o = align256(o + p->B * (size_t)pl->S_adj * 2 * p->D * 4);
+  pl->off_pA = o; o = align256(o + p->B * (size_t)pl->S * dn * 4);
+  pl->off_pD = o; o = align256(o + p->B * (size_t)pl->S * 2 * p->D * 4);
   pl->adj_bytes = o;
   return PR_OK;
 }
 
 View view(const pr_view *v) {
   View r{nullptr, 0, 0};
-  if (v) r = View{v->p, v->sb, v->st};
+  if (v && v->p) r = View{v->p, v->sb, v->st};  // an absent array has no strides
   return r;
 }
 
@@ -254,9 +264,10 @@ bool vec4_ok(const View &v, int esz) {
   return v.p == nullptr || (((uintptr_t)v.p % (4 * esz)) == 0 && v.sb % 4 == 0 && v.st % 4 == 0);
 }
 
-// offsets within 16 steps are 31-bit
-int stride_ok(const View &v) {
-  if (v.p && (v.st < 0 || v.st > (1 << 24))) return fail(PR_EUNSUPPORTED, "time stride %lld: 0 to 2^24", v.st);
+// a segment's offsets in an array are 31-bit, with the tiles fetched ahead
+int stride_ok(const View &v, const SsmPlan &pl, int esz) {
+  if (v.p && (v.st < 0 || (double)(pl.seglen + 8 * SSM_TL) * v.st * esz > 2147483000.0))
+    return fail(PR_EUNSUPPORTED, "time stride %lld over segments of %d steps passes 31 bits", v.st, pl.seglen);
   return PR_OK;
 }
 
@@ -272,7 +283,7 @@ int ssm_fill(const pr_ssm_problem *p, const SsmPlan &pl, const pr_ssm_inputs *in
            vec4_ok(a->Bm, esz) && vec4_ok(a->Cm, esz);
   int rc = PR_OK;
   for (const View *v : {&a->u, &a->dt, &a->z, &a->Bm, &a->Cm})
-    if ((rc = stride_ok(*v)) != PR_OK) return rc;
+    if ((rc = stride_ok(*v, pl, esz)) != PR_OK) return rc;
   if (p->N % 4 == 0 && (((uintptr_t)in->A | (uintptr_t)in->h0) & 15))
     return fail(PR_EINVAL, "A and h0 must be 16-byte aligned");
   return PR_OK;
@@ -323,7 +334,7 @@ int pararnn_ssm_scan(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_
   rc = check_ws(workspace, ws_bytes, pl.fwd_bytes);
   if (rc != PR_OK) return rc;
   a.y = view(y);
-  if ((rc = stride_ok(a.y)) != PR_OK) return rc;
+  if ((rc = stride_ok(a.y, pl, p->dtype == PR_BF16 ? 2 : 4)) != PR_OK) return rc;
   a.vec = a.vec && vec4_ok(a.y, p->dtype == PR_BF16 ? 2 : 4);
   a.hlast = h_last; a.states = states;
   if (p->N % 4 == 0 && (((uintptr_t)h_last | (uintptr_t)states) & 15))
@@ -357,14 +368,14 @@ int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const 
   a.dy = view(dy); a.du = view(&gr->u); a.ddt = view(&gr->dt); a.dz = view(&gr->z);
   a.dB = view(&gr->B); a.dC = view(&gr->C);
   for (const View *v : {&a.dy, &a.du, &a.ddt, &a.dz})
-    if ((rc = stride_ok(*v)) != PR_OK) return rc;
+    if ((rc = stride_ok(*v, pl, esz)) != PR_OK) return rc;
   a.vec = a.vec && vec4_ok(a.dy, esz) && vec4_ok(a.du, esz) && vec4_ok(a.ddt, esz) && vec4_ok(a.dz, esz);
   if (p->N % 4 == 0 && (((uintptr_t)states | (uintptr_t)dh_last | (uintptr_t)gr->h0) & 15))
     return fail(PR_EINVAL, "states, dh_last and dh0 must be 16-byte aligned");
   char *ws = (char *)workspace;
   a.agg = (float *)(ws + pl.off_agg); a.sumd = (float *)(ws + pl.off_sumd);
   a.part = (float *)(ws + pl.off_part); a.pA = (float *)(ws + pl.off_pA); a.pD = (float *)(ws + pl.off_pD);
-  a.S = pl.S_adj; a.seglen = pl.seglen_adj;
+  a.S = pl.S; a.seglen = pl.seglen;
   hipStream_t s = (hipStream_t)stream;
   if (a.S > 1) {
     if ((rc = launch_ssm(p->dtype, a, SSM_ADJ_AGG, s)) != PR_OK) return rc;

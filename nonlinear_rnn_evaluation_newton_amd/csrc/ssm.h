@@ -28,19 +28,20 @@ struct SsmArgs {
   int B, T, D, N, G, softplus;
   int dpg, cbg;                      // channels per group, channel blocks per group
   int S, seglen;                     // time segments and their steps (a multiple of SSM_TL)
+  int segs, seg0;                    // segments of a launch and the first of them (set by the launcher)
   int vec;                           // all arrays may be moved in vectors of four
 };
 
-// States per lane and lanes per channel of the scan kernels for N states.
+// States per lane and wavefronts per channel of the scan kernels for N states
+// (four lanes of a wavefront share a channel).
 struct SsmGeom {
-  int ns, lpc;
+  int ns, ws;
 };
 inline SsmGeom ssm_geom(int N) {
-  if (N <= 4) return {4, 1};
-  if (N <= 8) return {4, 2};
-  if (N <= 16) return {4, 4};
-  if (N <= 32) return {8, 4};
-  return {16, 4};
+  if (N <= 8) return {2, 1};
+  if (N <= 16) return {2, 2};
+  if (N <= 32) return {4, 2};
+  return {8, 2};
 }
 
 enum { SSM_FWD = 0, SSM_FWD_AGG = 1, SSM_ADJ = 2, SSM_ADJ_AGG = 3 };
@@ -83,6 +84,14 @@ __device__ inline float log1p_unit(float e) {
 __device__ inline float softplus_f(float v) {
   const float l = log1p_unit(exp_acc(-fabsf(v)));
   return (v > 0.f ? v : 0.f) + l;  // a NaN comes through l
+}
+
+// The same with a plain product for the exponential's argument: its error of
+// |v| 2^-24 is far below that of a v that was stored in 8 significant bits,
+// and five instructions fewer.
+__device__ inline float softplus_short(float v) {
+  const float l = log1p_unit(fexp(-fabsf(v)));
+  return (v > 0.f ? v : 0.f) + l;
 }
 
 // Steps of sequence b: all T, or its length, held to 0..T.
