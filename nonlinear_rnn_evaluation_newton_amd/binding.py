@@ -70,6 +70,13 @@ class SsmInputs(C.Structure):
                 ("D", C.c_void_p), ("dt_bias", C.c_void_p), ("h0", C.c_void_p), ("lengths", C.c_void_p)]
 
 
+class _SsmInputsFlat(C.Structure):
+    """The same layout without nested structures, which take longer to fill."""
+    _fields_ = [(a + "_" + f, c) for a in ("u", "dt", "z", "B", "C")
+                for f, c in (("p", C.c_void_p), ("sb", C.c_longlong), ("st", C.c_longlong))] + [
+        (a, C.c_void_p) for a in ("A", "D", "dt_bias", "h0", "lengths")]
+
+
 class SsmGrads(C.Structure):
     _fields_ = [("u", View), ("dt", View), ("z", View), ("B", View), ("C", View), ("A", C.c_void_p),
                 ("D", C.c_void_p), ("dt_bias", C.c_void_p), ("h0", C.c_void_p)]
@@ -329,35 +336,54 @@ def _strides(where, name, t, shape, adjacent):
         step *= shape[-k]
 
 
-def _need(where, name, t, shape, dtype, adjacent=1):
-    """The address of tensor t after a check of its shape, type and device;
-    None passes.  adjacent: trailing axes that must be laid out densely."""
-    if t is None:
-        return None
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{where}: {name} must be a {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+# These checks run on every call, single tokens' included, so they take the
+# short way through torch's attributes first.
+def _need(where, name, t, shape, dtype):
+    """The address of tensor t after a check of its shape, type, device and
+    adjacent last axis."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{where}: {name} must be a {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{where}: {name} must be on the GPU")
-    _strides(where, name, t, shape, adjacent)
+    if t.stride(-1) != 1:
+        _strides(where, name, t, shape, 1)
     return t.data_ptr()
 
 
 def _dense(where, name, t, shape, dtype):
-    return _need(where, name, t, shape, dtype, len(shape))
+    """The address of t, all of whose axes must be contiguous; None passes."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _need(where, name, t, shape, dtype)
+        _strides(where, name, t, shape, len(shape))
+    return t.data_ptr()
+
+
+def _flat(where, name, t, shape, dtype):
+    """The fields of a pr_view of t [B, T, channels] or, for single tokens, [B, channels]."""
+    if t is None:
+        return None, 0, 0
+    p = _need(where, name, t, shape, dtype)
+    s = t.stride()
+    return (p, s[0], s[1]) if len(s) == 3 else (p, s[0], 0)
 
 
 def _view(where, name, t, shape, dtype):
-    """pr_view of t [B, T, channels] or, for single tokens, [B, channels]."""
-    if t is None:
-        return View(None, 0, 0)
-    p = _need(where, name, t, shape, dtype)
-    return View(p, t.stride(0), t.stride(1) if len(shape) == 3 else 0)
+    return View(*_flat(where, name, t, shape, dtype))
+
+
+def _stream_of(t):
+    """The raw handle of the current stream of t's device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _rows(where, name, t, shape, dtype):
     if t is None:
         return None
-    return C.byref(Rows(_need(where, name, t, shape, dtype), t.stride(0)))
+    return C.byref(Rows(_need(where, name, t, shape, dtype), t.stride(0)))  # (one row: any stride)
 
 
 def _done(st, where, check=True):
@@ -384,7 +410,7 @@ def conv(x, w, bias, y, state_in=None, state_out=None, lengths=None, silu: bool 
                             _dense(n, "bias", bias, (D,), dt), _dense(n, "state_in", state_in, (B, W - 1, D), dt),
                             _dense(n, "lengths", lengths, (B,), torch.int32),
                             C.byref(_view(n, "y", y, (B, T, D), dt)),
-                            _dense(n, "state_out", state_out, (B, W - 1, D), dt), _stream())
+                            _dense(n, "state_out", state_out, (B, W - 1, D), dt), _stream_of(x))
     return _done(st, "pararnn_conv", check)
 
 
@@ -400,7 +426,7 @@ def conv_adjoint(x, w, bias, dy, dx, dw, dbias, workspace, state_in=None, dstate
         _dense(n, "lengths", lengths, (B,), torch.int32), C.byref(_view(n, "dy", dy, (B, T, D), dt)),
         _dense(n, "dstate_out", dstate_out, (B, W - 1, D), dt), C.byref(_view(n, "dx", dx, (B, T, D), dt)),
         _dense(n, "dw", dw, (D, W), f32), _dense(n, "dbias", dbias, (D,), f32),
-        _dense(n, "dstate_in", dstate_in, (B, W - 1, D), dt), *_ws(workspace), _stream())
+        _dense(n, "dstate_in", dstate_in, (B, W - 1, D), dt), *_ws(workspace), _stream_of(x))
     return _done(st, "pararnn_conv_adjoint", check)
 
 
@@ -413,7 +439,7 @@ def conv_step(x, w, bias, state, y, slots=None, silu: bool = True, check: bool =
     st = lib().pararnn_conv_step(C.byref(pb), C.byref(_view(n, "x", x, (B, D), dt)), _dense(n, "w", w, (D, W), dt),
                                  _dense(n, "bias", bias, (D,), dt), _dense(n, "state", state, (pool, W - 1, D), dt),
                                  pool, _dense(n, "slots", slots, (B,), torch.int32),
-                                 C.byref(_view(n, "y", y, (B, D), dt)), _stream())
+                                 C.byref(_view(n, "y", y, (B, D), dt)), _stream_of(x))
     return _done(st, "pararnn_conv_step", check)
 
 
@@ -430,16 +456,16 @@ def ssm_states_shape(B: int, T: int, D: int, N: int):
 def _ssm(where, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, softplus):
     import torch
     st, f32 = u.dtype, torch.float32
-    shape, (ch, N) = tuple(u.shape), A.shape
+    shape, (ch, N) = u.shape, A.shape
     B, T = shape[0], shape[1] if len(shape) == 3 else 1
     width = Bm.shape[-1]
     if width % N or not width:
         raise ValueError(f"{where}: B has {width} columns, not a multiple of the {N} states of A")
     bc = shape[:-1] + (width,)
     pb = SsmProblem(_dtype_code(st, where), B, T, shape[-1], N, width // N, int(softplus))
-    return pb, SsmInputs(
-        _view(where, "u", u, shape, st), _view(where, "dt", dt, shape, st), _view(where, "z", z, shape, st),
-        _view(where, "B", Bm, bc, st), _view(where, "C", Cm, bc, st), _dense(where, "A", A, (shape[-1], N), f32),
+    return pb, _SsmInputsFlat(
+        *_flat(where, "u", u, shape, st), *_flat(where, "dt", dt, shape, st), *_flat(where, "z", z, shape, st),
+        *_flat(where, "B", Bm, bc, st), *_flat(where, "C", Cm, bc, st), _dense(where, "A", A, (shape[-1], N), f32),
         _dense(where, "D", D, (ch,), f32), _dense(where, "dt_bias", dt_bias, (ch,), f32),
         _dense(where, "h0", h0, (B, ch, N), f32), _dense(where, "lengths", lengths, (B,), torch.int32))
 
@@ -451,10 +477,10 @@ def ssm_scan(u, dt, A, Bm, Cm, y, workspace, D=None, z=None, dt_bias=None, h0=No
     n = "ssm_scan"
     pb, inp = _ssm(n, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, softplus)
     st = lib().pararnn_ssm_scan(
-        C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, tuple(u.shape), u.dtype)),
+        C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, u.shape, u.dtype)),
         _dense(n, "h_last", h_last, (pb.B, pb.D, pb.N), torch.float32),
         _dense(n, "states", states, ssm_states_shape(pb.B, pb.T, pb.D, pb.N), torch.float32), *_ws(workspace),
-        _stream())
+        _stream_of(u))
     return _done(st, "pararnn_ssm_scan", check)
 
 
@@ -465,7 +491,7 @@ def ssm_scan_adjoint(u, dt, A, Bm, Cm, states, dy, workspace, D=None, z=None, dt
     import torch
     n, f32 = "ssm_scan_adjoint", torch.float32
     pb, inp = _ssm(n, u, dt, A, Bm, Cm, D, z, dt_bias, None, lengths, softplus)
-    shape, bc, t = tuple(u.shape), tuple(Bm.shape), u.dtype
+    shape, bc, t = u.shape, Bm.shape, u.dtype
     gr = SsmGrads(_view(n, "du", du, shape, t), _view(n, "ddt", ddt, shape, t), _view(n, "dz", dz, shape, t),
                   _view(n, "dB", dB, bc, t), _view(n, "dC", dC, bc, t), _dense(n, "dA", dA, (pb.D, pb.N), f32),
                   _dense(n, "dD", dD, (pb.D,), f32), _dense(n, "ddt_bias", ddt_bias, (pb.D,), f32),
@@ -473,7 +499,7 @@ def ssm_scan_adjoint(u, dt, A, Bm, Cm, states, dy, workspace, D=None, z=None, dt
     st = lib().pararnn_ssm_adjoint(
         C.byref(pb), C.byref(inp), _dense(n, "states", states, ssm_states_shape(pb.B, pb.T, pb.D, pb.N), f32),
         C.byref(_view(n, "dy", dy, shape, t)), _dense(n, "dh_last", dh_last, (pb.B, pb.D, pb.N), f32), C.byref(gr),
-        *_ws(workspace), _stream())
+        *_ws(workspace), _stream_of(u))
     return _done(st, "pararnn_ssm_adjoint", check)
 
 
@@ -484,9 +510,9 @@ def ssm_step(u, dt, A, Bm, Cm, state, y, D=None, z=None, dt_bias=None, slots=Non
     n = "ssm_step"
     pb, inp = _ssm(n, u, dt, A, Bm, Cm, D, z, dt_bias, None, None, softplus)
     pool = state.shape[0]
-    st = lib().pararnn_ssm_step(C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, tuple(u.shape), u.dtype)),
+    st = lib().pararnn_ssm_step(C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, u.shape, u.dtype)),
                                 _dense(n, "state", state, (pool, pb.D, pb.N), torch.float32), pool,
-                                _dense(n, "slots", slots, (pb.B,), torch.int32), _stream())
+                                _dense(n, "slots", slots, (pb.B,), torch.int32), _stream_of(u))
     return _done(st, "pararnn_ssm_step", check)
 
 
@@ -500,7 +526,7 @@ def rmsnorm(x, w, y=None, residual=None, sum_out=None, q=None, scale=None, eps: 
         C.byref(pb), _rows(where, "x", x, (rows, n), dt), _rows(where, "residual", residual, (rows, n), dt),
         _dense(where, "w", w, (n,), dt), _rows(where, "sum_out", sum_out, (rows, n), dt),
         _rows(where, "y", y, (rows, n), dt), _rows(where, "q", q, (rows, n), torch.int8),
-        _dense(where, "scale", scale, (rows,), torch.float32), _stream())
+        _dense(where, "scale", scale, (rows,), torch.float32), _stream_of(x))
     return _done(st, "pararnn_rmsnorm", check)
 
 
@@ -516,7 +542,7 @@ def rmsnorm_adjoint(s, w, dy, dx, dw, workspace, dsum=None, eps: float = 1e-5, c
     st = lib().pararnn_rmsnorm_adjoint(
         C.byref(pb), _rows(where, "s", s, (rows, n), dt), _dense(where, "w", w, (n,), dt),
         _rows(where, "dy", dy, (rows, n), dt), _rows(where, "dsum", dsum, (rows, n), dt),
-        _rows(where, "dx", dx, (rows, n), dt), _dense(where, "dw", dw, (n,), torch.float32), *_ws(workspace), _stream())
+        _rows(where, "dx", dx, (rows, n), dt), _dense(where, "dw", dw, (n,), torch.float32), *_ws(workspace), _stream_of(s))
     return _done(st, "pararnn_rmsnorm_adjoint", check)
 
 
@@ -527,7 +553,7 @@ def quant_rows(x, q, scale, check: bool = True) -> int:
     pb = NormProblem(_dtype_code(dt, where), n, rows, 0.0)
     st = lib().pararnn_quant_rows(C.byref(pb), _rows(where, "x", x, (rows, n), dt),
                                   _rows(where, "q", q, (rows, n), torch.int8),
-                                  _dense(where, "scale", scale, (rows,), torch.float32), _stream())
+                                  _dense(where, "scale", scale, (rows,), torch.float32), _stream_of(x))
     return _done(st, "pararnn_quant_rows", check)
 
 
@@ -543,7 +569,7 @@ def gemm_i8(a, a_scale, w, w_scale, out, workspace, bias=None, check: bool = Tru
         _dtype_code(dt, n), M, N, K, _need(n, "a", a, (M, K), torch.int8), a.stride(0),
         _dense(n, "a_scale", a_scale, (M,), f32), _need(n, "w", w, (N, K), torch.int8), w.stride(0),
         _dense(n, "w_scale", w_scale, (N,), f32), _dense(n, "bias", bias, (N,), dt),
-        _need(n, "out", out, (M, N), dt), out.stride(0), *_ws(workspace), _stream())
+        _need(n, "out", out, (M, N), dt), out.stride(0), *_ws(workspace), _stream_of(a))
     return _done(st, "pararnn_gemm_i8", check)
 
 

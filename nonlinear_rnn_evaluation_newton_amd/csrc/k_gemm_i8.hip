@@ -181,6 +181,202 @@ __global__ __launch_bounds__(256) void k_gemm8_tile(Gemm8Args g) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// The same product with operands that go straight from memory to shared
+// memory: a 16-byte buffer load of lane l fills bytes 16 l .. 16 l + 15 of a
+// 1 KB run (8 tile rows of 128 bytes), so staging takes no registers and no
+// stores; the layout above is made by which chunk each lane fetches.  Two
+// stages of one 128-byte K step, an array each, so that the compiler can tell
+// the stage being filled from the one being read.  Loads past M, N or the
+// split's K write zeros.  WM x WN wavefronts of 32 FM x 32 FN.
+typedef __amdgpu_buffer_rsrc_t G8Rsrc;
+typedef __attribute__((address_space(3))) void g8_lds_t;
+constexpr unsigned G8_OOB = 0x80000000u;
+
+// this wavefront's loads have landed and its reads are done, then all meet
+__device__ inline void g8_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <typename T, int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_gemm8_direct(Gemm8Args g) {
+  constexpr int BM = WM * FM * 32, BN = WN * FN * 32, NW = WM * WN, QA = BM / 8 / NW, QB = BN / 8 / NW;
+  static_assert(QA % 2 == 0 && QB % 2 == 0, "even numbers of loads");
+  __shared__ __attribute__((aligned(1024))) int8_t s0[(BM + BN) * TB], s1[(BM + BN) * TB];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN, h = lane >> 5;
+  // Blocks go to the 8 dies in turn: each die takes a contiguous run of tiles,
+  // eight rows of tiles at a time, so that its cache holds both operands' strips.
+  const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN, tiles = tiles_m * tiles_n;
+  int id = blockIdx.x;
+  if (tiles % 8 == 0) id = (id % 8) * (tiles / 8) + id / 8;
+  const int width = 8 * tiles_n, fm = (id / width) * 8, gm = min(tiles_m - fm, 8);
+  const int m0 = (fm + (id % width) % gm) * BM, n0 = ((id % width) / gm) * BN;
+  const int kb = blockIdx.y * g.kper, ke = g.K - kb < g.kper ? g.K : kb + g.kper;
+  const G8Rsrc ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(g.a + m0 * g.lda), 0,
+                                                      (int)(min(BM, g.M - m0) * g.lda), 0x00020000);
+  const G8Rsrc rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(g.w + n0 * g.ldw), 0,
+                                                      (int)(min(BN, g.N - n0) * g.ldw), 0x00020000);
+  // load u covers rows 8 u + lane / 8; its chunk swizzle r / 2 % 8 = 4 (u % 2) + lane / 16
+  const int rl = lane >> 3, ce = ((lane & 7) ^ (lane >> 4)) * 16, co = ((lane & 7) ^ (4 | (lane >> 4))) * 16;
+  const unsigned lda = (unsigned)g.lda, ldw = (unsigned)g.ldw;
+  const unsigned ae = rl * lda + ce, ao = rl * lda + co, be = rl * ldw + ce, bo = rl * ldw + co;
+  // the last 16 bytes of the last row lie inside the resource only with a row
+  // stride of K; rows are cut by the resource, K by the offset
+  auto dload = [&](int8_t *d, int k0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < QA; q++) {
+      const int u = wave * QA + q;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (g8_lds_t *)&d[u * 1024], 16,
+                                               k0 + ((q & 1) ? co : ce) < ke ? ((q & 1) ? ao : ae) : G8_OOB,
+                                               u * 8 * lda + k0, 0, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < QB; q++) {
+      const int u = wave * QB + q;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (g8_lds_t *)&d[BM * TB + u * 1024], 16,
+                                               k0 + ((q & 1) ? co : ce) < ke ? ((q & 1) ? bo : be) : G8_OOB,
+                                               u * 8 * ldw + k0, 0, 0);
+    }
+  };
+  i32x16 acc[FN][FM];
+#pragma unroll
+  for (int j = 0; j < FN; j++)
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+      for (int r = 0; r < 16; r++) acc[j][i][r] = 0;
+  const int ar = wm * FM * 32 + (lane & 31), br = wn * FN * 32 + (lane & 31);
+  // the next step's loads are in flight during the whole step; the fragments
+  // of the next 32 k are read while this 32's products run
+  auto step = [&](const int8_t *cur, int8_t *nx, int k0) __attribute__((always_inline)) {
+    if (k0 + TB < ke) dload(nx, k0 + TB);
+    i32x4 a[2][FM], b[2][FN];
+    auto frag = [&](int w, int s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < FM; i++) a[w][i] = *reinterpret_cast<const i32x4 *>(cur + t8_off(ar + i * 32, 2 * s + h));
+#pragma unroll
+      for (int j = 0; j < FN; j++)
+        b[w][j] = *reinterpret_cast<const i32x4 *>(cur + BM * TB + t8_off(br + j * 32, 2 * s + h));
+    };
+    frag(0, 0);
+    __builtin_amdgcn_sched_group_barrier(0x020, QA + QB, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, FM + FN, 0);
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+      if (s < 3) frag((s + 1) & 1, s + 1);
+#pragma unroll
+      for (int j = 0; j < FN; j++)
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+          acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[s & 1][j], a[s & 1][i], acc[j][i], 0, 0, 0);
+      if (s < 3) {
+        constexpr int PAIRS = FM + FN < FM * FN ? FM + FN : FM * FN;
+#pragma unroll
+        for (int r = 0; r < PAIRS; r++) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, FM * FN - PAIRS, 0);
+      }
+    }
+    g8_sync();
+  };
+  dload(s0, kb);
+  g8_sync();
+  int k0 = kb;
+  for (; k0 + TB < ke; k0 += 2 * TB) {
+    step(s0, s1, k0);
+    step(s1, s0, k0 + TB);
+  }
+  if (k0 < ke) step(s0, s1, k0);
+  // K splits leave their sums to k_gemm8_join
+  if (g.splits > 1) {
+#pragma unroll
+    for (int i = 0; i < FM; i++) {
+      const int m = m0 + (wm * FM + i) * 32 + (lane & 31);
+      if (m >= g.M) continue;
+#pragma unroll
+      for (int j = 0; j < FN; j++)
+#pragma unroll
+        for (int v4 = 0; v4 < 4; v4++) {
+          const int n = n0 + (wn * FN + j) * 32 + 8 * v4 + 4 * h;
+          int *o = g.part + ((long long)blockIdx.y * g.M + m) * g.N + n;
+          if (n + 4 <= g.N && (g.N & 3) == 0)
+            *reinterpret_cast<i32x4 *>(o) = i32x4{acc[j][i][4 * v4], acc[j][i][4 * v4 + 1], acc[j][i][4 * v4 + 2],
+                                                  acc[j][i][4 * v4 + 3]};
+          else
+            for (int c = 0; c < 4 && n + c < g.N; c++) o[c] = acc[j][i][4 * v4 + c];
+        }
+    }
+    return;
+  }
+  // Scaled results, 32 rows of a wavefront at a time, through its part of the
+  // first stage (every wavefront has passed its last read of it): a lane holds
+  // 4 columns of one row, which stored as they are would touch 32 rows with 16
+  // bytes each; read back by rows, an instruction stores whole 128-byte lines.
+  // 16-byte chunks are swizzled by the row as above.
+  constexpr int E = sizeof(T), CPR = FN * 32 * E / 16;  // chunks per row
+  int8_t *mine = s0 + wave * (32 * FN * 32 * E);
+  static_assert(NW * 32 * FN * 32 * E <= (int)sizeof(s0), "the results fit the stage");
+  const bool vec = (g.ldo * E) % 16 == 0 && ((uintptr_t)g.out & 15) == 0;
+  float sw[FN][16], bias[FN][16];  // of the lane's columns, loaded once
+#pragma unroll
+  for (int j = 0; j < FN; j++)
+#pragma unroll
+    for (int v = 0; v < 16; v++) {
+      const int n = n0 + (wn * FN + j) * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
+      sw[j][v] = n < g.N ? g.sw[n] : 0.f;
+      bias[j][v] = n < g.N && g.bias ? ldf((const T *)g.bias, n) : 0.f;
+    }
+#pragma unroll
+  for (int i = 0; i < FM; i++) {
+    const int mr = m0 + (wm * FM + i) * 32, r = lane & 31;
+    const float sa = mr + r < g.M ? g.sa[mr + r] : 0.f;
+#pragma unroll
+    for (int j = 0; j < FN; j++)
+#pragma unroll
+      for (int v4 = 0; v4 < 4; v4++) {
+        float o[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+          o[c] = fmaf((float)acc[j][i][4 * v4 + c], sa * sw[j][4 * v4 + c], bias[j][4 * v4 + c]);
+        const int byte = (j * 32 + 8 * v4 + 4 * h) * E, ch = (byte >> 4) ^ (r & (CPR - 1));
+        int8_t *q = mine + r * (CPR * 16) + ch * 16 + (byte & 15);
+        if constexpr (E == 2) {
+          uint2 u;
+          u.x = (unsigned)f2bf(o[0]) | ((unsigned)f2bf(o[1]) << 16);
+          u.y = (unsigned)f2bf(o[2]) | ((unsigned)f2bf(o[3]) << 16);
+          *reinterpret_cast<uint2 *>(q) = u;
+        } else {
+          *reinterpret_cast<float4 *>(q) = make_float4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wavefront's own stores, read by its other lanes
+#pragma unroll
+    for (int q = 0; q < 32 * CPR / 64; q++) {
+      const int e = q * 64 + lane, row = e / CPR, ch = e % CPR;
+      const int n = n0 + wn * FN * 32 + ch * (16 / E), m = mr + row;
+      const uint4 v = *reinterpret_cast<const uint4 *>(mine + row * (CPR * 16) + ((ch ^ (row & (CPR - 1))) << 4));
+      if (m < g.M && n < g.N) {
+        T *p = (T *)g.out + m * g.ldo + n;
+        if (vec && n + 16 / E <= g.N) {
+          *reinterpret_cast<uint4 *>(p) = v;
+        } else {
+          const T *x = reinterpret_cast<const T *>(&v);
+#pragma unroll
+          for (int c = 0; c < 16 / E; c++)
+            if (n + c < g.N) p[c] = x[c];
+        }
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+}
+
 template <typename T>
 __global__ void k_gemm8_join(Gemm8Args g) {
   const long long mn = (long long)g.M * g.N, i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
@@ -189,6 +385,11 @@ __global__ void k_gemm8_join(Gemm8Args g) {
   for (int k = 0; k < g.splits; k++) s += g.part[k * mn + i];
   const int m = (int)(i / g.N), n = (int)(i % g.N);
   stf((T *)g.out + m * g.ldo, n, scaled<T>(g, s, m, n));
+}
+
+// Edge of the block tile: 256 where its tiles fill the CUs, else 128.
+static int gemm8_tile(int M, int N) {
+  return (long long)((M + 255) / 256) * ((N + 255) / 256) >= 192 ? 256 : 128;
 }
 
 template <typename T, bool AL>
@@ -200,8 +401,16 @@ hipError_t gemm8_go(const Gemm8Args &g, hipStream_t s) {
     else k_gemm8_rows<T, 4, AL><<<grid, 512, 0, s>>>(g);
     return hipGetLastError();
   }
-  const long long tiles = (long long)((g.M + 127) / 128) * ((g.N + 127) / 128);
-  k_gemm8_tile<T, AL><<<dim3((unsigned)tiles, (unsigned)g.splits), 256, 0, s>>>(g);
+  const int tile = gemm8_tile(g.M, g.N);
+  const dim3 grid((unsigned)((long long)((g.M + tile - 1) / tile) * ((g.N + tile - 1) / tile)), (unsigned)g.splits);
+  // (the direct loads' offsets in a tile are 31-bit)
+  const bool direct = AL && g.lda < (1 << 22) && g.ldw < (1 << 22);
+  if (tile == 256 && direct) k_gemm8_direct<T, 2, 4, 4, 2><<<grid, 512, 0, s>>>(g);
+  else if (tile == 256) {
+    const dim3 small((unsigned)((long long)((g.M + 127) / 128) * ((g.N + 127) / 128)), (unsigned)g.splits);
+    k_gemm8_tile<T, AL><<<small, 256, 0, s>>>(g);
+  } else if (direct) k_gemm8_direct<T, 2, 2, 2, 2><<<grid, 256, 0, s>>>(g);
+  else k_gemm8_tile<T, AL><<<grid, 256, 0, s>>>(g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.splits == 1) return e;
   const long long mn = (long long)g.M * g.N;
@@ -214,7 +423,7 @@ hipError_t gemm8_go(const Gemm8Args &g, hipStream_t s) {
 static int gemm8_splits(int M, int N, int K, int *kper) {
   const long long tiles = (long long)((M + 127) / 128) * ((N + 127) / 128);
   const int steps = (K + TB - 1) / TB;
-  int s = M <= 64 ? 1 : (int)(256 / tiles);
+  int s = M <= 64 || gemm8_tile(M, N) == 256 ? 1 : (int)(256 / tiles);
   if (s > steps / 4) s = steps / 4;
   if (s < 1) s = 1;
   const int per = (steps + s - 1) / s;

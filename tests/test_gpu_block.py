@@ -365,7 +365,8 @@ def test_norm_many_rows_and_zero_row():
 @pytest.mark.parametrize("M,N,K,la,lw", [
     (1, 1, 1, 0, 0), (1, 16, 64, 0, 0), (3, 17, 100, 0, 0), (16, 64, 2048, 0, 16), (17, 130, 513, 3, 0),
     (33, 40, 4096, 16, 0), (64, 257, 300, 0, 0), (65, 129, 128, 0, 0), (128, 128, 256, 0, 0), (130, 300, 1000, 0, 8),
-    (200, 77, 5003, 0, 5), (300, 513, 640, 16, 32), (1000, 1100, 272, 0, 0), (520, 800, 2064, 0, 0)])
+    (200, 77, 5003, 0, 5), (300, 513, 640, 16, 32), (1000, 1100, 272, 0, 0), (520, 800, 2064, 0, 0),
+    (2900, 4053, 208, 0, 0), (3100, 4040, 16, 0, 16)])
 def test_product(dtype, M, N, K, la, lw):
     g = gen(M + N + K)
     a = torch.randint(-128, 128, (M, K), generator=g).to(torch.int8)
