@@ -1,5 +1,5 @@
 // Selective state space scan: the C entry points, the kernels that join the
-// time segments and the partial sums, and the single-token step.
+// time segments and add the partial sums, and the single-token step.
 #include <string>
 
 #include "pararnn.h"
@@ -8,11 +8,11 @@
 namespace pr {
 
 // ---------------------------------------------------------------------------
-// joining the segments
+// joining the pieces
 // ---------------------------------------------------------------------------
-// agg[b][s] (end state of segment s from zero) becomes the state that enters
-// segment s; a segment's decay is exp(A sum of delta).  REV: the same from
-// the last segment back, for the adjoint's carry.  One thread per (b, d, n).
+// agg[b][s] (end state of piece s from zero) becomes the state that enters
+// piece s; a piece's decay is exp(A sum of delta).  REV: the same from the
+// last piece back, for the adjoint's carry.  One thread per (b, d, n).
 template <bool REV>
 __global__ void k_ssm_join(const float *__restrict__ A, const float *__restrict__ first,
                            const float *__restrict__ sumd, float *__restrict__ agg, int B, int D, int N, int S) {
@@ -24,7 +24,7 @@ __global__ void k_ssm_join(const float *__restrict__ A, const float *__restrict_
   float carry = first ? first[i] : 0.f;
   const float *sd = sumd + b * S * D + d;
   float *ag = agg + b * S * dn + e;
-  constexpr int U = 8;  // segments whose loads are in flight together
+  constexpr int U = 8;  // pieces whose loads are in flight together
   for (int s0 = 0; s0 < S; s0 += U) {
     float v[U], m[U];
 #pragma unroll
@@ -46,35 +46,25 @@ __global__ void k_ssm_join(const float *__restrict__ A, const float *__restrict_
   }
 }
 
-// dB and dC of each (b, t, group, n): the sum over the group's channel blocks
-template <typename T>
-__global__ void k_ssm_bc_sum(const float *__restrict__ part, int nblk, int B, int T_, int G, int N, int NP,
-                             const int *__restrict__ lengths, View dB, View dC) {
-  const long long rows = (long long)B * T_ * G, cols = 2LL * NP;
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= rows * cols) return;
-  const int n2 = (int)(i % cols), n = n2 % NP;
-  if (n >= N) return;
-  const long long row = i / cols;
-  const int g = (int)(row % G);
-  const long long bt = row / G;
-  const int t = (int)(bt % T_), b = (int)(bt / T_);
-  const View &v = n2 < NP ? dB : dC;
-  if (!v.p) return;
-  float s = 0.f;
-  if (t < seq_len(lengths, b, T_)) {
-#pragma unroll 8
-    for (int k = 0; k < nblk; k++) s += part[k * rows * cols + i];
-  }
-  stf((T *)v.p, b * v.sb + t * v.st + (long long)g * N + n, s);
-}
+// ---------------------------------------------------------------------------
+// the adjoint's last sums, one launch
+// ---------------------------------------------------------------------------
+struct SsmSums {
+  const float *part, *pA, *pD;  // as in SsmArgs
+  const int *lengths;
+  View dB, dC;
+  float *dA, *dD, *dbias;       // may be null
+  int nblk, B, T, G, N, NP, P, D;
+  unsigned bc_blocks, a_blocks;  // blocks of the first two kinds
+};
 
+// out[j] = the sum over p of part[p * stride + j], in 64 bits in a fixed order:
 // 64 columns by 4 slices of the partials per block
-__global__ void k_part_sum(const float *__restrict__ part, int P, long long stride, long long cols,
-                           float *__restrict__ out) {
+__device__ inline void part_sum(const float *__restrict__ part, int P, long long stride, long long cols, long long blk,
+                                float *__restrict__ out) {
   __shared__ double sh[4][64];
   const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  const long long j = (long long)blockIdx.x * 64 + x;
+  const long long j = blk * 64 + x;
   double s = 0;
   if (j < cols) {
 #pragma unroll 4
@@ -83,6 +73,42 @@ __global__ void k_part_sum(const float *__restrict__ part, int P, long long stri
   sh[y][x] = s;
   __syncthreads();
   if (y == 0 && j < cols) out[j] = (float)((sh[0][x] + sh[1][x]) + (sh[2][x] + sh[3][x]));
+}
+
+// Blocks of three kinds: dB and dC of each (b, t, group, n) over the group's
+// channel blocks; dA over the (b, segment) partials; dD, then dbias, likewise.
+template <typename T>
+__global__ __launch_bounds__(256) void k_ssm_sums(SsmSums a) {
+  if (blockIdx.x >= a.bc_blocks) {
+    const unsigned i = blockIdx.x - a.bc_blocks;
+    if (i < a.a_blocks) {
+      part_sum(a.pA, a.P, (long long)a.D * a.N, (long long)a.D * a.N, i, a.dA);
+    } else {
+      const unsigned m = (i - a.a_blocks) & 1, blk = (i - a.a_blocks) >> 1;
+      float *o = m ? a.dbias : a.dD;
+      if (o) part_sum(a.pD + (long long)m * a.D, a.P, 2LL * a.D, a.D, blk, o);
+    }
+    return;
+  }
+  const long long rows = (long long)a.B * a.T * a.G, cols = 2LL * a.NP;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * cols) return;
+  const int n2 = (int)(i % cols), n = n2 % a.NP;
+  if (n >= a.N) return;
+  const long long row = i / cols, bt = row / a.G;
+  const int g = (int)(row % a.G), t = (int)(bt % a.T), b = (int)(bt / a.T);
+  const View &v = n2 < a.NP ? a.dB : a.dC;
+  if (!v.p) return;
+  float s = 0.f;
+  if (t < seq_len(a.lengths, b, a.T)) {
+#pragma unroll 8
+    for (int k = 0; k < a.nblk; k++) s += a.part[k * rows * cols + i];
+  }
+  stf((T *)v.p, b * v.sb + t * v.st + (long long)g * a.N + n, s);
+}
+
+__global__ __launch_bounds__(256) void k_part_sum(const float *part, int P, long long stride, long long cols, float *out) {
+  part_sum(part, P, stride, cols, blockIdx.x, out);
 }
 
 hipError_t launch_part_sum(const float *part, int P, long long stride, long long cols, float *out, hipStream_t s) {
@@ -196,14 +222,16 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
   } while (0)
 
 struct SsmPlan {
-  int cbg = 0, NP = 0, S = 1, seglen = 0;
-  size_t off_agg = 0, off_sumd = 0, off_part = 0, off_pA = 0, off_pD = 0, fwd_bytes = 0, adj_bytes = 0;
+  int cbg = 0, NP = 0, S = 1, seglen = 0, R = 1;
+  size_t off_agg = 0, off_sumd = 0, off_part = 0, off_pA = 0, off_pD = 0, off_acc = 0, fwd_bytes = 0, adj_bytes = 0;
 };
 
 // Time segments for `blocks` blocks over T steps: a block for each CU, at
 // least four tiles each; a segment's extent in any array below 2^31 bytes (16
 // steps are).
-void split_time(long long blocks, int T, long long max_tile_bytes, int *S, int *seglen) {
+// Two segments leave half of the CUs idle in the pass that prepares the split,
+// which one segment of the two takes part in: it takes that one in two pieces.
+void split_time(long long blocks, int T, long long max_tile_bytes, int *S, int *seglen, int *R) {
   const long long tiles = (T + SSM_TL - 1) / SSM_TL;
   long long s = (256 + blocks - 1) / blocks;
   const long long most = (tiles + 3) / 4;
@@ -212,6 +240,9 @@ void split_time(long long blocks, int T, long long max_tile_bytes, int *S, int *
   long long per = (tiles + s - 1) / s;
   const long long fit = ((1LL << 31) - (1LL << 30)) / max_tile_bytes;
   if (per > fit) per = fit;
+  *R = s == 2 && per > 3 ? 2 : 1;
+  if (*R == 2 && per < fit) per += per & 1;
+  if (per & 1) *R = 1;
   *seglen = (int)(per * SSM_TL);
   *S = (int)((tiles + per - 1) / per);
 }
@@ -237,9 +268,10 @@ int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
   long long tile = SSM_TL * 4 * width * esz;
   if (tile < (long long)p->D * p->N * 4) tile = (long long)p->D * p->N * 4;
   if (tile < SSM_TL * 8LL * p->G * pl->NP) tile = SSM_TL * 8LL * p->G * pl->NP;
+  if (p->N > 16 && tile < SSM_TL * 12LL * p->D) tile = SSM_TL * 12LL * p->D;
   if (tile > (1LL << 27)) return fail(PR_EUNSUPPORTED, "problem too large: %lld bytes in 16 steps", tile);
-  split_time(blocks, p->T, tile, &pl->S, &pl->seglen);
-  const size_t dn = (size_t)p->D * p->N, sm = pl->S;
+  split_time(blocks, p->T, tile, &pl->S, &pl->seglen, &pl->R);
+  const size_t dn = (size_t)p->D * p->N, sm = pl->S > 1 ? pl->S * pl->R : 1;
   if ((double)p->B * sm * dn * 4 > 1e13 || (double)p->B * p->T * p->G * pl->cbg * pl->NP * 8 > 1e13)
     return fail(PR_EUNSUPPORTED, "problem too large");
   size_t o = 0;
@@ -249,6 +281,7 @@ int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
   pl->off_part = o; o = align256(o + (size_t)pl->cbg * p->B * p->T * p->G * 2 * pl->NP * 4);
   pl->off_pA = o; o = align256(o + p->B * (size_t)pl->S * dn * 4);
   pl->off_pD = o; o = align256(o + p->B * (size_t)pl->S * 2 * p->D * 4);
+  pl->off_acc = o; o = align256(o + (p->N > 16 ? (size_t)p->B * p->T * 3 * p->D * 4 : 0));
   pl->adj_bytes = o;
   return PR_OK;
 }
@@ -279,7 +312,8 @@ int ssm_fill(const pr_ssm_problem *p, const SsmPlan &pl, const pr_ssm_inputs *in
   a->B = p->B; a->T = p->T; a->D = p->D; a->N = p->N; a->G = p->G; a->softplus = p->softplus != 0;
   a->dpg = p->D / p->G; a->cbg = pl.cbg;
   const int esz = p->dtype == PR_BF16 ? 2 : 4;
-  a->vec = a->dpg % 4 == 0 && p->N % 4 == 0 && vec4_ok(a->u, esz) && vec4_ok(a->dt, esz) && vec4_ok(a->z, esz) &&
+  // a lane's states are there or not as a whole: eight of them from 33 states on
+  a->vec = a->dpg % 4 == 0 && p->N % (p->N > 32 ? 8 : 4) == 0 && vec4_ok(a->u, esz) && vec4_ok(a->dt, esz) && vec4_ok(a->z, esz) &&
            vec4_ok(a->Bm, esz) && vec4_ok(a->Cm, esz);
   int rc = PR_OK;
   for (const View *v : {&a->u, &a->dt, &a->z, &a->Bm, &a->Cm})
@@ -305,7 +339,7 @@ int check_ws(const void *ws, size_t have, size_t need) {
 template <bool REV>
 int join(const SsmArgs &a, const float *first, hipStream_t s) {
   const long long n = (long long)a.B * a.D * a.N;
-  k_ssm_join<REV><<<dim3((unsigned)((n + 255) / 256)), 256, 0, s>>>(a.A, first, a.sumd, a.agg, a.B, a.D, a.N, a.S);
+  k_ssm_join<REV><<<dim3((unsigned)((n + 255) / 256)), 256, 0, s>>>(a.A, first, a.sumd, a.agg, a.B, a.D, a.N, a.SA);
   HIPCHK(hipGetLastError());
   return PR_OK;
 }
@@ -341,7 +375,7 @@ int pararnn_ssm_scan(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_
     return fail(PR_EINVAL, "h_last and states must be 16-byte aligned");
   char *ws = (char *)workspace;
   a.agg = (float *)(ws + pl.off_agg); a.sumd = (float *)(ws + pl.off_sumd);
-  a.S = pl.S; a.seglen = pl.seglen;
+  a.S = pl.S; a.seglen = pl.seglen; a.R = pl.R; a.SA = pl.S * pl.R;
   hipStream_t s = (hipStream_t)stream;
   if (a.S > 1) {
     if ((rc = launch_ssm(p->dtype, a, SSM_FWD_AGG, s)) != PR_OK) return rc;
@@ -375,27 +409,25 @@ int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const 
   char *ws = (char *)workspace;
   a.agg = (float *)(ws + pl.off_agg); a.sumd = (float *)(ws + pl.off_sumd);
   a.part = (float *)(ws + pl.off_part); a.pA = (float *)(ws + pl.off_pA); a.pD = (float *)(ws + pl.off_pD);
-  a.S = pl.S; a.seglen = pl.seglen;
+  a.acc = (float *)(ws + pl.off_acc);
+  a.S = pl.S; a.seglen = pl.seglen; a.R = pl.R; a.SA = pl.S * pl.R;
   hipStream_t s = (hipStream_t)stream;
   if (a.S > 1) {
     if ((rc = launch_ssm(p->dtype, a, SSM_ADJ_AGG, s)) != PR_OK) return rc;
     if ((rc = join<true>(a, dh_last, s)) != PR_OK) return rc;
   }
   if ((rc = launch_ssm(p->dtype, a, SSM_ADJ, s)) != PR_OK) return rc;
-  const int P = a.B * a.S;
-  const long long dn = (long long)a.D * a.N;
-  if (a.dB.p || a.dC.p) {
-    const long long n = (long long)a.B * a.T * a.G * 2 * pl.NP;
-    const dim3 grid((unsigned)((n + 255) / 256));
-    if (p->dtype == PR_BF16)
-      k_ssm_bc_sum<uint16_t><<<grid, 256, 0, s>>>(a.part, a.cbg, a.B, a.T, a.G, a.N, pl.NP, a.lengths, a.dB, a.dC);
-    else
-      k_ssm_bc_sum<float><<<grid, 256, 0, s>>>(a.part, a.cbg, a.B, a.T, a.G, a.N, pl.NP, a.lengths, a.dB, a.dC);
-    HIPCHK(hipGetLastError());
-  }
-  if (gr->A) HIPCHK(launch_part_sum(a.pA, P, dn, dn, gr->A, s));
-  if (gr->D) HIPCHK(launch_part_sum(a.pD, P, 2LL * a.D, a.D, gr->D, s));
-  if (gr->dt_bias) HIPCHK(launch_part_sum(a.pD + a.D, P, 2LL * a.D, a.D, gr->dt_bias, s));
+  SsmSums f{};
+  f.part = a.part; f.pA = a.pA; f.pD = a.pD; f.lengths = a.lengths; f.dB = a.dB; f.dC = a.dC;
+  f.dA = gr->A; f.dD = gr->D; f.dbias = gr->dt_bias;
+  f.nblk = a.cbg; f.B = a.B; f.T = a.T; f.G = a.G; f.N = a.N; f.NP = pl.NP; f.P = a.B * a.S; f.D = a.D;
+  if (a.dB.p || a.dC.p) f.bc_blocks = (unsigned)(((long long)a.B * a.T * a.G * 2 * pl.NP + 255) / 256);
+  if (gr->A) f.a_blocks = (unsigned)(((long long)a.D * a.N + 63) / 64);
+  const unsigned n = f.bc_blocks + f.a_blocks + (gr->D || gr->dt_bias ? 2 * ((a.D + 63) / 64) : 0);
+  if (n == 0) return PR_OK;
+  if (p->dtype == PR_BF16) k_ssm_sums<uint16_t><<<dim3(n), 256, 0, s>>>(f);
+  else k_ssm_sums<float><<<dim3(n), 256, 0, s>>>(f);
+  HIPCHK(hipGetLastError());
   return PR_OK;
 }
 

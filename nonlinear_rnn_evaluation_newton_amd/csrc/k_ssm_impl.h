@@ -70,12 +70,16 @@ __device__ inline void buf_load(unsigned *v, SRsrc r, unsigned at, unsigned so) 
     v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
   }
 }
+// A 16-byte store has its whole offset in the vector register: its data must not
+// be overwritten by the very next instruction, which the compiler sees to only
+// where the scalar offset is absent (with one, saved states came out wrong in
+// the last lanes where the next instruction took the first data register).
 template <int BYTES>
 __device__ inline void buf_store(const unsigned *v, SRsrc r, unsigned at, unsigned so) {
   if constexpr (BYTES == 2) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v[0], r, at, so, 0);
   if constexpr (BYTES == 4) __builtin_amdgcn_raw_buffer_store_b32(v[0], r, at, so, 0);
   if constexpr (BYTES == 8) __builtin_amdgcn_raw_buffer_store_b64(su32x2{v[0], v[1]}, r, at, so, 0);
-  if constexpr (BYTES == 16) __builtin_amdgcn_raw_buffer_store_b128(su32x4{v[0], v[1], v[2], v[3]}, r, at, so, 0);
+  if constexpr (BYTES == 16) __builtin_amdgcn_raw_buffer_store_b128(su32x4{v[0], v[1], v[2], v[3]}, r, at + so, 0, 0);
 }
 
 // nv elements (at most U) from byte `off` of the lane plus byte `so` of the
@@ -157,7 +161,7 @@ __device__ inline void fma_bcast_steps(float *acc, float c, float v0, float v1, 
       "v_fmac_f32_dpp %2, %4, %7 row_newbcast:%11 row_mask:0xf bank_mask:0xf\n\t"
       "v_fmac_f32_dpp %3, %4, %8 row_newbcast:%12 row_mask:0xf bank_mask:0xf\n\t"
       "s_nop 1"
-      : "+v"(acc[0]), "+v"(acc[1]), "+v"(acc[2]), "+v"(acc[3])
+      : "+&v"(acc[0]), "+&v"(acc[1]), "+&v"(acc[2]), "+&v"(acc[3])
       : "v"(c), "v"(v0), "v"(v1), "v"(v2), "v"(v3), "n"(I0), "n"(I0 + 1), "n"(I0 + 2), "n"(I0 + 3));
 }
 
@@ -304,7 +308,8 @@ __device__ inline void store_state(float *p, int n0, int N, bool on, const float
 // forward
 // ---------------------------------------------------------------------------
 // FULL: outputs, from the state that enters the segment (a.agg where S > 1,
-// else h0).  Not FULL: the segment's end state from zero and its sum of delta.
+// else h0).  Not FULL: the end state of a piece of a segment from zero, and its
+// sum of delta.
 template <typename T, int NS, int WS, bool FULL, bool VEC>
 __global__ __launch_bounds__(256 * WS) void k_ssm_fwd(SsmArgs a) {
   using P = Place<T, WS>;
@@ -324,7 +329,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_fwd(SsmArgs a) {
 #pragma unroll
   for (int k = 0; k < NS; k++) A2[k] *= 1.4426950408889634f;
   if constexpr (FULL) {
-    const float *hp = a.S > 1 ? a.agg + ((long long)w.b * a.S + w.s) * dn : a.h0 ? a.h0 + w.b * dn : nullptr;
+    const float *hp = a.S > 1 ? a.agg + ((long long)w.b * a.SA + w.s * a.R) * dn : a.h0 ? a.h0 + w.b * dn : nullptr;
     load_state<NS>(hp + (long long)w.d * a.N, n0, a.N, w.on && hp, h);
   } else {
 #pragma unroll
@@ -467,7 +472,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_fwd(SsmArgs a) {
     if (a.hlast && w.s == last)
       store_state<NS>(a.hlast + w.b * dn + (long long)w.d * a.N, n0, a.N, w.on, h);
   } else {
-    const long long at = (long long)w.b * a.S + w.s;
+    const long long at = (long long)w.b * a.SA + w.s;
     store_state<NS>(a.agg + at * dn + (long long)w.d * a.N, n0, a.N, w.on, h);
     if (w.j == 0 && w.ws == 0 && w.on) a.sumd[at * a.D + w.d] = dsum;
   }
@@ -478,7 +483,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_fwd(SsmArgs a) {
 // ---------------------------------------------------------------------------
 // With e_t = dy_t silu(z_t), the adjoint state g_t = C_t e_t + a_{t+1} g_{t+1}
 // runs backwards; r_t = a_t g_t is what a step hands to the one before it.
-// This pass: the segment's r at its first step from zero behind it.
+// This pass: a piece's r at its first step from zero behind it.
 template <typename T, int NS, int WS, bool VEC>
 __global__ __launch_bounds__(256 * WS) void k_ssm_adj_agg(SsmArgs a) {
   using P = Place<T, WS>;
@@ -574,43 +579,50 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj_agg(SsmArgs a) {
       constexpr int I = decltype(i)::value;
       if (tile - I >= 0) run_tile(ring[(I + 1) % PF], tile - I, std::integral_constant<int, I & 1>{});
     });
-  const long long at = (long long)w.b * a.S + w.s;
+  const long long at = (long long)w.b * a.SA + w.s;
   store_state<NS>(a.agg + at * dn + (long long)w.d * a.N, n0, a.N, w.on, r);
   if (w.j == 0 && w.ws == 0 && w.on) a.sumd[at * a.D + w.d] = dsum;
 }
 
-// The gradients of one segment.  A wavefront keeps two states per lane; NG
-// groups of 8 WS states run one after the other.  Per tile the states of its
-// 16 steps are made again from the saved one that enters it and stay in
-// registers with their decays for the walk back.
-template <typename T, int NG, int WS, bool VEC>
+// The gradients of one segment.  A wavefront keeps two states per lane, 8 WS
+// states in all, from state a.n_off on.  Per tile the states of its 16 steps
+// are made again from the saved one that enters it and stay in registers with
+// their decays for the walk back.  MULTI: more than 16 states, one launch for
+// each 16; the sums over states go through a.acc from one to the next, and the
+// last one makes the outputs.  (One kernel for all of more than 16 states did
+// not fit the registers.)
+template <typename T, int WS, bool MULTI, bool VEC>
 __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
   using P = Place<T, WS>;
   constexpr int CH = P::CH, TL = P::TL, UC = P::UC, NT = P::NT, YS = CH + 16, NS = 2;
-  constexpr int GP = 4 * WS * NS, NP = NG * GP;  // states of a group, padded number of states
-  constexpr int PF = 2;                          // tiles in flight
+  constexpr int GP = 4 * WS * NS;                // states of a launch
+  constexpr int RS = WS == 1 && !VEC ? 1 : 2;    // tiles in flight, as the registers allow
+  constexpr unsigned E = sizeof(T);
   struct Buf {
     float2 dx[TL][CH];                      // delta, delta u
     float e[TL][CH];
     float sum[3][WS][TL][YS];               // sums over a wavefront's states: C h, B g, A r h_{t-1}
-    float bc[4][TL][2 * NP];                // dB | dC of 16 channels
+    float bc[4][TL][2 * GP];                // dB | dC of 16 channels
   };
   __shared__ Buf buf[2];
   const P w(a);
   const bool gate = a.z.p != nullptr, sp = a.softplus != 0;
-  const int nt = (a.T + TL - 1) / TL, nl = (w.ws * 4 + w.j) * NS;  // nl: first state within a group
+  const int nt = (a.T + TL - 1) / TL, nl = (w.ws * 4 + w.j) * NS;  // nl: the lane's first state of these
   const long long dn = (long long)a.D * a.N;
   const long long at = (long long)w.b * a.S + w.s;
   const bool odd1 = w.lane & 1, odd2 = w.lane & 2;
 
-  float A[NG][NS], r[NG][NS], dA[NG][NS];
+  const int n0 = a.n_off + nl, NPT = a.NPT;
+
+  float A[NS], A2[NS], r[NS], dA[NS];
+  load_state<NS>(a.A + (long long)w.d * a.N, n0, a.N, w.on, A);
+  const float *rp0 = a.S > 1 ? a.agg + ((long long)w.b * a.SA + (w.s + 1) * a.R - 1) * dn
+                             : a.dhlast ? a.dhlast + w.b * dn : nullptr;
+  load_state<NS>(rp0 + (long long)w.d * a.N, n0, a.N, w.on && rp0, r);
 #pragma unroll
-  for (int g = 0; g < NG; g++) {
-    load_state<NS>(a.A + (long long)w.d * a.N, g * GP + nl, a.N, w.on, A[g]);
-    const float *rp = a.S > 1 ? a.agg + at * dn : a.dhlast ? a.dhlast + w.b * dn : nullptr;
-    load_state<NS>(rp + (long long)w.d * a.N, g * GP + nl, a.N, w.on && rp, r[g]);
-#pragma unroll
-    for (int k = 0; k < NS; k++) dA[g][k] = 0.f;
+  for (int k = 0; k < NS; k++) {
+    dA[k] = 0.f;
+    A2[k] = A[k] * 1.4426950408889634f;
   }
   float ub[UC], uD[UC], accD[UC] = {}, accb[UC] = {};
   w.param(a.bias, ub);
@@ -618,18 +630,21 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
 
   struct Slot {
     Raw<T, UC> u, d, y, z;
-    Raw<T, NS> B[NG], C[NG];
-    Raw<float, NS> h[NG];
   };
-  Slot ring[PF];
+  struct Coef {  // of one tile
+    Raw<T, NS> B, C;
+    Raw<float, NS> h;
+  };
+  Slot ring[RS];
+  Coef coef[2];
   const unsigned ou = w.unit(a.u), od = w.unit(a.dt), oy = w.unit(a.dy), oz = w.unit(a.z);
-  const unsigned oB = w.coef(a.Bm, a.N, nl), oC = w.coef(a.Cm, a.N, nl), oh = ((unsigned)w.d * a.N + nl) * 4u;
+  const unsigned oB = w.coef(a.Bm, a.N, n0), oC = w.coef(a.Cm, a.N, n0), oh = ((unsigned)w.d * a.N + n0) * 4u;
   const unsigned odu = w.unit(a.du), odd = w.unit(a.ddt), odz = w.unit(a.dz);
   const Rows<T> ru(a.u, w.b, w.t0), rd(a.dt, w.b, w.t0), ry(a.dy, w.b, w.t0), rz(a.z, w.b, w.t0);
   const Rows<T> rB(a.Bm, w.b, w.t0), rC(a.Cm, w.b, w.t0);
   const Rows<T> rdu(a.du, w.b, w.t0), rdd(a.ddt, w.b, w.t0), rdz(a.dz, w.b, w.t0);
   const SRsrc rh = s_rsrc(a.states + ((long long)w.b * nt + w.t0 / TL) * dn);
-  const SRsrc rp = s_rsrc(a.part + ((((long long)(w.cb - w.g * a.cbg) * a.B + w.b) * a.T + w.t0) * a.G + w.g) * (2 * NP));
+  const SRsrc rp = s_rsrc(a.part + ((((long long)(w.cb - w.g * a.cbg) * a.B + w.b) * a.T + w.t0) * a.G + w.g) * (2 * NPT) + a.n_off);
   // tiles run from the last to the first; one before the first reads nothing
   auto load_tile = [&](Slot &s, int tile) PR_INLINE {
     const int left = tile < 0 ? 0 : w.end - w.t0 - tile * TL;
@@ -639,29 +654,22 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
     s.d = load_u<T, UC, VEC>(rd.r, od, at * rd.tile, nv);
     s.y = load_u<T, UC, VEC>(ry.r, oy, at * ry.tile, nv);
     s.z = load_u<T, UC, VEC>(rz.r, oz, at * rz.tile, nv);
-#pragma unroll
-    for (int g = 0; g < NG; g++) {
-      const int nn = a.N - g * GP - nl, on = (w.lane & 15) < left ? nn : 0;
-      s.B[g] = load_u<T, NS, VEC>(rB.r, oB + g * GP * P::E, at * rB.tile, on);
-      s.C[g] = load_u<T, NS, VEC>(rC.r, oC + g * GP * P::E, at * rC.tile, on);
-      s.h[g] = load_u<float, NS, VEC>(rh, oh + g * GP * 4, at * (unsigned)dn * 4u, w.on && left > 0 ? nn : 0);
-    }
+  };
+  auto load_coef = [&](Coef &s, int tile) PR_INLINE {
+    const int left = tile < 0 ? 0 : w.end - w.t0 - tile * TL;
+    const unsigned at = tile < 0 ? 0u : (unsigned)tile;
+    const int nn = a.N - n0, on = (w.lane & 15) < left ? nn : 0;
+    s.B = load_u<T, NS, VEC>(rB.r, oB, at * rB.tile, on);
+    s.C = load_u<T, NS, VEC>(rC.r, oC, at * rC.tile, on);
+    s.h = load_u<float, NS, VEC>(rh, oh, at * (unsigned)dn * 4u, w.on && left > 0 ? nn : 0);
   };
   // c: of the staged tile, p: of the tile whose outputs are due (its buffer may
   // be refilled meanwhile)
   Raw<T, UC> cu{}, cd{}, cy{}, cz{}, pu{}, pd{}, py{}, pz{};
-  Raw<T, NS> tB[NG], tC[NG];
-  Raw<float, NS> th[NG];
   float cdl[UC] = {}, ce[UC] = {}, pdl[UC] = {}, pe[UC] = {};
   auto stage = [&](Slot &s, int tile, auto parity) PR_INLINE {
     Buf &f = buf[decltype(parity)::value];
     const bool live = tile >= 0 && w.t0 + tile * TL + w.ur < w.end;
-#pragma unroll
-    for (int g = 0; g < NG; g++) {
-      tB[g] = s.B[g];
-      tC[g] = s.C[g];
-      th[g] = s.h[g];
-    }
 #pragma unroll
     for (int i = 0; i < UC; i++) {
       const bool in = live && i < w.unv;
@@ -679,25 +687,38 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
     cd = s.d;
     cy = s.y;
     cz = s.z;
-    load_tile(s, tile - PF);
+    load_tile(s, tile - RS);
   };
+  // a.acc: [B][T][3][D]
+  const SRsrc racc = s_rsrc(MULTI ? a.acc + ((long long)w.b * a.T + w.t0) * 3 * a.D : nullptr, MULTI);
+  const unsigned oacc = ((unsigned)w.ur * 3 * a.D + w.ch0 + w.uc) * 4u, tacc = TL * 3u * a.D * 4u;
   // gradients of a finished tile from its sums (parity of its buffer)
   auto output = [&](int tile, int parity) PR_INLINE {
     const bool any = tile < w.ntiles;
     const int t0 = w.t0 + tile * TL, t = t0 + w.ur, left = any ? w.end - t0 : 0;
     const Buf &f = buf[parity];
-    float du[UC], ddt[UC], dz[UC];
+    float du[UC], ddt[UC], dz[UC], sums[3][UC];
+#pragma unroll
+    for (int m = 0; m < 3; m++) {
+#pragma unroll
+      for (int i = 0; i < UC; i++) {
+        sums[m][i] = f.sum[m][0][w.ur][w.uc + i];
+#pragma unroll
+        for (int q = 1; q < WS; q++) sums[m][i] += f.sum[m][q][w.ur][w.uc + i];
+      }
+      if constexpr (MULTI) {
+        const int nv = w.ur < left ? w.unv : 0;
+        const Raw<float, UC> x = load_u<float, UC, VEC>(racc, oacc + m * a.D * 4u, tile * tacc, a.n_off > 0 ? nv : 0);
+#pragma unroll
+        for (int i = 0; i < UC; i++) sums[m][i] += x.get(i);
+        store_u<float, UC, VEC>(racc, oacc + m * a.D * 4u, tile * tacc, sums[m], a.last ? 0 : nv);
+      }
+    }
+    const bool fin = !MULTI || a.last != 0;
 #pragma unroll
     for (int i = 0; i < UC; i++) {
-      const int cc = w.uc + i;
-      const bool in = w.ur < left && i < w.unv;
-      float sum[3];
-#pragma unroll
-      for (int m = 0; m < 3; m++) {
-        sum[m] = f.sum[m][0][w.ur][cc];
-#pragma unroll
-        for (int q = 1; q < WS; q++) sum[m] += f.sum[m][q][w.ur][cc];
-      }
+      const bool in = w.ur < left && i < w.unv && fin;
+      const float sum[3] = {sums[0][i], sums[1][i], sums[2][i]};
       const float u = pu.get(i), v = pd.get(i) + ub[i], e = pe[i];
       du[i] = in ? fmaf(pdl[i], sum[1], uD[i] * e) : 0.f;
       ddt[i] = in ? fmaf(u, sum[1], sum[2]) * (sp ? fsigm(v) : 1.f) : 0.f;
@@ -706,33 +727,24 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
       accD[i] = fmaf(e, in ? u : 0.f, accD[i]);
       accb[i] += ddt[i];
     }
-    const int nv = any && t < w.t1 ? w.unv : 0;
+    const int nv = any && t < w.t1 && fin ? w.unv : 0;
     store_u<T, UC, VEC>(rdu.r, odu, tile * rdu.tile, du, nv);
     store_u<T, UC, VEC>(rdd.r, odd, tile * rdd.tile, ddt, nv);
     store_u<T, UC, VEC>(rdz.r, odz, tile * rdz.tile, dz, nv);
     // dB | dC of each step, to this channel block's partial
 #pragma unroll
-    for (int i0 = 0; i0 < TL * 2 * NP; i0 += NT) {
-      const int i = i0 + (int)threadIdx.x, row = i / (2 * NP), n = i % (2 * NP);
+    for (int i0 = 0; i0 < TL * 2 * GP; i0 += NT) {
+      const int i = i0 + (int)threadIdx.x, row = i / (2 * GP), n = i % (2 * GP);
       const float v = (f.bc[0][row][n] + f.bc[1][row][n]) + (f.bc[2][row][n] + f.bc[3][row][n]);
       const unsigned uv = __float_as_uint(v);
-      buf_store<4>(&uv, rp, row < left ? (unsigned)(row * a.G * 2 * NP + n) * 4u : S_OOB,
-                   tile * (unsigned)(TL * a.G * 2 * NP) * 4u);
+      buf_store<4>(&uv, rp, row < left ? (unsigned)(row * a.G * 2 * NPT + (n < GP ? n : NPT + n - GP)) * 4u : S_OOB,
+                   tile * (unsigned)(TL * a.G * 2 * NPT) * 4u);
     }
   };
 
   auto run_tile = [&](Slot &next, int tile, auto parity) PR_INLINE {
     constexpr int p = decltype(parity)::value;
     Buf &f = buf[p];
-    float B[NG][NS], C[NG][NS], hin[NG][NS];
-#pragma unroll
-    for (int g = 0; g < NG; g++)
-#pragma unroll
-      for (int k = 0; k < NS; k++) {
-        B[g][k] = tB[g].get(k);
-        C[g][k] = tC[g].get(k);
-        hin[g][k] = th[g].get(k);
-      }
     lds_barrier();
     output(tile + 1, p ^ 1);
     pu = cu;
@@ -745,9 +757,16 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
       pe[i] = ce[i];
     }
     stage(next, tile - 1, std::integral_constant<int, p ^ 1>{});
+    {
+      float hs[TL][NS], as[TL][NS], B[NS], C[NS], hin[NS];
+      Coef &cf = coef[p];
 #pragma unroll
-    for (int g = 0; g < NG; g++) {
-      float hs[TL][NS], as[TL][NS];
+      for (int k = 0; k < NS; k++) {
+        B[k] = cf.B.get(k);
+        C[k] = cf.C.get(k);
+        hin[k] = cf.h.get(k);
+      }
+      load_coef(cf, tile - 2);
       // the states again; the decays and inputs of four steps before their chain
       unroll_up<TL / 4>([&](auto quad) PR_INLINE {
         constexpr int Q = decltype(quad)::value;
@@ -756,15 +775,15 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
           const float2 dx = f.dx[I][w.c];
 #pragma unroll
           for (int k = 0; k < NS; k++) {
-            as[I][k] = __builtin_amdgcn_exp2f(dx.x * (A[g][k] * 1.4426950408889634f));
-            hs[I][k] = row_bcast<I>(B[g][k]) * dx.y;
+            as[I][k] = __builtin_amdgcn_exp2f(dx.x * A2[k]);
+            hs[I][k] = row_bcast<I>(B[k]) * dx.y;
           }
         });
         unroll_up<4>([&](auto within) PR_INLINE {
           constexpr int I = Q * 4 + decltype(within)::value;
 #pragma unroll
           for (int k = 0; k < NS; k++)
-            hs[I][k] = fmaf(as[I][k], I > 0 ? hs[I > 0 ? I - 1 : 0][k] : hin[g][k], hs[I][k]);
+            hs[I][k] = fmaf(as[I][k], I > 0 ? hs[I > 0 ? I - 1 : 0][k] : hin[k], hs[I][k]);
         });
         // keeps the steps' temporaries from spreading over the whole tile
         __builtin_amdgcn_sched_barrier(0);
@@ -772,7 +791,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
       // (a value of its own: sharing the broadcasts of the first pass would keep
       // them in registers, as instructions apart)
 #pragma unroll
-      for (int k = 0; k < NS; k++) asm volatile("" : "+v"(B[g][k]));
+      for (int k = 0; k < NS; k++) asm volatile("" : "+v"(B[k]));
       unroll_up<TL / 4>([&](auto quad) PR_INLINE {
         constexpr int Q = TL / 4 - 1 - decltype(quad)::value;
         float gg[4][NS], q4[4][NS], sum[3][4];
@@ -788,28 +807,24 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
           constexpr int W = 3 - decltype(within)::value, I = Q * 4 + W;
 #pragma unroll
           for (int k = 0; k < NS; k++) {
-            gg[W][k] = fmaf(row_bcast<I>(C[g][k]), e[W], r[g][k]);
-            r[g][k] = as[I][k] * gg[W][k];
-            q4[W][k] = r[g][k] * (I > 0 ? hs[I > 0 ? I - 1 : 0][k] : hin[g][k]);
-            dA[g][k] = fmaf(dx[W].x, q4[W][k], dA[g][k]);
+            gg[W][k] = fmaf(row_bcast<I>(C[k]), e[W], r[k]);
+            r[k] = as[I][k] * gg[W][k];
+            q4[W][k] = r[k] * (I > 0 ? hs[I > 0 ? I - 1 : 0][k] : hin[k]);
+            dA[k] = fmaf(dx[W].x, q4[W][k], dA[k]);
           }
         });
         float(&h4)[4][NS] = *reinterpret_cast<float(*)[4][NS]>(&hs[Q * 4]);
-        sum_bcast<Q * 4, NS>(sum[0], C[g], h4);
-        sum_bcast<Q * 4, NS>(sum[1], B[g], gg);
+        sum_bcast<Q * 4, NS>(sum[0], C, h4);
+        sum_bcast<Q * 4, NS>(sum[1], B, gg);
 #pragma unroll
         for (int m = 0; m < 4; m++) {
-          float v = A[g][0] * q4[m][0];
+          float v = A[0] * q4[m][0];
 #pragma unroll
-          for (int k = 1; k < NS; k++) v = fmaf(A[g][k], q4[m][k], v);
+          for (int k = 1; k < NS; k++) v = fmaf(A[k], q4[m][k], v);
           sum[2][m] = v;
         }
 #pragma unroll
-        for (int m = 0; m < 3; m++) {
-          float &o = f.sum[m][w.ws][Q * 4 + w.j][w.c];  // the same lane adds each group's part
-          const float v = group_sums(sum[m]);
-          o = g > 0 ? o + v : v;
-        }
+        for (int m = 0; m < 3; m++) f.sum[m][w.ws][Q * 4 + w.j][w.c] = group_sums(sum[m]);
         // dB and dC of four steps, 16 values, over the 16 channels of each row:
         // every level sums pairs of lanes and packs two values into one
         // register, so that each lane of a row ends with the sum of one value
@@ -828,18 +843,20 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
         const float v = (odd1 ? p2[1] : p2[0]) + dpp_f<0xb1>(odd1 ? p2[0] : p2[1]);
         // lane l of a row: step bits l & 1 (high), l & 2 (low), dB or dC l & 4, state l & 8
         const int l = w.lane & 15;
-        f.bc[w.c >> 4][Q * 4 + (l & 1) * 2 + ((l >> 1) & 1)][((l >> 2) & 1) * NP + g * GP + nl + (l >> 3)] = v;
+        f.bc[w.c >> 4][Q * 4 + (l & 1) * 2 + ((l >> 1) & 1)][((l >> 2) & 1) * GP + nl + (l >> 3)] = v;
         __builtin_amdgcn_sched_barrier(0);
       });
     }
   };
   const int n = w.ntiles;
-  unroll_up<PF>([&](auto i) PR_INLINE { load_tile(ring[decltype(i)::value], n - 1 - decltype(i)::value); });
+  unroll_up<RS>([&](auto i) PR_INLINE { load_tile(ring[decltype(i)::value], n - 1 - decltype(i)::value); });
+  load_coef(coef[0], n - 1);
+  load_coef(coef[1], n - 2);
   stage(ring[0], n - 1, std::integral_constant<int, 0>{});
-  for (int tile = n - 1; tile >= 0; tile -= PF)
-    unroll_up<PF>([&](auto i) PR_INLINE {
+  for (int tile = n - 1; tile >= 0; tile -= 2)
+    unroll_up<2>([&](auto i) PR_INLINE {
       constexpr int I = decltype(i)::value;
-      if (tile - I >= 0) run_tile(ring[(I + 1) % PF], tile - I, std::integral_constant<int, I & 1>{});
+      if (tile - I >= 0) run_tile(ring[(I + 1) % RS], tile - I, std::integral_constant<int, I>{});
     });
   if (n > 0) {
     lds_barrier();
@@ -848,16 +865,14 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
   // steps past the length: zero gradients
   const float zero[UC] = {};
   for (int tile = n; w.t0 + tile * TL < w.t1; tile++) {
-    const int nv = w.t0 + tile * TL + w.ur < w.t1 ? w.unv : 0;
+    const int nv = w.t0 + tile * TL + w.ur < w.t1 && (!MULTI || a.last) ? w.unv : 0;
     store_u<T, UC, VEC>(rdu.r, odu, tile * rdu.tile, zero, nv);
     store_u<T, UC, VEC>(rdd.r, odd, tile * rdd.tile, zero, nv);
     store_u<T, UC, VEC>(rdz.r, odz, tile * rdz.tile, zero, nv);
   }
-#pragma unroll
-  for (int g = 0; g < NG; g++) {
-    store_state<NS>(a.pA + at * dn + (long long)w.d * a.N, g * GP + nl, a.N, w.on, dA[g]);
-    if (a.dh0 && w.s == 0) store_state<NS>(a.dh0 + w.b * dn + (long long)w.d * a.N, g * GP + nl, a.N, w.on, r[g]);
-  }
+  store_state<NS>(a.pA + at * dn + (long long)w.d * a.N, n0, a.N, w.on, dA);
+  if (a.dh0 && w.s == 0) store_state<NS>(a.dh0 + w.b * dn + (long long)w.d * a.N, n0, a.N, w.on, r);
+  if (MULTI && !a.last) return;
   // dD and the bias' gradient: over the tile's rows, which different threads hold
   __syncthreads();
   float *red = reinterpret_cast<float *>(&buf[0]);  // [2][TL][CH]
@@ -883,14 +898,23 @@ template <typename T, int NS, int WS, bool VEC>
 hipError_t ssm_go(SsmArgs a, int what, hipStream_t s) {
   // no segment starts from the last one's end state (the first one's, backwards)
   const bool part = what == SSM_FWD_AGG || what == SSM_ADJ_AGG;
-  a.segs = part ? a.S - 1 : a.S;
-  a.seg0 = what == SSM_ADJ_AGG ? 1 : 0;
+  a.segs = part ? a.SA - a.R : a.S;
+  a.seg0 = what == SSM_ADJ_AGG ? a.R : 0;
+  if (part) a.seglen /= a.R;
   const dim3 grid((unsigned)((long long)a.B * a.segs * a.G * a.cbg));
-  constexpr int NG = NS * WS > 4 ? NS * WS / 4 : 1;
+  constexpr bool MULTI = NS > 2;
   switch (what) {
     case SSM_FWD: k_ssm_fwd<T, NS, WS, true, VEC><<<grid, 256 * WS, 0, s>>>(a); break;
     case SSM_FWD_AGG: k_ssm_fwd<T, NS, WS, false, VEC><<<grid, 256 * WS, 0, s>>>(a); break;
-    case SSM_ADJ: k_ssm_adj<T, NG, WS, VEC><<<grid, 256 * WS, 0, s>>>(a); break;
+    case SSM_ADJ:
+      a.NPT = 4 * NS * WS;
+      for (a.n_off = 0; a.n_off < a.N; a.n_off += 8 * WS) {
+        a.last = a.n_off + 8 * WS >= a.N;
+        k_ssm_adj<T, WS, MULTI, VEC><<<grid, 256 * WS, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+      }
+      return hipSuccess;
     default: k_ssm_adj_agg<T, NS, WS, VEC><<<grid, 256 * WS, 0, s>>>(a); break;
   }
   return hipGetLastError();

@@ -22,13 +22,16 @@ struct SsmArgs {
   float *hlast, *states;             // may be null (states is required by the adjoint)
   const float *dhlast;               // adjoint, may be null
   float *dh0;                        // adjoint, may be null
-  float *agg, *sumd;                 // time split: per (b, segment) aggregates [D][N], sums of delta [D]
+  float *agg, *sumd;                 // time split: per (b, piece) end, then entering, states [D][N]; sums of delta [D]
   float *part;                       // adjoint: dB | dC partials [block of the group][B][T][G][2 NP]
   float *pA, *pD;                    // adjoint: [B S][D][N] and [B S][2][D] partials of dA, dD | dbias
   int B, T, D, N, G, softplus;
   int dpg, cbg;                      // channels per group, channel blocks per group
   int S, seglen;                     // time segments and their steps (a multiple of SSM_TL)
-  int segs, seg0;                    // segments of a launch and the first of them (set by the launcher)
+  int R, SA;                         // pieces of a segment in the passes that prepare the split, S R
+  float *acc;                        // adjoint of more than 16 states: sums over states, [B][T][3][D]
+  int n_off, last, NPT;              // its launches: first state, whether the last, padded number of states
+  int segs, seg0;                    // segments or pieces of a launch and the first of them (set by the launcher)
   int vec;                           // all arrays may be moved in vectors of four
 };
 

@@ -147,7 +147,10 @@ SCANS = [  # B, T, channels, N, G, gate, ragged, softplus
     (1, 1, 1, 1, 1, True, False, True), (2, 5, 3, 2, 1, False, True, True), (2, 16, 64, 16, 1, True, False, True),
     (3, 17, 65, 16, 1, True, True, True), (2, 100, 130, 5, 2, True, True, False), (2, 48, 72, 8, 2, False, True, True),
     (1, 320, 8, 16, 1, True, False, True), (2, 90, 40, 24, 1, True, True, True), (1, 70, 36, 32, 1, True, False, True),
-    (2, 50, 20, 64, 2, True, True, True), (3, 300, 33, 7, 1, True, True, True), (1, 31, 4, 64, 1, False, False, False)]
+    (2, 50, 20, 64, 2, True, True, True), (3, 300, 33, 7, 1, True, True, True), (1, 31, 4, 64, 1, False, False, False),
+    # many states: a launch of the adjoint for each 16, more tiles than are in flight
+    (2, 120, 24, 64, 1, True, False, True), (2, 120, 26, 64, 2, True, True, True), (1, 200, 64, 40, 1, True, True, True),
+    (1, 200, 68, 33, 1, False, False, True), (2, 120, 24, 32, 2, True, True, True), (1, 120, 30, 17, 1, True, False, True)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
@@ -193,6 +196,38 @@ def test_scan(dtype, case):
     few = nan(B, T, G * N, dtype=dtype)
     bd.ssm_scan_adjoint(*main, states, slot_in(cut(dy, n), 0, 0), ws, dh_last=dh.cuda(), **kw, dC=few)
     assert torch.equal(few, o["dC"])
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("case", [(2, 120, 24, 64, 1, True), (1, 200, 64, 40, 1, False), (2, 90, 72, 24, 2, True),
+                                  (2, 700, 8, 32, 1, True), (1, 33, 4, 20, 1, False), (2, 77, 132, 16, 1, True),
+                                  (2, 77, 12, 4, 1, False), (1, 100, 68, 36, 1, False), (2, 60, 12, 60, 1, True)])
+def test_scan_whole_arrays(dtype, case):
+    """The same on contiguous arrays, which the kernels move in vectors of four."""
+    B, T, ch, N, G, ragged = case
+    print("scan, whole arrays", dtype, case, flush=True)
+    g = gen(sum(case[:5]) + 1)
+    p = scan_problem(g, dtype, B, T, ch, N, G, True, True)
+    n = torch.tensor([T - 7] + [T] * (B - 1), dtype=torch.int32) if ragged else None
+    dh, dy = rnd(g, B, ch, N), rnd(g, B, T, ch, dtype=dtype)
+    dev = {k: None if v is None else v.cuda() for k, v in p.items()}
+    ws = torch.empty(bd.ssm_workspace_bytes(dtype, B, T, ch, N, G), dtype=torch.uint8, device="cuda").fill_(255)
+    y, hl, states = nan(B, T, ch, dtype=dtype), nan(B, ch, N), nan(*bd.ssm_states_shape(B, T, ch, N))
+    kw = dict(D=dev["D"], z=dev["z"], dt_bias=dev["dt_bias"], lengths=None if n is None else n.cuda())
+    main = (dev["u"], dev["dt"], dev["A"], dev["Bm"], dev["Cm"])
+    bd.ssm_scan(*main, y, ws, h_last=hl, states=states, **kw)
+    ry, rh = R.scan(**p, lengths=n)
+    near(y, ry, TOL, "y")
+    near(hl, rh, TOL, "h")
+    o = dict(du=nan(B, T, ch, dtype=dtype), ddt=nan(B, T, ch, dtype=dtype), dB=nan(B, T, G * N, dtype=dtype),
+             dC=nan(B, T, G * N, dtype=dtype), dA=nan(ch, N), dD=nan(ch), ddt_bias=nan(ch), dh0=nan(B, ch, N),
+             dz=nan(B, T, ch, dtype=dtype))
+    ws.fill_(255)
+    bd.ssm_scan_adjoint(*main, states, dy.cuda(), ws, dh_last=dh.cuda(), **kw, **o)
+    r = R.scan_grads(**p, dy=dy, lengths=n, dh_last=dh)
+    r["ddt_bias"] = r.pop("dbias")
+    for k, v in o.items():
+        near(v, r[k], SUM_TOL if k in ("dA", "dD", "ddt_bias", "dh0") else TOL, k)
 
 
 def test_scan_gradient_against_differences():
