@@ -590,7 +590,9 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj_agg(SsmArgs a) {
 // their decays for the walk back.  MULTI: more than 16 states, one launch for
 // each 16; the sums over states go through a.acc from one to the next, and the
 // last one makes the outputs.  (One kernel for all of more than 16 states did
-// not fit the registers.)
+// not fit the registers, and its copies of registers to make room were made
+// where a branch on lanes joined, with lanes still off: there are no such
+// branches in the loops of these kernels.)
 template <typename T, int WS, bool MULTI, bool VEC>
 __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
   using P = Place<T, WS>;
@@ -719,11 +721,15 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
     for (int i = 0; i < UC; i++) {
       const bool in = w.ur < left && i < w.unv && fin;
       const float sum[3] = {sums[0][i], sums[1][i], sums[2][i]};
-      const float u = pu.get(i), v = pd.get(i) + ub[i], e = pe[i];
-      du[i] = in ? fmaf(pdl[i], sum[1], uD[i] * e) : 0.f;
-      ddt[i] = in ? fmaf(u, sum[1], sum[2]) * (sp ? fsigm(v) : 1.f) : 0.f;
-      const float zz = pz.get(i), s = fsigm(zz), y0 = fmaf(uD[i], u, sum[0]);
-      dz[i] = in ? py.get(i) * y0 * (s * fmaf(zz, 1.f - s, 1.f)) : 0.f;  // stored where there is a gate
+      const float u = pu.get(i), v = pd.get(i) + ub[i], e = pe[i], zz = pz.get(i);
+      const float sg = fsigm(v), s = fsigm(zz), y0 = fmaf(uD[i], u, sum[0]);
+      float o[3] = {fmaf(pdl[i], sum[1], uD[i] * e), fmaf(u, sum[1], sum[2]) * (sp ? sg : 1.f),
+                    py.get(i) * y0 * (s * fmaf(zz, 1.f - s, 1.f))};  // dz: stored where there is a gate
+      // (values of their own, so that they are selected below and not branched to)
+      asm volatile("" : "+v"(o[0]), "+v"(o[1]), "+v"(o[2]));
+      du[i] = in ? o[0] : 0.f;
+      ddt[i] = in ? o[1] : 0.f;
+      dz[i] = in ? o[2] : 0.f;
       accD[i] = fmaf(e, in ? u : 0.f, accD[i]);
       accb[i] += ddt[i];
     }
