@@ -485,3 +485,21 @@ def test_other_stream_graph_and_repeats():
         for got, ref in zip((buf["c"], buf["h"], buf["o"]), want[k]):
             assert torch.equal(got, ref), k
     assert torch.equal(y0, y1)
+
+
+def test_example_block():
+    """The example's block: its loss falls, and single tokens continue a prompt
+    as the whole sequence does, up to the 8-bit rounding of products whose
+    inputs differ in the last bf16 digits (one step of 1/127 of a row's largest
+    value may flip: bounded by 2% of the largest output)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "selective_block.py")
+    spec = importlib.util.spec_from_file_location("selective_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    block = ex.Block(dim=64, seed=3)
+    losses = ex.train(block, steps=6)
+    assert losses[-1] < 0.95 * losses[0], losses
+    got, whole = ex.serve(block)
+    assert float((got.float() - whole.float()).abs().max()) <= 0.02 * float(whole.float().abs().max())
