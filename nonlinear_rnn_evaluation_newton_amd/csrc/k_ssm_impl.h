@@ -165,6 +165,23 @@ __device__ inline void fma_bcast_steps(float *acc, float c, float v0, float v1, 
       : "v"(c), "v"(v0), "v"(v1), "v"(v2), "v"(v3), "n"(I0), "n"(I0 + 1), "n"(I0 + 2), "n"(I0 + 3));
 }
 
+// o[w][k] = v[w] times c[k] of lane I0 + w, for two k
+template <int I0>
+__device__ inline void mul_bcast_steps(float (*o)[2], const float *c, const float *v) {
+  asm("s_nop 1\n\t"
+      "v_mul_f32_dpp %0, %8, %10 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %1, %9, %10 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %2, %8, %11 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %3, %9, %11 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %4, %8, %12 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %5, %9, %12 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %6, %8, %13 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %7, %9, %13 row_newbcast:%17 row_mask:0xf bank_mask:0xf"
+      : "=&v"(o[0][0]), "=&v"(o[0][1]), "=&v"(o[1][0]), "=&v"(o[1][1]), "=&v"(o[2][0]), "=&v"(o[2][1]), "=&v"(o[3][0]),
+        "=&v"(o[3][1])
+      : "v"(c[0]), "v"(c[1]), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "n"(I0), "n"(I0 + 1), "n"(I0 + 2), "n"(I0 + 3));
+}
+
 // The first two levels of sums over the 16 lanes of a row, 16 values to 4
 // registers: lanes 8 apart (the row's upper half takes the odd values), then 4
 // apart (the odd quads take the odd registers).  An instruction writes only the
@@ -304,6 +321,23 @@ __device__ inline void store_state(float *p, int n0, int N, bool on, const float
     if (on && n0 + i < N) p[n0 + i] = h[i];
 }
 
+// out[channel] = the sum over the rows of a tile, which different threads hold,
+// through the block's shared memory
+template <typename P, int UC>
+__device__ inline void sum_rows(const P &w, const float *v, float *sh, float *out) {
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < UC; i++) sh[w.ur * P::CH + w.uc + i] = v[i];
+  __syncthreads();
+  const int cc = threadIdx.x;
+  if (cc < w.nch) {
+    float s = 0.f;
+#pragma unroll
+    for (int row = 0; row < P::TL; row++) s += sh[row * P::CH + cc];
+    out[w.ch0 + cc] = s;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
@@ -335,7 +369,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_fwd(SsmArgs a) {
 #pragma unroll
     for (int k = 0; k < NS; k++) h[k] = 0.f;
   }
-  float dsum = 0.f, ub[UC], uD[UC];
+  float dsum[UC] = {}, ub[UC], uD[UC];  // dsum: not FULL, of the staged units
   w.param(a.bias, ub);
   w.param(FULL ? a.Dk : nullptr, uD);
 
@@ -388,6 +422,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_fwd(SsmArgs a) {
       const float v = delta_of<T>(s.d.get(i) + ub[i], sp);
       dx[2 * i] = live && i < w.unv ? v : 0.f;
       dx[2 * i + 1] = dx[2 * i] * s.u.get(i);
+      if (!FULL) dsum[i] += dx[2 * i];
     }
 #pragma unroll
     for (int i = 0; i < UC; i += 2)
@@ -428,7 +463,6 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_fwd(SsmArgs a) {
           ea[AHEAD ? Q & 1 : 0][W][k] = __builtin_amdgcn_exp2f(dx.x * A2[k]);
           xb[AHEAD ? Q & 1 : 0][W][k] = row_bcast<I>(B[k]) * dx.y;
         }
-        if (!FULL) dsum += dx.x;
       });
     };
     if constexpr (AHEAD) prepare(std::integral_constant<int, 0>{});
@@ -474,7 +508,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_fwd(SsmArgs a) {
   } else {
     const long long at = (long long)w.b * a.SA + w.s;
     store_state<NS>(a.agg + at * dn + (long long)w.d * a.N, n0, a.N, w.on, h);
-    if (w.j == 0 && w.ws == 0 && w.on) a.sumd[at * a.D + w.d] = dsum;
+    sum_rows<P, UC>(w, dsum, &sdx[0][0][0].x, a.sumd + at * a.D);
   }
 }
 
@@ -495,7 +529,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj_agg(SsmArgs a) {
   const int n0 = (w.ws * 4 + w.j) * NS;
   const long long dn = (long long)a.D * a.N;
   const bool gate = a.z.p != nullptr, sp = a.softplus != 0;
-  float A2[NS], r[NS], ub[UC], dsum = 0.f;
+  float A2[NS], r[NS], ub[UC], dsum[UC] = {};
   load_state<NS>(a.A + (long long)w.d * a.N, n0, a.N, w.on, A2);
   w.param(a.bias, ub);
 #pragma unroll
@@ -523,7 +557,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj_agg(SsmArgs a) {
   };
   auto stage = [&](Slot &s, int tile, auto parity) PR_INLINE {
     constexpr int p = decltype(parity)::value;
-    const bool live = w.t0 + tile * TL + w.ur < w.end;
+    const bool live = tile >= 0 && w.t0 + tile * TL + w.ur < w.end;
     tC = s.C;
     float o[2 * UC];
 #pragma unroll
@@ -531,6 +565,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj_agg(SsmArgs a) {
       const bool in = live && i < w.unv;
       const float v = delta_of<T>(s.d.get(i) + ub[i], sp), e = s.y.get(i) * gate_of(s.z.get(i), gate);
       o[2 * i] = in ? v : 0.f;
+      dsum[i] += o[2 * i];
       o[2 * i + 1] = in ? e : 0.f;
     }
 #pragma unroll
@@ -557,7 +592,6 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj_agg(SsmArgs a) {
           ea[AHEAD ? Q & 1 : 0][W][k] = __builtin_amdgcn_exp2f(de.x * A2[k]);
           ce[AHEAD ? Q & 1 : 0][W][k] = row_bcast<I>(C[k]) * de.y;
         }
-        dsum += de.x;
       });
     };
     if constexpr (AHEAD) prepare(std::integral_constant<int, TL / 4 - 1>{});
@@ -581,7 +615,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj_agg(SsmArgs a) {
     });
   const long long at = (long long)w.b * a.SA + w.s;
   store_state<NS>(a.agg + at * dn + (long long)w.d * a.N, n0, a.N, w.on, r);
-  if (w.j == 0 && w.ws == 0 && w.on) a.sumd[at * a.D + w.d] = dsum;
+  sum_rows<P, UC>(w, dsum, &sde[0][0][0].x, a.sumd + at * a.D);
 }
 
 // The gradients of one segment.  A wavefront keeps two states per lane, 8 WS
@@ -776,15 +810,15 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
       // the states again; the decays and inputs of four steps before their chain
       unroll_up<TL / 4>([&](auto quad) PR_INLINE {
         constexpr int Q = decltype(quad)::value;
-        unroll_up<4>([&](auto within) PR_INLINE {
-          constexpr int I = Q * 4 + decltype(within)::value;
-          const float2 dx = f.dx[I][w.c];
+        float x[4];
 #pragma unroll
-          for (int k = 0; k < NS; k++) {
-            as[I][k] = __builtin_amdgcn_exp2f(dx.x * A2[k]);
-            hs[I][k] = row_bcast<I>(B[k]) * dx.y;
-          }
-        });
+        for (int m = 0; m < 4; m++) {
+          const float2 dx = f.dx[Q * 4 + m][w.c];
+          x[m] = dx.y;
+#pragma unroll
+          for (int k = 0; k < NS; k++) as[Q * 4 + m][k] = __builtin_amdgcn_exp2f(dx.x * A2[k]);
+        }
+        mul_bcast_steps<Q * 4>(&hs[Q * 4], B, x);
         unroll_up<4>([&](auto within) PR_INLINE {
           constexpr int I = Q * 4 + decltype(within)::value;
 #pragma unroll

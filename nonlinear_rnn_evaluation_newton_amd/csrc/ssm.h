@@ -70,18 +70,12 @@ __device__ inline float exp_acc(float x) {
   return fabsf(x) < 128.f ? fmaf(e, r * 0.6931471805599453f, e) : e;
 }
 
-// log(1 + e) for 0 <= e <= 1 by 2 artanh(s), s = e / (2 + e) <= 1/3: the
-// series in s^2 <= 1/9 is cut where its next term is below 2e-8 of the sum.
+// log(1 + e) for 0 <= e <= 1: the logarithm of the rounded sum u, and what its
+// rounding left out, e - (u - 1), over u.  That quotient is taken without the
+// division: where u is not near 1 the term is below 2^-24 of the result.
 __device__ inline float log1p_unit(float e) {
-  const float s = e * frcp(2.f + e), q = s * s;
-  float p = 1.f / 13.f;
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
-  p = p * q;
-  return fmaf(2.f * s, p, 2.f * s);
+  const float u = 1.f + e;
+  return fmaf(__builtin_amdgcn_logf(u), 0.6931471805599453f, e - (u - 1.f));
 }
 
 __device__ inline float softplus_f(float v) {
