@@ -3,6 +3,8 @@
 // Bound by memory: x is read and y written once.  A thread takes V adjacent
 // channels (16 bytes where alignment allows) through a run of steps and keeps
 // the last W - 1 inputs in registers, so a run re-reads only W - 1 steps.
+#include <type_traits>
+
 #include "pararnn.h"
 #include "ssm.h"
 #include "vec.h"
@@ -87,14 +89,15 @@ __global__ __launch_bounds__(256) void k_conv_fwd(ConvArgs a) {
   }
 }
 
-// 32 channel vectors by 8 runs per block; dw and dbias of a block's runs are
-// joined in shared memory in a fixed order.
+// 64 channel vectors by 8 runs per block, a wavefront for each run, so that
+// where it stands in its sequence is a scalar; dw and dbias of a block's runs
+// are joined in shared memory in a fixed order.
 template <typename T, int V, int W>
-__global__ __launch_bounds__(256) void k_conv_adj(ConvArgs a) {
-  __shared__ float red[8][W + 1][32 * V];
-  const int nv = a.D / V, vb = (nv + 31) / 32;
-  const int x = threadIdx.x & 31, r8 = threadIdx.x >> 5;
-  const int dblk = (int)(blockIdx.x % vb) * 32, d = (dblk + x) * V;
+__global__ __launch_bounds__(512) void k_conv_adj(ConvArgs a) {
+  __shared__ float red[8][W + 1][64 * V];
+  const int nv = a.D / V, vb = (nv + 63) / 64;
+  const int x = threadIdx.x & 63, r8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int dblk = (int)(blockIdx.x % vb) * 64, d = (dblk + x) * V;
   const long long q = (long long)(blockIdx.x / vb) * 8 + r8;
   const bool on = d < a.D && q < (long long)a.B * a.runs;
   float gw[W][V], gb[V];
@@ -106,7 +109,7 @@ __global__ __launch_bounds__(256) void k_conv_adj(ConvArgs a) {
   }
   if (on) {
     const int run = (int)(q % a.runs), b = (int)(q / a.runs);
-    const int len = seq_len(a.lengths, b, a.T);
+    const int len = __builtin_amdgcn_readfirstlane(seq_len(a.lengths, b, a.T));
     const int t0 = run * a.run, t1 = a.T - t0 < a.run ? a.T : t0 + a.run;
     float w[W][V], bias[V], win[W][V], da[W][V];  // da[k]: of step t - W + 1 + k
     conv_weights<T, V, W>(a, d, w, bias);
@@ -122,52 +125,47 @@ __global__ __launch_bounds__(256) void k_conv_adj(ConvArgs a) {
     }
     const bool own_state = run == 0;
     constexpr int U = 4;
-    // W - 1 steps past the run give the da that its last inputs still need;
-    // the first run also walks back over the state's inputs
-    for (int t = t0; t < t1 + W - 1; t += U) {
-      VecOf<T, V> in[U], gy[U];
+    const T *xp = (const T *)a.x.p + b * a.x.sb + d, *gp = (const T *)a.dy.p + b * a.dy.sb + d;
+    // Step tt: da there, its share of dw, and the input gradient of step
+    // tt - W + 1, whose last tap it is.  FAST: tt and that step lie within the
+    // run, and no gradient of the state reaches it.
+    auto step = [&](auto fast, int tt, const VecOf<T, V> &in, const VecOf<T, V> &gy) __attribute__((always_inline)) {
+      constexpr bool FAST = decltype(fast)::value;
+      const bool own = FAST || tt < t1, live = FAST || tt < len;
+      float o[V];
 #pragma unroll
-      for (int u = 0; u < U; u++) {
-        const bool ok = t + u < len && t + u < t1 + W - 1;
-        in[u] = ldv<T, V>((const T *)a.x.p + b * a.x.sb + (t + u) * a.x.st + d, ok);
-        gy[u] = ldv<T, V>((const T *)a.dy.p + b * a.dy.sb + (t + u) * a.dy.st + d, ok);
-      }
+      for (int i = 0; i < V; i++) {
 #pragma unroll
-      for (int u = 0; u < U; u++) {
-        const int tt = t + u;
-        if (tt >= t1 + W - 1) break;
-        const bool own = tt < t1;
-        float o[V];
-#pragma unroll
-        for (int i = 0; i < V; i++) {
-#pragma unroll
-          for (int k = 0; k < W - 1; k++) {
-            win[k][i] = win[k + 1][i];
-            da[k][i] = da[k + 1][i];
-          }
-          win[W - 1][i] = in[u].f(i);
-          float s = bias[i];
-#pragma unroll
-          for (int k = 0; k < W; k++) s = fmaf(w[k][i], win[k][i], s);
-          float g = gy[u].f(i);
-          if (a.silu) {
-            const float p = fsigm(s);
-            g *= p * fmaf(s, 1.f - p, 1.f);
-          }
-          if (tt >= len) g = 0.f;
-          da[W - 1][i] = g;
-          if (own) {
-            gb[i] += g;
-#pragma unroll
-            for (int k = 0; k < W; k++) gw[k][i] = tt < len ? fmaf(g, win[k][i], gw[k][i]) : gw[k][i];
-          }
-          // the input of step tt - W + 1 meets tap W - 1 - k at step tt - W + 1 + k
-          float sum = 0.f;
-#pragma unroll
-          for (int k = 0; k < W; k++) sum = fmaf(w[W - 1 - k][i], da[k][i], sum);
-          o[i] = sum;
+        for (int k = 0; k < W - 1; k++) {
+          win[k][i] = win[k + 1][i];
+          da[k][i] = da[k + 1][i];
         }
-        const int st = tt - (W - 1);
+        win[W - 1][i] = in.f(i);
+        float s = bias[i];
+#pragma unroll
+        for (int k = 0; k < W; k++) s = fmaf(w[k][i], win[k][i], s);
+        float g = gy.f(i);
+        if (a.silu) {
+          const float p = fsigm(s);
+          g *= p * fmaf(s, 1.f - p, 1.f);
+        }
+        if (!live) g = 0.f;
+        da[W - 1][i] = g;
+        if (own && live) {
+          gb[i] += g;
+#pragma unroll
+          for (int k = 0; k < W; k++) gw[k][i] = fmaf(g, win[k][i], gw[k][i]);
+        }
+        // the input of step tt - W + 1 meets tap W - 1 - k at step tt - W + 1 + k
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; k++) sum = fmaf(w[W - 1 - k][i], da[k][i], sum);
+        o[i] = sum;
+      }
+      const int st = tt - (W - 1);
+      if constexpr (FAST) {
+        if (a.dx.p) stv<T, V>((T *)a.dx.p + b * a.dx.sb + st * a.dx.st + d, o);
+      } else {
         const bool state_step = st < 0 && own_state;
         if (a.dsout && (st >= t0 || state_step) && st >= len - (W - 1) && st < len) {
           const VecOf<T, V> g =
@@ -184,6 +182,30 @@ __global__ __launch_bounds__(256) void k_conv_adj(ConvArgs a) {
           stv<T, V>((T *)a.dsin + ((long long)b * (W - 1) + st + W - 1) * a.D + d, o);
         }
       }
+    };
+    // W - 1 steps past the run give the da that its last inputs still need;
+    // the first run also walks back over the state's inputs
+    int t = t0;
+    const int slow = t0 + W - 1, fast_end = len < t1 ? len : t1;
+    for (; t < slow && t < t1 + W - 1; t++) {
+      const bool ok = t < len;
+      const VecOf<T, V> in = ldv<T, V>(xp + t * a.x.st, ok), gy = ldv<T, V>(gp + t * a.dy.st, ok);
+      step(std::integral_constant<bool, false>{}, t, in, gy);
+    }
+    for (; t + U <= fast_end; t += U) {
+      VecOf<T, V> in[U], gy[U];
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        in[u] = ldv<T, V>(xp + (t + u) * a.x.st, true);
+        gy[u] = ldv<T, V>(gp + (t + u) * a.dy.st, true);
+      }
+#pragma unroll
+      for (int u = 0; u < U; u++) step(std::integral_constant<bool, true>{}, t + u, in[u], gy[u]);
+    }
+    for (; t < t1 + W - 1; t++) {
+      const bool ok = t < len;
+      const VecOf<T, V> in = ldv<T, V>(xp + t * a.x.st, ok), gy = ldv<T, V>(gp + t * a.dy.st, ok);
+      step(std::integral_constant<bool, false>{}, t, in, gy);
     }
   }
   if (!a.part) return;
@@ -195,8 +217,8 @@ __global__ __launch_bounds__(256) void k_conv_adj(ConvArgs a) {
   }
   __syncthreads();
   float *o = a.part + (long long)(blockIdx.x / vb) * (W + 1) * a.D;
-  for (int i = threadIdx.x; i < (W + 1) * 32 * V; i += 256) {
-    const int k = i / (32 * V), c = i % (32 * V), dd = dblk * V + c;
+  for (int i = threadIdx.x; i < (W + 1) * 64 * V; i += 512) {
+    const int k = i / (64 * V), c = i % (64 * V), dd = dblk * V + c;
     if (dd < a.D) {
       float s = 0.f;
 #pragma unroll
@@ -268,10 +290,15 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvStepArgs a) {
 }
 
 template <typename T, int V, int W>
-hipError_t conv_launch(const ConvArgs &a, bool adj, hipStream_t s) {
+hipError_t conv_fwd_launch(const ConvArgs &a, hipStream_t s) {
   const long long nv = a.D / V, q = (long long)a.B * a.runs;
-  if (adj) k_conv_adj<T, V, W><<<dim3((unsigned)(((nv + 31) / 32) * ((q + 7) / 8))), 256, 0, s>>>(a);
-  else k_conv_fwd<T, V, W><<<dim3((unsigned)(((nv + 255) / 256) * q)), 256, 0, s>>>(a);
+  k_conv_fwd<T, V, W><<<dim3((unsigned)(((nv + 255) / 256) * q)), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <typename T, int V, int W>
+hipError_t conv_adj_launch(const ConvArgs &a, hipStream_t s) {
+  const long long nv = a.D / V, q = (long long)a.B * a.runs;
+  k_conv_adj<T, V, W><<<dim3((unsigned)(((nv + 63) / 64) * ((q + 7) / 8))), 512, 0, s>>>(a);
   return hipGetLastError();
 }
 template <typename T, int V, int W>
@@ -288,19 +315,22 @@ hipError_t conv_step_launch(const ConvStepArgs &a, hipStream_t s) {
     case 3: return F<T, V, 3>(__VA_ARGS__);           \
     default: return F<T, V, 4>(__VA_ARGS__);          \
   }
-#define PR_CONV(F, ...)                               \
+#define PR_CONV(V16, F, ...)                          \
   if (dtype == PR_BF16) {                             \
-    if (vec) PR_CONV_W(uint16_t, 8, F, __VA_ARGS__)   \
+    if (vec) PR_CONV_W(uint16_t, V16, F, __VA_ARGS__) \
     PR_CONV_W(uint16_t, 1, F, __VA_ARGS__)            \
   }                                                   \
   if (vec) PR_CONV_W(float, 4, F, __VA_ARGS__)        \
   PR_CONV_W(float, 1, F, __VA_ARGS__)
 
 static hipError_t conv_dispatch(int dtype, int W, bool vec, const ConvArgs &a, bool adj, hipStream_t s) {
-  PR_CONV(conv_launch, a, adj, s)
+  if (adj) {
+    PR_CONV(4, conv_adj_launch, a, s)
+  }
+  PR_CONV(8, conv_fwd_launch, a, s)
 }
 static hipError_t conv_step_dispatch(int dtype, int W, bool vec, const ConvStepArgs &a, hipStream_t s) {
-  PR_CONV(conv_step_launch, a, s)
+  PR_CONV(8, conv_step_launch, a, s)
 }
 
 }  // namespace pr
@@ -347,7 +377,7 @@ size_t pararnn_conv_workspace_bytes(const pr_conv_problem *p) {
   if (conv_check(p) != PR_OK) return 0;
   int run, runs;
   size_t most = 0;
-  for (int V : {1, p->dtype == PR_BF16 ? 8 : 4}) {
+  for (int V : {1, 4}) {
     conv_runs(p, V, &run, &runs);
     const size_t n = (((size_t)p->B * runs + 7) / 8) * (p->W + 1) * p->D * 4;
     most = n > most ? n : most;
@@ -383,7 +413,7 @@ int pararnn_conv_adjoint(const pr_conv_problem *p, const pr_view *x, const void 
   const size_t need = pararnn_conv_workspace_bytes(p);
   if (!workspace || ws_bytes < need) return fail(PR_EWORKSPACE, "workspace %zu bytes < %zu", ws_bytes, need);
   if (((uintptr_t)workspace & 255) != 0) return fail(PR_EINVAL, "workspace must be 256-byte aligned");
-  const int V = p->dtype == PR_BF16 ? 8 : 4;
+  const int V = 4;
   const bool vec = p->D % V == 0 && vecv_ok(x, V) && vecv_ok(dy, V) && vecv_ok(dx, V) && al16(state_in) &&
                    al16(dstate_out) && al16(dstate_in);
   ConvArgs a{};

@@ -11,6 +11,8 @@ struct Vec;
 template <>
 struct Vec<uint16_t, 8> { typedef uint4 type; };
 template <>
+struct Vec<uint16_t, 4> { typedef uint2 type; };
+template <>
 struct Vec<float, 4> { typedef float4 type; };
 template <>
 struct Vec<uint16_t, 1> { typedef uint16_t type; };
