@@ -30,13 +30,23 @@ struct __attribute__((packed)) Bytes16 {
   i32x4 v;
 };
 // 16 bytes of a row from k on, zeros from `ke` on.  AL: 16-byte aligned and
-// ke a multiple of 16; else any alignment, the last bytes one by one.
+// ke a multiple of 16; else any alignment, and the row's last bytes come from
+// its last 16, moved down (one by one only in a row of fewer).
 template <bool AL>
 __device__ inline i32x4 load16(const int8_t *row, int k, int ke, bool on) {
   i32x4 v = {0, 0, 0, 0};
   if (!on || k >= ke) return v;
   if constexpr (AL) return *reinterpret_cast<const i32x4 *>(row + k);
   if (k + 16 <= ke) return reinterpret_cast<const Bytes16 *>(row + k)->v;
+  if (ke >= 16) {
+    v = reinterpret_cast<const Bytes16 *>(row + ke - 16)->v;
+    const int s = 8 * (k + 16 - ke);  // bits, 8..120
+    unsigned long long lo = (unsigned)v[0] | ((unsigned long long)(unsigned)v[1] << 32);
+    unsigned long long hi = (unsigned)v[2] | ((unsigned long long)(unsigned)v[3] << 32);
+    lo = s >= 64 ? hi >> (s - 64) : (lo >> s) | (hi << (64 - s));
+    hi = s >= 64 ? 0 : hi >> s;
+    return i32x4{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
+  }
 #pragma unroll
   for (int i = 0; i < 15; i++)
     if (k + i < ke) v[i / 4] |= (int)((unsigned)(uint8_t)row[k + i] << (8 * (i % 4)));
@@ -96,6 +106,106 @@ __global__ __launch_bounds__(512) void k_gemm8_rows(Gemm8Args g) {
       const int n = n0 + 4 * (l >> 4) + v;
       if (n < g.N) stf((T *)g.out + m * g.ldo, n, scaled<T>(g, s[v], m, n));
     }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// What a wavefront does with its 32 FM x 32 FN sums, from row mr0 and column
+// nc0 on: a lane holds row lane % 32 of each 32 x 32 tile and, per 4
+// registers, 4 adjacent columns 8 (v / 4) + 4 (lane / 32) ..
+// K splits leave them to k_gemm8_join.  Else scaled, 32 rows at a time, through
+// `mine`, a part of the block's shared memory of 32 rows that no other
+// wavefront uses any more: stored as they are, an instruction would touch 32
+// rows with a few bytes each; read back by rows it stores whole 128-byte lines.
+// 16-byte chunks are swizzled by the row.
+template <typename T, int FM, int FN>
+__device__ inline void g8_results(const Gemm8Args &g, i32x16 (*acc)[FM], int8_t *mine, int mr0, int nc0, int lane) {
+  const int h = lane >> 5, r = lane & 31;
+  if (g.splits > 1) {
+#pragma unroll
+    for (int i = 0; i < FM; i++) {
+      const int m = mr0 + i * 32 + r;
+      if (m >= g.M) continue;
+#pragma unroll
+      for (int j = 0; j < FN; j++)
+#pragma unroll
+        for (int v4 = 0; v4 < 4; v4++) {
+          const int n = nc0 + j * 32 + 8 * v4 + 4 * h;
+          int *o = g.part + ((long long)blockIdx.y * g.M + m) * g.N + n;
+          if (n + 4 <= g.N && (g.N & 3) == 0)
+            *reinterpret_cast<i32x4 *>(o) = i32x4{acc[j][i][4 * v4], acc[j][i][4 * v4 + 1], acc[j][i][4 * v4 + 2],
+                                                  acc[j][i][4 * v4 + 3]};
+          else
+            for (int c = 0; c < 4 && n + c < g.N; c++) o[c] = acc[j][i][4 * v4 + c];
+        }
+    }
+    return;
+  }
+  constexpr int E = sizeof(T), CPR = FN * 32 * E / 16;  // chunks per row
+  const bool vec = (g.ldo * E) % 16 == 0 && ((uintptr_t)g.out & 15) == 0;
+  float sw[FN][16], bias[FN][16];  // of the lane's columns, loaded once
+#pragma unroll
+  for (int j = 0; j < FN; j++)
+#pragma unroll
+    for (int v = 0; v < 16; v++) {
+      const int n = nc0 + j * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
+      sw[j][v] = n < g.N ? g.sw[n] : 0.f;
+      bias[j][v] = n < g.N && g.bias ? ldf((const T *)g.bias, n) : 0.f;
+    }
+#pragma unroll
+  for (int i = 0; i < FM; i++) {
+    const int mr = mr0 + i * 32;
+    const float sa = mr + r < g.M ? g.sa[mr + r] : 0.f;
+#pragma unroll
+    for (int j = 0; j < FN; j++)
+#pragma unroll
+      for (int v4 = 0; v4 < 4; v4++) {
+        float o[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+          o[c] = fmaf((float)acc[j][i][4 * v4 + c], sa * sw[j][4 * v4 + c], bias[j][4 * v4 + c]);
+        const int byte = (j * 32 + 8 * v4 + 4 * h) * E, ch = (byte >> 4) ^ (r & (CPR - 1));
+        int8_t *q = mine + r * (CPR * 16) + ch * 16 + (byte & 15);
+        if constexpr (E == 2) {
+          uint2 u;
+          u.x = (unsigned)f2bf(o[0]) | ((unsigned)f2bf(o[1]) << 16);
+          u.y = (unsigned)f2bf(o[2]) | ((unsigned)f2bf(o[3]) << 16);
+          *reinterpret_cast<uint2 *>(q) = u;
+        } else {
+          *reinterpret_cast<float4 *>(q) = make_float4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wavefront's own stores, read by its other lanes
+    if (vec) {
+#pragma unroll
+      for (int q = 0; q < 32 * CPR / 64; q++) {
+        const int e = q * 64 + lane, row = e / CPR, ch = e % CPR;
+        const int n = nc0 + ch * (16 / E), m = mr + row;
+        const uint4 v = *reinterpret_cast<const uint4 *>(mine + row * (CPR * 16) + ((ch ^ (row & (CPR - 1))) << 4));
+        if (m < g.M && n < g.N) {
+          T *p = (T *)g.out + m * g.ldo + n;
+          if (n + 16 / E <= g.N) {
+            *reinterpret_cast<uint4 *>(p) = v;
+          } else {
+            const T *x = reinterpret_cast<const T *>(&v);
+#pragma unroll
+            for (int c = 0; c < 16 / E; c++)
+              if (n + c < g.N) p[c] = x[c];
+          }
+        }
+      }
+    } else {  // rows of any alignment: neighbouring lanes store neighbouring elements
+      constexpr int NC = FN * 32, RP = 64 / NC > 0 ? 64 / NC : 1, CP = NC / 64 > 0 ? NC / 64 : 1;
+#pragma unroll 8
+      for (int q = 0; q < 32 / RP * CP; q++) {
+        const int row = q / CP * RP + (NC < 64 ? lane / NC : 0), col = (q % CP) * 64 + lane % (NC < 64 ? NC : 64);
+        const int ch = col * E >> 4, n = nc0 + col, m = mr + row;
+        const T x = *reinterpret_cast<const T *>(mine + row * (CPR * 16) + ((ch ^ (row & (CPR - 1))) << 4) +
+                                                 (col * E & 15));
+        if (m < g.M && n < g.N) ((T *)g.out)[m * g.ldo + n] = x;
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
@@ -163,22 +273,7 @@ __global__ __launch_bounds__(256) void k_gemm8_tile(Gemm8Args g) {
     __syncthreads();
     buf ^= 1;
   }
-  // a lane holds row m = lane % 32 of each 32 x 32 tile and, per 4 registers,
-  // 4 adjacent columns 8 (v / 4) + 4 (lane / 32) ..
-#pragma unroll
-  for (int i = 0; i < 2; i++) {
-    const int m = m0 + wm * 64 + i * 32 + (lane & 31);
-    if (m >= g.M) continue;
-#pragma unroll
-    for (int j = 0; j < 2; j++)
-#pragma unroll
-      for (int v = 0; v < 16; v++) {
-        const int n = n0 + wn * 64 + j * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
-        if (n >= g.N) continue;
-        if (g.splits > 1) g.part[((long long)blockIdx.y * g.M + m) * g.N + n] = acc[j][i][v];
-        else stf((T *)g.out + m * g.ldo, n, scaled<T>(g, acc[j][i][v], m, n));
-      }
-  }
+  g8_results<T, 2, 2>(g, acc, &sA[0][0] + wave * (32 * 64 * (int)sizeof(T)), m0 + wm * 64, n0 + wn * 64, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -205,6 +300,7 @@ template <typename T, int WM, int WN, int FM, int FN>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_gemm8_direct(Gemm8Args g) {
   constexpr int BM = WM * FM * 32, BN = WN * FN * 32, NW = WM * WN, QA = BM / 8 / NW, QB = BN / 8 / NW;
   static_assert(QA % 2 == 0 && QB % 2 == 0, "even numbers of loads");
+  static_assert(NW * 32 * FN * 32 * (int)sizeof(T) <= (BM + BN) * TB, "the results fit a stage");
   __shared__ __attribute__((aligned(1024))) int8_t s0[(BM + BN) * TB], s1[(BM + BN) * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN, h = lane >> 5;
@@ -293,88 +389,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_gemm8_direct(Gemm8Args g) {
     step(s1, s0, k0 + TB);
   }
   if (k0 < ke) step(s0, s1, k0);
-  // K splits leave their sums to k_gemm8_join
-  if (g.splits > 1) {
-#pragma unroll
-    for (int i = 0; i < FM; i++) {
-      const int m = m0 + (wm * FM + i) * 32 + (lane & 31);
-      if (m >= g.M) continue;
-#pragma unroll
-      for (int j = 0; j < FN; j++)
-#pragma unroll
-        for (int v4 = 0; v4 < 4; v4++) {
-          const int n = n0 + (wn * FN + j) * 32 + 8 * v4 + 4 * h;
-          int *o = g.part + ((long long)blockIdx.y * g.M + m) * g.N + n;
-          if (n + 4 <= g.N && (g.N & 3) == 0)
-            *reinterpret_cast<i32x4 *>(o) = i32x4{acc[j][i][4 * v4], acc[j][i][4 * v4 + 1], acc[j][i][4 * v4 + 2],
-                                                  acc[j][i][4 * v4 + 3]};
-          else
-            for (int c = 0; c < 4 && n + c < g.N; c++) o[c] = acc[j][i][4 * v4 + c];
-        }
-    }
-    return;
-  }
-  // Scaled results, 32 rows of a wavefront at a time, through its part of the
-  // first stage (every wavefront has passed its last read of it): a lane holds
-  // 4 columns of one row, which stored as they are would touch 32 rows with 16
-  // bytes each; read back by rows, an instruction stores whole 128-byte lines.
-  // 16-byte chunks are swizzled by the row as above.
-  constexpr int E = sizeof(T), CPR = FN * 32 * E / 16;  // chunks per row
-  int8_t *mine = s0 + wave * (32 * FN * 32 * E);
-  static_assert(NW * 32 * FN * 32 * E <= (int)sizeof(s0), "the results fit the stage");
-  const bool vec = (g.ldo * E) % 16 == 0 && ((uintptr_t)g.out & 15) == 0;
-  float sw[FN][16], bias[FN][16];  // of the lane's columns, loaded once
-#pragma unroll
-  for (int j = 0; j < FN; j++)
-#pragma unroll
-    for (int v = 0; v < 16; v++) {
-      const int n = n0 + (wn * FN + j) * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
-      sw[j][v] = n < g.N ? g.sw[n] : 0.f;
-      bias[j][v] = n < g.N && g.bias ? ldf((const T *)g.bias, n) : 0.f;
-    }
-#pragma unroll
-  for (int i = 0; i < FM; i++) {
-    const int mr = m0 + (wm * FM + i) * 32, r = lane & 31;
-    const float sa = mr + r < g.M ? g.sa[mr + r] : 0.f;
-#pragma unroll
-    for (int j = 0; j < FN; j++)
-#pragma unroll
-      for (int v4 = 0; v4 < 4; v4++) {
-        float o[4];
-#pragma unroll
-        for (int c = 0; c < 4; c++)
-          o[c] = fmaf((float)acc[j][i][4 * v4 + c], sa * sw[j][4 * v4 + c], bias[j][4 * v4 + c]);
-        const int byte = (j * 32 + 8 * v4 + 4 * h) * E, ch = (byte >> 4) ^ (r & (CPR - 1));
-        int8_t *q = mine + r * (CPR * 16) + ch * 16 + (byte & 15);
-        if constexpr (E == 2) {
-          uint2 u;
-          u.x = (unsigned)f2bf(o[0]) | ((unsigned)f2bf(o[1]) << 16);
-          u.y = (unsigned)f2bf(o[2]) | ((unsigned)f2bf(o[3]) << 16);
-          *reinterpret_cast<uint2 *>(q) = u;
-        } else {
-          *reinterpret_cast<float4 *>(q) = make_float4(o[0], o[1], o[2], o[3]);
-        }
-      }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wavefront's own stores, read by its other lanes
-#pragma unroll
-    for (int q = 0; q < 32 * CPR / 64; q++) {
-      const int e = q * 64 + lane, row = e / CPR, ch = e % CPR;
-      const int n = n0 + wn * FN * 32 + ch * (16 / E), m = mr + row;
-      const uint4 v = *reinterpret_cast<const uint4 *>(mine + row * (CPR * 16) + ((ch ^ (row & (CPR - 1))) << 4));
-      if (m < g.M && n < g.N) {
-        T *p = (T *)g.out + m * g.ldo + n;
-        if (vec && n + 16 / E <= g.N) {
-          *reinterpret_cast<uint4 *>(p) = v;
-        } else {
-          const T *x = reinterpret_cast<const T *>(&v);
-#pragma unroll
-          for (int c = 0; c < 16 / E; c++)
-            if (n + c < g.N) p[c] = x[c];
-        }
-      }
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  }
+  g8_results<T, FM, FN>(g, acc, s0 + wave * (32 * FN * 32 * (int)sizeof(T)), m0 + wm * FM * 32, n0 + wn * FN * 32, lane);
 }
 
 template <typename T>
