@@ -57,15 +57,26 @@ __device__ inline float to_storage(float v) {
   return ldf(&t, 0);
 }
 
-// q = y / scale to the nearest, ties to even, by a true division: the product
-// with a reciprocal would move values next to a tie.  NaN becomes 0.
+// q = y / scale to the nearest, ties to even.  The quotient is the correctly
+// rounded one (the product with a reciprocal alone would move values next to a
+// tie): with inv the rounded reciprocal, the product's exact remainder times
+// inv corrects it, three operations for a division's dozen.  Scales near the
+// ends of the range, a row's infinity among them, are divided by.  NaN becomes 0.
 template <int V>
 __device__ inline void store_q(int8_t *p, const float *y, float scale) {
   VecOf<int8_t, V> o;
+  const bool plain = scale > 1e-30f && scale < 1e30f;
+  const float inv = plain ? __fdiv_rn(1.f, scale) : 0.f;
 #pragma unroll
   for (int i = 0; i < V; i++) {
-    const float q = scale > 0.f ? rintf(__fdiv_rn(y[i], scale)) : 0.f;
-    o.e[i] = (int8_t)(int)fminf(fmaxf(q, -127.f), 127.f);
+    float q;
+    if (plain) {
+      q = y[i] * inv;
+      q = fmaf(fmaf(-q, scale, y[i]), inv, q);
+    } else {
+      q = scale > 0.f ? __fdiv_rn(y[i], scale) : 0.f;
+    }
+    o.e[i] = (int8_t)(int)fminf(fmaxf(rintf(q), -127.f), 127.f);
   }
   *reinterpret_cast<typename Vec<int8_t, V>::type *>(p) = o.v;
 }

@@ -59,20 +59,28 @@ struct SsmSums {
 };
 
 // out[j] = the sum over p of part[p * stride + j], in 64 bits in a fixed order:
-// 64 columns by 4 slices of the partials per block
+// COLS columns by SL slices of the partials per block, eight loads in flight
+template <int COLS, int SL>
 __device__ inline void part_sum(const float *__restrict__ part, int P, long long stride, long long cols, long long blk,
                                 float *__restrict__ out) {
-  __shared__ double sh[4][64];
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  const long long j = blk * 64 + x;
+  __shared__ double sh[SL][COLS];
+  const int x = threadIdx.x % COLS, y = threadIdx.x / COLS;
+  const long long j = blk * COLS + x;
   double s = 0;
-  if (j < cols) {
-#pragma unroll 4
-    for (int p = y; p < P; p += 4) s += (double)part[p * stride + j];
-  }
+  if (j < cols)
+    for (int p0 = y; p0 < P; p0 += 8 * SL) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; q++) v[q] = p0 + SL * q < P ? part[(p0 + SL * q) * stride + j] : 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; q++) s += (double)v[q];
+    }
   sh[y][x] = s;
-  __syncthreads();
-  if (y == 0 && j < cols) out[j] = (float)((sh[0][x] + sh[1][x]) + (sh[2][x] + sh[3][x]));
+  for (int h = SL / 2; h >= 1; h >>= 1) {
+    __syncthreads();
+    if (y < h) sh[y][x] += sh[y + h][x];
+  }
+  if (y == 0 && j < cols) out[j] = (float)sh[0][x];
 }
 
 // Blocks of three kinds: dB and dC of each (b, t, group, n) over the group's
@@ -82,11 +90,11 @@ __global__ __launch_bounds__(256) void k_ssm_sums(SsmSums a) {
   if (blockIdx.x >= a.bc_blocks) {
     const unsigned i = blockIdx.x - a.bc_blocks;
     if (i < a.a_blocks) {
-      part_sum(a.pA, a.P, (long long)a.D * a.N, (long long)a.D * a.N, i, a.dA);
+      part_sum<32, 8>(a.pA, a.P, (long long)a.D * a.N, (long long)a.D * a.N, i, a.dA);
     } else {
       const unsigned m = (i - a.a_blocks) & 1, blk = (i - a.a_blocks) >> 1;
       float *o = m ? a.dbias : a.dD;
-      if (o) part_sum(a.pD + (long long)m * a.D, a.P, 2LL * a.D, a.D, blk, o);
+      if (o) part_sum<32, 8>(a.pD + (long long)m * a.D, a.P, 2LL * a.D, a.D, blk, o);
     }
     return;
   }
@@ -107,13 +115,14 @@ __global__ __launch_bounds__(256) void k_ssm_sums(SsmSums a) {
   stf((T *)v.p, b * v.sb + t * v.st + (long long)g * a.N + n, s);
 }
 
-__global__ __launch_bounds__(256) void k_part_sum(const float *part, int P, long long stride, long long cols, float *out) {
-  part_sum(part, P, stride, cols, blockIdx.x, out);
+// for many partials of few columns
+__global__ __launch_bounds__(1024) void k_part_sum(const float *part, int P, long long stride, long long cols, float *out) {
+  part_sum<16, 64>(part, P, stride, cols, blockIdx.x, out);
 }
 
 hipError_t launch_part_sum(const float *part, int P, long long stride, long long cols, float *out, hipStream_t s) {
   if (cols < 1) return hipSuccess;
-  k_part_sum<<<dim3((unsigned)((cols + 63) / 64)), 256, 0, s>>>(part, P, stride, cols, out);
+  k_part_sum<<<dim3((unsigned)((cols + 15) / 16)), 1024, 0, s>>>(part, P, stride, cols, out);
   return hipGetLastError();
 }
 
@@ -422,8 +431,8 @@ int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const 
   f.dA = gr->A; f.dD = gr->D; f.dbias = gr->dt_bias;
   f.nblk = a.cbg; f.B = a.B; f.T = a.T; f.G = a.G; f.N = a.N; f.NP = pl.NP; f.P = a.B * a.S; f.D = a.D;
   if (a.dB.p || a.dC.p) f.bc_blocks = (unsigned)(((long long)a.B * a.T * a.G * 2 * pl.NP + 255) / 256);
-  if (gr->A) f.a_blocks = (unsigned)(((long long)a.D * a.N + 63) / 64);
-  const unsigned n = f.bc_blocks + f.a_blocks + (gr->D || gr->dt_bias ? 2 * ((a.D + 63) / 64) : 0);
+  if (gr->A) f.a_blocks = (unsigned)(((long long)a.D * a.N + 31) / 32);
+  const unsigned n = f.bc_blocks + f.a_blocks + (gr->D || gr->dt_bias ? 2 * ((a.D + 31) / 32) : 0);
   if (n == 0) return PR_OK;
   if (p->dtype == PR_BF16) k_ssm_sums<uint16_t><<<dim3(n), 256, 0, s>>>(f);
   else k_ssm_sums<float><<<dim3(n), 256, 0, s>>>(f);
