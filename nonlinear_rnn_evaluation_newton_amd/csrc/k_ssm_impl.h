@@ -14,8 +14,12 @@
 // the WS wavefronts where the output is made.
 //
 // Bound by vector arithmetic: per (step, channel, state) a product, an
-// exponential (two issue slots), a product and two fused multiply-adds, beside
-// about 50 instructions per (step, channel) shared by its states.
+// exponential (two issue slots), a product and two fused multiply-adds; what
+// the states of a (step, channel) share is nearly as much again at 16 states.
+// Measured (bf16, 2048 channels, 16 states): 8 x 4096 steps 376 us, 2.9e12
+// (step, channel, state) a second, 82% of the issue slots of its instructions;
+// with unaligned arrays, element by element, 595 us.  The adjoint of 4 x 2048
+// steps 255 us, with two preparing passes of 35 and 40 us.
 #pragma once
 
 #include <utility>
