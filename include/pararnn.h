@@ -407,7 +407,8 @@ int pararnn_ssm_step(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_
  *   s = x + r, rounded to storage (the stream that goes on is what is normed)
  *   y = s / sqrt(mean(s^2) + eps) * w
  * in the storage dtype (y) or in 8 bits (q, scale): scale = max|y| / 127,
- * q = y / scale to the nearest, ties to even; a row of zeros has scale 0.
+ * q = y / scale to the nearest, ties to even; a row of zeros has scale 0, and
+ * one with an infinity or a NaN has that as its scale and q = 0.
  * Exactly one of y and q is given.  x, r, s, y, q: [rows, n] with row strides
  * (in elements); r NULL: s = x; s (sum_out) NULL: not written.  w: [n] in the
  * storage dtype or NULL (= 1); q int8, scale [rows] fp32.

@@ -65,7 +65,8 @@ __device__ inline float to_storage(float v) {
 // rounded one (the product with a reciprocal alone would move values next to a
 // tie): with inv the rounded reciprocal, the product's exact remainder times
 // inv corrects it, three operations for a division's dozen.  Scales near the
-// ends of the range, a row's infinity among them, are divided by.  NaN becomes 0.
+// ends of the range are divided by.  A row with an infinity or a NaN is all 0:
+// its scale carries that on.
 template <int V>
 __device__ inline void store_q(int8_t *p, const float *y, float scale) {
   VecOf<int8_t, V> o;
@@ -78,7 +79,7 @@ __device__ inline void store_q(int8_t *p, const float *y, float scale) {
       q = y[i] * inv;
       q = fmaf(fmaf(-q, scale, y[i]), inv, q);
     } else {
-      q = scale > 0.f ? __fdiv_rn(y[i], scale) : 0.f;
+      q = scale > 0.f && scale < __builtin_inff() ? __fdiv_rn(y[i], scale) : 0.f;
     }
     o.e[i] = (int8_t)(int)fminf(fmaxf(rintf(q), -127.f), 127.f);
   }

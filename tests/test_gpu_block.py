@@ -487,6 +487,30 @@ def test_other_stream_graph_and_repeats():
     assert torch.equal(y0, y1)
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_quant_rows_ends_of_the_range(dtype):
+    """Rows that hold an infinity or a NaN (all 0, the scale says so), rows whose
+    scale is tiny or huge, and values that lie on ties."""
+    n = 96
+    x = torch.zeros(7, n)
+    x[0], x[0, 5] = 1.0, float("inf")
+    x[1], x[1, 90] = 2.0, float("nan")
+    x[2], x[2, 3] = -1.0, float("-inf")
+    x[3] = torch.arange(n) * 2.0 ** -126  # scales below the smallest normal number's reach
+    x[4] = torch.arange(n) * 2.0 ** 120
+    x[5], x[5, 0] = torch.arange(n) - 40.5, 127.0  # scale 1: every value a tie
+    x = x.to(dtype)
+    q, scale = torch.full((7, n), 99, dtype=torch.int8).cuda(), nan(7)
+    bd.quant_rows(x.cuda(), q, scale)
+    q, scale = q.cpu(), scale.cpu()
+    assert torch.isinf(scale[[0, 2]]).all() and torch.isnan(scale[1]) and scale[6] == 0
+    assert (q[[0, 1, 2, 6]] == 0).all()
+    for r in (3, 4, 5):
+        want = torch.round(x[r].float() / scale[r])
+        assert torch.equal(q[r].float(), want), r
+        assert float(scale[r]) == float(x[r].float().abs().max() * torch.tensor(1 / 127)), r
+
+
 def test_example_block():
     """The example's block: its loss falls, and single tokens continue a prompt
     as the whole sequence does, up to the 8-bit rounding of products whose
