@@ -12,6 +12,7 @@
 // us (20 us by tiles); 8192 cubed 446 us, 2.5 POP/s; 16384 x 8192 x 2048 348 us
 // (the library's product to 32-bit integers 333 to 350 us), 360 with 128 tiles,
 // 409 staged through registers.
+#include "direct_rows.h"
 #include "pararnn.h"
 #include "ssm.h"
 
@@ -287,10 +288,10 @@ __global__ __launch_bounds__(256) void k_gemm8_tile(Gemm8Args g) {
 // stores; the layout above is made by which chunk each lane fetches.  Two
 // stages of one 128-byte K step, an array each, so that the compiler can tell
 // the stage being filled from the one being read.  Loads past M, N or the
-// split's K write zeros.  WM x WN wavefronts of 32 FM x 32 FN.
+// split's K write zeros: their vector offset lies outside the resource.
+// WM x WN wavefronts of 32 FM x 32 FN.
 typedef __amdgpu_buffer_rsrc_t G8Rsrc;
 typedef __attribute__((address_space(3))) void g8_lds_t;
-constexpr unsigned G8_OOB = 0x80000000u;
 
 // this wavefront's loads have landed and its reads are done, then all meet
 __device__ inline void g8_sync() {
@@ -303,7 +304,7 @@ __device__ inline void g8_sync() {
 template <typename T, int WM, int WN, int FM, int FN>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_gemm8_direct(Gemm8Args g) {
   constexpr int BM = WM * FM * 32, BN = WN * FN * 32, NW = WM * WN, QA = BM / 8 / NW, QB = BN / 8 / NW;
-  static_assert(QA % 2 == 0 && QB % 2 == 0, "even numbers of loads");
+  static_assert(QA % 2 == 0 && QB % 2 == 0 && QA <= 4 && QB <= 4, "even numbers of loads, at most four");
   static_assert(NW * 32 * FN * 32 * (int)sizeof(T) <= (BM + BN) * TB, "the results fit a stage");
   __shared__ __attribute__((aligned(1024))) int8_t s0[(BM + BN) * TB], s1[(BM + BN) * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -320,27 +321,22 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_gemm8_direct(Gemm8Args g) {
                                                       (int)(min(BM, g.M - m0) * g.lda), 0x00020000);
   const G8Rsrc rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(g.w + n0 * g.ldw), 0,
                                                       (int)(min(BN, g.N - n0) * g.ldw), 0x00020000);
-  // load u covers rows 8 u + lane / 8; its chunk swizzle r / 2 % 8 = 4 (u % 2) + lane / 16
-  const int rl = lane >> 3, ce = ((lane & 7) ^ (lane >> 4)) * 16, co = ((lane & 7) ^ (4 | (lane >> 4))) * 16;
-  const unsigned lda = (unsigned)g.lda, ldw = (unsigned)g.ldw;
-  const unsigned ae = rl * lda + ce, ao = rl * lda + co, be = rl * ldw + ce, bo = rl * ldw + co;
-  // the last 16 bytes of the last row lie inside the resource only with a row
-  // stride of K; rows are cut by the resource, K by the offset
+  // (a load's chunk takes two values per lane: its number is even or odd)
+  const int ce = direct_chunk(0, lane), co = direct_chunk(1, lane);
+  unsigned ao[4], bo[4];
+#pragma unroll
+  for (int q = 0; q < QA; q++) ao[q] = direct_offset(wave * QA + q, lane, g.M - m0, (unsigned)g.lda);
+#pragma unroll
+  for (int q = 0; q < QB; q++) bo[q] = direct_offset(wave * QB + q, lane, g.N - n0, (unsigned)g.ldw);
   auto dload = [&](int8_t *d, int k0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < QA; q++) {
-      const int u = wave * QA + q;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (g8_lds_t *)&d[u * 1024], 16,
-                                               k0 + ((q & 1) ? co : ce) < ke ? ((q & 1) ? ao : ae) : G8_OOB,
-                                               u * 8 * lda + k0, 0, 0);
-    }
+    for (int q = 0; q < QA; q++)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (g8_lds_t *)&d[(wave * QA + q) * 1024], 16,
+                                               k0 + ((q & 1) ? co : ce) < ke ? ao[q] : DIRECT_OOB, k0, 0, 0);
 #pragma unroll
-    for (int q = 0; q < QB; q++) {
-      const int u = wave * QB + q;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (g8_lds_t *)&d[BM * TB + u * 1024], 16,
-                                               k0 + ((q & 1) ? co : ce) < ke ? ((q & 1) ? bo : be) : G8_OOB,
-                                               u * 8 * ldw + k0, 0, 0);
-    }
+    for (int q = 0; q < QB; q++)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (g8_lds_t *)&d[BM * TB + (wave * QB + q) * 1024], 16,
+                                               k0 + ((q & 1) ? co : ce) < ke ? bo[q] : DIRECT_OOB, k0, 0, 0);
   };
   i32x16 acc[FN][FM];
 #pragma unroll
