@@ -9,6 +9,7 @@
 // K-contiguous so every lane reads its MFMA operand with one vector load.
 // Long-K products (dW_x) split K over blocks into an fp32 workspace that a
 // second kernel sums in a fixed order.
+#include "direct_rows.h"
 #include "internal.h"
 
 namespace pr {
@@ -548,25 +549,24 @@ __global__ __launch_bounds__(DGT, 1) void k_gemm_bf16_dl(const GemmArgs g, int t
   const uint16_t *B = (const uint16_t *)g.B + (size_t)n0 * g.ldb;
   const GRsrc ra = g_rsrc(A, (unsigned)(min(BT, g.M - m0) * g.lda * 2));
   const GRsrc rb = g_rsrc(B, (unsigned)(min(BT, g.N - n0) * g.ldb * 2));
-  // instruction q of wavefront w fills slots 64 (DQ w + q) + lane: row
-  // r = 8 (DQ w + q) + lane / 8, physical slot lane % 8, so the chunk swizzle
-  // (r >> 1) & 7 = 4 (q & 1) + lane / 16 (DQ is even) takes two values per
-  // lane; the row's wavefront-uniform part goes in the scalar offset
-  static_assert(DQ % 2 == 0, "even number of direct loads");
-  const int rl = lane >> 3, kce = ((lane & 7) ^ (lane >> 4)) * 8, kco = ((lane & 7) ^ (4 | (lane >> 4))) * 8;
-  const unsigned va_e = (unsigned)(rl * g.lda + kce) * 2u, va_o = (unsigned)(rl * g.lda + kco) * 2u;
-  const unsigned vb_e = (unsigned)(rl * g.ldb + kce) * 2u, vb_o = (unsigned)(rl * g.ldb + kco) * 2u;
+  // instruction q of wavefront w is load DQ w + q of the tile; its chunk
+  // swizzle takes two values per lane (DQ is even)
+  static_assert(DQ % 2 == 0 && DQ <= 4, "even number of direct loads, at most four");
+  const int kce = direct_chunk(0, lane) / 2, kco = direct_chunk(1, lane) / 2;
+  unsigned va[4], vb[4];
+#pragma unroll
+  for (int q = 0; q < DQ; q++) {
+    va[q] = direct_offset(wid * DQ + q, lane, g.M - m0, (unsigned)g.lda * 2u);
+    vb[q] = direct_offset(wid * DQ + q, lane, g.N - n0, (unsigned)g.ldb * 2u);
+  }
   auto dload = [&](uint16_t *d, int k0) {
 #pragma unroll
     for (int q = 0; q < DQ; q++) {
-      const int kc = (q & 1) ? kco : kce;
-      const bool in = k0 + kc < ke;
+      const bool in = k0 + ((q & 1) ? kco : kce) < ke;
       const int u = wid * DQ + q;
-      const unsigned sa = (unsigned)(u * 8 * g.lda + k0) * 2u, sb = (unsigned)(u * 8 * g.ldb + k0) * 2u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t *)&d[u * 512], 16,
-                                               in ? ((q & 1) ? va_o : va_e) : 0x80000000u, sa, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t *)&d[BT * BK + u * 512], 16,
-                                               in ? ((q & 1) ? vb_o : vb_e) : 0x80000000u, sb, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t *)&d[u * 512], 16, in ? va[q] : DIRECT_OOB, k0 * 2, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t *)&d[BT * BK + u * 512], 16, in ? vb[q] : DIRECT_OOB,
+                                               k0 * 2, 0, 0);
     }
   };
 

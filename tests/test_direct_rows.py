@@ -66,7 +66,7 @@ def test_direct_loads_stay_in_their_rows(tmp_path):
     assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout
 
 
-@pytest.mark.parametrize("kernel", ["k_gemm_i8.hip"])
+@pytest.mark.parametrize("kernel", ["k_gemm.hip", "k_gemm_i8.hip"])
 def test_kernels_take_their_offsets_from_it(kernel):
     text = open(os.path.join(CSRC, kernel)).read()
     loads = text.count("__builtin_amdgcn_raw_ptr_buffer_load_lds(")
