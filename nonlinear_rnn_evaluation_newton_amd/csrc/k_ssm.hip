@@ -11,8 +11,13 @@ namespace pr {
 // joining the pieces
 // ---------------------------------------------------------------------------
 // agg[b][s] (end state of piece s from zero) becomes the state that enters
-// piece s; a piece's decay is exp(A sum of delta).  REV: the same from the
+// piece s; a piece's factor is exp(A sum of delta).  REV: the same from the
 // last piece back, for the adjoint's carry.  One thread per (b, d, n).
+// The factor is applied as its root, twice: over a whole piece it may pass the
+// range of fp32, for states that grow (A > 0), where the state that it meets is
+// small enough for the step by step product to stay inside.  The root is held
+// to finite values, so that a state of 0 stays 0, as it does step by step, and
+// any other overflows (a NaN of the sum comes through the end state).
 template <bool REV>
 __global__ void k_ssm_join(const float *__restrict__ A, const float *__restrict__ first,
                            const float *__restrict__ sumd, float *__restrict__ agg, int B, int D, int N, int S) {
@@ -20,7 +25,7 @@ __global__ void k_ssm_join(const float *__restrict__ A, const float *__restrict_
   if (i >= B * dn) return;
   const long long b = i / dn, e = i % dn;
   const int d = (int)(e / N);
-  const float A2 = A[e] * 1.4426950408889634f;
+  const float Ah = A[e] * (0.5f * 1.4426950408889634f);
   float carry = first ? first[i] : 0.f;
   const float *sd = sumd + b * S * D + d;
   float *ag = agg + b * S * dn + e;
@@ -40,7 +45,8 @@ __global__ void k_ssm_join(const float *__restrict__ A, const float *__restrict_
       const int s = REV ? S - 1 - s0 - q : s0 + q;
       if (s0 + q < S) {
         ag[s * dn] = carry;
-        carry = fmaf(__builtin_amdgcn_exp2f(m[q] * A2), carry, v[q]);
+        const float f = fminf(__builtin_amdgcn_exp2f(m[q] * Ah), 3.402823466e38f);
+        carry = fmaf(f, f * carry, v[q]);
       }
     }
   }

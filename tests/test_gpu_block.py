@@ -297,6 +297,50 @@ def test_scan_split_over_time(dtype, B, T, ch, N):
         near(v, r[k], 4 * (SUM_TOL if k in ("dA", "dD", "ddt_bias", "dh0") else TOL), k)
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("case", ["silent start and end", "up and down"])
+def test_scan_split_growing_states(dtype, case):
+    """States that grow (A > 0), with time split into segments of 64 steps over
+    each of which exp(A sum of delta) = e^96 is beyond fp32, while the states and
+    their adjoints stay inside step by step: inputs only in the last 40 steps and
+    outputs' gradients only in the first 40, or step sizes that change their
+    sign.  Relative errors: a step's decay is off by at most 4e-7 (its argument's
+    two roundings and the exponential's), 448 steps of a state that keeps its
+    past by 1.8e-4, under 4 TOL."""
+    g = gen(21)
+    B, T, ch, N = 1, 448, 12, 4
+    p = scan_problem(g, dtype, B, T, ch, N, 1, False, False)
+    p["A"] = torch.full((ch, N), 2.0)
+    p["A"][::2, 1] = -0.5
+    p["D"] = None
+    dy, h0, dh = rnd(g, B, T, ch, dtype=dtype), None, None
+    if case == "up and down":
+        sign = 1.0 - 2.0 * (torch.arange(T) // 64 % 2)
+        p["dt"] = (0.75 * sign)[None, :, None].expand(B, T, ch).contiguous().to(dtype)
+        p["u"] = torch.zeros_like(p["u"])
+        dy[:, :] = 0
+        h0, dh = rnd(g, B, ch, N) * 1e-25, rnd(g, B, ch, N) * 1e-25
+    else:
+        p["dt"] = torch.full((B, T, ch), 0.75, dtype=dtype)
+        p["u"][:, :T - 40] = 0
+        dy[:, 40:] = 0
+    dev = {k: None if v is None else v.cuda() for k, v in p.items()}
+    ws = torch.empty(bd.ssm_workspace_bytes(dtype, B, T, ch, N), dtype=torch.uint8, device="cuda").fill_(255)
+    y, hl, states = nan(B, T, ch, dtype=dtype), nan(B, ch, N), nan(*bd.ssm_states_shape(B, T, ch, N))
+    main = (dev["u"], dev["dt"], dev["A"], dev["Bm"], dev["Cm"])
+    bd.ssm_scan(*main, y, ws, h0=None if h0 is None else h0.cuda(), h_last=hl, states=states, softplus=False)
+    ry, rh, hs = R.scan(**p, h0=h0, sp=False, keep=True)
+    near(y, ry, 4 * TOL, "y")
+    near(hl, rh, 4 * TOL, "h")
+    near(states, torch.stack(hs[:-1][::16], 1), 4 * TOL, "states")
+    o = dict(du=nan(B, T, ch, dtype=dtype), ddt=nan(B, T, ch, dtype=dtype), dB=nan(B, T, N, dtype=dtype),
+             dC=nan(B, T, N, dtype=dtype), dA=nan(ch, N), dh0=nan(B, ch, N))
+    bd.ssm_scan_adjoint(*main, states, dy.cuda(), ws, dh_last=None if dh is None else dh.cuda(), softplus=False, **o)
+    r = R.scan_grads(**p, dy=dy, h0=h0, dh_last=dh, sp=False)
+    for k, v in o.items():
+        near(v, r[k], 4 * (SUM_TOL if k in ("dA", "dh0") else TOL), k)
+
+
 def test_scan_extreme_steps():
     """Step sizes from 1e-9 to 60: decays of 1 and of 0, softplus at both ends."""
     g = gen(5)
