@@ -392,7 +392,12 @@ def _done(st, where, check=True):
     return st
 
 
-def _ws(workspace):
+def _ws(where, workspace):
+    """Address and bytes of the workspace, into which kernels write."""
+    if not workspace.is_contiguous():
+        raise ValueError(f"{where}: the workspace must be contiguous, got strides {workspace.stride()}")
+    if not workspace.is_cuda:
+        raise ValueError(f"{where}: the workspace must be on the GPU")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -426,7 +431,7 @@ def conv_adjoint(x, w, bias, dy, dx, dw, dbias, workspace, state_in=None, dstate
         _dense(n, "lengths", lengths, (B,), torch.int32), C.byref(_view(n, "dy", dy, (B, T, D), dt)),
         _dense(n, "dstate_out", dstate_out, (B, W - 1, D), dt), C.byref(_view(n, "dx", dx, (B, T, D), dt)),
         _dense(n, "dw", dw, (D, W), f32), _dense(n, "dbias", dbias, (D,), f32),
-        _dense(n, "dstate_in", dstate_in, (B, W - 1, D), dt), *_ws(workspace), _stream_of(x))
+        _dense(n, "dstate_in", dstate_in, (B, W - 1, D), dt), *_ws(n, workspace), _stream_of(x))
     return _done(st, "pararnn_conv_adjoint", check)
 
 
@@ -479,7 +484,7 @@ def ssm_scan(u, dt, A, Bm, Cm, y, workspace, D=None, z=None, dt_bias=None, h0=No
     st = lib().pararnn_ssm_scan(
         C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, u.shape, u.dtype)),
         _dense(n, "h_last", h_last, (pb.B, pb.D, pb.N), torch.float32),
-        _dense(n, "states", states, ssm_states_shape(pb.B, pb.T, pb.D, pb.N), torch.float32), *_ws(workspace),
+        _dense(n, "states", states, ssm_states_shape(pb.B, pb.T, pb.D, pb.N), torch.float32), *_ws(n, workspace),
         _stream_of(u))
     return _done(st, "pararnn_ssm_scan", check)
 
@@ -499,7 +504,7 @@ def ssm_scan_adjoint(u, dt, A, Bm, Cm, states, dy, workspace, D=None, z=None, dt
     st = lib().pararnn_ssm_adjoint(
         C.byref(pb), C.byref(inp), _dense(n, "states", states, ssm_states_shape(pb.B, pb.T, pb.D, pb.N), f32),
         C.byref(_view(n, "dy", dy, shape, t)), _dense(n, "dh_last", dh_last, (pb.B, pb.D, pb.N), f32), C.byref(gr),
-        *_ws(workspace), _stream_of(u))
+        *_ws(n, workspace), _stream_of(u))
     return _done(st, "pararnn_ssm_adjoint", check)
 
 
@@ -542,7 +547,7 @@ def rmsnorm_adjoint(s, w, dy, dx, dw, workspace, dsum=None, eps: float = 1e-5, c
     st = lib().pararnn_rmsnorm_adjoint(
         C.byref(pb), _rows(where, "s", s, (rows, n), dt), _dense(where, "w", w, (n,), dt),
         _rows(where, "dy", dy, (rows, n), dt), _rows(where, "dsum", dsum, (rows, n), dt),
-        _rows(where, "dx", dx, (rows, n), dt), _dense(where, "dw", dw, (n,), torch.float32), *_ws(workspace), _stream_of(s))
+        _rows(where, "dx", dx, (rows, n), dt), _dense(where, "dw", dw, (n,), torch.float32), *_ws(where, workspace), _stream_of(s))
     return _done(st, "pararnn_rmsnorm_adjoint", check)
 
 
@@ -569,7 +574,7 @@ def gemm_i8(a, a_scale, w, w_scale, out, workspace, bias=None, check: bool = Tru
         _dtype_code(dt, n), M, N, K, _need(n, "a", a, (M, K), torch.int8), a.stride(0),
         _dense(n, "a_scale", a_scale, (M,), f32), _need(n, "w", w, (N, K), torch.int8), w.stride(0),
         _dense(n, "w_scale", w_scale, (N,), f32), _dense(n, "bias", bias, (N,), dt),
-        _need(n, "out", out, (M, N), dt), out.stride(0), *_ws(workspace), _stream_of(a))
+        _need(n, "out", out, (M, N), dt), out.stride(0), *_ws(n, workspace), _stream_of(a))
     return _done(st, "pararnn_gemm_i8", check)
 
 

@@ -174,3 +174,14 @@ def test_binding_refuses_what_the_library_cannot_see():
         bd._need("f", "w", torch.zeros(3, 7), (3, 8), torch.float32)
     with pytest.raises(ValueError, match="contiguous"):
         bd._strides("f", "w", torch.zeros(8, 3).t(), (3, 8), 1)
+
+
+def test_workspace_is_checked_in_python():
+    """Kernels write through the workspace's address: one in host memory, or
+    one whose bytes are not all its own, is refused."""
+    with pytest.raises(ValueError, match="ssm_scan: the workspace must be on the GPU"):
+        bd._ws("ssm_scan", torch.empty(1 << 10, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="contiguous"):
+        bd._ws("ssm_scan", torch.empty(1, dtype=torch.uint8).expand(1 << 20))
+    with pytest.raises(ValueError, match="contiguous"):
+        bd._ws("ssm_scan", torch.empty(64, 64, dtype=torch.uint8)[:, ::2])

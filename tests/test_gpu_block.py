@@ -571,3 +571,19 @@ def test_example_block():
     assert losses[-1] < 0.95 * losses[0], losses
     got, whole = ex.serve(block)
     assert float((got.float() - whole.float()).abs().max()) <= 0.02 * float(whole.float().abs().max())
+
+
+def test_host_workspace_is_refused():
+    """Every call that takes a workspace refuses one in host memory before it launches anything."""
+    z = lambda *s, dtype=F: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    host = torch.empty(1 << 20, dtype=torch.uint8)
+    x, w, A, bc, a8 = z(2, 32, 16), z(16, 4), z(16, 8), z(2, 32, 8), z(80, 16, dtype=torch.int8)
+    states, rows = z(*bd.ssm_states_shape(2, 32, 16, 8)), z(64, 16)
+    for name, call in (
+            ("conv_adjoint", lambda: bd.conv_adjoint(x, w, None, x, None, w, None, host)),
+            ("ssm_scan", lambda: bd.ssm_scan(x, x, A, bc, bc, z(2, 32, 16), host)),
+            ("ssm_scan_adjoint", lambda: bd.ssm_scan_adjoint(x, x, A, bc, bc, states, x, host, du=z(2, 32, 16))),
+            ("rmsnorm_adjoint", lambda: bd.rmsnorm_adjoint(rows, None, rows, None, z(16), host)),
+            ("gemm_i8", lambda: bd.gemm_i8(a8, z(80), a8, z(80), z(80, 80), host))):
+        with pytest.raises(ValueError, match=name + ": the workspace must be on the GPU"):
+            call()
