@@ -458,11 +458,13 @@ def ssm_states_shape(B: int, T: int, D: int, N: int):
     return B, -(-T // SSM_STATE_STEPS), D, N
 
 
-def _ssm(where, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, softplus):
+def _ssm(where, axes, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, softplus):
     import torch
     st, f32 = u.dtype, torch.float32
     shape, (ch, N) = u.shape, A.shape
-    B, T = shape[0], shape[1] if len(shape) == 3 else 1
+    if len(shape) != axes:
+        raise ValueError(f"{where}: u must be [B, {'T, ' if axes == 3 else ''}channels], got {tuple(shape)}")
+    B, T = shape[0], shape[1] if axes == 3 else 1
     width = Bm.shape[-1]
     if width % N or not width:
         raise ValueError(f"{where}: B has {width} columns, not a multiple of the {N} states of A")
@@ -480,7 +482,7 @@ def ssm_scan(u, dt, A, Bm, Cm, y, workspace, D=None, z=None, dt_bias=None, h0=No
     """pararnn_ssm_scan: the selective scan of u [B, T, channels] into y."""
     import torch
     n = "ssm_scan"
-    pb, inp = _ssm(n, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, softplus)
+    pb, inp = _ssm(n, 3, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, softplus)
     st = lib().pararnn_ssm_scan(
         C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, u.shape, u.dtype)),
         _dense(n, "h_last", h_last, (pb.B, pb.D, pb.N), torch.float32),
@@ -495,7 +497,7 @@ def ssm_scan_adjoint(u, dt, A, Bm, Cm, states, dy, workspace, D=None, z=None, dt
     """pararnn_ssm_adjoint: gradients of ssm_scan from the states it saved; any output may be None."""
     import torch
     n, f32 = "ssm_scan_adjoint", torch.float32
-    pb, inp = _ssm(n, u, dt, A, Bm, Cm, D, z, dt_bias, None, lengths, softplus)
+    pb, inp = _ssm(n, 3, u, dt, A, Bm, Cm, D, z, dt_bias, None, lengths, softplus)
     shape, bc, t = u.shape, Bm.shape, u.dtype
     gr = SsmGrads(_view(n, "du", du, shape, t), _view(n, "ddt", ddt, shape, t), _view(n, "dz", dz, shape, t),
                   _view(n, "dB", dB, bc, t), _view(n, "dC", dC, bc, t), _dense(n, "dA", dA, (pb.D, pb.N), f32),
@@ -513,7 +515,7 @@ def ssm_step(u, dt, A, Bm, Cm, state, y, D=None, z=None, dt_bias=None, slots=Non
     """pararnn_ssm_step: one token u [B, channels] per sequence on the fp32 pool state [slots, channels, N]."""
     import torch
     n = "ssm_step"
-    pb, inp = _ssm(n, u, dt, A, Bm, Cm, D, z, dt_bias, None, None, softplus)
+    pb, inp = _ssm(n, 2, u, dt, A, Bm, Cm, D, z, dt_bias, None, None, softplus)
     pool = state.shape[0]
     st = lib().pararnn_ssm_step(C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, u.shape, u.dtype)),
                                 _dense(n, "state", state, (pool, pb.D, pb.N), torch.float32), pool,

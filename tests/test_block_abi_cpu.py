@@ -185,3 +185,16 @@ def test_workspace_is_checked_in_python():
         bd._ws("ssm_scan", torch.empty(1, dtype=torch.uint8).expand(1 << 20))
     with pytest.raises(ValueError, match="contiguous"):
         bd._ws("ssm_scan", torch.empty(64, 64, dtype=torch.uint8)[:, ::2])
+
+
+def test_scan_takes_sequences_and_its_step_takes_tokens():
+    """Sequences given to the step would have had their first token computed and
+    the rest of y left as it was; a batch of tokens given to the scan is not one sequence."""
+    A, seq, tok, ws = torch.zeros(16, 8), torch.zeros(2, 5, 16), torch.zeros(2, 16), torch.empty(1 << 10, dtype=torch.uint8)
+    bc, bt = torch.zeros(2, 5, 8), torch.zeros(2, 8)
+    with pytest.raises(ValueError, match=r"ssm_step: u must be \[B, channels\]"):
+        bd.ssm_step(seq, seq, A, bc, bc, torch.zeros(2, 16, 8), seq)
+    with pytest.raises(ValueError, match=r"ssm_scan: u must be \[B, T, channels\]"):
+        bd.ssm_scan(tok, tok, A, bt, bt, tok, ws)
+    with pytest.raises(ValueError, match=r"ssm_scan_adjoint: u must be \[B, T, channels\]"):
+        bd.ssm_scan_adjoint(tok, tok, A, bt, bt, torch.zeros(2, 1, 16, 8), tok, ws)
