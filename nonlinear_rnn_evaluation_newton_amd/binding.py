@@ -97,8 +97,9 @@ _lib = None
 
 def lib():
     """Load libpararnn.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _several_gpus
     if _lib is None:
+        import torch
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: run __graft_entry__.build() first")
         L = C.CDLL(LIB_PATH)
@@ -153,6 +154,7 @@ def lib():
                 ("gemm_i8", I, [I, I, I, I, P, LL, P, P, LL, P, P, P, LL, P, S, P])):
             f = getattr(L, "pararnn_" + name)
             f.restype, f.argtypes = res, args
+        _several_gpus = torch.cuda.device_count() > 1
         _lib = L
     return _lib
 
@@ -336,6 +338,16 @@ def _strides(where, name, t, shape, adjacent):
         step *= shape[-k]
 
 
+_several_gpus = False  # set where the library is loaded
+
+
+def _same_device(where, name, t):
+    """Kernels are launched on the current device, for its memory and its stream."""
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{where}: {name} is on GPU {t.get_device()}, the current one is {torch.cuda.current_device()}")
+
+
 # These checks run on every call, single tokens' included, so they take the
 # short way through torch's attributes first.
 def _need(where, name, t, shape, dtype):
@@ -346,6 +358,8 @@ def _need(where, name, t, shape, dtype):
                          f"got {t.dtype} {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{where}: {name} must be on the GPU")
+    if _several_gpus:
+        _same_device(where, name, t)
     if t.stride(-1) != 1:
         _strides(where, name, t, shape, 1)
     return t.data_ptr()
@@ -355,7 +369,7 @@ def _dense(where, name, t, shape, dtype):
     """The address of t, all of whose axes must be contiguous; None passes."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or _several_gpus or not t.is_contiguous():
         _need(where, name, t, shape, dtype)
         _strides(where, name, t, shape, len(shape))
     return t.data_ptr()
@@ -375,7 +389,7 @@ def _view(where, name, t, shape, dtype):
 
 
 def _stream_of(t):
-    """The raw handle of the current stream of t's device."""
+    """The raw handle of the current stream of t's device, which is the current one."""
     import torch
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
@@ -398,6 +412,8 @@ def _ws(where, workspace):
         raise ValueError(f"{where}: the workspace must be contiguous, got strides {workspace.stride()}")
     if not workspace.is_cuda:
         raise ValueError(f"{where}: the workspace must be on the GPU")
+    if _several_gpus:
+        _same_device(where, "the workspace", workspace)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -460,6 +476,7 @@ def ssm_states_shape(B: int, T: int, D: int, N: int):
 
 def _ssm(where, axes, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, softplus):
     import torch
+    lib()  # before the tensors' checks, which depend on the GPUs there are
     st, f32 = u.dtype, torch.float32
     shape, (ch, N) = u.shape, A.shape
     if len(shape) != axes:

@@ -198,3 +198,35 @@ def test_scan_takes_sequences_and_its_step_takes_tokens():
         bd.ssm_scan(tok, tok, A, bt, bt, tok, ws)
     with pytest.raises(ValueError, match=r"ssm_scan_adjoint: u must be \[B, T, channels\]"):
         bd.ssm_scan_adjoint(tok, tok, A, bt, bt, torch.zeros(2, 1, 16, 8), tok, ws)
+
+
+class OnGpu:
+    """Stands for a contiguous tensor on GPU `at`, of which the checks only look at this."""
+
+    def __init__(self, t, at):
+        self.t, self.at, self.is_cuda, self.dtype, self.shape = t, at, True, t.dtype, t.shape
+
+    def get_device(self):
+        return self.at
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("what", ["_need", "_dense", "_ws"])
+def test_tensors_of_another_gpu_are_refused(what, monkeypatch):
+    """With several GPUs, a tensor of one that is not current would be reached
+    from the current one, or launched on the wrong stream."""
+    bd.lib()
+    monkeypatch.setattr(bd, "_several_gpus", True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    t = torch.zeros(4, 8)
+
+    def call(at):
+        x = OnGpu(t, at)
+        return bd._ws("f", x) if what == "_ws" else getattr(bd, what)("f", "x", x, (4, 8), torch.float32)
+
+    with pytest.raises(ValueError, match="is on GPU 0, the current one is 1"):
+        call(0)
+    got = call(1)
+    assert got == ((t.data_ptr(), 128) if what == "_ws" else t.data_ptr())
