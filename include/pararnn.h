@@ -438,8 +438,9 @@ int pararnn_quant_rows(const pr_norm_problem *p, const pr_rows *x, const pr_rows
  * Product of 8-bit integers with a scale for each row of a (token) and of w
  * (output channel): out[m][n] = (sum_k a[m][k] w[n][k]) sa[m] sw[n] + bias[n].
  * The sum is exact in 32-bit integers (K < 131072).  a [M, K], w [N, K] int8
- * with row strides; sa [M], sw [N] fp32; out [M, N] and bias [N] (or NULL)
- * in `dtype`.  workspace: 256-byte aligned, pararnn_gemm_i8_workspace_bytes.
+ * with row strides (of at least a row's length; of a single row they are not
+ * looked at); sa [M], sw [N] fp32; out [M, N] and bias [N] (or NULL) in
+ * `dtype`.  workspace: 256-byte aligned, pararnn_gemm_i8_workspace_bytes.
  */
 size_t pararnn_gemm_i8_workspace_bytes(int M, int N, int K);
 int pararnn_gemm_i8(int dtype, int M, int N, int K, const signed char *a, long long lda, const float *sa,

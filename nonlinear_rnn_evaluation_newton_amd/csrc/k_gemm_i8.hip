@@ -490,6 +490,9 @@ int pararnn_gemm_i8(int dtype, int M, int N, int K, const signed char *a, long l
   const int rc = gemm8_check(M, N, K);
   if (rc != PR_OK) return rc;
   if (!a || !sa || !w || !sw || !out) return fail(PR_EINVAL, "a, sa, w, sw and out are required");
+  // one row has no stride: whatever stands for it (1 where it was a column) is not looked at
+  if (M == 1) { lda = (K + 15LL) & ~15LL; ldo = N; }
+  if (N == 1) ldw = (K + 15LL) & ~15LL;
   if (lda < K || ldw < K || ldo < N)
     return fail(PR_EINVAL, "row strides %lld, %lld, %lld are below K = %d, K, N = %d", lda, ldw, ldo, K, N);
   const size_t need = pararnn_gemm_i8_workspace_bytes(M, N, K);

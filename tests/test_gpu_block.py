@@ -587,3 +587,25 @@ def test_host_workspace_is_refused():
             ("gemm_i8", lambda: bd.gemm_i8(a8, z(80), a8, z(80), z(80, 80), host))):
         with pytest.raises(ValueError, match=name + ": the workspace must be on the GPU"):
             call()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 64), (1, 1, 100), (70, 1, 64), (1, 300, 5)])
+def test_product_of_single_rows(dtype, M, N, K):
+    """Operands and outputs of one row that were columns: their row stride is 1, and says nothing."""
+    g = gen(M + N + K)
+
+    def row(t):  # the same values; of one row: a transposed column
+        return t.cuda() if t.shape[0] > 1 else t.t().clone(memory_format=torch.contiguous_format).cuda().t()
+
+    a, w = (torch.randint(-128, 128, s, generator=g).to(torch.int8) for s in ((M, K), (N, K)))
+    sa, sw = torch.rand(M, generator=g) + 0.1, torch.rand(N, generator=g) + 0.1
+    ac, wc, out = row(a), row(w), row(torch.full((M, N), float("nan"), dtype=dtype))
+    assert M > 1 or (ac.stride(0) == 1 and out.stride(0) == 1)
+    assert N > 1 or wc.stride(0) == 1
+    ws = torch.empty(bd.gemm_i8_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
+    bd.gemm_i8(ac, sa.cuda(), wc, sw.cuda(), out, ws)
+    # as in test_product: an exact sum and four roundings
+    ref = (a.double() @ w.double().t()) * (sa.double()[:, None] * sw.double())
+    err = (out.double().cpu() - ref).abs()
+    assert (err <= (4 * 2.0 ** -24 + (2.0 ** -8 if dtype == BF else 2.0 ** -24)) * ref.abs() + 1e-30).all(), err.max()
