@@ -351,8 +351,9 @@ int pararnn_conv_adjoint(const pr_conv_problem *p, const pr_view *x, const void 
                          const void *state_in, const int *lengths, const pr_view *dy, const void *dstate_out,
                          const pr_view *dx, float *dw, float *dbias, void *dstate_in, void *workspace,
                          size_t ws_bytes, void *stream);
-/* One token for each of B sequences (p->T is ignored): x, y [B, D] with row
- * strides sb; state [nslots, W-1, D] is read and shifted in place.          */
+/* One token for each of B sequences (p->T is not used and may be 0): x, y
+ * [B, D] with row strides sb; state [nslots, W-1, D] is read and shifted in
+ * place.                                                                    */
 int pararnn_conv_step(const pr_conv_problem *p, const pr_view *x, const void *w, const void *bias, void *state,
                       int nslots, const int *slots, const pr_view *y, void *stream);
 
@@ -397,8 +398,8 @@ int pararnn_ssm_scan(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_
 int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const float *states, const pr_view *dy,
                         const float *dh_last, const pr_ssm_grads *grads, void *workspace, size_t ws_bytes,
                         void *stream);
-/* One token for each of B sequences (p->T, h0 and lengths are ignored; row
- * strides sb): state [nslots, D, N] fp32 is updated in place.               */
+/* One token for each of B sequences (p->T, h0 and lengths are not used, T may
+ * be 0; row strides sb): state [nslots, D, N] fp32 is updated in place.     */
 int pararnn_ssm_step(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_view *y, float *state, int nslots,
                      const int *slots, void *stream);
 

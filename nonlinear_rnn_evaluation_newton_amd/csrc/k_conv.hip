@@ -349,10 +349,11 @@ namespace {
     if (e_ != hipSuccess) return fail(PR_EHIP, "%s: %s", #expr, hipGetErrorString(e_));     \
   } while (0)
 
-int conv_check(const pr_conv_problem *p) {
+// step: single tokens, T is not used and may be 0
+int conv_check(const pr_conv_problem *p, bool step = false) {
   if (!p) return fail(PR_EINVAL, "problem is NULL");
   if (p->dtype != PR_F32 && p->dtype != PR_BF16) return fail(PR_EINVAL, "unknown dtype %d", p->dtype);
-  if (p->B < 1 || p->T < 1 || p->D < 1 || p->W < 1)
+  if (p->B < 1 || p->T < (step ? 0 : 1) || p->D < 1 || p->W < 1)
     return fail(PR_EINVAL, "sizes must be >= 1 (B=%d T=%d D=%d W=%d)", p->B, p->T, p->D, p->W);
   if (p->W > 4) return fail(PR_EUNSUPPORTED, "W = %d taps: at most 4", p->W);
   if (p->T > (1 << 30)) return fail(PR_EUNSUPPORTED, "T = %d: at most 2^30", p->T);
@@ -441,7 +442,7 @@ int pararnn_conv_adjoint(const pr_conv_problem *p, const pr_view *x, const void 
 int pararnn_conv_step(const pr_conv_problem *p, const pr_view *x, const void *w, const void *bias, void *state,
                       int nslots, const int *slots, const pr_view *y, void *stream) {
   clear_error();
-  int rc = conv_check(p);
+  int rc = conv_check(p, true);
   if (rc != PR_OK) return rc;
   if (!x || !x->p || !w || !y || !y->p || (!state && p->W > 1)) return fail(PR_EINVAL, "x, w, state and y are required");
   if (nslots < 1 || (!slots && nslots < p->B)) return fail(PR_EINVAL, "%d states for %d sequences", nslots, p->B);

@@ -265,15 +265,22 @@ void split_time(long long blocks, int T, long long max_tile_bytes, int *S, int *
   *S = (int)((tiles + per - 1) / per);
 }
 
-int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
+// step: single tokens, T is not used and may be 0
+int ssm_check(const pr_ssm_problem *p, bool step) {
   if (!p) return fail(PR_EINVAL, "problem is NULL");
   if (p->dtype != PR_F32 && p->dtype != PR_BF16) return fail(PR_EINVAL, "unknown dtype %d", p->dtype);
-  if (p->B < 1 || p->T < 1 || p->D < 1 || p->N < 1 || p->G < 1)
+  if (p->B < 1 || p->T < (step ? 0 : 1) || p->D < 1 || p->N < 1 || p->G < 1)
     return fail(PR_EINVAL, "sizes must be >= 1 (B=%d T=%d D=%d N=%d G=%d)", p->B, p->T, p->D, p->N, p->G);
   if (p->D % p->G != 0) return fail(PR_EINVAL, "G = %d does not divide D = %d", p->G, p->D);
   if (p->N > 64) return fail(PR_EUNSUPPORTED, "N = %d states: at most 64", p->N);
   if (p->T > (1 << 30)) return fail(PR_EUNSUPPORTED, "T = %d: at most 2^30", p->T);
   if (p->D > (1 << 22)) return fail(PR_EUNSUPPORTED, "D = %d: at most 2^22", p->D);
+  return PR_OK;
+}
+
+int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
+  const int rc = ssm_check(p, false);
+  if (rc != PR_OK) return rc;
   const SsmGeom g = ssm_geom(p->N);
   const int dpg = p->D / p->G;
   pl->cbg = (dpg + 63) / 64;
@@ -452,14 +459,13 @@ int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const 
 int pararnn_ssm_step(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_view *y, float *state, int nslots,
                      const int *slots, void *stream) {
   clear_error();
-  SsmPlan pl;
-  int rc = ssm_plan(p, &pl);
+  const int rc = ssm_check(p, true);
   if (rc != PR_OK) return rc;
+  if (p->B > 65535) return fail(PR_EUNSUPPORTED, "B = %d: at most 65535", p->B);
   if (!in) return fail(PR_EINVAL, "inputs are NULL");
   if (!in->u.p || !in->dt.p || !in->B.p || !in->C.p || !in->A || !y || !y->p || !state)
     return fail(PR_EINVAL, "u, dt, A, B, C, y and the states are required");
   if (nslots < 1 || (!slots && nslots < p->B)) return fail(PR_EINVAL, "%d states for %d sequences", nslots, p->B);
-  if (p->B > 65535) return fail(PR_EUNSUPPORTED, "B = %d: at most 65535", p->B);
   if (p->N % 4 == 0 && (((uintptr_t)state | (uintptr_t)in->A) & 15))
     return fail(PR_EINVAL, "A and the states must be 16-byte aligned");
   SsmStepArgs a{};

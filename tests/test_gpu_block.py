@@ -609,3 +609,32 @@ def test_product_of_single_rows(dtype, M, N, K):
     ref = (a.double() @ w.double().t()) * (sa.double()[:, None] * sw.double())
     err = (out.double().cpu() - ref).abs()
     assert (err <= (4 * 2.0 ** -24 + (2.0 ** -8 if dtype == BF else 2.0 ** -24)) * ref.abs() + 1e-30).all(), err.max()
+
+
+def test_steps_do_not_use_the_number_of_steps():
+    """The single-token calls take a problem whose T is 0 or one that a whole
+    sequence of that size would be too large for."""
+    import ctypes as C
+    L, g = bd.lib(), gen(4)
+    B, ch, N, W = 3, 24, 16, 4
+    dev = {k: v.cuda() for k, v in scan_problem(g, F, B, 1, ch, N, 1, True).items()}
+    w, b, x = rnd(g, ch, W).cuda(), rnd(g, ch).cuda(), rnd(g, B, ch).cuda()
+    taps0, h0 = rnd(g, B, W - 1, ch).cuda(), rnd(g, B, ch, N).cuda()
+
+    def run(T):
+        taps, h, yc, ys = taps0.clone(), h0.clone(), nan(B, ch), nan(B, ch)
+        view = lambda t: bd.View(t.data_ptr(), t.stride(0), 0)  # noqa: E731
+        st = C.c_void_p(torch.cuda.current_stream().cuda_stream)
+        assert L.pararnn_conv_step(C.byref(bd.ConvProblem(bd.PR_F32, B, T, ch, W, 1)), C.byref(view(x)), bd._p(w),
+                                   bd._p(b), bd._p(taps), B, None, C.byref(view(yc)), st) == bd.PR_OK, T
+        inp = bd.SsmInputs(*(view(dev[k][:, 0]) for k in ("u", "dt", "z", "Bm", "Cm")), dev["A"].data_ptr(),
+                           dev["D"].data_ptr(), dev["dt_bias"].data_ptr(), None, None)
+        assert L.pararnn_ssm_step(C.byref(bd.SsmProblem(bd.PR_F32, B, T, ch, N, 1, 1)), C.byref(inp),
+                                  C.byref(view(ys)), bd._p(h), B, None, st) == bd.PR_OK, T
+        return taps, h, yc, ys
+
+    want = run(1)
+    assert all(torch.isfinite(v).all() for v in want)
+    for T in (0, 1 << 30):
+        for got, ref in zip(run(T), want):
+            assert torch.equal(got, ref), T
