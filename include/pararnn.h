@@ -358,7 +358,8 @@ int pararnn_conv_step(const pr_conv_problem *p, const pr_view *x, const void *w,
                       int nslots, const int *slots, const pr_view *y, void *stream);
 
 /*
- * Selective state space scan, per channel d and state n:
+ * Selective state space scan, per channel d and state n (time strides up to
+ * 2^31 / 144 bytes, any over the batch):
  *   delta_t = softplus(dt_t + dt_bias) (or the sum itself)
  *   h_t[d][n] = exp(delta_t[d] A[d][n]) h_{t-1}[d][n] + delta_t[d] u_t[d] B_t[g][n]
  *   y_t[d] = (sum_n C_t[g][n] h_t[d][n] + D[d] u_t[d]) silu(z_t[d])

@@ -300,7 +300,7 @@ int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
   if ((double)p->B * sm * dn * 4 > 1e13 || (double)p->B * p->T * p->G * pl->cbg * pl->NP * 8 > 1e13)
     return fail(PR_EUNSUPPORTED, "problem too large");
   size_t o = 0;
-  pl->off_agg = o; o = align256(o + (sm > 1 ? p->B * sm * dn * 4 : 0));
+  pl->off_agg = o; o = align256(o + p->B * sm * dn * 4);  // (one state: what goes from window to window)
   pl->off_sumd = o; o = align256(o + (sm > 1 ? p->B * sm * p->D * 4 : 0));
   pl->fwd_bytes = o > 256 ? o : 256;
   pl->off_part = o; o = align256(o + (size_t)pl->cbg * p->B * p->T * p->G * 2 * pl->NP * 4);
@@ -311,9 +311,9 @@ int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
   return PR_OK;
 }
 
-View view(const pr_view *v) {
+View view(const pr_view *v, int T) {
   View r{nullptr, 0, 0};
-  if (v && v->p) r = View{v->p, v->sb, v->st};  // an absent array has no strides
+  if (v && v->p) r = View{v->p, v->sb, T > 1 ? v->st : 0};  // an absent array has no strides, one step none over time
   return r;
 }
 
@@ -322,17 +322,24 @@ bool vec4_ok(const View &v, int esz) {
   return v.p == nullptr || (((uintptr_t)v.p % (4 * esz)) == 0 && v.sb % 4 == 0 && v.st % 4 == 0);
 }
 
-// a segment's offsets in an array are 31-bit, with the tiles fetched ahead
-int stride_ok(const View &v, const SsmPlan &pl, int esz) {
-  if (v.p && (v.st < 0 || (double)(pl.seglen + 8 * SSM_TL) * v.st * esz > 2147483000.0))
-    return fail(PR_EUNSUPPORTED, "time stride %lld over segments of %d steps passes 31 bits", v.st, pl.seglen);
+// A segment's offsets in an array are 31-bit, with the tiles fetched ahead.
+// Where time strides are too long for the plan's segments, *steps becomes what
+// they allow, and time goes in windows of that many, one launch after another.
+int stride_steps(const View &v, int esz, int *steps) {
+  if (!v.p || v.st == 0) return PR_OK;
+  if (v.st < 0) return fail(PR_EUNSUPPORTED, "time stride %lld is negative", v.st);
+  const long long most = v.st > 2147483000LL / (9 * SSM_TL * esz) ? 0 : 2147483000LL / (v.st * esz) - 8 * SSM_TL;
+  if (most < SSM_TL)
+    return fail(PR_EUNSUPPORTED, "time stride %lld: at most %lld elements", v.st, 2147483000LL / (9 * SSM_TL * esz));
+  if (most < *steps) *steps = (int)(most / SSM_TL * SSM_TL);
   return PR_OK;
 }
 
-int ssm_fill(const pr_ssm_problem *p, const SsmPlan &pl, const pr_ssm_inputs *in, SsmArgs *a) {
+int ssm_fill(const pr_ssm_problem *p, const SsmPlan &pl, const pr_ssm_inputs *in, SsmArgs *a, int *steps) {
   if (!in) return fail(PR_EINVAL, "inputs are NULL");
   if (!in->u.p || !in->dt.p || !in->B.p || !in->C.p || !in->A) return fail(PR_EINVAL, "u, dt, A, B and C are required");
-  a->u = view(&in->u); a->dt = view(&in->dt); a->z = view(&in->z); a->Bm = view(&in->B); a->Cm = view(&in->C);
+  a->u = view(&in->u, p->T); a->dt = view(&in->dt, p->T); a->z = view(&in->z, p->T);
+  a->Bm = view(&in->B, p->T); a->Cm = view(&in->C, p->T);
   a->A = in->A; a->Dk = in->D; a->bias = in->dt_bias; a->h0 = in->h0; a->lengths = in->lengths;
   a->B = p->B; a->T = p->T; a->D = p->D; a->N = p->N; a->G = p->G; a->softplus = p->softplus != 0;
   a->dpg = p->D / p->G; a->cbg = pl.cbg;
@@ -342,7 +349,7 @@ int ssm_fill(const pr_ssm_problem *p, const SsmPlan &pl, const pr_ssm_inputs *in
            vec4_ok(a->Bm, esz) && vec4_ok(a->Cm, esz);
   int rc = PR_OK;
   for (const View *v : {&a->u, &a->dt, &a->z, &a->Bm, &a->Cm})
-    if ((rc = stride_ok(*v, pl, esz)) != PR_OK) return rc;
+    if ((rc = stride_steps(*v, esz, steps)) != PR_OK) return rc;
   if (p->N % 4 == 0 && (((uintptr_t)in->A | (uintptr_t)in->h0) & 15))
     return fail(PR_EINVAL, "A and h0 must be 16-byte aligned");
   return PR_OK;
@@ -369,6 +376,14 @@ int join(const SsmArgs &a, const float *first, hipStream_t s) {
   return PR_OK;
 }
 
+// Time in windows of `steps` steps: no segments side by side, one state per
+// sequence (which the join kernel fills) goes from launch to launch.
+void windows(SsmArgs *a, int steps) {
+  a->S = a->R = a->SA = 1;
+  a->seglen = steps;
+  a->carry = a->agg;
+}
+
 }  // namespace
 
 extern "C" {
@@ -387,13 +402,14 @@ int pararnn_ssm_scan(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_
   int rc = ssm_plan(p, &pl);
   if (rc != PR_OK) return rc;
   SsmArgs a{};
-  rc = ssm_fill(p, pl, in, &a);
+  int steps = pl.seglen;
+  rc = ssm_fill(p, pl, in, &a, &steps);
   if (rc != PR_OK) return rc;
   if (!y || !y->p) return fail(PR_EINVAL, "y is required");
   rc = check_ws(workspace, ws_bytes, pl.fwd_bytes);
   if (rc != PR_OK) return rc;
-  a.y = view(y);
-  if ((rc = stride_ok(a.y, pl, p->dtype == PR_BF16 ? 2 : 4)) != PR_OK) return rc;
+  a.y = view(y, p->T);
+  if ((rc = stride_steps(a.y, p->dtype == PR_BF16 ? 2 : 4, &steps)) != PR_OK) return rc;
   a.vec = a.vec && vec4_ok(a.y, p->dtype == PR_BF16 ? 2 : 4);
   a.hlast = h_last; a.states = states;
   if (p->N % 4 == 0 && (((uintptr_t)h_last | (uintptr_t)states) & 15))
@@ -402,6 +418,13 @@ int pararnn_ssm_scan(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_
   a.agg = (float *)(ws + pl.off_agg); a.sumd = (float *)(ws + pl.off_sumd);
   a.S = pl.S; a.seglen = pl.seglen; a.R = pl.R; a.SA = pl.S * pl.R;
   hipStream_t s = (hipStream_t)stream;
+  if (steps < pl.seglen) {
+    windows(&a, steps);
+    if ((rc = join<false>(a, a.h0, s)) != PR_OK) return rc;
+    for (a.win = 0; (long long)a.win * steps < p->T; a.win++)
+      if ((rc = launch_ssm(p->dtype, a, SSM_FWD, s)) != PR_OK) return rc;
+    return PR_OK;
+  }
   if (a.S > 1) {
     if ((rc = launch_ssm(p->dtype, a, SSM_FWD_AGG, s)) != PR_OK) return rc;
     if ((rc = join<false>(a, a.h0, s)) != PR_OK) return rc;
@@ -416,7 +439,8 @@ int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const 
   int rc = ssm_plan(p, &pl);
   if (rc != PR_OK) return rc;
   SsmArgs a{};
-  rc = ssm_fill(p, pl, in, &a);
+  int steps = pl.seglen;
+  rc = ssm_fill(p, pl, in, &a, &steps);
   if (rc != PR_OK) return rc;
   if (!states || !dy || !dy->p || !gr) return fail(PR_EINVAL, "states, dy and the gradients' struct are required");
   if (gr->z.p && !in->z.p) return fail(PR_EINVAL, "dz without z");
@@ -424,10 +448,10 @@ int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const 
   if (rc != PR_OK) return rc;
   const int esz = p->dtype == PR_BF16 ? 2 : 4;
   a.states = (float *)states; a.dhlast = dh_last; a.dh0 = gr->h0;
-  a.dy = view(dy); a.du = view(&gr->u); a.ddt = view(&gr->dt); a.dz = view(&gr->z);
-  a.dB = view(&gr->B); a.dC = view(&gr->C);
+  a.dy = view(dy, p->T); a.du = view(&gr->u, p->T); a.ddt = view(&gr->dt, p->T); a.dz = view(&gr->z, p->T);
+  a.dB = view(&gr->B, p->T); a.dC = view(&gr->C, p->T);
   for (const View *v : {&a.dy, &a.du, &a.ddt, &a.dz})
-    if ((rc = stride_ok(*v, pl, esz)) != PR_OK) return rc;
+    if ((rc = stride_steps(*v, esz, &steps)) != PR_OK) return rc;
   a.vec = a.vec && vec4_ok(a.dy, esz) && vec4_ok(a.du, esz) && vec4_ok(a.ddt, esz) && vec4_ok(a.dz, esz);
   if (p->N % 4 == 0 && (((uintptr_t)states | (uintptr_t)dh_last | (uintptr_t)gr->h0) & 15))
     return fail(PR_EINVAL, "states, dh_last and dh0 must be 16-byte aligned");
@@ -437,11 +461,20 @@ int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const 
   a.acc = (float *)(ws + pl.off_acc);
   a.S = pl.S; a.seglen = pl.seglen; a.R = pl.R; a.SA = pl.S * pl.R;
   hipStream_t s = (hipStream_t)stream;
-  if (a.S > 1) {
-    if ((rc = launch_ssm(p->dtype, a, SSM_ADJ_AGG, s)) != PR_OK) return rc;
+  if (steps < pl.seglen) {
+    windows(&a, steps);
     if ((rc = join<true>(a, dh_last, s)) != PR_OK) return rc;
+    for (a.win = (p->T - 1) / steps; a.win >= 0; a.win--) {
+      if ((rc = launch_ssm(p->dtype, a, SSM_ADJ, s)) != PR_OK) return rc;
+      a.accum = 1;
+    }
+  } else {
+    if (a.S > 1) {
+      if ((rc = launch_ssm(p->dtype, a, SSM_ADJ_AGG, s)) != PR_OK) return rc;
+      if ((rc = join<true>(a, dh_last, s)) != PR_OK) return rc;
+    }
+    if ((rc = launch_ssm(p->dtype, a, SSM_ADJ, s)) != PR_OK) return rc;
   }
-  if ((rc = launch_ssm(p->dtype, a, SSM_ADJ, s)) != PR_OK) return rc;
   SsmSums f{};
   f.part = a.part; f.pA = a.pA; f.pD = a.pD; f.lengths = a.lengths; f.dB = a.dB; f.dC = a.dC;
   f.dA = gr->A; f.dD = gr->D; f.dbias = gr->dt_bias;

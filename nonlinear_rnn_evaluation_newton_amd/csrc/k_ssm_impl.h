@@ -367,7 +367,10 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_fwd(SsmArgs a) {
 #pragma unroll
   for (int k = 0; k < NS; k++) A2[k] *= 1.4426950408889634f;
   if constexpr (FULL) {
-    const float *hp = a.S > 1 ? a.agg + ((long long)w.b * a.SA + w.s * a.R) * dn : a.h0 ? a.h0 + w.b * dn : nullptr;
+    const float *hp = a.carry   ? a.carry + w.b * dn
+                      : a.S > 1 ? a.agg + ((long long)w.b * a.SA + w.s * a.R) * dn
+                      : a.h0    ? a.h0 + w.b * dn
+                                : nullptr;
     load_state<NS>(hp + (long long)w.d * a.N, n0, a.N, w.on && hp, h);
   } else {
 #pragma unroll
@@ -509,6 +512,7 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_fwd(SsmArgs a) {
     const int last = w.len > 0 ? (w.len - 1) / a.seglen : 0;
     if (a.hlast && w.s == last)
       store_state<NS>(a.hlast + w.b * dn + (long long)w.d * a.N, n0, a.N, w.on, h);
+    if (a.carry) store_state<NS>(a.carry + w.b * dn + (long long)w.d * a.N, n0, a.N, w.on, h);
   } else {
     const long long at = (long long)w.b * a.SA + w.s;
     store_state<NS>(a.agg + at * dn + (long long)w.d * a.N, n0, a.N, w.on, h);
@@ -649,15 +653,17 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
   const bool gate = a.z.p != nullptr, sp = a.softplus != 0;
   const int nt = (a.T + TL - 1) / TL, nl = (w.ws * 4 + w.j) * NS;  // nl: the lane's first state of these
   const long long dn = (long long)a.D * a.N;
-  const long long at = (long long)w.b * a.S + w.s;
+  const long long at = a.carry ? w.b : (long long)w.b * a.S + w.s;
   const bool odd1 = w.lane & 1, odd2 = w.lane & 2;
 
   const int n0 = a.n_off + nl, NPT = a.NPT;
 
   float A[NS], A2[NS], r[NS], dA[NS];
   load_state<NS>(a.A + (long long)w.d * a.N, n0, a.N, w.on, A);
-  const float *rp0 = a.S > 1 ? a.agg + ((long long)w.b * a.SA + (w.s + 1) * a.R - 1) * dn
-                             : a.dhlast ? a.dhlast + w.b * dn : nullptr;
+  const float *rp0 = a.carry    ? a.carry + w.b * dn
+                     : a.S > 1  ? a.agg + ((long long)w.b * a.SA + (w.s + 1) * a.R - 1) * dn
+                     : a.dhlast ? a.dhlast + w.b * dn
+                                : nullptr;
   load_state<NS>(rp0 + (long long)w.d * a.N, n0, a.N, w.on && rp0, r);
 #pragma unroll
   for (int k = 0; k < NS; k++) {
@@ -914,8 +920,15 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
     store_u<T, UC, VEC>(rdd.r, odd, tile * rdd.tile, zero, nv);
     store_u<T, UC, VEC>(rdz.r, odz, tile * rdz.tile, zero, nv);
   }
+  if (a.accum) {
+    float before[NS];
+    load_state<NS>(a.pA + at * dn + (long long)w.d * a.N, n0, a.N, w.on, before);
+#pragma unroll
+    for (int k = 0; k < NS; k++) dA[k] += before[k];
+  }
   store_state<NS>(a.pA + at * dn + (long long)w.d * a.N, n0, a.N, w.on, dA);
   if (a.dh0 && w.s == 0) store_state<NS>(a.dh0 + w.b * dn + (long long)w.d * a.N, n0, a.N, w.on, r);
+  if (a.carry) store_state<NS>(a.carry + w.b * dn + (long long)w.d * a.N, n0, a.N, w.on, r);
   if (MULTI && !a.last) return;
   // dD and the bias' gradient: over the tile's rows, which different threads hold
   __syncthreads();
@@ -932,7 +945,8 @@ __global__ __launch_bounds__(256 * WS) void k_ssm_adj(SsmArgs a) {
       float v = 0.f;
 #pragma unroll
       for (int row = 0; row < TL; row++) v += red[(m * TL + row) * CH + cc];
-      a.pD[(at * 2 + m) * a.D + w.ch0 + cc] = v;
+      float *o = a.pD + (at * 2 + m) * a.D + w.ch0 + cc;
+      *o = a.accum ? *o + v : v;
     }
   }
 }
@@ -943,7 +957,7 @@ hipError_t ssm_go(SsmArgs a, int what, hipStream_t s) {
   // no segment starts from the last one's end state (the first one's, backwards)
   const bool part = what == SSM_FWD_AGG || what == SSM_ADJ_AGG;
   a.segs = part ? a.SA - a.R : a.S;
-  a.seg0 = what == SSM_ADJ_AGG ? a.R : 0;
+  a.seg0 = what == SSM_ADJ_AGG ? a.R : a.win;
   if (part) a.seglen /= a.R;
   const dim3 grid((unsigned)((long long)a.B * a.segs * a.G * a.cbg));
   constexpr bool MULTI = NS > 2;

@@ -32,6 +32,9 @@ struct SsmArgs {
   float *acc;                        // adjoint of more than 16 states: sums over states, [B][T][3][D]
   int n_off, last, NPT;              // its launches: first state, whether the last, padded number of states
   int segs, seg0;                    // segments or pieces of a launch and the first of them (set by the launcher)
+  // long time strides: the segments are launched one after another (S = 1)
+  float *carry;                      // null, or [B][D][N]: the state that enters the segment, then the one that leaves it
+  int win, accum;                    // the segment; adjoint: whether dA, dD and dbias go on from what pA and pD hold
   int vec;                           // all arrays may be moved in vectors of four
 };
 

@@ -230,3 +230,22 @@ def test_tensors_of_another_gpu_are_refused(what, monkeypatch):
         call(0)
     got = call(1)
     assert got == ((t.data_ptr(), 128) if what == "_ws" else t.data_ptr())
+
+
+def test_scan_time_strides():
+    """Strides that 16 steps and the tiles fetched ahead cannot be reached with, and negative ones, are refused."""
+    L = bd.lib()
+    for dtype, most in ((bd.PR_F32, 2147483000 // (144 * 4)), (bd.PR_BF16, 2147483000 // (144 * 2))):
+        pb = bd.SsmProblem(dtype, 2, 64, 32, 16, 2, 1)
+        fw, ad = (L.pararnn_ssm_workspace_bytes(ref(pb), k) for k in (0, 1))
+        for st in (most + 1, 1 << 40, -32):
+            far = bd.View(256, 64, st)
+            for k in ("u", "dt", "z", "B", "C"):
+                assert L.pararnn_ssm_scan(ref(pb), ref(ssm_inputs(**{k: far})), ref(VIEW), None, None, V, fw,
+                                          None) == bd.PR_EUNSUPPORTED, (k, st)
+            assert L.pararnn_ssm_scan(ref(pb), ref(ssm_inputs()), ref(far), None, None, V, fw, None) == bd.PR_EUNSUPPORTED
+            for k in ("u", "dt", "z"):
+                gr = bd.SsmGrads(**{k: far})
+                assert L.pararnn_ssm_adjoint(ref(pb), ref(ssm_inputs(z=VIEW)), V, ref(VIEW), None, ref(gr), V, ad,
+                                             None) == bd.PR_EUNSUPPORTED, (k, st)
+        assert "stride" in bd.last_error()

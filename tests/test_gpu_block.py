@@ -638,3 +638,50 @@ def test_steps_do_not_use_the_number_of_steps():
     for T in (0, 1 << 30):
         for got, ref in zip(run(T), want):
             assert torch.equal(got, ref), T
+
+
+@pytest.mark.parametrize("dtype,T", [(BF, 1900), (F, 900)])
+@pytest.mark.parametrize("B,ch,N,G,ragged", [
+    (3, 40, 16, 1, True), (1, 20, 24, 2, False),  # time is split into short segments
+    (256, 8, 4, 1, True), (256, 6, 20, 2, True), (260, 4, 16, 1, False)])  # one segment, beyond 31-bit offsets
+def test_scan_of_far_steps(dtype, T, B, ch, N, G, ragged):
+    """Time-major slices of rows of 2^20 elements: an array's steps lie up to 4 GB
+    apart, which the kernels' 31-bit offsets reach only in windows of time.  The
+    states' memory is over hundreds of steps: 4 TOL, as for the split."""
+    g = gen(T + B + ch + N)
+    p = scan_problem(g, dtype, B, T, ch, N, G, True)
+    n = None
+    if ragged:
+        n = torch.randint(0, T + 1, (B,), generator=g).int()
+        n[:3] = torch.tensor([T - 333, 0, T])
+    h0, dh, dy = rnd(g, B, ch, N), rnd(g, B, ch, N), rnd(g, B, T, ch, dtype=dtype)
+    rows = torch.empty(T, 1 << 20, dtype=dtype, device="cuda")
+    at = [0]
+
+    def far(x):  # [B, T, columns], stored step by step in the wide rows
+        v = rows[:, at[0]:at[0] + B * x.shape[2]].unflatten(1, (B, x.shape[2])).transpose(0, 1)
+        at[0] += B * x.shape[2] + (B * x.shape[2]) % 2
+        v.copy_(x)
+        assert v.stride(1) == 1 << 20
+        return v
+
+    u, dt, z, Bm, Cm = (far(cut(p[k], n)) for k in ("u", "dt", "z", "Bm", "Cm"))
+    gy = far(cut(dy, n))
+    empty = lambda c: far(torch.full((B, T, c), float("nan")))  # noqa: E731
+    y, o = empty(ch), dict(du=empty(ch), ddt=empty(ch), dz=empty(ch), dB=empty(G * N), dC=empty(G * N))
+    nc = None if n is None else n.cuda()
+    dev = {k: p[k].cuda() for k in ("A", "D", "dt_bias")}
+    ws = torch.empty(bd.ssm_workspace_bytes(dtype, B, T, ch, N, G), dtype=torch.uint8, device="cuda").fill_(255)
+    states, hl = nan(*bd.ssm_states_shape(B, T, ch, N)), h0.cuda()
+    kw = dict(D=dev["D"], z=z, dt_bias=dev["dt_bias"], lengths=nc)
+    bd.ssm_scan(u, dt, dev["A"], Bm, Cm, y, ws, h0=hl, h_last=hl, states=states, **kw)  # (the state in place)
+    ry, rh = R.scan(**p, h0=h0, lengths=n)
+    near(y, ry, 4 * TOL, "y")
+    near(hl, rh, 4 * TOL, "h")
+    o.update(dA=nan(ch, N), dD=nan(ch), ddt_bias=nan(ch), dh0=nan(B, ch, N))
+    ws.fill_(255)
+    bd.ssm_scan_adjoint(u, dt, dev["A"], Bm, Cm, states, gy, ws, dh_last=dh.cuda(), **kw, **o)
+    r = R.scan_grads(**p, dy=dy, h0=h0, lengths=n, dh_last=dh)
+    r["ddt_bias"] = r.pop("dbias")
+    for k, v in o.items():
+        near(v, r[k], 4 * (SUM_TOL if k in ("dA", "dD", "ddt_bias", "dh0") else TOL), k)
