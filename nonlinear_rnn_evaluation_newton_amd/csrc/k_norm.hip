@@ -91,7 +91,7 @@ __global__ __launch_bounds__(256) void k_norm(NormArgs a) {
   constexpr int RPB = 256 / TPR;
   __shared__ float sh[2][4];
   const int x = threadIdx.x % TPR;
-  const long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+  const long long row = flat_block() * RPB + threadIdx.x / TPR;
   if (row >= a.rows) return;  // whole wavefronts, whole rows
   const T *xp = (const T *)a.x + row * a.lx, *rp = a.r ? (const T *)a.r + row * a.lr : nullptr;
   T *sp = a.s ? (T *)a.s + row * a.ls : nullptr;
@@ -290,7 +290,8 @@ __global__ __launch_bounds__(256) void k_norm_adj(NormArgs a) {
       }
     }
   } else {
-    const long long row = blockIdx.x;
+    const long long row = flat_block();
+    if (row >= a.rows) return;
     const T *sp = (const T *)a.s + row * a.ls, *gp = (const T *)a.dy + row * a.ldy;
     float ss = 0.f, dot = 0.f;
     for (int c = x; c < a.n; c += 256) {
@@ -354,11 +355,11 @@ static int norm_adj_blocks(long long rows, int rpb) {
 template <typename T, int V, int TPR, int NV>
 hipError_t norm_go(const NormArgs &a, int mode, hipStream_t s) {
   constexpr int RPB = 256 / TPR;
-  const dim3 grid((unsigned)((a.rows + RPB - 1) / RPB));
+  const dim3 grid = flat_grid((a.rows + RPB - 1) / RPB);
   if (mode == NORM_Y) k_norm<T, V, TPR, NV, NORM_Y><<<grid, 256, 0, s>>>(a);
   else if (mode == NORM_Q) k_norm<T, V, TPR, NV, NORM_Q><<<grid, 256, 0, s>>>(a);
   else if (mode == NORM_QUANT) k_norm<T, V, TPR, NV, NORM_QUANT><<<grid, 256, 0, s>>>(a);
-  else k_norm_adj<T, V, TPR, NV><<<dim3(NV > 0 ? norm_adj_blocks(a.rows, RPB) : (unsigned)a.rows), 256, 0, s>>>(a);
+  else k_norm_adj<T, V, TPR, NV><<<NV > 0 ? dim3(norm_adj_blocks(a.rows, RPB)) : grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

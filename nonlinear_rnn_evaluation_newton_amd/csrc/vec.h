@@ -6,6 +6,14 @@
 
 namespace pr {
 
+// A grid of more blocks than one dimension takes (2^32 threads): rows of 2^20
+// blocks.  The last row may hold blocks past the end, which return at once.
+inline dim3 flat_grid(long long blocks) {
+  const long long x = blocks < (1 << 20) ? blocks : 1 << 20;
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+__device__ inline long long flat_block() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
+
 template <typename T, int V>
 struct Vec;
 template <>

@@ -685,3 +685,22 @@ def test_scan_of_far_steps(dtype, T, B, ch, N, G, ragged):
     r["ddt_bias"] = r.pop("dbias")
     for k, v in o.items():
         near(v, r[k], 4 * (SUM_TOL if k in ("dA", "dD", "ddt_bias", "dh0") else TOL), k)
+
+
+@pytest.mark.parametrize("n", [2, 3])
+def test_norm_of_very_many_rows(n):
+    """More rows than one grid dimension has threads for (2^32, 64 a row)."""
+    rows = (1 << 26) + 5
+    x = torch.randn(rows, n, device="cuda", generator=torch.Generator("cuda").manual_seed(n))
+    y, q, scale = nan(rows, n), torch.full((rows, n), 99, dtype=torch.int8, device="cuda"), nan(rows)
+    bd.rmsnorm(x, None, y=y, eps=1e-5)
+    bd.quant_rows(x, q, scale)
+    # the whole range, a block of rows at a time; values are below sqrt(n), sums of n terms
+    for r0 in range(0, rows, 1 << 24):
+        d = x[r0:r0 + (1 << 24)].double()
+        want = d / torch.sqrt((d * d).mean(1, keepdim=True) + 1e-5)
+        assert float((y[r0:r0 + (1 << 24)].double() - want).abs().max()) <= TOL, r0
+        s = scale[r0:r0 + (1 << 24), None].double()
+        assert float((s[:, 0] * 127 / d.abs().amax(1) - 1).abs().max()) <= 1e-6, r0
+        # half a step, and the quotient's rounding
+        assert float((q[r0:r0 + (1 << 24)].double() - d / s).abs().max()) <= 0.5 + 1e-5, r0
