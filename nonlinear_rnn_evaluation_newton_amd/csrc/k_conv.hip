@@ -45,9 +45,10 @@ __device__ inline void conv_weights(const ConvArgs &a, int d, float (*w)[V], flo
 template <typename T, int V, int W>
 __global__ __launch_bounds__(256) void k_conv_fwd(ConvArgs a) {
   const int nv = a.D / V, vb = (nv + 255) / 256;
-  const int d = ((int)(blockIdx.x % vb) * 256 + threadIdx.x) * V;
-  const int q = (int)(blockIdx.x / vb), run = q % a.runs, b = q / a.runs;
-  if (d >= a.D) return;
+  const unsigned blk = (unsigned)flat_block();
+  const int d = ((int)(blk % vb) * 256 + threadIdx.x) * V;
+  const int q = (int)(blk / vb), run = q % a.runs, b = q / a.runs;
+  if (d >= a.D || b >= a.B) return;
   const int len = seq_len(a.lengths, b, a.T);
   const int t0 = run * a.run, t1 = a.T - t0 < a.run ? a.T : t0 + a.run;
   float w[W][V], bias[V], win[W][V];  // win[k]: the input of step t - W + 1 + k
@@ -101,8 +102,9 @@ __global__ __launch_bounds__(512) void k_conv_adj(ConvArgs a) {
   __shared__ float red[8][W + 1][64 * V];
   const int nv = a.D / V, vb = (nv + 63) / 64;
   const int x = threadIdx.x & 63, r8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int dblk = (int)(blockIdx.x % vb) * 64, d = (dblk + x) * V;
-  const long long q = (long long)(blockIdx.x / vb) * 8 + r8;
+  const unsigned blk = (unsigned)flat_block();
+  const int dblk = (int)(blk % vb) * 64, d = (dblk + x) * V;
+  const long long q = (long long)(blk / vb) * 8 + r8;
   const bool on = d < a.D && q < (long long)a.B * a.runs;
   float gw[W][V], gb[V];
 #pragma unroll
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(512) void k_conv_adj(ConvArgs a) {
       step(std::integral_constant<bool, false>{}, t, in, gy);
     }
   }
-  if (!a.part) return;
+  if (!a.part || (long long)(blk / vb) * 8 >= (long long)a.B * a.runs) return;  // (past the end: a block as a whole)
 #pragma unroll
   for (int i = 0; i < V; i++) {
 #pragma unroll
@@ -220,7 +222,7 @@ __global__ __launch_bounds__(512) void k_conv_adj(ConvArgs a) {
     red[r8][W][x * V + i] = gb[i];
   }
   __syncthreads();
-  float *o = a.part + (long long)(blockIdx.x / vb) * (W + 1) * a.D;
+  float *o = a.part + (long long)(blk / vb) * (W + 1) * a.D;
   for (int i = threadIdx.x; i < (W + 1) * 64 * V; i += 512) {
     const int k = i / (64 * V), c = i % (64 * V), dd = dblk * V + c;
     if (dd < a.D) {
@@ -296,13 +298,13 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvStepArgs a) {
 template <typename T, int V, int W>
 hipError_t conv_fwd_launch(const ConvArgs &a, hipStream_t s) {
   const long long nv = a.D / V, q = (long long)a.B * a.runs;
-  k_conv_fwd<T, V, W><<<dim3((unsigned)(((nv + 255) / 256) * q)), 256, 0, s>>>(a);
+  k_conv_fwd<T, V, W><<<flat_grid(((nv + 255) / 256) * q), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 template <typename T, int V, int W>
 hipError_t conv_adj_launch(const ConvArgs &a, hipStream_t s) {
   const long long nv = a.D / V, q = (long long)a.B * a.runs;
-  k_conv_adj<T, V, W><<<dim3((unsigned)(((nv + 63) / 64) * ((q + 7) / 8))), 512, 0, s>>>(a);
+  k_conv_adj<T, V, W><<<flat_grid(((nv + 63) / 64) * ((q + 7) / 8)), 512, 0, s>>>(a);
   return hipGetLastError();
 }
 template <typename T, int V, int W>

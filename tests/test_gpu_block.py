@@ -704,3 +704,40 @@ def test_norm_of_very_many_rows(n):
         assert float((s[:, 0] * 127 / d.abs().amax(1) - 1).abs().max()) <= 1e-6, r0
         # half a step, and the quotient's rounding
         assert float((q[r0:r0 + (1 << 24)].double() - d / s).abs().max()) <= 0.5 + 1e-5, r0
+
+
+def test_conv_of_very_many_runs():
+    """More runs of steps than one grid dimension has threads for: 2^24 blocks
+    of the forward kernel, 2^23 of the adjoint.  One channel, two taps."""
+    g = torch.Generator("cuda").manual_seed(2)
+    w, b = torch.tensor([[0.5, -1.25]], dtype=BF, device="cuda"), torch.tensor([0.25], dtype=BF, device="cuda")
+
+    def draw(B, T):
+        return torch.empty(B, T, 1, dtype=BF, device="cuda").normal_(generator=g)
+
+    def before(x):  # a_t of the double sequences x [B, T]
+        past = torch.cat([torch.zeros_like(x[:, :1]), x[:, :-1]], 1)
+        return 0.25 + 0.5 * past - 1.25 * x
+
+    def check(got, want, where):  # one rounding to bf16, few in 32 bits
+        assert bool(((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + TOL).all()), where
+
+    B, T = (1 << 20) + 3, 1024
+    x = draw(B, T)
+    y = nan(B, T, 1, dtype=BF)
+    bd.conv(x, w, b, y)
+    for r in range(0, B, 1 << 16):
+        a = before(x[r:r + (1 << 16), :, 0].double())
+        check(y[r:r + (1 << 16), :, 0], a * torch.sigmoid(a), r)
+    del x, y
+    B, T = (1 << 16) + 1, 1 << 16
+    x, dy = draw(B, T), draw(B, T)
+    dx = nan(B, T, 1, dtype=BF)
+    bd.conv_adjoint(x, w, b, dy, dx, None, None,
+                    torch.empty(bd.conv_workspace_bytes(BF, B, T, 1, 2), dtype=torch.uint8, device="cuda"))
+    for r in range(0, B, 1 << 10):
+        a = before(x[r:r + (1 << 10), :, 0].double())
+        p = torch.sigmoid(a)
+        da = dy[r:r + (1 << 10), :, 0].double() * (p + a * p * (1 - p))
+        later = torch.cat([da[:, 1:], torch.zeros_like(da[:, :1])], 1)
+        check(dx[r:r + (1 << 10), :, 0], 0.5 * later - 1.25 * da, r)
