@@ -4,6 +4,7 @@
 
 #include "pararnn.h"
 #include "ssm.h"
+#include "vec.h"
 
 namespace pr {
 
@@ -21,7 +22,7 @@ namespace pr {
 template <bool REV>
 __global__ void k_ssm_join(const float *__restrict__ A, const float *__restrict__ first,
                            const float *__restrict__ sumd, float *__restrict__ agg, int B, int D, int N, int S) {
-  const long long dn = (long long)D * N, i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long dn = (long long)D * N, i = flat_block() * 256 + threadIdx.x;
   if (i >= B * dn) return;
   const long long b = i / dn, e = i % dn;
   const int d = (int)(e / N);
@@ -61,7 +62,7 @@ struct SsmSums {
   View dB, dC;
   float *dA, *dD, *dbias;       // may be null
   int nblk, B, T, G, N, NP, P, D;
-  unsigned bc_blocks, a_blocks;  // blocks of the first two kinds
+  unsigned bc_blocks, a_blocks;  // blocks of the first two kinds, of which the first walk their outputs
 };
 
 // out[j] = the sum over p of part[p * stride + j], in 64 bits in a fixed order:
@@ -105,30 +106,30 @@ __global__ __launch_bounds__(256) void k_ssm_sums(SsmSums a) {
     return;
   }
   const long long rows = (long long)a.B * a.T * a.G, cols = 2LL * a.NP;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * cols) return;
-  const int n2 = (int)(i % cols), n = n2 % a.NP;
-  if (n >= a.N) return;
-  const long long row = i / cols, bt = row / a.G;
-  const int g = (int)(row % a.G), t = (int)(bt % a.T), b = (int)(bt / a.T);
-  const View &v = n2 < a.NP ? a.dB : a.dC;
-  if (!v.p) return;
-  float s = 0.f;
-  if (t < seq_len(a.lengths, b, a.T)) {
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < rows * cols; i += a.bc_blocks * 256LL) {
+    const int n2 = (int)(i % cols), n = n2 % a.NP;
+    if (n >= a.N) continue;
+    const long long row = i / cols, bt = row / a.G;
+    const int g = (int)(row % a.G), t = (int)(bt % a.T), b = (int)(bt / a.T);
+    const View &v = n2 < a.NP ? a.dB : a.dC;
+    if (!v.p) continue;
+    float s = 0.f;
+    if (t < seq_len(a.lengths, b, a.T)) {
 #pragma unroll 8
-    for (int k = 0; k < a.nblk; k++) s += a.part[k * rows * cols + i];
+      for (int k = 0; k < a.nblk; k++) s += a.part[k * rows * cols + i];
+    }
+    stf((T *)v.p, b * v.sb + t * v.st + (long long)g * a.N + n, s);
   }
-  stf((T *)v.p, b * v.sb + t * v.st + (long long)g * a.N + n, s);
 }
 
 // for many partials of few columns
 __global__ __launch_bounds__(1024) void k_part_sum(const float *part, int P, long long stride, long long cols, float *out) {
-  part_sum<16, 64>(part, P, stride, cols, blockIdx.x, out);
+  part_sum<16, 64>(part, P, stride, cols, flat_block(), out);
 }
 
 hipError_t launch_part_sum(const float *part, int P, long long stride, long long cols, float *out, hipStream_t s) {
   if (cols < 1) return hipSuccess;
-  k_part_sum<<<dim3((unsigned)((cols + 15) / 16)), 1024, 0, s>>>(part, P, stride, cols, out);
+  k_part_sum<<<flat_grid((cols + 15) / 16), 1024, 0, s>>>(part, P, stride, cols, out);
   return hipGetLastError();
 }
 
@@ -286,7 +287,6 @@ int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
   pl->cbg = (dpg + 63) / 64;
   pl->NP = 4 * g.ns * g.ws;
   const long long blocks = (long long)p->B * p->G * pl->cbg;
-  if (blocks > (1LL << 24)) return fail(PR_EUNSUPPORTED, "problem too large: %lld channel blocks", blocks);
   const int esz = p->dtype == PR_BF16 ? 2 : 4;
   // rows as slices of projections up to four times as wide as they need be
   const long long width = p->D > (long long)p->G * p->N ? p->D : (long long)p->G * p->N;
@@ -296,6 +296,9 @@ int ssm_plan(const pr_ssm_problem *p, SsmPlan *pl) {
   if (p->N > 16 && tile < SSM_TL * 12LL * p->D) tile = SSM_TL * 12LL * p->D;
   if (tile > (1LL << 27)) return fail(PR_EUNSUPPORTED, "problem too large: %lld bytes in 16 steps", tile);
   split_time(blocks, p->T, tile, &pl->S, &pl->seglen, &pl->R);
+  // a launch has 2^32 threads at most, 512 a block
+  if (blocks * pl->S * pl->R >= (1LL << 23))
+    return fail(PR_EUNSUPPORTED, "problem too large: %lld blocks of channels, %d segments", blocks, pl->S * pl->R);
   const size_t dn = (size_t)p->D * p->N, sm = pl->S > 1 ? pl->S * pl->R : 1;
   if ((double)p->B * sm * dn * 4 > 1e13 || (double)p->B * p->T * p->G * pl->cbg * pl->NP * 8 > 1e13)
     return fail(PR_EUNSUPPORTED, "problem too large");
@@ -371,7 +374,7 @@ int check_ws(const void *ws, size_t have, size_t need) {
 template <bool REV>
 int join(const SsmArgs &a, const float *first, hipStream_t s) {
   const long long n = (long long)a.B * a.D * a.N;
-  k_ssm_join<REV><<<dim3((unsigned)((n + 255) / 256)), 256, 0, s>>>(a.A, first, a.sumd, a.agg, a.B, a.D, a.N, a.SA);
+  k_ssm_join<REV><<<flat_grid((n + 255) / 256), 256, 0, s>>>(a.A, first, a.sumd, a.agg, a.B, a.D, a.N, a.SA);
   HIPCHK(hipGetLastError());
   return PR_OK;
 }
@@ -479,7 +482,9 @@ int pararnn_ssm_adjoint(const pr_ssm_problem *p, const pr_ssm_inputs *in, const 
   f.part = a.part; f.pA = a.pA; f.pD = a.pD; f.lengths = a.lengths; f.dB = a.dB; f.dC = a.dC;
   f.dA = gr->A; f.dD = gr->D; f.dbias = gr->dt_bias;
   f.nblk = a.cbg; f.B = a.B; f.T = a.T; f.G = a.G; f.N = a.N; f.NP = pl.NP; f.P = a.B * a.S; f.D = a.D;
-  if (a.dB.p || a.dC.p) f.bc_blocks = (unsigned)(((long long)a.B * a.T * a.G * 2 * pl.NP + 255) / 256);
+  // a thread for each output, up to what one grid dimension takes beside the other kinds
+  const long long bc = ((long long)a.B * a.T * a.G * 2 * pl.NP + 255) / 256;
+  if (a.dB.p || a.dC.p) f.bc_blocks = (unsigned)(bc < (1 << 23) ? bc : 1 << 23);
   if (gr->A) f.a_blocks = (unsigned)(((long long)a.D * a.N + 31) / 32);
   const unsigned n = f.bc_blocks + f.a_blocks + (gr->D || gr->dt_bias ? 2 * ((a.D + 31) / 32) : 0);
   if (n == 0) return PR_OK;

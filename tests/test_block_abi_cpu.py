@@ -249,3 +249,15 @@ def test_scan_time_strides():
                 assert L.pararnn_ssm_adjoint(ref(pb), ref(ssm_inputs(z=VIEW)), V, ref(VIEW), None, ref(gr), V, ad,
                                              None) == bd.PR_EUNSUPPORTED, (k, st)
         assert "stride" in bd.last_error()
+
+
+def test_scan_launches_that_no_grid_takes():
+    """One grid dimension takes 2^32 threads: 2^23 blocks of channels of all sequences are refused."""
+    L = bd.lib()
+
+    def size(B, D, G=1):
+        return L.pararnn_ssm_workspace_bytes(ref(bd.SsmProblem(bd.PR_BF16, B, 16, D, 16, G, 1)), 0)
+
+    assert size(1 << 18, 31 * 64) > 0 and size(1 << 18, 31, 31) > 0
+    assert size(1 << 18, 32 * 64) == 0 and size(1 << 18, 32, 32) == 0
+    assert "blocks" in bd.last_error()

@@ -741,3 +741,29 @@ def test_conv_of_very_many_runs():
         da = dy[r:r + (1 << 10), :, 0].double() * (p + a * p * (1 - p))
         later = torch.cat([da[:, 1:], torch.zeros_like(da[:, :1])], 1)
         check(dx[r:r + (1 << 10), :, 0], 0.5 * later - 1.25 * da, r)
+
+
+def test_scan_gradients_of_very_many_groups():
+    """dB and dC of more (step, group, state) than one grid dimension has
+    threads for (2^32; 16 for each step and group of up to 8 states): some
+    sequences of the batch against the 64-bit form."""
+    g = torch.Generator("cuda").manual_seed(3)
+    B, T, ch, N = (1 << 16) + 1, 64, 64, 1
+
+    def draw(*shape, dtype=BF, std=1.0):
+        return torch.empty(*shape, dtype=dtype, device="cuda").normal_(std=std, generator=g)
+
+    p = dict(u=draw(B, T, ch), dt=draw(B, T, ch, std=0.5), A=-(draw(ch, N, dtype=F).abs() + 0.2), Bm=draw(B, T, ch),
+             Cm=draw(B, T, ch))
+    y, states, dy = nan(B, T, ch, dtype=BF), nan(*bd.ssm_states_shape(B, T, ch, N)), draw(B, T, ch)
+    ws = torch.empty(bd.ssm_workspace_bytes(BF, B, T, ch, N, ch), dtype=torch.uint8, device="cuda")
+    bd.ssm_scan(p["u"], p["dt"], p["A"], p["Bm"], p["Cm"], y, ws, states=states)
+    o = dict(dB=nan(B, T, ch, dtype=BF), dC=nan(B, T, ch, dtype=BF))
+    bd.ssm_scan_adjoint(p["u"], p["dt"], p["A"], p["Bm"], p["Cm"], states, dy, ws, **o)
+    rows = torch.tensor([0, 1, 30000, 65535, 65536])
+    q = {k: v.cpu() if k == "A" else v[rows].cpu() for k, v in p.items()}
+    near(y[rows], R.scan(**q)[0], TOL, "y")
+    r = R.scan_grads(**q, dy=dy[rows].cpu())
+    for k, v in o.items():
+        assert torch.isfinite(v).all(), k
+        near(v[rows], r[k], TOL, k)
