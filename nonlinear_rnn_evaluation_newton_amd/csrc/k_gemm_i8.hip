@@ -464,8 +464,10 @@ namespace {
 int gemm8_check(int M, int N, int K) {
   if (M < 1 || N < 1 || K < 1) return fail(PR_EINVAL, "sizes must be >= 1 (M=%d N=%d K=%d)", M, N, K);
   if (K >= 131072) return fail(PR_EUNSUPPORTED, "K = %d: sums of 131072 products may pass 32 bits", K);
-  if ((double)M * N > 1e12 || (double)((M + 127) / 128) * ((N + 127) / 128) > 2e9)
-    return fail(PR_EUNSUPPORTED, "problem too large");
+  if (M > (1 << 30) || N > (1 << 30)) return fail(PR_EUNSUPPORTED, "M = %d, N = %d: at most 2^30", M, N);
+  // a launch has 2^32 threads at most: 512 for 16 columns, 256 for a tile
+  const double blocks = M <= 64 ? (N + 15) / 16 * 2.0 : (double)((M + 127) / 128) * ((N + 127) / 128);
+  if (blocks >= (1 << 24)) return fail(PR_EUNSUPPORTED, "problem too large: %d x %d results", M, N);
   return PR_OK;
 }
 

@@ -8,11 +8,13 @@ namespace pr {
 
 // A grid of more blocks than one dimension takes (2^32 threads): rows of 2^20
 // blocks.  The last row may hold blocks past the end, which return at once.
+// (A block's number does not take the grid's size, a load at the start of the
+// kernel.)
 inline dim3 flat_grid(long long blocks) {
   const long long x = blocks < (1 << 20) ? blocks : 1 << 20;
   return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
 }
-__device__ inline long long flat_block() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
+__device__ inline long long flat_block() { return ((long long)blockIdx.y << 20) + blockIdx.x; }
 
 template <typename T, int V>
 struct Vec;

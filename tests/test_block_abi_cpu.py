@@ -261,3 +261,13 @@ def test_scan_launches_that_no_grid_takes():
     assert size(1 << 18, 31 * 64) > 0 and size(1 << 18, 31, 31) > 0
     assert size(1 << 18, 32 * 64) == 0 and size(1 << 18, 32, 32) == 0
     assert "blocks" in bd.last_error()
+
+
+def test_products_that_no_grid_takes():
+    """A launch has 2^32 threads at most; more were cut without an error: few
+    rows of 2^27 columns, and more of them where there are 2^24 tiles of 128 x 128."""
+    size = bd.gemm_i8_workspace_bytes
+    assert size(64, (1 << 27) - 16, 16) > 0 and size(1 << 20, (1 << 18) - 128, 16) > 0
+    for M, N in ((64, (1 << 27) - 15), (1, 1 << 30), (1 << 20, 1 << 18), (1 << 30, 1 << 18)):
+        assert size(M, N, 16) == 0 and "large" in bd.last_error(), (M, N)
+    assert size(100, (1 << 30) + 1, 16) == 0 and size((1 << 31) - 1, 1, 16) == 0
