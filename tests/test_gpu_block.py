@@ -767,3 +767,85 @@ def test_scan_gradients_of_very_many_groups():
     for k, v in o.items():
         assert torch.isfinite(v).all(), k
         near(v[rows], r[k], TOL, k)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("B,T,ch,N,G", [
+    # one segment of 14 tiles: every number of states per lane and of wavefronts, with and without vectors
+    (256, 210, 8, 3, 1), (256, 210, 8, 16, 1), (256, 210, 8, 24, 1), (256, 210, 8, 64, 1), (256, 210, 7, 8, 1),
+    (256, 210, 6, 16, 1), (256, 210, 7, 17, 1), (256, 210, 6, 33, 2), (256, 210, 8, 12, 2),
+    # two segments prepared in two pieces, the odd number of tiles of each rounded up
+    (200, 150, 8, 16, 1), (180, 140, 8, 40, 1), (200, 150, 5, 7, 1),
+    # pieces of 10 tiles
+    (130, 600, 12, 8, 1), (130, 600, 8, 16, 1), (130, 600, 6, 20, 1), (128, 600, 8, 32, 1)])
+def test_scan_long_segments(dtype, B, T, ch, N, G):
+    """Enough blocks that a segment is longer than the tiles that are in flight
+    at once: the rings of prefetched tiles go round.  Ragged; rounding grows
+    with the steps of a state that keeps its past (TOL: 320)."""
+    print("long segments", dtype, B, T, ch, N, G, flush=True)
+    g = gen(B + T + ch + N + G)
+    p = scan_problem(g, dtype, B, T, ch, N, G, True)
+    n = torch.randint(0, T + 1, (B,), generator=g).int()
+    n[:4] = torch.tensor([T, 0, T - 1, 1])
+    h0, dh, dy = rnd(g, B, ch, N), rnd(g, B, ch, N), rnd(g, B, T, ch, dtype=dtype)
+    dev = {k: (cut(v, n) if v.dim() == 3 else v).cuda() for k, v in p.items()}
+    ws = torch.empty(bd.ssm_workspace_bytes(dtype, B, T, ch, N, G), dtype=torch.uint8, device="cuda").fill_(255)
+    y, hl, states = nan(B, T, ch, dtype=dtype), nan(B, ch, N), nan(*bd.ssm_states_shape(B, T, ch, N))
+    kw = dict(D=dev["D"], z=dev["z"], dt_bias=dev["dt_bias"], lengths=n.cuda())
+    main = (dev["u"], dev["dt"], dev["A"], dev["Bm"], dev["Cm"])
+    bd.ssm_scan(*main, y, ws, h0=h0.cuda(), h_last=hl, states=states, **kw)
+    ry, rh = R.scan(**p, h0=h0, lengths=n)
+    more = max(1.0, T / 320)
+    near(y, ry, more * TOL, "y")
+    near(hl, rh, more * TOL, "h")
+    o = dict(du=nan(B, T, ch, dtype=dtype), ddt=nan(B, T, ch, dtype=dtype), dB=nan(B, T, G * N, dtype=dtype),
+             dC=nan(B, T, G * N, dtype=dtype), dA=nan(ch, N), dD=nan(ch), ddt_bias=nan(ch), dh0=nan(B, ch, N),
+             dz=nan(B, T, ch, dtype=dtype))
+    ws.fill_(255)
+    bd.ssm_scan_adjoint(*main, states, cut(dy, n).cuda(), ws, dh_last=dh.cuda(), **kw, **o)
+    r = R.scan_grads(**p, dy=dy, h0=h0, lengths=n, dh_last=dh)
+    r["ddt_bias"] = r.pop("dbias")
+    for k, v in o.items():
+        near(v, r[k], more * (SUM_TOL if k in ("dA", "dD", "ddt_bias", "dh0") else TOL), k)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("B,T,D,W", [(1024, 2049, 16, 4), (8192, 2100, 8, 3), (1024, 2000, 7, 4), (2200, 1999, 5, 2)])
+def test_conv_long_runs(dtype, B, T, D, W):
+    """Enough sequences that a thread takes runs of 16 to 64 steps, whose loops
+    go round; ragged.  The reference is the definition in 64 bits on the GPU."""
+    g = torch.Generator("cuda").manual_seed(B + T + D + W)
+
+    def draw(*shape, std=1.0):
+        return torch.randn(*shape, device="cuda", generator=g).mul_(std).to(dtype)
+
+    x, dy, w, b = draw(B, T, D), draw(B, T, D), draw(D, W, std=0.5), draw(D)
+    n = torch.randint(0, T + 1, (B,), device="cuda", generator=g).int()
+    n[:4] = torch.tensor([T, 0, T - 1, 1])
+    on = (torch.arange(T, device="cuda")[None] < n[:, None])[..., None]
+    st, dst = draw(B, W - 1, D), draw(B, W - 1, D)
+    zero = torch.zeros((), dtype=R.F64, device="cuda")
+    full = torch.cat([st.double(), torch.where(on, x.double(), zero)], 1)  # [B, W - 1 + T, D]
+    a = b.double() + sum(full[:, k:k + T] * w[:, k].double() for k in range(W))
+    p = torch.sigmoid(a)
+    da = torch.where(on, dy.double() * (p + a * p * (1 - p)), zero)
+    r = dict(y=torch.where(on, a * p, zero), dbias=da.sum((0, 1)),
+             dw=torch.stack([(da * full[:, k:k + T]).sum((0, 1)) for k in range(W)], 1))
+    del a, p
+    gf = torch.zeros_like(full)
+    for k in range(W):
+        gf[:, k:k + T] += da * w[:, k].double()
+    last = n.long()[:, None] + torch.arange(W - 1, device="cuda")  # where the state after the last step lies in `full`
+    r["state"] = full.gather(1, last[..., None].expand(-1, -1, D))
+    gf.scatter_add_(1, last[..., None].expand(-1, -1, D), dst.double())
+    r["dstate"], r["dx"] = gf[:, :W - 1], gf[:, W - 1:]
+
+    masked = [torch.where(on, t, torch.full((), float("nan"), dtype=dtype, device="cuda")) for t in (x, dy)]
+    y, so, dx, ds = (nan(*s, dtype=dtype) for s in ((B, T, D), (B, W - 1, D), (B, T, D), (B, W - 1, D)))
+    dw, db = nan(D, W), nan(D)
+    bd.conv(masked[0], w, b, y, state_in=st, state_out=so, lengths=n)
+    ws = torch.empty(bd.conv_workspace_bytes(dtype, B, T, D, W), dtype=torch.uint8, device="cuda")
+    bd.conv_adjoint(masked[0], w, b, masked[1], dx, dw, db, ws, state_in=st, dstate_out=dst, dstate_in=ds, lengths=n)
+    for k, v, tol in (("y", y, TOL), ("state", so, 0), ("dx", dx, TOL), ("dstate", ds, TOL), ("dw", dw, SUM_TOL),
+                      ("dbias", db, SUM_TOL)):
+        near(v, r[k].cpu(), tol, k)
