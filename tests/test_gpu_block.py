@@ -849,3 +849,40 @@ def test_conv_long_runs(dtype, B, T, D, W):
     for k, v, tol in (("y", y, TOL), ("state", so, 0), ("dx", dx, TOL), ("dstate", ds, TOL), ("dw", dw, SUM_TOL),
                       ("dbias", db, SUM_TOL)):
         near(v, r[k].cpu(), tol, k)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_step_sizes_from_end_to_end(dtype):
+    """softplus and its derivative from dt = -80 to 80, each step size in a
+    sequence of its own from a state of 0, without D: every state, output and
+    gradient is the step size (or its derivative) times numbers of order 1 of
+    one sign, and is held to TOL of its own value (an error in 32 bits: the
+    exponential's argument, |dt| 2^-23 = 1e-5 at most, and a few roundings)."""
+    g = gen(8)
+    B, ch, N = 161, 8, 4
+    dt = torch.linspace(-80, 80, B)[:, None, None].expand(B, 1, ch).to(dtype).contiguous()
+
+    def positive(*shape):
+        return (torch.rand(*shape, generator=g) + 0.5).to(dtype)
+
+    p = dict(u=positive(B, 1, ch), dt=dt, A=-(torch.rand(ch, N, generator=g) + 0.2), Bm=positive(B, 1, N),
+             Cm=positive(B, 1, N))
+    dy = positive(B, 1, ch)
+    dev = {k: v.cuda() for k, v in p.items()}
+    main = tuple(dev[k] for k in ("u", "dt", "A", "Bm", "Cm"))
+    ws = torch.empty(bd.ssm_workspace_bytes(dtype, B, 1, ch, N), dtype=torch.uint8, device="cuda")
+    y, hl, states = nan(B, 1, ch, dtype=dtype), nan(B, ch, N), nan(*bd.ssm_states_shape(B, 1, ch, N))
+    bd.ssm_scan(*main, y, ws, h_last=hl, states=states)
+    o = dict(du=nan(B, 1, ch, dtype=dtype), ddt=nan(B, 1, ch, dtype=dtype), dB=nan(B, 1, N, dtype=dtype),
+             dC=nan(B, 1, N, dtype=dtype))
+    bd.ssm_scan_adjoint(*main, states, dy.cuda(), ws, **o)
+    ys, hs = nan(B, ch, dtype=dtype), torch.zeros(B, ch, N, device="cuda")
+    bd.ssm_step(*(v if v is dev["A"] else v[:, 0] for v in main), hs, ys)
+    ry, rh = R.scan(**p)
+    r = R.scan_grads(**p, dy=dy)
+    for k, got, want in [("y", y, ry), ("h", hl, rh), ("step's y", ys, ry[:, 0]), ("step's h", hs, rh)] + [
+            (k, v, r[k]) for k, v in o.items()]:
+        assert torch.isfinite(got).all() and (want > 0).all(), k
+        unit = 2.0 ** -8 if got.dtype == BF else 0.0
+        err = ((got.double().cpu() - want) / want).abs().flatten(1).amax(1)
+        assert (err <= TOL + unit).all(), (k, float(err.max()), float(dt[err.argmax(), 0, 0]))
