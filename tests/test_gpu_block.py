@@ -886,3 +886,118 @@ def test_step_sizes_from_end_to_end(dtype):
         unit = 2.0 ** -8 if got.dtype == BF else 0.0
         err = ((got.double().cpu() - want) / want).abs().flatten(1).amax(1)
         assert (err <= TOL + unit).all(), (k, float(err.max()), float(dt[err.argmax(), 0, 0]))
+
+
+# ---------------------------------------------------------------------------
+# operands beyond 2^31 bytes and elements: few values in rows that lie far apart
+# ---------------------------------------------------------------------------
+def far_rows(x, ld, at=64):
+    """x [rows, n] on the GPU with row stride ld, from element `at` of a buffer on."""
+    rows, n = x.shape
+    buf = torch.empty((rows - 1) * ld + at + n, dtype=x.dtype, device="cuda")
+    v = buf.as_strided((rows, n), (ld, 1), at)
+    v.copy_(x)
+    return v
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("n", [300, 2048, 20000])
+def test_norm_of_far_rows(dtype, n):
+    g = gen(n)
+    rows, ld, eps = 6, 1 << 29, 1e-5  # the last row begins 5 or 10 GB after the first
+    x, r, dy, ds, w = (rnd(g, *s, dtype=dtype) for s in ((rows, n),) * 4 + ((n,),))
+    s = (x.float() + r.float()).to(dtype)
+    empty = far_rows(torch.full((rows, n), float("nan"), dtype=dtype), ld)
+    so, y = nan(rows, n, dtype=dtype), empty
+    bd.rmsnorm(far_rows(x, ld), w.cuda(), residual=r.cuda(), sum_out=so, y=y, eps=eps)
+    assert torch.equal(so.cpu(), s)
+    near(y, R.norm(s, w, eps), TOL, "y")
+    q, scale = far_rows(torch.full((rows, n), 99, dtype=torch.int8), ld), nan(rows)
+    bd.quant_rows(far_rows(s, ld), q, scale)
+    rq, rs = R.quant(s.double())
+    near(scale, rs, 1e-6, "scale")
+    assert (q.double().cpu() - rq).abs().max() <= 1 and float((q.cpu() != rq).double().mean()) <= 1e-3 + 2 / rq.numel()
+    dx, dw = far_rows(torch.full((rows, n), float("nan"), dtype=dtype), ld), nan(n)
+    ws = torch.empty(bd.rmsnorm_workspace_bytes(dtype, rows, n), dtype=torch.uint8, device="cuda").fill_(255)
+    bd.rmsnorm_adjoint(far_rows(s, ld), w.cuda(), far_rows(dy, ld), dx, dw, ws, dsum=ds.cuda(), eps=eps)
+    rx, rw = R.norm_grads(s, w, dy, eps, ds)
+    near(dx, rx, TOL, "dx")
+    near(dw, rw, SUM_TOL, "dw")
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("M,N,K,lda,ldw,ldo", [
+    (5, 40, 256, 1 << 30, 1 << 27, 1 << 28), (130, 257, 272, 1 << 25, 1 << 24, 1 << 25),  # few rows, tiles
+    (1100, 1030, 256, (1 << 22) - 16, (1 << 22) - 16, 1 << 21),  # loads straight to shared memory
+    (100, 70, 77, 1 << 25, (1 << 26) + 3, 1 << 25)])
+def test_product_of_far_rows(dtype, M, N, K, lda, ldw, ldo):
+    g = gen(M + N + K)
+    a, w = (torch.randint(-128, 128, s, generator=g).to(torch.int8) for s in ((M, K), (N, K)))
+    sa, sw = torch.rand(M, generator=g) + 0.1, torch.rand(N, generator=g) + 0.1
+    out = far_rows(torch.full((M, N), float("nan"), dtype=dtype), ldo)
+    ws = torch.empty(bd.gemm_i8_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda").fill_(255)
+    bd.gemm_i8(far_rows(a, lda), sa.cuda(), far_rows(w, ldw), sw.cuda(), out, ws)
+    # as in test_product: an exact sum and roundings of 2^-24
+    ref = (a.double() @ w.double().t()) * (sa.double()[:, None] * sw.double())
+    err = (out.double().cpu() - ref).abs()
+    assert torch.isfinite(err).all()
+    assert (err <= (4 * 2.0 ** -24 + (2.0 ** -8 if dtype == BF else 2.0 ** -24)) * ref.abs() + 1e-30).all(), err.max()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("D", [16, 21])
+def test_conv_of_far_steps(dtype, D):
+    """Time-major slices of rows of 2^20 elements: steps up to 5 GB apart."""
+    g = gen(D)
+    B, T, W = 3, 1300, 4
+    x, dy, w, b = (rnd(g, *s, dtype=dtype) for s in ((B, T, D), (B, T, D), (D, W), (D,)))
+    n = torch.tensor([T, 0, T - 200], dtype=torch.int32)
+    rows = torch.empty(T, 1 << 20, dtype=dtype, device="cuda")
+
+    def far(t, at):
+        v = rows[:, at:at + B * D].unflatten(1, (B, D)).transpose(0, 1)
+        v.copy_(t)
+        return v
+
+    xc, gy = far(cut(x, n), 0), far(cut(dy, n), 128)
+    y, dx = (far(torch.full((B, T, D), float("nan")), at) for at in (256, 512))
+    bd.conv(xc, w.cuda(), b.cuda(), y, lengths=n.cuda())
+    near(y, R.conv(x, w, b, None, n)[0], TOL, "y")
+    dw, db = nan(D, W), nan(D)
+    ws = torch.empty(bd.conv_workspace_bytes(dtype, B, T, D, W), dtype=torch.uint8, device="cuda").fill_(255)
+    bd.conv_adjoint(xc, w.cuda(), b.cuda(), gy, dx, dw, db, ws, lengths=n.cuda())
+    r = R.conv_grads(x, w, dy, b, None, None, n)
+    for k, v, tol in (("dx", dx, TOL), ("dw", dw, SUM_TOL), ("dbias", db, SUM_TOL)):
+        near(v, r[k], tol, k)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_steps_on_large_pools(dtype):
+    """State pools of more than 2^32 bytes: sequences whose rows lie at their end."""
+    g = gen(31)
+    B, ch, N, W = 4, 256, 64, 4
+    pool = 70000  # scan: 4.6 GB
+    slots = torch.tensor([pool - 1, 0, 35001, pool - 2], dtype=torch.int32)
+    p = scan_problem(g, dtype, B, 1, ch, N, 1, True)
+    dev = {k: v.cuda() for k, v in p.items()}
+    st = rnd(g, B, ch, N)
+    state, y = torch.zeros(pool, ch, N, device="cuda"), nan(B, ch, dtype=dtype)
+    state[slots.long().cuda()] = st.cuda()
+    bd.ssm_step(dev["u"][:, 0], dev["dt"][:, 0], dev["A"], dev["Bm"][:, 0], dev["Cm"][:, 0], state, y, D=dev["D"],
+                z=dev["z"][:, 0], dt_bias=dev["dt_bias"], slots=slots.cuda())
+    ry, rh = R.scan(**p, h0=st)
+    near(y, ry[:, 0], TOL, "y")
+    near(state[slots.long().cuda()], rh, TOL, "state")
+    assert int((state[1:35001] != 0).sum()) == 0 and int((state[35002:pool - 2] != 0).sum()) == 0
+    del state
+    ch = 8192
+    pool = (1 << 32) // ((W - 1) * ch * (2 if dtype == BF else 4)) + 3
+    slots = torch.tensor([pool - 1, 0, pool // 2, pool - 2], dtype=torch.int32)
+    x, w, b, st = (rnd(g, *s, dtype=dtype) for s in ((B, ch), (ch, W), (ch,), (B, W - 1, ch)))
+    state, y = torch.zeros(pool, W - 1, ch, dtype=dtype, device="cuda"), nan(B, ch, dtype=dtype)
+    state[slots.long().cuda()] = st.cuda()
+    bd.conv_step(x.cuda(), w.cuda(), b.cuda(), state, y, slots=slots.cuda())
+    ry, rs = R.conv(x[:, None], w, b, st)
+    near(y, ry[:, 0], TOL, "y")
+    near(state[slots.long().cuda()], rs, 0, "state")
+    assert int((state[1:pool // 2] != 0).sum()) == 0
