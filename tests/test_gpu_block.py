@@ -1001,3 +1001,16 @@ def test_steps_on_large_pools(dtype):
     near(y, ry[:, 0], TOL, "y")
     near(state[slots.long().cuda()], rs, 0, "state")
     assert int((state[1:pool // 2] != 0).sum()) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("rows,n", [(7, 512), (5, 77), (2, 20000)])
+def test_norm_gradient_in_place(dtype, rows, n):
+    """dx over the gradient that arrives at the sum: the same bits as apart from it."""
+    g = gen(rows + n)
+    s, dy, ds, w = (rnd(g, *k, dtype=dtype).cuda() for k in ((rows, n),) * 3 + ((n,),))
+    ws = torch.empty(bd.rmsnorm_workspace_bytes(dtype, rows, n), dtype=torch.uint8, device="cuda").fill_(255)
+    dx, dw, dw2, same = nan(rows, n, dtype=dtype), nan(n), nan(n), ds.clone()
+    bd.rmsnorm_adjoint(s, w, dy, dx, dw, ws, dsum=ds)
+    bd.rmsnorm_adjoint(s, w, dy, same, dw2, ws, dsum=same)
+    assert torch.isfinite(dx).all() and torch.equal(same, dx) and torch.equal(dw2, dw)
