@@ -310,6 +310,7 @@ int pararnn_lsim(int B, int T, int nx, int m, int p, const float *A, const float
  * lies at p[b * sb + t * st + c] (strides in elements, channels adjacent), so
  * a slice of a wider projection is read in place.  Storage is fp32 or bf16;
  * arithmetic, states and sums are fp32 or wider and round to storage once.
+ * Outputs overlap no input and no other output, except where it is said.
  *
  * Ragged batches.  `lengths` (int32 device array [B], may be NULL) holds each
  * sequence's number of steps, taken within 0..T.  Steps past it are not read
@@ -408,9 +409,10 @@ int pararnn_ssm_step(const pr_ssm_problem *p, const pr_ssm_inputs *in, const pr_
  * Root-mean-square norm with the residual's addition, per row of n:
  *   s = x + r, rounded to storage (the stream that goes on is what is normed)
  *   y = s / sqrt(mean(s^2) + eps) * w
- * in the storage dtype (y) or in 8 bits (q, scale): scale = max|y| / 127,
- * q = y / scale to the nearest, ties to even; a row of zeros has scale 0, and
- * one with an infinity or a NaN has that as its scale and q = 0.
+ * in the storage dtype (y) or in 8 bits (q, scale): scale = max|y| / 127 (as a
+ * product with 1/127), q = y / scale to the nearest, ties to even; a row of
+ * zeros has scale 0, and one with an infinity or a NaN has that as its scale and
+ * q = 0.  Squares are summed in fp32.  s may be x or r.
  * Exactly one of y and q is given.  x, r, s, y, q: [rows, n] with row strides
  * (in elements); r NULL: s = x; s (sum_out) NULL: not written.  w: [n] in the
  * storage dtype or NULL (= 1); q int8, scale [rows] fp32.
@@ -428,7 +430,7 @@ typedef struct {
 int pararnn_rmsnorm(const pr_norm_problem *p, const pr_rows *x, const pr_rows *r, const void *w, const pr_rows *sum_out,
                     const pr_rows *y, const pr_rows *q, float *scale, void *stream);
 /* Gradient of sum <dy, y> + sum <dsum, s> with respect to s (the gradient of x
- * and of r) and to w (fp32 [n]); dsum, dx and dw may be NULL.               */
+ * and of r) and to w (fp32 [n]); dsum, dx and dw may be NULL.  dx may be dsum. */
 size_t pararnn_rmsnorm_workspace_bytes(const pr_norm_problem *p);
 int pararnn_rmsnorm_adjoint(const pr_norm_problem *p, const pr_rows *s, const void *w, const pr_rows *dy,
                             const pr_rows *dsum, const pr_rows *dx, float *dw, void *workspace, size_t ws_bytes,
@@ -438,7 +440,7 @@ int pararnn_quant_rows(const pr_norm_problem *p, const pr_rows *x, const pr_rows
 
 /*
  * Product of 8-bit integers with a scale for each row of a (token) and of w
- * (output channel): out[m][n] = (sum_k a[m][k] w[n][k]) sa[m] sw[n] + bias[n].
+ * (output channel): out[m][n] = (sum_k a[m][k] w[n][k]) (sa[m] sw[n]) + bias[n].
  * The sum is exact in 32-bit integers (K < 131072).  a [M, K], w [N, K] int8
  * with row strides (of at least a row's length; of a single row they are not
  * looked at); sa [M], sw [N] fp32; out [M, N] and bias [N] (or NULL) in

@@ -3,10 +3,11 @@
 // Bound by memory: x is read and y written once.  A thread takes V adjacent
 // channels (16 bytes where alignment allows) through a run of steps and keeps
 // the last W - 1 inputs in registers, so a run re-reads only W - 1 steps.
-// Measured (bf16, 8 x 4096 x 2048, 4 taps): 56 us, 4.8 TB/s; the adjoint 89 us,
-// 4.5 TB/s, with four channels a lane (eight, and half the wavefronts: 116 to
-// 110 us before the runs' own loop); its weights' sums 5 us; a step of 48
-// sequences 4 us, a launch.
+// Measured (8 x 4096 x 2048, 4 taps; each kernel in calls one after another, and
+// after 1 GiB of other writes): bf16 57 and 82 us, 4.7 and 3.3 TB/s, the adjoint
+// 89 and 92 us, 4.5 TB/s, with four channels a lane (eight, and half the
+// wavefronts: 116 to 110 us before the runs' own loop); fp32 94 and 128, the
+// adjoint 178 us; its weights' sums 5 us; a step of 48 sequences 4 us, a launch.
 #include <type_traits>
 
 #include "pararnn.h"

@@ -8,10 +8,13 @@
 // straight into the operand registers of v_mfma_i32_16x16x64_i8, the rows of
 // a (from cache) likewise, and the wavefronts' sums meet in shared memory.
 // More rows: tiles staged through shared memory, v_mfma_i32_32x32x32_i8.
-// Measured (to bf16): 16 x 4096 x 2048 5 us on the device, 64 x 4096 x 4096 14
-// us (20 us by tiles); 8192 cubed 446 us, 2.5 POP/s; 16384 x 8192 x 2048 348 us
-// (the library's product to 32-bit integers 333 to 350 us), 360 with 128 tiles,
-// 409 staged through registers.
+// Measured (to bf16, calls one after another on the same operands, which the
+// caches hold in part; in brackets after 1 GiB of other writes): 16 x 4096 x 2048
+// 5 us (7.5; by tiles 10), 64 x 4096 x 4096 13 us (19; by tiles 13 as well);
+// 8192 cubed 439 to 485 us on three machines, 2.3 to 2.5 POP/s; 16384 x 8192 x
+// 2048 300 to 342 us (the library's product to 32-bit integers 291), and where it
+// took 312, 359 with 128 tiles and 425 staged through registers; 5000 x 1111 x
+// 1111, of any alignment, 27 us (34).
 #include "direct_rows.h"
 #include "pararnn.h"
 #include "ssm.h"
@@ -403,7 +406,7 @@ __global__ void k_gemm8_join(Gemm8Args g) {
 }
 
 // Edge of the block tile: 256 where its tiles fill the CUs, else 128 (4096
-// cubed, 256 tiles: 68 us, 79 with 128; 1024 x 4096 x 4096, 64 tiles: 45 us, 31
+// cubed, 256 tiles: 73 us, 85 with 128; 1024 x 4096 x 4096, 64 tiles: 43 us, 30
 // with 128).
 static int gemm8_tile(int M, int N) {
   return (long long)((M + 255) / 256) * ((N + 255) / 256) >= 192 ? 256 : 128;
@@ -436,8 +439,8 @@ hipError_t gemm8_go(const Gemm8Args &g, hipStream_t s) {
 }
 
 // Splits of K where the tiles alone leave CUs idle: enough blocks for one
-// round of the device, at least four K steps each (128 x 4096 x 4096: 19.0 us,
-// 20.6 unsplit; 301 x 1030 x 1000: 18.0 and 19.0).
+// round of the device, at least four K steps each (128 x 4096 x 4096: 18.0 us,
+// 20.2 unsplit; 301 x 1030 x 1000: 17.0 and 18.6).
 static int gemm8_splits(int M, int N, int K, int *kper) {
   const long long tiles = (long long)((M + 127) / 128) * ((N + 127) / 128);
   const int steps = (K + TB - 1) / TB;

@@ -5,11 +5,15 @@
 // Bound by memory.  A row's values stay in registers between the sum of
 // squares, the maximum and the output, so every array is read or written
 // once: one wavefront holds a row of up to 64 x 4 vectors, a block one of up
-// to 256 x 8; longer rows are read again (from cache) for each pass.
-// Measured (bf16, rows of 2048): 16384 rows with the residual 43 us, 6.2 TB/s
-// with what the last-level cache holds; 8192 rows to 8 bits 21 us; the adjoint
-// of 16384 rows 45 us and 7 us for the weight's sums; 16384 rows to 8 bits
-// without a norm 33 us, 3.0 TB/s from memory.
+// to 256 x 8; longer rows are read again (from cache) for each pass.  Squares are
+// summed in fp32: a row whose sum overflows (values of 1e18 and more) gives y = 0.
+// Measured (rows of 2048; calls one after another, whose inputs the last-level
+// cache holds in part, and after 1 GiB of other writes): bf16 16384 rows with
+// the residual 42 and 75 us, 8192 rows to 8 bits 20 and 36, the adjoint of 16384
+// rows 45 and 48 and 7 us for the weight's sums, 16384 rows to 8 bits without a
+// norm 17 and 31 (a wavefront has one row's loads in flight, then none while it
+// reduces and stores); fp32 93 and 119, 32 and 64, 77 and 113, 24 and 52.  2048
+// rows of 20000 in bf16, element by element: 104 and 136 us.
 #include "pararnn.h"
 #include "ssm.h"
 #include "vec.h"

@@ -245,11 +245,16 @@ struct SsmPlan {
 // Time segments for `blocks` blocks over T steps: a block for each CU, at
 // least four tiles each; a segment's extent in any array below 2^31 bytes (16
 // steps are).
-// (1 x 32768 x 256 in fp32: 98 us with 64 segments, 294 with 16, 2647 with one;
-// training on 4 x 2048 x 2048: 433 us with two, 646 with one.)
+// (1 x 32768 x 256 in fp32: 90 us with 64 segments, 289 with 16, 2613 with one;
+// training on 4 x 2048 x 2048, 128 blocks: 411 us with two, 643 with one.)
+// Between 129 and 255 blocks two segments take as many rounds of the device as
+// one of twice the length, and their preparation is lost: 8 x 2048 steps of 1536
+// channels, 192 blocks, 203 us, 171 unsplit; training 750 and 652.  Below, 5 of
+// those sequences, 120 blocks: with three segments 146 and 522 us, with two 123
+// and 411, with one 171 and 644.
 // Two segments leave half of the CUs idle in the pass that prepares the split,
 // which one segment of the two takes part in: it takes that one in two pieces
-// (the same training: 433 us, 476 in one piece).
+// (training on 4 x 2048 x 2048: 411 us, 470 in one piece).
 void split_time(long long blocks, int T, long long max_tile_bytes, int *S, int *seglen, int *R) {
   const long long tiles = (T + SSM_TL - 1) / SSM_TL;
   long long s = (256 + blocks - 1) / blocks;

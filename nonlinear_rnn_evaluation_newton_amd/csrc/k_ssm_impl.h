@@ -16,10 +16,12 @@
 // Bound by vector arithmetic: per (step, channel, state) a product, an
 // exponential (two issue slots), a product and two fused multiply-adds; what
 // the states of a (step, channel) share is nearly as much again at 16 states.
-// Measured (bf16, 2048 channels, 16 states): 8 x 4096 steps 376 us, 2.9e12
-// (step, channel, state) a second, 82% of the issue slots of its instructions;
-// with unaligned arrays, element by element, 595 us.  The adjoint of 4 x 2048
-// steps 255 us, with two preparing passes of 35 and 40 us.
+// Measured (bf16, 2048 channels, 16 states; calls one after another): 8 x 4096
+// steps 343 us, 3.1e12 (step, channel, state) a second, vector instructions
+// being issued in 82% of the cycles; with unaligned arrays, element by element,
+// 587 us; 32 states 509 us, 64 states 882 us.  The adjoint of 4 x 2048 steps 236
+// us (85% of the cycles), with two preparing passes of 32 and 37 us; of more
+// states 340 us for each 16.
 #pragma once
 
 #include <utility>

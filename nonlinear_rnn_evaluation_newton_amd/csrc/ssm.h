@@ -41,7 +41,7 @@ struct SsmArgs {
 // States per lane and wavefronts per channel of the scan kernels for N states
 // (four lanes of a wavefront share a channel).  Sixteen states on one wavefront
 // of four each would take fewer instructions, but leave one wavefront a SIMD:
-// 368 against 379 us where the blocks fill the device (8 x 4096 x 2048), and
+// 366 against 342 us also where the blocks fill the device (8 x 4096 x 2048), and
 // the adjoint has registers for two states a lane only.
 struct SsmGeom {
   int ns, ws;
