@@ -1014,3 +1014,32 @@ def test_norm_gradient_in_place(dtype, rows, n):
     bd.rmsnorm_adjoint(s, w, dy, dx, dw, ws, dsum=ds)
     bd.rmsnorm_adjoint(s, w, dy, same, dw2, ws, dsum=same)
     assert torch.isfinite(dx).all() and torch.equal(same, dx) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("rows,n", [(4200, 320), (4200, 800), (4100, 1608), (1100, 2400), (1100, 5600), (1100, 12008)])
+def test_norm_of_part_rows(dtype, rows, n):
+    """Rows that end inside the last vectors of every number of threads and
+    vectors a row can have, more of them than the adjoint has blocks."""
+    g = gen(rows + n)
+    x, r, dy, ds, w = (rnd(g, *s, dtype=dtype) for s in ((rows, n),) * 4 + ((n,),))
+    s = (x.float() + r.float()).to(dtype)
+    so, y = nan(rows, n, dtype=dtype), nan(rows, n, dtype=dtype)
+    bd.rmsnorm(x.cuda(), w.cuda(), residual=r.cuda(), sum_out=so, y=y)
+    assert torch.equal(so.cpu(), s)
+    ref = R.norm(s, w, 1e-5)
+    near(y, ref, TOL, "y")
+    for quant_of, call in ((ref, lambda: bd.rmsnorm(x.cuda(), w.cuda(), residual=r.cuda(), q=q, scale=scale)),
+                           (s.double(), lambda: bd.quant_rows(s.cuda(), q, scale))):
+        q, scale = torch.full((rows, n), 99, dtype=torch.int8, device="cuda"), nan(rows)
+        call()
+        rq, rs = R.quant(quant_of)
+        near(scale, rs, 1e-6, "scale")
+        off = (q.double().cpu() - rq).abs()  # (on the other side of a tie, as in test_norm)
+        assert off.max() <= 1 and float((off > 0).double().mean()) <= 1e-3
+    ws = torch.empty(bd.rmsnorm_workspace_bytes(dtype, rows, n), dtype=torch.uint8, device="cuda").fill_(255)
+    dx, dw = nan(rows, n, dtype=dtype), nan(n)
+    bd.rmsnorm_adjoint(s.cuda(), w.cuda(), dy.cuda(), dx, dw, ws, dsum=ds.cuda())
+    rx, rw = R.norm_grads(s, w, dy, 1e-5, ds)
+    near(dx, rx, TOL, "dx")
+    near(dw, rw, SUM_TOL, "dw")
