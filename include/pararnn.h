@@ -451,6 +451,121 @@ int pararnn_gemm_i8(int dtype, int M, int N, int K, const signed char *a, long l
                     const signed char *w, long long ldw, const float *sw, const void *bias, void *out, long long ldo,
                     void *workspace, size_t ws_bytes, void *stream);
 
+/* ---- operators of a gated recurrent block --------------------------------- */
+/*
+ * Token mixers whose state is one real number per channel with a decay that
+ * the token gates, the norms around such a block, and projections on 4-bit
+ * weights.  What is said above of streams, strides, storage, ragged batches
+ * and pools holds for them too; arrays may have any alignment of an element.
+ */
+
+/*
+ * Gated linear recurrence, per channel d:
+ *   r_t = sigm(rg_t + r_bias), i_t = sigm(ig_t + i_bias)
+ *   a_t = exp(-decay r_t)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t,  y_t = h_t
+ * decay >= 0 and finite; where 1 - a_t^2 is 0 (a decay of 0, a closed gate)
+ * the input's term and its gradients are 0.
+ *   x, r, i [B, T, D] (r, i: the gates rg, ig before the sigmoid), y   storage dtype
+ *   decay [D], r_bias [D] or NULL, i_bias [D] or NULL                  fp32
+ *   h0 [B, D] or NULL (= 0)                                            fp32
+ *   h_last  [B, D] or NULL: the state after the last step (may be h0)
+ *   states  NULL, or [B, ceil(T / 128), D] fp32: the state that enters every
+ *           128th step, for the adjoint (not written from a sequence's length on)
+ */
+#define PR_GATED_STATE_STEPS 128
+typedef struct {
+  int dtype; /* PR_F32 or PR_BF16 */
+  int B, T, D;
+} pr_gated_problem;
+typedef struct {
+  pr_view x, r, i;
+  const float *decay, *r_bias, *i_bias, *h0;
+  const int *lengths;
+} pr_gated_inputs;
+/* Gradients; any pointer may be NULL. */
+typedef struct {
+  pr_view x, r, i;
+  float *decay, *r_bias, *i_bias, *h0;
+} pr_gated_grads;
+size_t pararnn_gated_workspace_bytes(const pr_gated_problem *p, int with_adjoint);
+int pararnn_gated_scan(const pr_gated_problem *p, const pr_gated_inputs *in, const pr_view *y, float *h_last,
+                       float *states, void *workspace, size_t ws_bytes, void *stream);
+/* Gradients of sum <dy, y> + sum <dh_last, h_last> (dh_last may be NULL) from
+ * the states that the forward call saved on the same inputs (h0 is not read). */
+int pararnn_gated_adjoint(const pr_gated_problem *p, const pr_gated_inputs *in, const float *states, const pr_view *dy,
+                          const float *dh_last, const pr_gated_grads *grads, void *workspace, size_t ws_bytes,
+                          void *stream);
+/* One token for each of B sequences (p->T, h0 and lengths are not used, T may
+ * be 0; row strides sb): state [nslots, D] fp32 is updated in place.        */
+int pararnn_gated_step(const pr_gated_problem *p, const pr_gated_inputs *in, const pr_view *y, float *state, int nslots,
+                       const int *slots, void *stream);
+
+/*
+ * The norms around a block, joined with its gate and the residual's scale, per
+ * row of n:
+ *   u = x / sqrt(mean(x^2) + eps) * w * scale * act(z)
+ *   t = residual + u, rounded to storage (what goes on is what is normed)
+ *   y = t / sqrt(mean(t^2) + eps) * w_next
+ * act(z) = z sigm(z) (PR_GATE_SILU), sigm(z) (PR_GATE_SIGMOID), or 1 without z.
+ * Squares are summed in fp32.  x, z, residual, t, y: [rows, n] with row
+ * strides; z, residual and y may be NULL (no gate, t = u, no norm after).  w,
+ * scale, w_next: [n] in the storage dtype or NULL (= 1).  t may be the residual.
+ */
+#define PR_GATE_SILU 1
+#define PR_GATE_SIGMOID 2
+typedef struct {
+  int dtype; /* PR_F32 or PR_BF16 */
+  int n;
+  long long rows;
+  float eps; /* >= 0 */
+  int gate;  /* PR_GATE_* (not looked at without z) */
+} pr_block_norm_problem;
+int pararnn_block_norm(const pr_block_norm_problem *p, const pr_rows *x, const pr_rows *z, const pr_rows *residual,
+                       const void *w, const void *scale, const void *w_next, const pr_rows *t, const pr_rows *y,
+                       void *stream);
+/*
+ * Gradients of sum <dy, y> + sum <dt, t> at the inputs x and z and the stored t
+ * (t is read only where dy is given; at least one of dy and dt is).  dx, dz,
+ * dres [rows, n] and dw, dscale, dw_next (fp32 [n]) may be NULL; dz needs z,
+ * dw_next needs dy.  dres may be dt.
+ */
+typedef struct {
+  pr_rows x, z, res;
+  float *w, *scale, *w_next;
+} pr_block_norm_grads;
+size_t pararnn_block_norm_workspace_bytes(const pr_block_norm_problem *p);
+int pararnn_block_norm_adjoint(const pr_block_norm_problem *p, const pr_rows *x, const pr_rows *z, const void *w,
+                               const void *scale, const void *w_next, const pr_rows *t, const pr_rows *dt,
+                               const pr_rows *dy, const pr_block_norm_grads *grads, void *workspace, size_t ws_bytes,
+                               void *stream);
+
+/*
+ * Weights in 4 bits with a scale, and where wanted a zero point, for each group
+ * of `group` columns of a row (a multiple of 32; the last group of a row may be
+ * shorter): w[n][k] = (q[n][k] - zero[n][k / group]) scale[n][k / group].
+ *   q      [N, ceil(K / 2)] bytes with row stride ldq: column k in the low four
+ *          bits of byte k / 2 where k is even, in the high ones where it is odd
+ *   scale, zero [N, ceil(K / group)] in the storage dtype; zero NULL (= 8)
+ */
+/* out[m][n] = sum_k x[m][k] w[n][k] + bias[n] for few rows x (decoding
+ * batches; any number is computed, 64 at a time).  x [M, K], out [M, N] with row
+ * strides, bias [N] or NULL, all in `dtype`.  Products are exact, sums in fp32. */
+int pararnn_gemm_w4(int dtype, int M, int N, int K, int group, const void *x, long long ldx, const unsigned char *q,
+                    long long ldq, const void *scale, const void *zero, const void *bias, void *out, long long ldo,
+                    void *stream);
+/* The 4-bit form of w [N, K] (row stride ldw).  Without zero: scale = max|w| / 7
+ * (as a product with 1/7, rounded to storage), q = w / scale to the nearest,
+ * ties to even, plus 8; with it: scale = (hi - lo) / 15 for lo = min(w, 0), hi =
+ * max(w, 0), zero = -lo / scale, to the nearest and held to 0..15.  q is held to
+ * 0..15.  A group of zeros has scale 0; one with an infinity or a NaN has that
+ * as its scale, and q is its zero (8 where not asked for).                   */
+int pararnn_quant_w4(int dtype, int N, int K, int group, const void *w, long long ldw, unsigned char *q, long long ldq,
+                     void *scale, void *zero, void *stream);
+/* The values that q stands for, w [N, K] with row stride ldw in `dtype`. */
+int pararnn_dequant_w4(int dtype, int N, int K, int group, const unsigned char *q, long long ldq, const void *scale,
+                       const void *zero, void *w, long long ldw, void *stream);
+
 /*
  * Kernel timing for profiling and benchmarks (per calling thread).
  * pararnn_trace(1) clears the counters and starts bracketing, with HIP events

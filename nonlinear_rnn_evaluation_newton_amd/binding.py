@@ -27,9 +27,14 @@ EXPORTS = ["pararnn_workspace_bytes", "pararnn_solve", "pararnn_adjoint", "parar
            "pararnn_solve_elk", "pararnn_affine_scan_noalloc", "pararnn_conv", "pararnn_conv_workspace_bytes",
            "pararnn_conv_adjoint", "pararnn_conv_step", "pararnn_ssm_workspace_bytes", "pararnn_ssm_scan",
            "pararnn_ssm_adjoint", "pararnn_ssm_step", "pararnn_rmsnorm", "pararnn_rmsnorm_workspace_bytes",
-           "pararnn_rmsnorm_adjoint", "pararnn_quant_rows", "pararnn_gemm_i8_workspace_bytes", "pararnn_gemm_i8"]
+           "pararnn_rmsnorm_adjoint", "pararnn_quant_rows", "pararnn_gemm_i8_workspace_bytes", "pararnn_gemm_i8",
+           "pararnn_gated_workspace_bytes", "pararnn_gated_scan", "pararnn_gated_adjoint", "pararnn_gated_step",
+           "pararnn_block_norm", "pararnn_block_norm_workspace_bytes", "pararnn_block_norm_adjoint", "pararnn_gemm_w4",
+           "pararnn_quant_w4", "pararnn_dequant_w4"]
 NOALLOC_SCRATCH_BYTES = 16 << 20  # PR_NOALLOC_SCRATCH_BYTES
 SSM_STATE_STEPS = 16  # PR_SSM_STATE_STEPS
+GATED_STATE_STEPS = 128  # PR_GATED_STATE_STEPS
+GATES = {"silu": 1, "sigmoid": 2}  # PR_GATE_*
 
 
 class Problem(C.Structure):
@@ -80,6 +85,36 @@ class _SsmInputsFlat(C.Structure):
 class SsmGrads(C.Structure):
     _fields_ = [("u", View), ("dt", View), ("z", View), ("B", View), ("C", View), ("A", C.c_void_p),
                 ("D", C.c_void_p), ("dt_bias", C.c_void_p), ("h0", C.c_void_p)]
+
+
+class GatedProblem(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("B", C.c_int), ("T", C.c_int), ("D", C.c_int)]
+
+
+class GatedInputs(C.Structure):
+    _fields_ = [("x", View), ("r", View), ("i", View), ("decay", C.c_void_p), ("r_bias", C.c_void_p),
+                ("i_bias", C.c_void_p), ("h0", C.c_void_p), ("lengths", C.c_void_p)]
+
+
+class _GatedInputsFlat(C.Structure):
+    """The same layout without nested structures, which take longer to fill."""
+    _fields_ = [(a + "_" + f, c) for a in ("x", "r", "i")
+                for f, c in (("p", C.c_void_p), ("sb", C.c_longlong), ("st", C.c_longlong))] + [
+        (a, C.c_void_p) for a in ("decay", "r_bias", "i_bias", "h0", "lengths")]
+
+
+class GatedGrads(C.Structure):
+    _fields_ = [("x", View), ("r", View), ("i", View), ("decay", C.c_void_p), ("r_bias", C.c_void_p),
+                ("i_bias", C.c_void_p), ("h0", C.c_void_p)]
+
+
+class BlockNormProblem(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("n", C.c_int), ("rows", C.c_longlong), ("eps", C.c_float), ("gate", C.c_int)]
+
+
+class BlockNormGrads(C.Structure):
+    _fields_ = [("x", Rows), ("z", Rows), ("res", Rows), ("w", C.c_void_p), ("scale", C.c_void_p),
+                ("w_next", C.c_void_p)]
 
 
 class NormProblem(C.Structure):
@@ -151,7 +186,17 @@ def lib():
                 ("rmsnorm_adjoint", I, [P, P, P, P, P, P, P, P, S, P]),
                 ("quant_rows", I, [P, P, P, P, P]),
                 ("gemm_i8_workspace_bytes", S, [I, I, I]),
-                ("gemm_i8", I, [I, I, I, I, P, LL, P, P, LL, P, P, P, LL, P, S, P])):
+                ("gemm_i8", I, [I, I, I, I, P, LL, P, P, LL, P, P, P, LL, P, S, P]),
+                ("gated_workspace_bytes", S, [P, I]),
+                ("gated_scan", I, [P, P, P, P, P, P, S, P]),
+                ("gated_adjoint", I, [P, P, P, P, P, P, P, S, P]),
+                ("gated_step", I, [P, P, P, P, I, P, P]),
+                ("block_norm", I, [P, P, P, P, P, P, P, P, P, P]),
+                ("block_norm_workspace_bytes", S, [P]),
+                ("block_norm_adjoint", I, [P, P, P, P, P, P, P, P, P, P, P, S, P]),
+                ("gemm_w4", I, [I, I, I, I, I, P, LL, P, LL, P, P, P, P, LL, P]),
+                ("quant_w4", I, [I, I, I, I, P, LL, P, LL, P, P, P]),
+                ("dequant_w4", I, [I, I, I, I, P, LL, P, P, P, LL, P])):
             f = getattr(L, "pararnn_" + name)
             f.restype, f.argtypes = res, args
         _several_gpus = torch.cuda.device_count() > 1
@@ -595,6 +640,168 @@ def gemm_i8(a, a_scale, w, w_scale, out, workspace, bias=None, check: bool = Tru
         _dense(n, "w_scale", w_scale, (N,), f32), _dense(n, "bias", bias, (N,), dt),
         _need(n, "out", out, (M, N), dt), out.stride(0), *_ws(n, workspace), _stream_of(a))
     return _done(st, "pararnn_gemm_i8", check)
+
+
+# ---------------------------------------------------------------------------
+# operators of a gated recurrent block
+# ---------------------------------------------------------------------------
+def gated_workspace_bytes(dtype, B: int, T: int, D: int, with_adjoint: bool = True) -> int:
+    return lib().pararnn_gated_workspace_bytes(C.byref(GatedProblem(_dtype_code(dtype, "gated"), B, T, D)),
+                                               int(with_adjoint))
+
+
+def gated_states_shape(B: int, T: int, D: int):
+    """Shape of the fp32 states that gated_scan saves for gated_scan_adjoint."""
+    return B, -(-T // GATED_STATE_STEPS), D
+
+
+def _gated(where, axes, x, r, i, decay, r_bias, i_bias, h0, lengths):
+    import torch
+    lib()  # before the tensors' checks, which depend on the GPUs there are
+    st, f32, shape = x.dtype, torch.float32, x.shape
+    if len(shape) != axes:
+        raise ValueError(f"{where}: x must be [B, {'T, ' if axes == 3 else ''}channels], got {tuple(shape)}")
+    B, D = shape[0], shape[-1]
+    pb = GatedProblem(_dtype_code(st, where), B, shape[1] if axes == 3 else 1, D)
+    return pb, _GatedInputsFlat(
+        *_flat(where, "x", x, shape, st), *_flat(where, "r", r, shape, st), *_flat(where, "i", i, shape, st),
+        _dense(where, "decay", decay, (D,), f32), _dense(where, "r_bias", r_bias, (D,), f32),
+        _dense(where, "i_bias", i_bias, (D,), f32), _dense(where, "h0", h0, (B, D), f32),
+        _dense(where, "lengths", lengths, (B,), torch.int32))
+
+
+def gated_scan(x, r, i, decay, y, workspace, r_bias=None, i_bias=None, h0=None, h_last=None, states=None, lengths=None,
+               check: bool = True) -> int:
+    """pararnn_gated_scan: the gated recurrence of x [B, T, channels] with gates r and i into y."""
+    import torch
+    n, f32 = "gated_scan", torch.float32
+    pb, inp = _gated(n, 3, x, r, i, decay, r_bias, i_bias, h0, lengths)
+    st = lib().pararnn_gated_scan(
+        C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, x.shape, x.dtype)),
+        _dense(n, "h_last", h_last, (pb.B, pb.D), f32),
+        _dense(n, "states", states, gated_states_shape(pb.B, pb.T, pb.D), f32), *_ws(n, workspace), _stream_of(x))
+    return _done(st, "pararnn_gated_scan", check)
+
+
+def gated_scan_adjoint(x, r, i, decay, states, dy, workspace, r_bias=None, i_bias=None, lengths=None, dh_last=None,
+                       dx=None, dr=None, di=None, ddecay=None, dr_bias=None, di_bias=None, dh0=None,
+                       check: bool = True) -> int:
+    """pararnn_gated_adjoint: gradients of gated_scan from the states it saved; any output may be None."""
+    import torch
+    n, f32, shape, t = "gated_scan_adjoint", torch.float32, x.shape, x.dtype
+    pb, inp = _gated(n, 3, x, r, i, decay, r_bias, i_bias, None, lengths)
+    B, D = pb.B, pb.D
+    gr = GatedGrads(_view(n, "dx", dx, shape, t), _view(n, "dr", dr, shape, t), _view(n, "di", di, shape, t),
+                    _dense(n, "ddecay", ddecay, (D,), f32), _dense(n, "dr_bias", dr_bias, (D,), f32),
+                    _dense(n, "di_bias", di_bias, (D,), f32), _dense(n, "dh0", dh0, (B, D), f32))
+    st = lib().pararnn_gated_adjoint(
+        C.byref(pb), C.byref(inp), _dense(n, "states", states, gated_states_shape(B, pb.T, D), f32),
+        C.byref(_view(n, "dy", dy, shape, t)), _dense(n, "dh_last", dh_last, (B, D), f32), C.byref(gr),
+        *_ws(n, workspace), _stream_of(x))
+    return _done(st, "pararnn_gated_adjoint", check)
+
+
+def gated_step(x, r, i, decay, state, y, r_bias=None, i_bias=None, slots=None, check: bool = True) -> int:
+    """pararnn_gated_step: one token x [B, channels] per sequence on the fp32 pool state [slots, channels]."""
+    import torch
+    n = "gated_step"
+    pb, inp = _gated(n, 2, x, r, i, decay, r_bias, i_bias, None, None)
+    pool = state.shape[0]
+    st = lib().pararnn_gated_step(C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, x.shape, x.dtype)),
+                                  _dense(n, "state", state, (pool, pb.D), torch.float32), pool,
+                                  _dense(n, "slots", slots, (pb.B,), torch.int32), _stream_of(x))
+    return _done(st, "pararnn_gated_step", check)
+
+
+def _gate_code(where, z, gate):
+    if gate not in GATES:
+        raise ValueError(f"{where}: gate must be one of {sorted(GATES)}, got {gate!r}")
+    return GATES[gate] if z is not None else 0
+
+
+def block_norm(x, w, t, z=None, gate: str = "silu", scale=None, residual=None, y=None, w_next=None, eps: float = 1e-5,
+               check: bool = True) -> int:
+    """pararnn_block_norm of x [rows, n]: t = residual + norm(x) w scale act(z) and, where y is given, y = norm(t) w_next."""
+    lib()
+    shape, dt, where = x.shape, x.dtype, "block_norm"
+    rows, n = shape
+    pb = BlockNormProblem(_dtype_code(dt, where), n, rows, eps, _gate_code(where, z, gate))
+    st = lib().pararnn_block_norm(
+        C.byref(pb), _rows(where, "x", x, shape, dt), _rows(where, "z", z, shape, dt),
+        _rows(where, "residual", residual, shape, dt), _dense(where, "w", w, (n,), dt),
+        _dense(where, "scale", scale, (n,), dt), _dense(where, "w_next", w_next, (n,), dt),
+        _rows(where, "t", t, shape, dt), _rows(where, "y", y, shape, dt), _stream_of(x))
+    return _done(st, "pararnn_block_norm", check)
+
+
+def block_norm_workspace_bytes(dtype, rows: int, n: int) -> int:
+    """Workspace of block_norm_adjoint for rows stored in the torch type dtype."""
+    pb = BlockNormProblem(_dtype_code(dtype, "block_norm"), n, rows, 0.0, 0)
+    return lib().pararnn_block_norm_workspace_bytes(C.byref(pb))
+
+
+def block_norm_adjoint(x, w, dx, workspace, z=None, gate: str = "silu", scale=None, w_next=None, t=None, dt=None,
+                       dy=None, dz=None, dres=None, dw=None, dscale=None, dw_next=None, eps: float = 1e-5,
+                       check: bool = True) -> int:
+    """pararnn_block_norm_adjoint: gradients of block_norm at x, z and the stored t from dt and dy; any output may be None."""
+    import torch
+    lib()
+    shape, st, where, f32 = x.shape, x.dtype, "block_norm_adjoint", torch.float32
+    rows, n = shape
+    pb = BlockNormProblem(_dtype_code(st, where), n, rows, eps, _gate_code(where, z, gate))
+
+    def out(name, v):
+        return Rows(None, 0) if v is None else Rows(_need(where, name, v, shape, st), v.stride(0))
+
+    gr = BlockNormGrads(out("dx", dx), out("dz", dz), out("dres", dres), _dense(where, "dw", dw, (n,), f32),
+                        _dense(where, "dscale", dscale, (n,), f32), _dense(where, "dw_next", dw_next, (n,), f32))
+    rc = lib().pararnn_block_norm_adjoint(
+        C.byref(pb), _rows(where, "x", x, shape, st), _rows(where, "z", z, shape, st), _dense(where, "w", w, (n,), st),
+        _dense(where, "scale", scale, (n,), st), _dense(where, "w_next", w_next, (n,), st),
+        _rows(where, "t", t, shape, st), _rows(where, "dt", dt, shape, st), _rows(where, "dy", dy, shape, st),
+        C.byref(gr), *_ws(where, workspace), _stream_of(x))
+    return _done(rc, "pararnn_block_norm_adjoint", check)
+
+
+def _w4(where, q, scale, zero, N, K, group, dt):
+    """Addresses of a 4-bit weight matrix's parts: q, its row stride, scale, zero."""
+    import torch
+    if group < 1:
+        raise ValueError(f"{where}: groups must have at least one column, got {group}")
+    shape = (N, -(-K // group))
+    return (_need(where, "q", q, (N, (K + 1) // 2), torch.uint8), q.stride(0),
+            _dense(where, "scale", scale, shape, dt), _dense(where, "zero", zero, shape, dt))
+
+
+def gemm_w4(x, q, scale, out, group: int, zero=None, bias=None, check: bool = True) -> int:
+    """pararnn_gemm_w4: out [M, N] = x [M, K] times the 4-bit weights q [N, (K + 1) / 2], plus bias."""
+    n, dt = "gemm_w4", x.dtype
+    lib()
+    (M, K), N = x.shape, q.shape[0]
+    st = lib().pararnn_gemm_w4(_dtype_code(dt, n), M, N, K, group, _need(n, "x", x, (M, K), dt), x.stride(0),
+                               *_w4(n, q, scale, zero, N, K, group, dt), _dense(n, "bias", bias, (N,), dt),
+                               _need(n, "out", out, (M, N), dt), out.stride(0), _stream_of(x))
+    return _done(st, "pararnn_gemm_w4", check)
+
+
+def quant_w4(w, q, scale, group: int, zero=None, check: bool = True) -> int:
+    """pararnn_quant_w4: w [N, K] in 4 bits, q uint8 [N, (K + 1) / 2] with scale (and zero) [N, groups]."""
+    n, dt = "quant_w4", w.dtype
+    lib()
+    N, K = w.shape
+    st = lib().pararnn_quant_w4(_dtype_code(dt, n), N, K, group, _need(n, "w", w, (N, K), dt), w.stride(0),
+                                *_w4(n, q, scale, zero, N, K, group, dt), _stream_of(w))
+    return _done(st, "pararnn_quant_w4", check)
+
+
+def dequant_w4(q, scale, w, group: int, zero=None, check: bool = True) -> int:
+    """pararnn_dequant_w4: the values w [N, K] that q stands for."""
+    n, dt = "dequant_w4", w.dtype
+    lib()
+    N, K = w.shape
+    st = lib().pararnn_dequant_w4(_dtype_code(dt, n), N, K, group, *_w4(n, q, scale, zero, N, K, group, dt),
+                                  _need(n, "w", w, (N, K), dt), w.stride(0), _stream_of(w))
+    return _done(st, "pararnn_dequant_w4", check)
 
 
 # ---------------------------------------------------------------------------

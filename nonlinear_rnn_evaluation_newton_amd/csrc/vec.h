@@ -62,4 +62,56 @@ __device__ inline void stv(T *p, const float *f) {
   *reinterpret_cast<typename Vec<T, V>::type *>(p) = r.v;
 }
 
+// The same at any alignment of an element (one access where all V are there,
+// which the hardware takes unaligned; the first n one by one where they are not).
+template <int BYTES>
+struct WordsOf;
+template <>
+struct WordsOf<32> { typedef unsigned type __attribute__((ext_vector_type(8))); };
+template <>
+struct WordsOf<16> { typedef unsigned type __attribute__((ext_vector_type(4))); };
+template <>
+struct WordsOf<8> { typedef unsigned type __attribute__((ext_vector_type(2))); };
+template <>
+struct WordsOf<4> { typedef unsigned type; };
+template <typename T, int V>
+struct __attribute__((packed, aligned(sizeof(T)))) Packed {
+  typename WordsOf<sizeof(T) * V>::type v;
+};
+template <typename T, int V>
+struct VecU {
+  union {
+    typename WordsOf<sizeof(T) * V>::type v;
+    T e[V];
+  };
+  __device__ float f(int i) const { return ldf(e, i); }
+};
+template <typename T, int V>
+__device__ inline VecU<T, V> ldu(const T *p, int n) {
+  VecU<T, V> r;
+#pragma unroll
+  for (int i = 0; i < V; i++) r.e[i] = 0;
+  if (n >= V) {
+    r.v = reinterpret_cast<const Packed<T, V> *>(p)->v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V - 1; i++)
+      if (i < n) r.e[i] = p[i];
+  }
+  return r;
+}
+template <typename T, int V>
+__device__ inline void stu(T *p, const float *f, int n) {
+  VecU<T, V> r;
+#pragma unroll
+  for (int i = 0; i < V; i++) stf(r.e, i, f[i]);
+  if (n >= V) {
+    reinterpret_cast<Packed<T, V> *>(p)->v = r.v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V - 1; i++)
+      if (i < n) p[i] = r.e[i];
+  }
+}
+
 }  // namespace pr
