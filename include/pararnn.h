@@ -460,7 +460,8 @@ int pararnn_gemm_i8(int dtype, int M, int N, int K, const signed char *a, long l
  */
 
 /*
- * Gated linear recurrence, per channel d:
+ * Gated linear recurrence, per channel d (time strides of 0 to 2^22 elements,
+ * any over the batch; D up to 2^22):
  *   r_t = sigm(rg_t + r_bias), i_t = sigm(ig_t + i_bias)
  *   a_t = exp(-decay r_t)
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t,  y_t = h_t
@@ -470,10 +471,10 @@ int pararnn_gemm_i8(int dtype, int M, int N, int K, const signed char *a, long l
  *   decay [D], r_bias [D] or NULL, i_bias [D] or NULL                  fp32
  *   h0 [B, D] or NULL (= 0)                                            fp32
  *   h_last  [B, D] or NULL: the state after the last step (may be h0)
- *   states  NULL, or [B, ceil(T / 128), D] fp32: the state that enters every
- *           128th step, for the adjoint (not written from a sequence's length on)
+ *   states  NULL, or [B, ceil(T / 64), D] fp32: the state that enters every
+ *           64th step, for the adjoint (not written from a sequence's length on)
  */
-#define PR_GATED_STATE_STEPS 128
+#define PR_GATED_STATE_STEPS 64
 typedef struct {
   int dtype; /* PR_F32 or PR_BF16 */
   int B, T, D;

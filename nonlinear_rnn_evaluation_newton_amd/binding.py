@@ -33,7 +33,7 @@ EXPORTS = ["pararnn_workspace_bytes", "pararnn_solve", "pararnn_adjoint", "parar
            "pararnn_quant_w4", "pararnn_dequant_w4"]
 NOALLOC_SCRATCH_BYTES = 16 << 20  # PR_NOALLOC_SCRATCH_BYTES
 SSM_STATE_STEPS = 16  # PR_SSM_STATE_STEPS
-GATED_STATE_STEPS = 128  # PR_GATED_STATE_STEPS
+GATED_STATE_STEPS = 64  # PR_GATED_STATE_STEPS
 GATES = {"silu": 1, "sigmoid": 2}  # PR_GATE_*
 
 

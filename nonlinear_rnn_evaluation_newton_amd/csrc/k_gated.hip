@@ -5,6 +5,8 @@
 // Adjoint, with g_t = dy_t + a_{t+1} g_{t+1}:
 //   dx = g m i, di = g m x i (1 - i), dv = g (a^2 / m i x - a h_{t-1}),
 //   dr = dv decay r (1 - r), ddecay = sum dv r
+#include <type_traits>
+
 #include "pararnn.h"
 #include "ssm.h"
 #include "vec.h"
@@ -21,14 +23,13 @@ struct GatedArgs {
   float *dh0;                // adjoint, may be null
   float *part;               // adjoint: partials of ddecay | dr_bias | di_bias, [part][3][D]
   int B, T, D;
+  int cb, tiles, tt, nst;    // columns of channels a sequence, tiles a column, steps a tile, saved states a sequence
 };
 
-constexpr int GS = 128;  // steps between two saved states
-
-// What a step's gates give: a = e^-v and 1 - a^2 for v = decay r, both gates
-// and their complements.
+// What a step's gates give: both gates, and a = e^-v and m = sqrt(1 - a^2) for
+// v = decay r (m = 0 where 1 - a^2 is no normal number).
 struct GateVals {
-  float r, r1, i, i1, a, m2;
+  float r, i, a, m;
 };
 template <typename T>
 __device__ inline float gate_exp(float x) {
@@ -38,13 +39,8 @@ __device__ inline float gate_exp(float x) {
 template <typename T>
 __device__ inline GateVals gate_vals(float rg, float ig, float decay) {
   GateVals o;
-  const float er = gate_exp<T>(-rg), ei = gate_exp<T>(-ig);
-  o.r = frcp(1.f + er);
-  o.i = frcp(1.f + ei);
-  // 1 - sigm = e sigm keeps the digits of a gate that is nearly open (where e
-  // is infinite the product is NaN, which the minimum drops)
-  o.r1 = fminf(er * o.r, 1.f);
-  o.i1 = fminf(ei * o.i, 1.f);
+  o.r = frcp(1.f + gate_exp<T>(-rg));
+  o.i = frcp(1.f + gate_exp<T>(-ig));
   const float v = decay * o.r;
   o.a = gate_exp<T>(-v);
   // 1 - e^-w for w = 2 v: the difference where little is lost, else its series
@@ -55,100 +51,543 @@ __device__ inline GateVals gate_vals(float rg, float ig, float decay) {
   s = fmaf(w, s, 1.f / 6.f);
   s = fmaf(w, s, -0.5f);
   s = fmaf(w, s, 1.f);
-  o.m2 = w < 0.25f ? w * s : fmaf(-o.a, o.a, 1.f);
+  const float m2 = w < 0.25f ? w * s : fmaf(-o.a, o.a, 1.f);
+  o.m = m2 >= 1.17549435e-38f ? __builtin_amdgcn_sqrtf(m2) : 0.f;
   return o;
 }
-constexpr float GATE_TINY = 1.17549435e-38f;  // 1 - a^2 below it counts as 0
 
-// One thread per (sequence, channel) through all steps.
-template <typename T>
-__global__ __launch_bounds__(64) void k_gated_fwd(GatedArgs a) {
-  const long long id = flat_block() * 64 + threadIdx.x;
-  if (id >= (long long)a.B * a.D) return;
-  const int d = (int)(id % a.D), b = (int)(id / a.D);
-  const int len = seq_len(a.lengths, b, a.T);
-  const float decay = a.decay[d], rb = a.rb ? a.rb[d] : 0.f, ib = a.ib ? a.ib[d] : 0.f;
-  float h = a.h0 ? a.h0[id] : 0.f;
-  const int nst = (a.T + GS - 1) / GS;
-  for (int t = 0; t < a.T; t++) {
-    if (t < len) {
-      if (a.states && t % GS == 0) a.states[((long long)b * nst + t / GS) * a.D + d] = h;
-      const GateVals g = gate_vals<T>(ldf((const T *)a.r.p, b * a.r.sb + t * a.r.st + d) + rb,
-                                      ldf((const T *)a.i.p, b * a.i.sb + t * a.i.st + d) + ib, decay);
-      const float m = g.m2 >= GATE_TINY ? __builtin_amdgcn_sqrtf(g.m2) : 0.f;
-      h = fmaf(g.a, h, m * g.i * ldf((const T *)a.x.p, b * a.x.sb + t * a.x.st + d));
-    }
-    stf((T *)a.y.p, b * a.y.sb + t * a.y.st + d, t < len ? h : 0.f);
+// ---------------------------------------------------------------------------
+// tiles
+// ---------------------------------------------------------------------------
+// A block takes 64 channels (a column of tiles) and a tile of steps: a lane
+// holds four adjacent channels, a wavefront four rows of K steps each.  Every
+// lane composes its steps, one wavefront joins the rows and the tiles before,
+// and every lane then walks its steps again from its row's state, so that each
+// input is read once.
+constexpr int G_CH = 64;
+constexpr int G_SUPER = 16;  // tiles of a super tile
+
+// State between the tiles of a column.  A tile publishes what it does to a
+// state, h -> A h + B; the last of 16 publishes the same of all 16, and, once it
+// is known, the state that leaves them.  A tile's state is the one that enters
+// its super tile, taken through the tiles before it in order, and that one is
+// the first state, taken through the super tiles in order: the same products and
+// sums whatever was published when it looked, so results repeat bit by bit.
+//   Words of 64 bits, A or 0 above B or the state; all ones: not there yet.  The
+// word is read and written whole, so nothing has to be ordered around it.
+//   Tiles of a column are handed out in order by a counter: a tile waits only for
+// blocks that already run, whatever else runs on the device.
+struct GatedChain {
+  unsigned *ticket;                        // [columns], 64 bytes apart
+  unsigned long long *agg, *sagg, *spre;   // [tile][column][64], [super][column][64], [super][column][64]
+  long long cols;
+};
+constexpr unsigned G_NONE = 0xffffffffu;
+__device__ inline unsigned long long chain_word(float A, float B) {
+  const unsigned h = __float_as_uint(A);
+  return ((unsigned long long)(h == G_NONE ? 0x7fc00000u : h) << 32) | __float_as_uint(B);
+}
+__device__ inline bool chain_there(unsigned long long w) { return (unsigned)(w >> 32) != G_NONE; }
+__device__ inline float chain_A(unsigned long long w) { return __uint_as_float((unsigned)(w >> 32)); }
+__device__ inline float chain_B(unsigned long long w) { return __uint_as_float((unsigned)w); }
+
+// The state that enters tile j (j-th in the order of the chain) of column c,
+// for one channel a lane, after the tile's own A, B were published; `first`: the
+// column's first state, read by tile 0 alone.  A wait that sees nothing for
+// PR_SPIN_LIMIT polls gives up with a NaN.
+__device__ inline float chain_enter(const GatedChain &ch, long long c, int j, int tiles, float A, float B, float first) {
+  const unsigned lane = threadIdx.x & 63;
+  const int s = j / G_SUPER, q = j % G_SUPER;
+  const long long step = ch.cols * 64;
+  // the words' addresses without the lane: uniform
+  unsigned long long *agg = ch.agg + s * (G_SUPER * step) + c * 64, *sagg = ch.sagg + s * step + c * 64,
+                     *spre = ch.spre + s * step + c * 64;
+  unsigned long long w[G_SUPER - 1];
+  int polls = 0;
+  if (j == 0) {
+    if (tiles > 1) st_agent64(spre + lane, chain_word(0.f, first));
+    return first;
   }
-  if (a.hlast) a.hlast[id] = h;
+  while (true) {
+    bool ok = true;
+    long long st = step;
+    asm volatile("" : "+s"(st));  // addresses made where they are used: kept over the loop they would take 60 registers
+#pragma unroll
+    for (int i = 0; i < G_SUPER - 1; i++)
+      if (i < q) w[i] = ld_agent64(agg + i * st + lane);
+#pragma unroll
+    for (int i = 0; i < G_SUPER - 1; i++)
+      if (i < q) ok = ok && chain_there(w[i]);
+    if (__all(ok)) break;
+    if (++polls > PR_SPIN_LIMIT) return __builtin_nanf("");
+    __builtin_amdgcn_s_sleep(1);
+  }
+  float SA = A, SB = B;
+  const bool closes = q == G_SUPER - 1 && j + 1 < tiles;
+  if (closes) {
+    SA = chain_A(w[0]);
+    SB = chain_B(w[0]);
+#pragma unroll
+    for (int i = 1; i < G_SUPER - 1; i++) {
+      SB = fmaf(chain_A(w[i]), SB, chain_B(w[i]));
+      SA *= chain_A(w[i]);
+    }
+    SB = fmaf(A, SB, B);
+    SA *= A;
+    st_agent64(sagg + lane, chain_word(SA, SB));
+  }
+  // the state that enters the super tile: there, or from one of the 8 before it
+  float h;
+  while (true) {
+    constexpr int W = 8;
+    const unsigned long long p = ld_agent64(spre + lane);
+    bool ok = chain_there(p);
+    h = chain_B(p);
+    if (__all(ok)) break;
+    unsigned long long pre[W], ag[W];
+    long long st = step;
+    asm volatile("" : "+s"(st));
+#pragma unroll
+    for (int i = 0; i < W; i++)
+      if (s - 1 - i >= 0) {
+        pre[i] = ld_agent64(spre - (i + 1) * st + lane);
+        ag[i] = ld_agent64(sagg - (i + 1) * st + lane);
+      } else {
+        pre[i] = ag[i] = ~0ull;
+      }
+    int from = -1;  // the nearest state that was published, with all that follows it
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < W; i++) {
+      all = all && chain_there(ag[i]);
+      if (from < 0 && all && chain_there(pre[i])) from = i;
+    }
+    float v = 0.f;
+#pragma unroll
+    for (int i = W - 1; i >= 0; i--) {
+      if (i == from) v = chain_B(pre[i]);
+      if (i <= from) v = fmaf(chain_A(ag[i]), v, chain_B(ag[i]));
+    }
+    if (!ok) {
+      ok = from >= 0;
+      h = v;
+    }
+    if (__all(ok)) break;
+    if (++polls > PR_SPIN_LIMIT) return __builtin_nanf("");
+    __builtin_amdgcn_s_sleep(1);
+  }
+  if (closes) st_agent64(spre + step + lane, chain_word(0.f, fmaf(SA, h, SB)));
+#pragma unroll
+  for (int i = 0; i < G_SUPER - 1; i++)
+    if (i < q) h = fmaf(chain_A(w[i]), h, chain_B(w[i]));
+  return h;
 }
 
-// The same back in time: the states of 16 steps at a time are made again from
-// the saved one.
+__global__ __launch_bounds__(256) void k_gated_clear(uint4 *p, long long n) {
+  for (long long i = flat_block() * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * gridDim.y * 256)
+    p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
+// A tile's steps of one [B, T, D] array: the tile's first step (uniform), with
+// 32-bit offsets of at most 128 steps from it.
+struct TileOf {
+  char *base;
+  unsigned st;  // bytes
+};
 template <typename T>
-__global__ __launch_bounds__(64) void k_gated_adj(GatedArgs a) {
-  const long long id = flat_block() * 64 + threadIdx.x;
-  if (id >= (long long)a.B * a.D) return;
-  const int d = (int)(id % a.D), b = (int)(id / a.D);
-  const int len = seq_len(a.lengths, b, a.T);
-  const float decay = a.decay[d], rb = a.rb ? a.rb[d] : 0.f, ib = a.ib ? a.ib[d] : 0.f;
-  const int nst = (a.T + GS - 1) / GS;
-  float mu = a.dhlast ? a.dhlast[id] : 0.f, sv = 0.f, sr = 0.f, si = 0.f;
-  auto vals = [&](int t, float *x) {
-    *x = ldf((const T *)a.x.p, b * a.x.sb + t * a.x.st + d);
-    return gate_vals<T>(ldf((const T *)a.r.p, b * a.r.sb + t * a.r.st + d) + rb,
-                        ldf((const T *)a.i.p, b * a.i.sb + t * a.i.st + d) + ib, decay);
+__device__ inline TileOf tile_of(const View &v, int b, long long t0) {
+  return TileOf{(char *)((T *)v.p + b * v.sb + t0 * v.st), (unsigned)v.st * (unsigned)sizeof(T)};
+}
+
+// Where a lane stands.
+struct GatedAt {
+  int d, n;     // first channel, channels from it on
+  int t0, row;  // the tile's first step, the lane's first step in it
+  int len;      // steps of the sequence
+};
+// Four channels of the K steps of a lane in N arrays, all loads in flight
+// together.  Not FULL: steps past the end read the last one, lanes past the last
+// channel others of the row, whose values nobody uses.
+template <typename T, bool FULL, int K, int N>
+__device__ inline void ld_steps(const TileOf (&v)[N], const GatedAt &p, int D, VecU<T, 4> (&r)[N][K]) {
+  if (FULL || D >= 4) {
+    const int dd = FULL || p.d < D - 4 ? p.d : D - 4, m = p.d - dd, last = p.len - 1 - p.t0;
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      const int s = FULL || p.row + k < last ? p.row + k : last;
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        // (FULL: one offset for all steps of an array)
+        const unsigned off = (unsigned)(FULL ? p.row : s) * v[j].st + (unsigned)dd * (unsigned)sizeof(T);
+        r[j][k].v = reinterpret_cast<const Packed<T, 4> *>(v[j].base + (FULL ? (long long)k * v[j].st : 0) + off)->v;
+      }
+    }
+    if constexpr (!FULL)
+#pragma unroll
+      for (int k = 0; k < K; k++)
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+          VecU<T, 4> &e = r[j][k];
+          const T e1 = e.e[1], e2 = e.e[2], e3 = e.e[3];
+          e.e[0] = m == 0 ? e.e[0] : m == 1 ? e1 : m == 2 ? e2 : e3;
+          e.e[1] = m == 0 ? e1 : m == 1 ? e2 : e3;
+          e.e[2] = m == 0 ? e2 : e3;
+        }
+  } else {
+    const int last = p.len - 1 - p.t0;
+#pragma unroll
+    for (int k = 0; k < K; k++)
+#pragma unroll
+      for (int j = 0; j < N; j++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const unsigned off = (unsigned)(p.row + k < last ? p.row + k : last) * v[j].st;
+          r[j][k].e[i] = reinterpret_cast<const T *>(v[j].base + off)[p.d + i < D ? p.d + i : D - 1];
+        }
+  }
+}
+template <typename T, bool FULL>
+__device__ inline void st_step(const TileOf &v, const GatedAt &p, int k, int T_, const float *o) {
+  const unsigned off = (unsigned)p.row * v.st + (unsigned)p.d * (unsigned)sizeof(T);
+  T *q = (T *)(v.base + (long long)k * v.st + off);
+  if constexpr (FULL) stu<T, 4>(q, o, 4);
+  else if (p.t0 + p.row + k < T_ && p.n > 0) stu<T, 4>(q, o, p.n);
+}
+template <typename T>
+__device__ inline void zero_steps(const View &v, int b, const GatedAt &p, int K, int T_) {
+  const float z[4] = {0.f, 0.f, 0.f, 0.f};
+  if (v.p)
+    for (int k = 0; k < K; k++) st_step<T, false>(tile_of<T>(v, b, p.t0), p, k, T_, z);
+}
+
+struct GatedConsts {
+  float decay[4], rb[4], ib[4];
+};
+__device__ inline GatedConsts gated_consts(const GatedArgs &a, const GatedAt &p) {
+  GatedConsts c;
+  const VecU<float, 4> d = ldu<float, 4>(a.decay + p.d, p.n), r = ldu<float, 4>(a.rb + p.d, a.rb ? p.n : 0),
+                       i = ldu<float, 4>(a.ib + p.d, a.ib ? p.n : 0);
+#pragma unroll
+  for (int v = 0; v < 4; v++) {
+    c.decay[v] = d.f(v);
+    c.rb[v] = r.f(v);
+    c.ib[v] = i.f(v);
+  }
+  return c;
+}
+
+// The block's column and tile (in the order of the chain); false: none left.
+__device__ inline bool gated_tile(const GatedArgs &a, const GatedChain &ch, int *sh, long long *c, int *j) {
+  const long long blk = flat_block();
+  if (blk >= ch.cols * a.tiles) return false;
+  *c = blk % ch.cols;
+  *j = 0;
+  if (a.tiles > 1) {
+    if (threadIdx.x == 0) *sh = (int)(add_agent(ch.ticket + *c * 16, 1u) + 1u);  // (starts at all ones)
+    __syncthreads();
+    *j = __builtin_amdgcn_readfirstlane(*sh);
+  }
+  return true;
+}
+
+// Blocks of up to four wavefronts that compute, and one more that joins.
+template <typename T, int K, int NW>
+__global__ __launch_bounds__(64 * (NW + 1), 4) void k_gated_fwd(GatedArgs a, GatedChain ch) {
+  __shared__ float lA[4 * NW * G_CH], lB[4 * NW * G_CH];
+  __shared__ int sh;
+  long long c;
+  int tile;
+  if (!gated_tile(a, ch, &sh, &c, &tile)) return;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = (blockDim.x >> 6) - 1;
+  const int b = (int)(c / a.cb), d0 = (int)(c % a.cb) * G_CH;
+  const int len = __builtin_amdgcn_readfirstlane(seq_len(a.lengths, b, a.T));
+  const int live = len > 0 ? (len - 1) / a.tt + 1 : 0;  // tiles of the sequence that hold steps
+  if (w == nw) {  // the rows' states; a lane for each channel
+    const bool on = d0 + lane < a.D;
+    const long long sd = (long long)b * a.D + d0 + lane;
+    float first = 0.f;
+    if (tile == 0 && a.h0 && on) first = a.h0[sd];
+    if (tile >= live) {
+      if (tile == 0 && a.hlast && on) a.hlast[sd] = first;
+      return;
+    }
+    const int rows = nw * 4;
+    lds_barrier();
+    float h = first;
+    if (live > 1) {
+      float tA = lA[lane], tB = lB[lane];
+#pragma unroll 3
+      for (int q = 1; q < rows; q++) {
+        const float qa = lA[q * G_CH + lane];
+        tB = fmaf(qa, tB, lB[q * G_CH + lane]);
+        tA *= qa;
+      }
+      if (tile + 1 < live) st_agent64(ch.agg + (tile * ch.cols + c) * 64 + (unsigned)lane, chain_word(tA, tB));
+      h = chain_enter(ch, c, tile, live, tA, tB, first);
+    }
+#pragma unroll 4
+    for (int q = 0; q < rows; q++) {
+      const float qa = lA[q * G_CH + lane], qb = lB[q * G_CH + lane];
+      lB[q * G_CH + lane] = h;
+      h = fmaf(qa, h, qb);
+    }
+    lds_barrier();
+    if (tile + 1 == live && a.hlast && on) a.hlast[sd] = h;
+    return;
+  }
+  GatedAt p;
+  p.d = d0 + (lane & 15) * 4;
+  p.n = a.D - p.d;
+  p.len = len;
+  p.t0 = tile * a.tt;
+  p.row = (w * 4 + (lane >> 4)) * K;
+  if (tile >= live) {
+    zero_steps<T>(a.y, b, p, K, a.T);
+    return;
+  }
+  auto body = [&](auto full) __attribute__((always_inline)) {
+    constexpr bool FULL = decltype(full)::value;
+    float ga[K][4], gb[K][4], A[4], B[4];
+    {
+      const TileOf in[3] = {tile_of<T>(a.r, b, p.t0), tile_of<T>(a.i, b, p.t0), tile_of<T>(a.x, b, p.t0)};
+      VecU<T, 4> raw[3][K];
+      ld_steps<T, FULL, K>(in, p, a.D, raw);
+      const GatedConsts cs = gated_consts(a, p);
+#pragma unroll
+      for (int k = 0; k < K; k++) {
+        const bool on = FULL || p.t0 + p.row + k < len;
+#pragma unroll
+        for (int v = 0; v < 4; v++) {
+          const GateVals g = gate_vals<T>(raw[0][k].f(v) + cs.rb[v], raw[1][k].f(v) + cs.ib[v], cs.decay[v]);
+          ga[k][v] = on ? g.a : 1.f;
+          gb[k][v] = on ? g.m * g.i * raw[2][k].f(v) : 0.f;
+          A[v] = k ? A[v] * ga[k][v] : ga[k][v];
+          B[v] = k ? fmaf(ga[k][v], B[v], gb[k][v]) : gb[k][v];
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one step's temporaries at a time
+      }
+    }
+    const int at = (w * 4 + (lane >> 4)) * G_CH + (lane & 15) * 4;
+    *reinterpret_cast<float4 *>(lA + at) = make_float4(A[0], A[1], A[2], A[3]);
+    *reinterpret_cast<float4 *>(lB + at) = make_float4(B[0], B[1], B[2], B[3]);
+    lds_barrier();
+    lds_barrier();
+    const float4 h4 = *reinterpret_cast<const float4 *>(lB + at);
+    float h[4] = {h4.x, h4.y, h4.z, h4.w};
+    const int t = p.t0 + p.row;
+    if (a.states && t % PR_GATED_STATE_STEPS == 0 && t < len && p.n > 0)
+      stu<float, 4>(a.states + ((long long)b * a.nst + t / PR_GATED_STATE_STEPS) * a.D + p.d, h, p.n);
+    const TileOf ty = tile_of<T>(a.y, b, p.t0);
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      float o[4];
+#pragma unroll
+      for (int v = 0; v < 4; v++) {
+        h[v] = fmaf(ga[k][v], h[v], gb[k][v]);
+        o[v] = FULL || t + k < len ? h[v] : 0.f;
+      }
+      st_step<T, FULL>(ty, p, k, a.T, o);
+    }
   };
-  for (int t0 = (a.T - 1) / 16 * 16; t0 >= 0; t0 -= 16) {
-    float hp[16];
-    const int c0 = t0 / GS * GS;
-    float h = c0 < len ? a.states[((long long)b * nst + c0 / GS) * a.D + d] : 0.f;
-    for (int t = c0; t < t0 + 16; t++) {
-      if (t >= t0) {
-#pragma unroll
-        for (int k = 0; k < 16; k++)
-          if (t == t0 + k) hp[k] = h;
-      }
-      if (t < len) {
-        float x;
-        const GateVals g = vals(t, &x);
-        h = fmaf(g.a, h, (g.m2 >= GATE_TINY ? __builtin_amdgcn_sqrtf(g.m2) : 0.f) * g.i * x);
-      }
+  if ((tile + 1) * (long long)a.tt <= len && d0 + G_CH <= a.D) body(std::integral_constant<bool, true>{});
+  else body(std::integral_constant<bool, false>{});
+}
+
+// The adjoint, tiles from the last to the first.  mu is what the steps after a
+// step add to its state's gradient: mu_{t-1} = a_t (dy_t + mu_t), the same A as
+// forwards.  The tile's states are made again from the saved one.
+template <typename T, int K, int NW, int WPS>
+__global__ __launch_bounds__(64 * (NW + 1), WPS) void k_gated_adj(GatedArgs a, GatedChain ch) {
+  __shared__ float lds[3][4 * NW * G_CH];
+  __shared__ int sh;
+  float *lA = lds[0], *lF = lds[1], *lR = lds[2];
+  long long c;
+  int order;
+  if (!gated_tile(a, ch, &sh, &c, &order)) return;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = (blockDim.x >> 6) - 1;
+  const int rows = nw * 4, tile = a.tiles - 1 - order;
+  const int b = (int)(c / a.cb), d0 = (int)(c % a.cb) * G_CH;
+  const int len = __builtin_amdgcn_readfirstlane(seq_len(a.lengths, b, a.T));
+  const int live = len > 0 ? (len - 1) / a.tt + 1 : 0;
+  float *part = a.part ? a.part + ((long long)b * a.tiles + tile) * 3 * a.D + d0 : nullptr;
+  if (w == nw) {
+    const bool on = d0 + lane < a.D;
+    const long long sd = (long long)b * a.D + d0 + lane;
+    const int j = live - 1 - tile;  // place in the chain
+    float first = 0.f;
+    if ((j == 0 || (tile == 0 && live == 0)) && a.dhlast && on) first = a.dhlast[sd];
+    if (tile >= live) {
+      if (tile == 0 && on && a.dh0) a.dh0[sd] = first;
+      return;
     }
-#pragma unroll
-    for (int k = 15; k >= 0; k--) {
-      const int t = t0 + k;
-      if (t >= a.T) continue;
-      float ox = 0.f, orr = 0.f, oi = 0.f;
-      if (t < len) {
-        float x;
-        const GateVals g = vals(t, &x);
-        const float rm = g.m2 >= GATE_TINY ? __builtin_amdgcn_rsqf(g.m2) : 0.f, m = g.m2 * rm;
-        const float gg = mu + ldf((const T *)a.y.p, b * a.y.sb + t * a.y.st + d);
-        const float gi = gg * g.i;
-        ox = gi * m;
-        oi = ox * x * g.i1;
-        const float dv = g.a * fmaf(gi * x, g.a * rm, -gg * hp[k]);
-        sv = fmaf(dv, g.r, sv);
-        orr = dv * decay * g.r * g.r1;
-        sr += orr;
-        si += oi;
-        mu = gg * g.a;
+    float h = on ? a.states[((long long)b * a.nst + (long long)tile * a.tt / PR_GATED_STATE_STEPS) * a.D + d0 + lane] : 0.f;
+    lds_barrier();
+    float mu = first;
+    if (live > 1) {
+      float tA = lA[(rows - 1) * G_CH + lane], tB = lR[(rows - 1) * G_CH + lane];
+#pragma unroll 3
+      for (int q = rows - 2; q >= 0; q--) {
+        const float qa = lA[q * G_CH + lane];
+        tB = fmaf(qa, tB, lR[q * G_CH + lane]);
+        tA *= qa;
       }
-      if (a.dx.p) stf((T *)a.dx.p, b * a.dx.sb + t * a.dx.st + d, ox);
-      if (a.dr.p) stf((T *)a.dr.p, b * a.dr.sb + t * a.dr.st + d, orr);
-      if (a.di.p) stf((T *)a.di.p, b * a.di.sb + t * a.di.st + d, oi);
+      if (j + 1 < live) st_agent64(ch.agg + (j * ch.cols + c) * 64 + (unsigned)lane, chain_word(tA, tB));
+      mu = chain_enter(ch, c, j, live, tA, tB, first);
     }
+#pragma unroll 4
+    for (int q = 0; q < rows; q++) {
+      const int m = rows - 1 - q;
+      const float fa = lA[q * G_CH + lane], fb = lF[q * G_CH + lane], ra = lA[m * G_CH + lane], rb = lR[m * G_CH + lane];
+      lF[q * G_CH + lane] = h;
+      lR[m * G_CH + lane] = mu;
+      h = fmaf(fa, h, fb);
+      mu = fmaf(ra, mu, rb);
+    }
+    lds_barrier();
+    if (tile == 0 && a.dh0 && on) a.dh0[sd] = mu;
+    if (!part) return;
+    lds_barrier();
+    lds_barrier();
+    return;
   }
-  if (a.dh0) a.dh0[id] = mu;
-  if (a.part) {
-    float *p = a.part + (long long)b * 3 * a.D + d;
-    p[0] = sv;
-    p[a.D] = sr;
-    p[2LL * a.D] = si;
+  GatedAt p;
+  p.d = d0 + (lane & 15) * 4;
+  p.n = a.D - p.d;
+  p.len = len;
+  p.t0 = tile * a.tt;
+  p.row = (w * 4 + (lane >> 4)) * K;
+  if (tile >= live) {
+    zero_steps<T>(a.dx, b, p, K, a.T);
+    zero_steps<T>(a.dr, b, p, K, a.T);
+    zero_steps<T>(a.di, b, p, K, a.T);
+    if (part)
+      for (int q = threadIdx.x; q < 3 * G_CH; q += 64 * nw)
+        if (d0 + q % G_CH < a.D) part[(long long)(q / G_CH) * a.D + q % G_CH] = 0.f;
+    return;
+  }
+  const int at = (w * 4 + (lane >> 4)) * G_CH + (lane & 15) * 4;
+  float sums[3][4] = {};
+  auto body = [&](auto full) __attribute__((always_inline)) {
+    constexpr bool FULL = decltype(full)::value;
+    float ga[K][4], gm[K][4], gr[K][4], gi[K][4], cv[K][4], A[4], F[4];
+    VecU<T, 4> x[K], gy[K];
+    {
+      const TileOf in[4] = {tile_of<T>(a.r, b, p.t0), tile_of<T>(a.i, b, p.t0), tile_of<T>(a.x, b, p.t0),
+                            tile_of<T>(a.y, b, p.t0)};
+      VecU<T, 4> raw[4][K];
+      ld_steps<T, FULL, K>(in, p, a.D, raw);
+#pragma unroll
+      for (int k = 0; k < K; k++) {
+        x[k] = raw[2][k];
+        gy[k] = raw[3][k];
+      }
+      const GatedConsts cs = gated_consts(a, p);
+#pragma unroll
+      for (int k = 0; k < K; k++) {
+        const bool on = FULL || p.t0 + p.row + k < len;
+#pragma unroll
+        for (int v = 0; v < 4; v++) {
+          const GateVals g = gate_vals<T>(raw[0][k].f(v) + cs.rb[v], raw[1][k].f(v) + cs.ib[v], cs.decay[v]);
+          if (!on) x[k].e[v] = gy[k].e[v] = 0;
+          ga[k][v] = on ? g.a : 1.f;  // a step that is not there keeps mu and the state, and has no gradients
+          gm[k][v] = on ? g.m : 0.f;
+          gr[k][v] = on ? g.r : 0.f;
+          gi[k][v] = on ? g.i : 0.f;
+          const float bb = gm[k][v] * gi[k][v] * x[k].f(v);
+          A[v] = k ? A[v] * ga[k][v] : ga[k][v];
+          F[v] = k ? fmaf(ga[k][v], F[v], bb) : bb;
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one step's temporaries at a time
+      }
+    }
+    float R[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = K - 1; k >= 0; k--)
+#pragma unroll
+      for (int v = 0; v < 4; v++) R[v] = ga[k][v] * (gy[k].f(v) + R[v]);
+    *reinterpret_cast<float4 *>(lA + at) = make_float4(A[0], A[1], A[2], A[3]);
+    *reinterpret_cast<float4 *>(lF + at) = make_float4(F[0], F[1], F[2], F[3]);
+    *reinterpret_cast<float4 *>(lR + at) = make_float4(R[0], R[1], R[2], R[3]);
+    lds_barrier();
+    lds_barrier();
+    // (the inputs stay as they were stored: unpacked they would take twice the registers)
+#pragma unroll
+    for (int k = 0; k < K; k++) asm volatile("" : "+v"(x[k].v), "+v"(gy[k].v));
+    const float4 h4 = *reinterpret_cast<const float4 *>(lF + at), m4 = *reinterpret_cast<const float4 *>(lR + at);
+    float h[4] = {h4.x, h4.y, h4.z, h4.w}, mu[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+    for (int k = 0; k < K; k++)
+#pragma unroll
+      for (int v = 0; v < 4; v++) {
+        // dv = g cv; m becomes m i
+        const float m = gm[k][v], u = gi[k][v] * x[k].f(v), a1 = ga[k][v];
+        cv[k][v] = a1 * fmaf(a1 * (m > 0.f ? frcp(m) : 0.f), u, -h[v]);
+        h[v] = fmaf(a1, h[v], m * u);
+        gm[k][v] = m * gi[k][v];
+      }
+    const VecU<float, 4> decay = ldu<float, 4>(a.decay + p.d, p.n);
+    const TileOf ox_ = tile_of<T>(a.dx, b, p.t0), or_ = tile_of<T>(a.dr, b, p.t0), oi_ = tile_of<T>(a.di, b, p.t0);
+#pragma unroll
+    for (int k = K - 1; k >= 0; k--) {
+      const bool on = FULL || p.t0 + p.row + k < len;
+      float ox[4], orr[4], oi[4];
+#pragma unroll
+      for (int v = 0; v < 4; v++) {
+        const float g = gy[k].f(v) + mu[v], dv = on ? g * cv[k][v] : 0.f, r = gr[k][v], i = gi[k][v];
+        ox[v] = on ? g * gm[k][v] : 0.f;
+        oi[v] = ox[v] * x[k].f(v) * (1.f - i);
+        orr[v] = dv * decay.f(v) * (r * (1.f - r));
+        sums[0][v] = fmaf(dv, r, sums[0][v]);
+        sums[1][v] += orr[v];
+        sums[2][v] += oi[v];
+        mu[v] = ga[k][v] * g;
+      }
+      if (a.dx.p) st_step<T, FULL>(ox_, p, k, a.T, ox);
+      if (a.dr.p) st_step<T, FULL>(or_, p, k, a.T, orr);
+      if (a.di.p) st_step<T, FULL>(oi_, p, k, a.T, oi);
+    }
+  };
+  if ((tile + 1) * (long long)a.tt <= len && d0 + G_CH <= a.D) body(std::integral_constant<bool, true>{});
+  else body(std::integral_constant<bool, false>{});
+  if (!part) return;
+  lds_barrier();  // the rows' states have been read
+#pragma unroll
+  for (int s = 0; s < 3; s++)
+    *reinterpret_cast<float4 *>(lds[s] + at) = make_float4(sums[s][0], sums[s][1], sums[s][2], sums[s][3]);
+  lds_barrier();
+  for (int q = threadIdx.x; q < 3 * G_CH; q += 64 * nw) {
+    float v = 0.f;
+    for (int m = 0; m < rows; m++) v += lds[q / G_CH][m * G_CH + q % G_CH];
+    if (d0 + q % G_CH < a.D) part[(long long)(q / G_CH) * a.D + q % G_CH] = v;
   }
 }
 
+// ddecay, dr_bias and dr_bias from the tiles' partials [P][3][D], in 64 bits in a
+// fixed order: 32 columns by 8 slices of the partials a block.
+__global__ __launch_bounds__(256) void k_gated_sums(const float *__restrict__ part, int P, int D, float *o0, float *o1,
+                                                    float *o2) {
+  __shared__ double sh[8][32];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, k = blockIdx.y, d = (int)blockIdx.x * 32 + x;
+  float *o = k == 0 ? o0 : k == 1 ? o1 : o2;
+  if (!o) return;
+  double s = 0;
+  if (d < D)
+    for (int p0 = y; p0 < P; p0 += 64) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; q++) v[q] = p0 + 8 * q < P ? part[((p0 + 8LL * q) * 3 + k) * D + d] : 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; q++) s += (double)v[q];
+    }
+  sh[y][x] = s;
+  __syncthreads();
+  if (y == 0 && d < D)
+    o[d] = (float)(((sh[0][x] + sh[1][x]) + (sh[2][x] + sh[3][x])) + ((sh[4][x] + sh[5][x]) + (sh[6][x] + sh[7][x])));
+}
+
+// ---------------------------------------------------------------------------
+// one token
+// ---------------------------------------------------------------------------
 struct GatedStepArgs {
   const void *x, *r, *i;
   void *y;
@@ -176,8 +615,7 @@ __global__ __launch_bounds__(256) void k_gated_step(GatedStepArgs a) {
 #pragma unroll
     for (int k = 0; k < V; k++) {
       const GateVals g = gate_vals<T>(r.f(k) + rb.f(k), i.f(k) + ib.f(k), dc.f(k));
-      const float m = g.m2 >= GATE_TINY ? __builtin_amdgcn_sqrtf(g.m2) : 0.f;
-      o[k] = fmaf(g.a, h.f(k), m * g.i * x.f(k));
+      o[k] = fmaf(g.a, h.f(k), g.m * g.i * x.f(k));
     }
     stu<float, V>(hp, o, n);
   }
@@ -203,30 +641,89 @@ int gated_check(const pr_gated_problem *p, bool step) {
   if (p->B < 1 || p->T < (step ? 0 : 1) || p->D < 1)
     return fail(PR_EINVAL, "sizes must be >= 1 (B=%d T=%d D=%d)", p->B, p->T, p->D);
   if (p->T > (1 << 30)) return fail(PR_EUNSUPPORTED, "T = %d: at most 2^30", p->T);
-  if (p->D > (1 << 24)) return fail(PR_EUNSUPPORTED, "D = %d: at most 2^24", p->D);
+  if (p->D > (1 << 22)) return fail(PR_EUNSUPPORTED, "D = %d: at most 2^22", p->D);
   return PR_OK;
 }
 
-struct GatedPlan {
-  size_t fwd_bytes, adj_bytes;
+// Steps of a lane and wavefronts of a tile: forwards a lane keeps a and b of
+// each step, back five values and two inputs.
+struct GatedGeom {
+  int k, nw;
 };
-int gated_plan(const pr_gated_problem *p, GatedPlan *pl) {
+GatedGeom gated_geom(int dtype, bool adj) {
+  if (!adj) return dtype == PR_BF16 ? GatedGeom{8, 4} : GatedGeom{4, 4};
+  return GatedGeom{2, 8};
+}
+
+struct GatedPlan {
+  int waves, tt, tiles, cb;
+  long long cols;
+  size_t off_agg, off_sagg, off_spre, off_part, clear, bytes;
+};
+int gated_plan(const pr_gated_problem *p, bool adj, GatedPlan *pl) {
   const int rc = gated_check(p, false);
   if (rc != PR_OK) return rc;
-  if ((double)p->B * p->T * p->D > 1e13) return fail(PR_EUNSUPPORTED, "problem too large");
-  pl->fwd_bytes = 256;
-  pl->adj_bytes = ((size_t)p->B * 3 * p->D * 4 + 255) & ~(size_t)255;
+  const GatedGeom g = gated_geom(p->dtype, adj);
+  const int k4 = 4 * g.k;  // steps of a wavefront
+  pl->waves = p->T >= g.nw * k4 ? g.nw : (p->T + k4 - 1) / k4;
+  pl->tt = pl->waves * k4;
+  pl->tiles = (p->T + pl->tt - 1) / pl->tt;
+  pl->cb = (p->D + G_CH - 1) / G_CH;
+  pl->cols = (long long)p->B * pl->cb;
+  if ((double)pl->cols * pl->tiles * 64 > 1e12) return fail(PR_EUNSUPPORTED, "problem too large");
+  size_t o = 0;
+  const size_t words = (size_t)pl->cols * 64 * 8, supers = (pl->tiles + G_SUPER - 1) / G_SUPER;
+  if (pl->tiles > 1) {
+    o = (size_t)pl->cols * 64;
+    pl->off_agg = o; o += words * pl->tiles;
+    pl->off_sagg = o; o += words * supers;
+    pl->off_spre = o; o += words * supers;
+  } else {
+    pl->off_agg = pl->off_sagg = pl->off_spre = 0;
+  }
+  pl->clear = o;
+  o = (o + 255) & ~(size_t)255;
+  pl->off_part = o;
+  if (adj) o += ((size_t)p->B * pl->tiles * 3 * p->D * 4 + 255) & ~(size_t)255;
+  pl->bytes = o > 256 ? o : 256;
+  return PR_OK;
+}
+
+// The chain in the workspace, marked as empty where there is one.
+hipError_t gated_chain(const GatedPlan &pl, void *workspace, GatedChain *ch, hipStream_t s) {
+  char *ws = (char *)workspace;
+  ch->ticket = (unsigned *)ws;
+  ch->agg = (unsigned long long *)(ws + pl.off_agg);
+  ch->sagg = (unsigned long long *)(ws + pl.off_sagg);
+  ch->spre = (unsigned long long *)(ws + pl.off_spre);
+  ch->cols = pl.cols;
+  if (!pl.clear) return hipSuccess;
+  const long long n = (long long)(pl.clear / 16), blocks = (n + 255) / 256;
+  k_gated_clear<<<(unsigned)(blocks < 2048 ? blocks : 2048), 256, 0, s>>>((uint4 *)ws, n);
+  return hipGetLastError();
+}
+
+// A tile's offsets in an array are 32-bit: at most 128 steps of 2^22 elements of 4 bytes.
+int stride_ok(const View &v, int T) {
+  if (v.p && T > 1 && (v.st < 0 || v.st > (1 << 22)))
+    return fail(PR_EUNSUPPORTED, "time stride %lld: 0 to 2^22 elements", v.st);
   return PR_OK;
 }
 
 View view(const pr_view *v) { return v && v->p ? View{v->p, v->sb, v->st} : View{nullptr, 0, 0}; }
 
-int gated_fill(const pr_gated_problem *p, const pr_gated_inputs *in, GatedArgs *a) {
+int gated_fill(const pr_gated_problem *p, const GatedPlan &pl, const pr_gated_inputs *in, GatedArgs *a) {
   if (!in) return fail(PR_EINVAL, "inputs are NULL");
   if (!in->x.p || !in->r.p || !in->i.p || !in->decay) return fail(PR_EINVAL, "x, r, i and decay are required");
   a->x = view(&in->x); a->r = view(&in->r); a->i = view(&in->i);
+  for (const View *v : {&a->x, &a->r, &a->i}) {
+    const int rc = stride_ok(*v, p->T);
+    if (rc != PR_OK) return rc;
+  }
   a->decay = in->decay; a->rb = in->r_bias; a->ib = in->i_bias; a->h0 = in->h0; a->lengths = in->lengths;
   a->B = p->B; a->T = p->T; a->D = p->D;
+  a->cb = pl.cb; a->tiles = pl.tiles; a->tt = pl.tt;
+  a->nst = (p->T + PR_GATED_STATE_STEPS - 1) / PR_GATED_STATE_STEPS;
   return PR_OK;
 }
 
@@ -242,26 +739,29 @@ extern "C" {
 
 size_t pararnn_gated_workspace_bytes(const pr_gated_problem *p, int with_adjoint) {
   clear_error();
-  GatedPlan pl;
-  if (gated_plan(p, &pl) != PR_OK) return 0;
-  return with_adjoint && pl.adj_bytes > pl.fwd_bytes ? pl.adj_bytes : pl.fwd_bytes;
+  GatedPlan fw, ad;
+  if (gated_plan(p, false, &fw) != PR_OK || gated_plan(p, true, &ad) != PR_OK) return 0;
+  return with_adjoint && ad.bytes > fw.bytes ? ad.bytes : fw.bytes;
 }
 
 int pararnn_gated_scan(const pr_gated_problem *p, const pr_gated_inputs *in, const pr_view *y, float *h_last,
                        float *states, void *workspace, size_t ws_bytes, void *stream) {
   clear_error();
   GatedPlan pl;
-  int rc = gated_plan(p, &pl);
+  int rc = gated_plan(p, false, &pl);
   if (rc != PR_OK) return rc;
   GatedArgs a{};
-  if ((rc = gated_fill(p, in, &a)) != PR_OK) return rc;
+  if ((rc = gated_fill(p, pl, in, &a)) != PR_OK) return rc;
   if (!y || !y->p) return fail(PR_EINVAL, "y is required");
-  if ((rc = check_ws(workspace, ws_bytes, pl.fwd_bytes)) != PR_OK) return rc;
+  if ((rc = check_ws(workspace, ws_bytes, pl.bytes)) != PR_OK) return rc;
   a.y = view(y); a.hlast = h_last; a.states = states;
+  if ((rc = stride_ok(a.y, p->T)) != PR_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  const dim3 grid = flat_grid(((long long)a.B * a.D + 63) / 64);
-  if (p->dtype == PR_BF16) k_gated_fwd<uint16_t><<<grid, 64, 0, s>>>(a);
-  else k_gated_fwd<float><<<grid, 64, 0, s>>>(a);
+  GatedChain ch;
+  HIPCHK(gated_chain(pl, workspace, &ch, s));
+  const dim3 grid = flat_grid(pl.cols * pl.tiles);
+  if (p->dtype == PR_BF16) k_gated_fwd<uint16_t, 8, 4><<<grid, 64 * (pl.waves + 1), 0, s>>>(a, ch);
+  else k_gated_fwd<float, 4, 4><<<grid, 64 * (pl.waves + 1), 0, s>>>(a, ch);
   HIPCHK(hipGetLastError());
   return PR_OK;
 }
@@ -271,25 +771,30 @@ int pararnn_gated_adjoint(const pr_gated_problem *p, const pr_gated_inputs *in, 
                           void *stream) {
   clear_error();
   GatedPlan pl;
-  int rc = gated_plan(p, &pl);
+  int rc = gated_plan(p, true, &pl);
   if (rc != PR_OK) return rc;
   GatedArgs a{};
-  if ((rc = gated_fill(p, in, &a)) != PR_OK) return rc;
+  if ((rc = gated_fill(p, pl, in, &a)) != PR_OK) return rc;
   if (!states || !dy || !dy->p || !gr) return fail(PR_EINVAL, "states, dy and the gradients' struct are required");
-  if ((rc = check_ws(workspace, ws_bytes, pl.adj_bytes)) != PR_OK) return rc;
+  if ((rc = check_ws(workspace, ws_bytes, pl.bytes)) != PR_OK) return rc;
   a.y = view(dy); a.dx = view(&gr->x); a.dr = view(&gr->r); a.di = view(&gr->i);
+  for (const View *v : {&a.y, &a.dx, &a.dr, &a.di})
+    if ((rc = stride_ok(*v, p->T)) != PR_OK) return rc;
   a.states = (float *)states; a.dhlast = dh_last; a.dh0 = gr->h0; a.h0 = nullptr;
   const bool sums = gr->decay || gr->r_bias || gr->i_bias;
-  a.part = sums ? (float *)workspace : nullptr;
+  char *ws = (char *)workspace;
+  a.part = sums ? (float *)(ws + pl.off_part) : nullptr;
   hipStream_t s = (hipStream_t)stream;
-  const dim3 grid = flat_grid(((long long)a.B * a.D + 63) / 64);
-  if (p->dtype == PR_BF16) k_gated_adj<uint16_t><<<grid, 64, 0, s>>>(a);
-  else k_gated_adj<float><<<grid, 64, 0, s>>>(a);
+  GatedChain ch;
+  HIPCHK(gated_chain(pl, workspace, &ch, s));
+  const dim3 grid = flat_grid(pl.cols * pl.tiles);
+  if (p->dtype == PR_BF16) k_gated_adj<uint16_t, 2, 8, 5><<<grid, 64 * (pl.waves + 1), 0, s>>>(a, ch);
+  else k_gated_adj<float, 2, 8, 5><<<grid, 64 * (pl.waves + 1), 0, s>>>(a, ch);
   HIPCHK(hipGetLastError());
   if (!sums) return PR_OK;
-  float *out[3] = {gr->decay, gr->r_bias, gr->i_bias};
-  for (int k = 0; k < 3; k++)
-    if (out[k]) HIPCHK(launch_part_sum(a.part + (long long)k * a.D, a.B, 3LL * a.D, a.D, out[k], s));
+  k_gated_sums<<<dim3((unsigned)((p->D + 31) / 32), 3), 256, 0, s>>>(a.part, p->B * pl.tiles, p->D, gr->decay,
+                                                                      gr->r_bias, gr->i_bias);
+  HIPCHK(hipGetLastError());
   return PR_OK;
 }
 

@@ -26,7 +26,7 @@ def gated_inputs(**kw):
 
 @pytest.mark.parametrize("bad,code", [
     (dict(dtype=9), bd.PR_EINVAL), (dict(B=0), bd.PR_EINVAL), (dict(T=0), bd.PR_EINVAL), (dict(D=-1), bd.PR_EINVAL),
-    (dict(T=(1 << 30) + 1), bd.PR_EUNSUPPORTED), (dict(D=(1 << 24) + 1), bd.PR_EUNSUPPORTED),
+    (dict(T=(1 << 30) + 1), bd.PR_EUNSUPPORTED), (dict(D=(1 << 22) + 1), bd.PR_EUNSUPPORTED),
     (dict(B=1 << 30, T=1 << 30), bd.PR_EUNSUPPORTED)])
 def test_gated_problems(bad, code):
     L = bd.lib()
@@ -54,6 +54,9 @@ def test_gated_arguments():
         assert scan(inp=gated_inputs(**{k: NOVIEW})) == bd.PR_EINVAL, k
     assert scan(inp=gated_inputs(decay=None)) == bd.PR_EINVAL and scan(inp=None) == bd.PR_EINVAL
     assert scan(y=None) == bd.PR_EINVAL and scan(y=NOVIEW) == bd.PR_EINVAL
+    far = bd.View(256, 4096, (1 << 22) + 1)
+    for v in (far, bd.View(256, 4096, -64)):
+        assert scan(inp=gated_inputs(r=v)) == bd.PR_EUNSUPPORTED and scan(y=v) == bd.PR_EUNSUPPORTED
     assert scan(n=fw - 1) == bd.PR_EWORKSPACE and scan(ws=None) == bd.PR_EWORKSPACE
     assert scan(ws=C.c_void_p(264)) == bd.PR_EINVAL
 
@@ -62,6 +65,7 @@ def test_gated_arguments():
 
     assert adj(states=None) == bd.PR_EINVAL and adj(dy=None) == bd.PR_EINVAL and adj(gr=None) == bd.PR_EINVAL
     assert adj(n=ad - 1) == bd.PR_EWORKSPACE
+    assert adj(dy=far) == bd.PR_EUNSUPPORTED and adj(gr=bd.GatedGrads(i=far)) == bd.PR_EUNSUPPORTED
 
     def step(p=pb, inp=gated_inputs(), y=VIEW, state=V, pool=4, slots=None):
         return L.pararnn_gated_step(ref(p), ref(inp), ref(y), state, pool, slots, None)

@@ -115,9 +115,9 @@ def test_gated(dtype, case):
     ry, rh, hs = R.gated(**p, h0=h0, lengths=n, keep=True)
     near(y, ry, TOL, "y")
     near(hl, rh, TOL, "h")
-    want, on = torch.stack(hs[:-1][::128], 1), torch.ones(B, states.shape[1], dtype=torch.bool)
+    want, on = torch.stack(hs[:-1][::bd.GATED_STATE_STEPS], 1), torch.ones(B, states.shape[1], dtype=torch.bool)
     if n is not None:
-        on = torch.arange(states.shape[1])[None] * 128 < n[:, None]
+        on = torch.arange(states.shape[1])[None] * bd.GATED_STATE_STEPS < n[:, None]
     near(states.cpu()[on], want[on], TOL, "states")
     same = h0.cuda()  # the state in place
     ws.fill_(255)
