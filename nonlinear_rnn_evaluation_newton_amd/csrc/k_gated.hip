@@ -27,32 +27,50 @@ struct GatedArgs {
 };
 
 // What a step's gates give: both gates, and a = e^-v and m = sqrt(1 - a^2) for
-// v = decay r (m = 0 where 1 - a^2 is no normal number).
+// v = decay r.
 struct GateVals {
   float r, i, a, m;
 };
+constexpr float LOG2E = 1.4426950408889634f;
+// A channel's constants.  Rows stored in 8 significant bits take plain products
+// for the exponentials' arguments, with the constants folded in; fp32 ones carry
+// the products in two words.
 template <typename T>
-__device__ inline float gate_exp(float x) {
-  if constexpr (sizeof(T) == 2) return fexp(x);
-  else return exp_acc(x);
-}
+struct GateConsts {
+  static constexpr bool SHORT = sizeof(T) == 2;
+  float rb, ib, nd, d2;  // SHORT: the biases and the decay times -log2 e; d2 = 2 decay
+  __device__ GateConsts(float decay, float r_bias, float i_bias)
+      : rb(SHORT ? -LOG2E * r_bias : r_bias), ib(SHORT ? -LOG2E * i_bias : i_bias), nd(SHORT ? -LOG2E * decay : -decay),
+        d2(decay + decay) {}
+};
 template <typename T>
-__device__ inline GateVals gate_vals(float rg, float ig, float decay) {
+__device__ inline GateVals gate_vals(float rg, float ig, const GateConsts<T> &c) {
   GateVals o;
-  o.r = frcp(1.f + gate_exp<T>(-rg));
-  o.i = frcp(1.f + gate_exp<T>(-ig));
-  const float v = decay * o.r;
-  o.a = gate_exp<T>(-v);
-  // 1 - e^-w for w = 2 v: the difference where little is lost, else its series
-  // (the first term left out is below w^6 / 5040 of it, 5e-8 at w = 1/4)
-  const float w = v + v;
-  float s = fmaf(w, -1.f / 720.f, 1.f / 120.f);
-  s = fmaf(w, s, -1.f / 24.f);
-  s = fmaf(w, s, 1.f / 6.f);
+  const float w0 = c.d2;
+  if constexpr (GateConsts<T>::SHORT) {
+    o.r = frcp(1.f + __builtin_amdgcn_exp2f(fmaf(rg, -LOG2E, c.rb)));
+    o.i = frcp(1.f + __builtin_amdgcn_exp2f(fmaf(ig, -LOG2E, c.ib)));
+    o.a = __builtin_amdgcn_exp2f(c.nd * o.r);
+  } else {
+    o.r = frcp(1.f + exp_acc(-(rg + c.rb)));
+    o.i = frcp(1.f + exp_acc(-(ig + c.ib)));
+    o.a = exp_acc(c.nd * o.r);
+  }
+  // 1 - e^-w for w = 2 v: the difference where little is lost, else its series.
+  // SHORT: up to w^4, the first term left out is below w^4 / 120 of it, 1.3e-7 at
+  // w = 1/16, where the difference has lost 4 bits; else up to w^6, 5e-8 at 1/4.
+  const float w = w0 * o.r;
+  float s;
+  if constexpr (GateConsts<T>::SHORT) {
+    s = fmaf(w, -1.f / 24.f, 1.f / 6.f);
+  } else {
+    s = fmaf(w, -1.f / 720.f, 1.f / 120.f);
+    s = fmaf(w, s, -1.f / 24.f);
+    s = fmaf(w, s, 1.f / 6.f);
+  }
   s = fmaf(w, s, -0.5f);
   s = fmaf(w, s, 1.f);
-  const float m2 = w < 0.25f ? w * s : fmaf(-o.a, o.a, 1.f);
-  o.m = m2 >= 1.17549435e-38f ? __builtin_amdgcn_sqrtf(m2) : 0.f;
+  o.m = __builtin_amdgcn_sqrtf(w < (GateConsts<T>::SHORT ? 0.0625f : 0.25f) ? w * s : fmaf(-o.a, o.a, 1.f));
   return o;
 }
 
@@ -65,10 +83,10 @@ __device__ inline GateVals gate_vals(float rg, float ig, float decay) {
 // and every lane then walks its steps again from its row's state, so that each
 // input is read once.
 constexpr int G_CH = 64;
-constexpr int G_SUPER = 16;  // tiles of a super tile
+constexpr int G_SUPER = 8;  // tiles of a super tile
 
 // State between the tiles of a column.  A tile publishes what it does to a
-// state, h -> A h + B; the last of 16 publishes the same of all 16, and, once it
+// state, h -> A h + B; the last of 8 publishes the same of all 8, and, once it
 // is known, the state that leaves them.  A tile's state is the one that enters
 // its super tile, taken through the tiles before it in order, and that one is
 // the first state, taken through the super tiles in order: the same products and
@@ -99,13 +117,12 @@ __device__ inline float chain_enter(const GatedChain &ch, long long c, int j, in
   const unsigned lane = threadIdx.x & 63;
   const int s = j / G_SUPER, q = j % G_SUPER;
   const long long step = ch.cols * 64;
-  // the words' addresses without the lane: uniform
-  unsigned long long *agg = ch.agg + s * (G_SUPER * step) + c * 64, *sagg = ch.sagg + s * step + c * 64,
-                     *spre = ch.spre + s * step + c * 64;
-  unsigned long long w[G_SUPER - 1];
+  unsigned long long *agg = ch.agg + (s * (G_SUPER * step) + c * 64 + lane), *sagg = ch.sagg + (s * step + c * 64 + lane),
+                     *spre = ch.spre + (s * step + c * 64 + lane);
+  unsigned long long w[G_SUPER - 1], p;
   int polls = 0;
   if (j == 0) {
-    if (tiles > 1) st_agent64(spre + lane, chain_word(0.f, first));
+    if (tiles > 1) st_agent64(spre, chain_word(0.f, first));
     return first;
   }
   while (true) {
@@ -114,7 +131,8 @@ __device__ inline float chain_enter(const GatedChain &ch, long long c, int j, in
     asm volatile("" : "+s"(st));  // addresses made where they are used: kept over the loop they would take 60 registers
 #pragma unroll
     for (int i = 0; i < G_SUPER - 1; i++)
-      if (i < q) w[i] = ld_agent64(agg + i * st + lane);
+      if (i < q) w[i] = ld_agent64(agg + i * st);
+    p = ld_agent64(spre);
 #pragma unroll
     for (int i = 0; i < G_SUPER - 1; i++)
       if (i < q) ok = ok && chain_there(w[i]);
@@ -134,13 +152,12 @@ __device__ inline float chain_enter(const GatedChain &ch, long long c, int j, in
     }
     SB = fmaf(A, SB, B);
     SA *= A;
-    st_agent64(sagg + lane, chain_word(SA, SB));
+    st_agent64(sagg, chain_word(SA, SB));
   }
-  // the state that enters the super tile: there, or from one of the 8 before it
+  // the state that enters the super tile: there, or from one of the 4 before it
   float h;
   while (true) {
-    constexpr int W = 8;
-    const unsigned long long p = ld_agent64(spre + lane);
+    constexpr int W = 4;
     bool ok = chain_there(p);
     h = chain_B(p);
     if (__all(ok)) break;
@@ -150,8 +167,8 @@ __device__ inline float chain_enter(const GatedChain &ch, long long c, int j, in
 #pragma unroll
     for (int i = 0; i < W; i++)
       if (s - 1 - i >= 0) {
-        pre[i] = ld_agent64(spre - (i + 1) * st + lane);
-        ag[i] = ld_agent64(sagg - (i + 1) * st + lane);
+        pre[i] = ld_agent64(spre - (i + 1) * st);
+        ag[i] = ld_agent64(sagg - (i + 1) * st);
       } else {
         pre[i] = ag[i] = ~0ull;
       }
@@ -175,8 +192,9 @@ __device__ inline float chain_enter(const GatedChain &ch, long long c, int j, in
     if (__all(ok)) break;
     if (++polls > PR_SPIN_LIMIT) return __builtin_nanf("");
     __builtin_amdgcn_s_sleep(1);
+    p = ld_agent64(spre);
   }
-  if (closes) st_agent64(spre + step + lane, chain_word(0.f, fmaf(SA, h, SB)));
+  if (closes) st_agent64(spre + step, chain_word(0.f, fmaf(SA, h, SB)));
 #pragma unroll
   for (int i = 0; i < G_SUPER - 1; i++)
     if (i < q) h = fmaf(chain_A(w[i]), h, chain_B(w[i]));
@@ -260,27 +278,25 @@ __device__ inline void zero_steps(const View &v, int b, const GatedAt &p, int K,
     for (int k = 0; k < K; k++) st_step<T, false>(tile_of<T>(v, b, p.t0), p, k, T_, z);
 }
 
-struct GatedConsts {
-  float decay[4], rb[4], ib[4];
+template <typename T>
+struct Consts4 {
+  GateConsts<T> c[4];
 };
-__device__ inline GatedConsts gated_consts(const GatedArgs &a, const GatedAt &p) {
-  GatedConsts c;
-  const VecU<float, 4> d = ldu<float, 4>(a.decay + p.d, p.n), r = ldu<float, 4>(a.rb + p.d, a.rb ? p.n : 0),
-                       i = ldu<float, 4>(a.ib + p.d, a.ib ? p.n : 0);
-#pragma unroll
-  for (int v = 0; v < 4; v++) {
-    c.decay[v] = d.f(v);
-    c.rb[v] = r.f(v);
-    c.ib[v] = i.f(v);
-  }
-  return c;
+template <typename T>
+__device__ inline Consts4<T> gated_consts(const float *decay, const float *rb, const float *ib, int d, int n) {
+  const VecU<float, 4> e = ldu<float, 4>(decay + d, n), r = ldu<float, 4>(rb + d, rb ? n : 0),
+                       i = ldu<float, 4>(ib + d, ib ? n : 0);
+  return {{{e.f(0), r.f(0), i.f(0)}, {e.f(1), r.f(1), i.f(1)}, {e.f(2), r.f(2), i.f(2)}, {e.f(3), r.f(3), i.f(3)}}};
 }
 
 // The block's column and tile (in the order of the chain); false: none left.
 __device__ inline bool gated_tile(const GatedArgs &a, const GatedChain &ch, int *sh, long long *c, int *j) {
   const long long blk = flat_block();
   if (blk >= ch.cols * a.tiles) return false;
+  // blocks go to the eight XCDs in turn: one XCD takes columns side by side, whose
+  // pieces of a row meet in its cache and in memory (8 x 4096 x 2048: 8 and 3 %)
   *c = blk % ch.cols;
+  if (ch.cols % 8 == 0) *c = (*c % 8) * (ch.cols / 8) + *c / 8;
   *j = 0;
   if (a.tiles > 1) {
     if (threadIdx.x == 0) *sh = (int)(add_agent(ch.ticket + *c * 16, 1u) + 1u);  // (starts at all ones)
@@ -290,51 +306,21 @@ __device__ inline bool gated_tile(const GatedArgs &a, const GatedChain &ch, int 
   return true;
 }
 
-// Blocks of up to four wavefronts that compute, and one more that joins.
-template <typename T, int K, int NW>
-__global__ __launch_bounds__(64 * (NW + 1), 4) void k_gated_fwd(GatedArgs a, GatedChain ch) {
+template <typename T, int K, int NW, int WPS>
+__global__ __launch_bounds__(64 * NW, WPS) void k_gated_fwd(GatedArgs a, GatedChain ch) {
   __shared__ float lA[4 * NW * G_CH], lB[4 * NW * G_CH];
   __shared__ int sh;
   long long c;
   int tile;
   if (!gated_tile(a, ch, &sh, &c, &tile)) return;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = (blockDim.x >> 6) - 1;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
   const int b = (int)(c / a.cb), d0 = (int)(c % a.cb) * G_CH;
   const int len = __builtin_amdgcn_readfirstlane(seq_len(a.lengths, b, a.T));
   const int live = len > 0 ? (len - 1) / a.tt + 1 : 0;  // tiles of the sequence that hold steps
-  if (w == nw) {  // the rows' states; a lane for each channel
-    const bool on = d0 + lane < a.D;
-    const long long sd = (long long)b * a.D + d0 + lane;
-    float first = 0.f;
-    if (tile == 0 && a.h0 && on) first = a.h0[sd];
-    if (tile >= live) {
-      if (tile == 0 && a.hlast && on) a.hlast[sd] = first;
-      return;
-    }
-    const int rows = nw * 4;
-    lds_barrier();
-    float h = first;
-    if (live > 1) {
-      float tA = lA[lane], tB = lB[lane];
-#pragma unroll 3
-      for (int q = 1; q < rows; q++) {
-        const float qa = lA[q * G_CH + lane];
-        tB = fmaf(qa, tB, lB[q * G_CH + lane]);
-        tA *= qa;
-      }
-      if (tile + 1 < live) st_agent64(ch.agg + (tile * ch.cols + c) * 64 + (unsigned)lane, chain_word(tA, tB));
-      h = chain_enter(ch, c, tile, live, tA, tB, first);
-    }
-#pragma unroll 4
-    for (int q = 0; q < rows; q++) {
-      const float qa = lA[q * G_CH + lane], qb = lB[q * G_CH + lane];
-      lB[q * G_CH + lane] = h;
-      h = fmaf(qa, h, qb);
-    }
-    lds_barrier();
-    if (tile + 1 == live && a.hlast && on) a.hlast[sd] = h;
-    return;
-  }
+  const bool owns = w == 0 && d0 + lane < a.D;  // wavefront 0 joins: a lane for each channel
+  const long long sd = (long long)b * a.D + d0 + lane;
+  float first = 0.f;
+  if (tile == 0 && a.h0 && owns) first = a.h0[sd];
   GatedAt p;
   p.d = d0 + (lane & 15) * 4;
   p.n = a.D - p.d;
@@ -343,6 +329,7 @@ __global__ __launch_bounds__(64 * (NW + 1), 4) void k_gated_fwd(GatedArgs a, Gat
   p.row = (w * 4 + (lane >> 4)) * K;
   if (tile >= live) {
     zero_steps<T>(a.y, b, p, K, a.T);
+    if (tile == 0 && a.hlast && owns) a.hlast[sd] = first;
     return;
   }
   auto body = [&](auto full) __attribute__((always_inline)) {
@@ -352,13 +339,13 @@ __global__ __launch_bounds__(64 * (NW + 1), 4) void k_gated_fwd(GatedArgs a, Gat
       const TileOf in[3] = {tile_of<T>(a.r, b, p.t0), tile_of<T>(a.i, b, p.t0), tile_of<T>(a.x, b, p.t0)};
       VecU<T, 4> raw[3][K];
       ld_steps<T, FULL, K>(in, p, a.D, raw);
-      const GatedConsts cs = gated_consts(a, p);
+      const Consts4<T> cs = gated_consts<T>(a.decay, a.rb, a.ib, p.d, p.n);
 #pragma unroll
       for (int k = 0; k < K; k++) {
         const bool on = FULL || p.t0 + p.row + k < len;
 #pragma unroll
         for (int v = 0; v < 4; v++) {
-          const GateVals g = gate_vals<T>(raw[0][k].f(v) + cs.rb[v], raw[1][k].f(v) + cs.ib[v], cs.decay[v]);
+          const GateVals g = gate_vals<T>(raw[0][k].f(v), raw[1][k].f(v), cs.c[v]);
           ga[k][v] = on ? g.a : 1.f;
           gb[k][v] = on ? g.m * g.i * raw[2][k].f(v) : 0.f;
           A[v] = k ? A[v] * ga[k][v] : ga[k][v];
@@ -371,6 +358,28 @@ __global__ __launch_bounds__(64 * (NW + 1), 4) void k_gated_fwd(GatedArgs a, Gat
     *reinterpret_cast<float4 *>(lA + at) = make_float4(A[0], A[1], A[2], A[3]);
     *reinterpret_cast<float4 *>(lB + at) = make_float4(B[0], B[1], B[2], B[3]);
     lds_barrier();
+    if (w == 0) {
+      const int rows = nw * 4;
+      float h = first;
+      if (live > 1) {
+        float tA = lA[lane], tB = lB[lane];
+#pragma unroll 3
+        for (int q = 1; q < rows; q++) {
+          const float qa = lA[q * G_CH + lane];
+          tB = fmaf(qa, tB, lB[q * G_CH + lane]);
+          tA *= qa;
+        }
+        if (tile + 1 < live) st_agent64(ch.agg + (tile * ch.cols + c) * 64 + (unsigned)lane, chain_word(tA, tB));
+        h = chain_enter(ch, c, tile, live, tA, tB, first);
+      }
+#pragma unroll 4
+      for (int q = 0; q < rows; q++) {
+        const float qa = lA[q * G_CH + lane], qb = lB[q * G_CH + lane];
+        lB[q * G_CH + lane] = h;
+        h = fmaf(qa, h, qb);
+      }
+      if (tile + 1 == live && a.hlast && owns) a.hlast[sd] = h;
+    }
     lds_barrier();
     const float4 h4 = *reinterpret_cast<const float4 *>(lB + at);
     float h[4] = {h4.x, h4.y, h4.z, h4.w};
@@ -397,59 +406,27 @@ __global__ __launch_bounds__(64 * (NW + 1), 4) void k_gated_fwd(GatedArgs a, Gat
 // step add to its state's gradient: mu_{t-1} = a_t (dy_t + mu_t), the same A as
 // forwards.  The tile's states are made again from the saved one.
 template <typename T, int K, int NW, int WPS>
-__global__ __launch_bounds__(64 * (NW + 1), WPS) void k_gated_adj(GatedArgs a, GatedChain ch) {
+__global__ __launch_bounds__(64 * NW, WPS) void k_gated_adj(GatedArgs a, GatedChain ch) {
   __shared__ float lds[3][4 * NW * G_CH];
+  __shared__ float4 lcv[K][64 * NW];  // dv = g cv
   __shared__ int sh;
   float *lA = lds[0], *lF = lds[1], *lR = lds[2];
   long long c;
   int order;
   if (!gated_tile(a, ch, &sh, &c, &order)) return;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = (blockDim.x >> 6) - 1;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
   const int rows = nw * 4, tile = a.tiles - 1 - order;
   const int b = (int)(c / a.cb), d0 = (int)(c % a.cb) * G_CH;
   const int len = __builtin_amdgcn_readfirstlane(seq_len(a.lengths, b, a.T));
   const int live = len > 0 ? (len - 1) / a.tt + 1 : 0;
   float *part = a.part ? a.part + ((long long)b * a.tiles + tile) * 3 * a.D + d0 : nullptr;
-  if (w == nw) {
-    const bool on = d0 + lane < a.D;
-    const long long sd = (long long)b * a.D + d0 + lane;
-    const int j = live - 1 - tile;  // place in the chain
-    float first = 0.f;
-    if ((j == 0 || (tile == 0 && live == 0)) && a.dhlast && on) first = a.dhlast[sd];
-    if (tile >= live) {
-      if (tile == 0 && on && a.dh0) a.dh0[sd] = first;
-      return;
-    }
-    float h = on ? a.states[((long long)b * a.nst + (long long)tile * a.tt / PR_GATED_STATE_STEPS) * a.D + d0 + lane] : 0.f;
-    lds_barrier();
-    float mu = first;
-    if (live > 1) {
-      float tA = lA[(rows - 1) * G_CH + lane], tB = lR[(rows - 1) * G_CH + lane];
-#pragma unroll 3
-      for (int q = rows - 2; q >= 0; q--) {
-        const float qa = lA[q * G_CH + lane];
-        tB = fmaf(qa, tB, lR[q * G_CH + lane]);
-        tA *= qa;
-      }
-      if (j + 1 < live) st_agent64(ch.agg + (j * ch.cols + c) * 64 + (unsigned)lane, chain_word(tA, tB));
-      mu = chain_enter(ch, c, j, live, tA, tB, first);
-    }
-#pragma unroll 4
-    for (int q = 0; q < rows; q++) {
-      const int m = rows - 1 - q;
-      const float fa = lA[q * G_CH + lane], fb = lF[q * G_CH + lane], ra = lA[m * G_CH + lane], rb = lR[m * G_CH + lane];
-      lF[q * G_CH + lane] = h;
-      lR[m * G_CH + lane] = mu;
-      h = fmaf(fa, h, fb);
-      mu = fmaf(ra, mu, rb);
-    }
-    lds_barrier();
-    if (tile == 0 && a.dh0 && on) a.dh0[sd] = mu;
-    if (!part) return;
-    lds_barrier();
-    lds_barrier();
-    return;
-  }
+  const int j = live - 1 - tile;  // place in the chain
+  const bool on = d0 + lane < a.D;
+  const long long sd = (long long)b * a.D + d0 + lane;
+  float first = 0.f, start = 0.f;  // wavefront 0 joins back in time, the last one forwards: a lane for each channel
+  if (w == 0 && (j == 0 || (tile == 0 && live == 0)) && a.dhlast && on) first = a.dhlast[sd];
+  if (w == nw - 1 && on && tile < live)
+    start = a.states[((long long)b * a.nst + (long long)tile * a.tt / PR_GATED_STATE_STEPS) * a.D + d0 + lane];
   GatedAt p;
   p.d = d0 + (lane & 15) * 4;
   p.n = a.D - p.d;
@@ -463,13 +440,14 @@ __global__ __launch_bounds__(64 * (NW + 1), WPS) void k_gated_adj(GatedArgs a, G
     if (part)
       for (int q = threadIdx.x; q < 3 * G_CH; q += 64 * nw)
         if (d0 + q % G_CH < a.D) part[(long long)(q / G_CH) * a.D + q % G_CH] = 0.f;
+    if (tile == 0 && w == 0 && on && a.dh0) a.dh0[sd] = first;
     return;
   }
   const int at = (w * 4 + (lane >> 4)) * G_CH + (lane & 15) * 4;
   float sums[3][4] = {};
   auto body = [&](auto full) __attribute__((always_inline)) {
     constexpr bool FULL = decltype(full)::value;
-    float ga[K][4], gm[K][4], gr[K][4], gi[K][4], cv[K][4], A[4], F[4];
+    float ga[K][4], gm[K][4], gr[K][4], gi[K][4], A[4], F[4];
     VecU<T, 4> x[K], gy[K];
     {
       const TileOf in[4] = {tile_of<T>(a.r, b, p.t0), tile_of<T>(a.i, b, p.t0), tile_of<T>(a.x, b, p.t0),
@@ -481,13 +459,13 @@ __global__ __launch_bounds__(64 * (NW + 1), WPS) void k_gated_adj(GatedArgs a, G
         x[k] = raw[2][k];
         gy[k] = raw[3][k];
       }
-      const GatedConsts cs = gated_consts(a, p);
+      const Consts4<T> cs = gated_consts<T>(a.decay, a.rb, a.ib, p.d, p.n);
 #pragma unroll
       for (int k = 0; k < K; k++) {
         const bool on = FULL || p.t0 + p.row + k < len;
 #pragma unroll
         for (int v = 0; v < 4; v++) {
-          const GateVals g = gate_vals<T>(raw[0][k].f(v) + cs.rb[v], raw[1][k].f(v) + cs.ib[v], cs.decay[v]);
+          const GateVals g = gate_vals<T>(raw[0][k].f(v), raw[1][k].f(v), cs.c[v]);
           if (!on) x[k].e[v] = gy[k].e[v] = 0;
           ga[k][v] = on ? g.a : 1.f;  // a step that is not there keeps mu and the state, and has no gradients
           gm[k][v] = on ? g.m : 0.f;
@@ -505,35 +483,73 @@ __global__ __launch_bounds__(64 * (NW + 1), WPS) void k_gated_adj(GatedArgs a, G
     for (int k = K - 1; k >= 0; k--)
 #pragma unroll
       for (int v = 0; v < 4; v++) R[v] = ga[k][v] * (gy[k].f(v) + R[v]);
+    // (the inputs stay as they were stored: unpacked they would take twice the registers)
+#pragma unroll
+    for (int k = 0; k < K; k++) asm volatile("" : "+v"(x[k].v), "+v"(gy[k].v));
     *reinterpret_cast<float4 *>(lA + at) = make_float4(A[0], A[1], A[2], A[3]);
     *reinterpret_cast<float4 *>(lF + at) = make_float4(F[0], F[1], F[2], F[3]);
     *reinterpret_cast<float4 *>(lR + at) = make_float4(R[0], R[1], R[2], R[3]);
     lds_barrier();
+    if (w == nw - 1) {
+      float h = start;
+#pragma unroll 4
+      for (int q = 0; q < rows; q++) {
+        const float qa = lA[q * G_CH + lane], qb = lF[q * G_CH + lane];
+        lF[q * G_CH + lane] = h;
+        h = fmaf(qa, h, qb);
+      }
+    }
+    if (w == 0) {
+      float mu = first;
+      if (live > 1) {
+        float tA = lA[(rows - 1) * G_CH + lane], tB = lR[(rows - 1) * G_CH + lane];
+#pragma unroll 3
+        for (int q = rows - 2; q >= 0; q--) {
+          const float qa = lA[q * G_CH + lane];
+          tB = fmaf(qa, tB, lR[q * G_CH + lane]);
+          tA *= qa;
+        }
+        if (j + 1 < live) st_agent64(ch.agg + (j * ch.cols + c) * 64 + (unsigned)lane, chain_word(tA, tB));
+        mu = chain_enter(ch, c, j, live, tA, tB, first);
+      }
+#pragma unroll 4
+      for (int q = rows - 1; q >= 0; q--) {
+        const float qa = lA[q * G_CH + lane], qb = lR[q * G_CH + lane];
+        lR[q * G_CH + lane] = mu;
+        mu = fmaf(qa, mu, qb);
+      }
+      if (tile == 0 && a.dh0 && on) a.dh0[sd] = mu;
+    }
     lds_barrier();
     // (the inputs stay as they were stored: unpacked they would take twice the registers)
 #pragma unroll
     for (int k = 0; k < K; k++) asm volatile("" : "+v"(x[k].v), "+v"(gy[k].v));
     const float4 h4 = *reinterpret_cast<const float4 *>(lF + at), m4 = *reinterpret_cast<const float4 *>(lR + at);
     float h[4] = {h4.x, h4.y, h4.z, h4.w}, mu[4] = {m4.x, m4.y, m4.z, m4.w};
+    // forwards through the lane's steps; m becomes m i
 #pragma unroll
-    for (int k = 0; k < K; k++)
+    for (int k = 0; k < K; k++) {
+      float cv[4];
 #pragma unroll
       for (int v = 0; v < 4; v++) {
-        // dv = g cv; m becomes m i
         const float m = gm[k][v], u = gi[k][v] * x[k].f(v), a1 = ga[k][v];
-        cv[k][v] = a1 * fmaf(a1 * (m > 0.f ? frcp(m) : 0.f), u, -h[v]);
+        cv[v] = a1 * fmaf(a1 * (m > 0.f ? frcp(m) : 0.f), u, -h[v]);
         h[v] = fmaf(a1, h[v], m * u);
         gm[k][v] = m * gi[k][v];
       }
+      lcv[k][threadIdx.x] = make_float4(cv[0], cv[1], cv[2], cv[3]);  // (read by this lane alone)
+    }
     const VecU<float, 4> decay = ldu<float, 4>(a.decay + p.d, p.n);
     const TileOf ox_ = tile_of<T>(a.dx, b, p.t0), or_ = tile_of<T>(a.dr, b, p.t0), oi_ = tile_of<T>(a.di, b, p.t0);
 #pragma unroll
     for (int k = K - 1; k >= 0; k--) {
-      const bool on = FULL || p.t0 + p.row + k < len;
+      const bool on = FULL || p.t0 + p.row + k < len;  // (in this step)
       float ox[4], orr[4], oi[4];
+      const float4 c4 = lcv[k][threadIdx.x];
+      const float cv[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
       for (int v = 0; v < 4; v++) {
-        const float g = gy[k].f(v) + mu[v], dv = on ? g * cv[k][v] : 0.f, r = gr[k][v], i = gi[k][v];
+        const float g = gy[k].f(v) + mu[v], dv = on ? g * cv[v] : 0.f, r = gr[k][v], i = gi[k][v];
         ox[v] = on ? g * gm[k][v] : 0.f;
         oi[v] = ox[v] * x[k].f(v) * (1.f - i);
         orr[v] = dv * decay.f(v) * (r * (1.f - r));
@@ -562,27 +578,29 @@ __global__ __launch_bounds__(64 * (NW + 1), WPS) void k_gated_adj(GatedArgs a, G
   }
 }
 
-// ddecay, dr_bias and dr_bias from the tiles' partials [P][3][D], in 64 bits in a
-// fixed order: 32 columns by 8 slices of the partials a block.
-__global__ __launch_bounds__(256) void k_gated_sums(const float *__restrict__ part, int P, int D, float *o0, float *o1,
-                                                    float *o2) {
-  __shared__ double sh[8][32];
+// ddecay, dr_bias and di_bias from the tiles' partials [P][3][D], in 64 bits in a
+// fixed order: 32 columns by 32 slices of the partials a block.
+__global__ __launch_bounds__(1024) void k_gated_sums(const float *__restrict__ part, int P, int D, float *o0, float *o1,
+                                                     float *o2) {
+  __shared__ double sh[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5, k = blockIdx.y, d = (int)blockIdx.x * 32 + x;
   float *o = k == 0 ? o0 : k == 1 ? o1 : o2;
   if (!o) return;
   double s = 0;
   if (d < D)
-    for (int p0 = y; p0 < P; p0 += 64) {
+    for (int p0 = y; p0 < P; p0 += 256) {
       float v[8];
 #pragma unroll
-      for (int q = 0; q < 8; q++) v[q] = p0 + 8 * q < P ? part[((p0 + 8LL * q) * 3 + k) * D + d] : 0.f;
+      for (int q = 0; q < 8; q++) v[q] = p0 + 32 * q < P ? part[((p0 + 32LL * q) * 3 + k) * D + d] : 0.f;
 #pragma unroll
       for (int q = 0; q < 8; q++) s += (double)v[q];
     }
   sh[y][x] = s;
-  __syncthreads();
-  if (y == 0 && d < D)
-    o[d] = (float)(((sh[0][x] + sh[1][x]) + (sh[2][x] + sh[3][x])) + ((sh[4][x] + sh[5][x]) + (sh[6][x] + sh[7][x])));
+  for (int h = 16; h >= 1; h >>= 1) {
+    __syncthreads();
+    if (y < h) sh[y][x] += sh[y + h][x];
+  }
+  if (y == 0 && d < D) o[d] = (float)sh[0][x];
 }
 
 // ---------------------------------------------------------------------------
@@ -610,11 +628,11 @@ __global__ __launch_bounds__(256) void k_gated_step(GatedStepArgs a) {
     float *hp = a.state + (long long)slot * a.D + d;
     const VecU<T, V> x = ldu<T, V>((const T *)a.x + b * a.sx + d, n), r = ldu<T, V>((const T *)a.r + b * a.sr + d, n),
                      i = ldu<T, V>((const T *)a.i + b * a.si + d, n);
-    const VecU<float, V> h = ldu<float, V>(hp, n), dc = ldu<float, V>(a.decay + d, n),
-                         rb = ldu<float, V>(a.rb + d, a.rb ? n : 0), ib = ldu<float, V>(a.ib + d, a.ib ? n : 0);
+    const VecU<float, V> h = ldu<float, V>(hp, n);
+    const Consts4<T> cs = gated_consts<T>(a.decay, a.rb, a.ib, d, n);
 #pragma unroll
     for (int k = 0; k < V; k++) {
-      const GateVals g = gate_vals<T>(r.f(k) + rb.f(k), i.f(k) + ib.f(k), dc.f(k));
+      const GateVals g = gate_vals<T>(r.f(k), i.f(k), cs.c[k]);
       o[k] = fmaf(g.a, h.f(k), g.m * g.i * x.f(k));
     }
     stu<float, V>(hp, o, n);
@@ -652,7 +670,7 @@ struct GatedGeom {
 };
 GatedGeom gated_geom(int dtype, bool adj) {
   if (!adj) return dtype == PR_BF16 ? GatedGeom{8, 4} : GatedGeom{4, 4};
-  return GatedGeom{2, 8};
+  return dtype == PR_BF16 ? GatedGeom{4, 4} : GatedGeom{2, 8};
 }
 
 struct GatedPlan {
@@ -760,8 +778,8 @@ int pararnn_gated_scan(const pr_gated_problem *p, const pr_gated_inputs *in, con
   GatedChain ch;
   HIPCHK(gated_chain(pl, workspace, &ch, s));
   const dim3 grid = flat_grid(pl.cols * pl.tiles);
-  if (p->dtype == PR_BF16) k_gated_fwd<uint16_t, 8, 4><<<grid, 64 * (pl.waves + 1), 0, s>>>(a, ch);
-  else k_gated_fwd<float, 4, 4><<<grid, 64 * (pl.waves + 1), 0, s>>>(a, ch);
+  if (p->dtype == PR_BF16) k_gated_fwd<uint16_t, 8, 4, 4><<<grid, 64 * pl.waves, 0, s>>>(a, ch);
+  else k_gated_fwd<float, 4, 4, 4><<<grid, 64 * pl.waves, 0, s>>>(a, ch);
   HIPCHK(hipGetLastError());
   return PR_OK;
 }
@@ -788,11 +806,11 @@ int pararnn_gated_adjoint(const pr_gated_problem *p, const pr_gated_inputs *in, 
   GatedChain ch;
   HIPCHK(gated_chain(pl, workspace, &ch, s));
   const dim3 grid = flat_grid(pl.cols * pl.tiles);
-  if (p->dtype == PR_BF16) k_gated_adj<uint16_t, 2, 8, 5><<<grid, 64 * (pl.waves + 1), 0, s>>>(a, ch);
-  else k_gated_adj<float, 2, 8, 5><<<grid, 64 * (pl.waves + 1), 0, s>>>(a, ch);
+  if (p->dtype == PR_BF16) k_gated_adj<uint16_t, 4, 4, 3><<<grid, 64 * pl.waves, 0, s>>>(a, ch);
+  else k_gated_adj<float, 2, 8, 4><<<grid, 64 * pl.waves, 0, s>>>(a, ch);
   HIPCHK(hipGetLastError());
   if (!sums) return PR_OK;
-  k_gated_sums<<<dim3((unsigned)((p->D + 31) / 32), 3), 256, 0, s>>>(a.part, p->B * pl.tiles, p->D, gr->decay,
+  k_gated_sums<<<dim3((unsigned)((p->D + 31) / 32), 3), 1024, 0, s>>>(a.part, p->B * pl.tiles, p->D, gr->decay,
                                                                       gr->r_bias, gr->i_bias);
   HIPCHK(hipGetLastError());
   return PR_OK;
