@@ -22,14 +22,22 @@ struct BnArgs {
   float eps;
 };
 
-// act(z) and its derivative
+// act(z) and its derivative.  The gate's kind is the same for a whole launch:
+// selects, so that no branch stands between the loads of a row.
+struct Gate {
+  bool there, silu;
+};
 struct Act {
   float v, d;
 };
-__device__ inline Act bn_act(int gate, float z) {
+__device__ inline float act_v(const Gate &g, float z) {
   const float p = fsigm(z);
-  if (gate == PR_GATE_SIGMOID) return Act{p, p * (1.f - p)};
-  return Act{z * p, p * fmaf(z, 1.f - p, 1.f)};
+  return g.there ? (g.silu ? z * p : p) : 1.f;
+}
+__device__ inline Act act_vd(const Gate &g, float z) {
+  const float p = fsigm(z), s = p * (1.f - p);
+  if (!g.there) return Act{1.f, 0.f};
+  return g.silu ? Act{z * p, fmaf(z, s, p)} : Act{p, s};
 }
 template <typename T>
 __device__ inline float to_storage(float v) {
@@ -51,6 +59,247 @@ __device__ inline float block_sum(float v, float *sh) {
   return (sh[0] + sh[1]) + (sh[2] + sh[3]);
 }
 
+// Rows that stay in registers: TPR threads a row, NV vectors of V elements (16
+// bytes) a thread.  EDGE: n is no multiple of V, and a row's last vector is its
+// last V elements, of which the first `dup` belong to the vector before: they are
+// left out of the sums, and written twice with the same values.
+template <typename T>
+constexpr int bn_v() { return 16 / (int)sizeof(T); }
+struct BnAt {
+  int c, dup;  // first element, or -1; elements that another thread counts
+};
+template <typename T, int TPR, bool EDGE>
+__device__ inline BnAt bn_at(int x, int m, int n) {
+  constexpr int V = bn_v<T>();
+  const int c = (x + m * TPR) * V;
+  if (c >= n) return BnAt{-1, V};
+  if (EDGE && c > n - V) return BnAt{n - V, c - (n - V)};
+  return BnAt{c, 0};
+}
+template <typename T>
+__device__ inline VecU<T, bn_v<T>()> bn_ld(const void *p, long long row, long long ld, const BnAt &at, bool there) {
+  return ldu<T, bn_v<T>()>((const T *)p + row * ld + at.c, there && at.c >= 0 ? bn_v<T>() : 0);
+}
+// N sums over the threads of a row, the same in all of them, in a fixed order;
+// rows of several wavefronts use one half of sh for each call, in turn.
+template <int TPR, int N>
+__device__ inline void row_sums(float (&v)[N], float (*sh)[16]) {
+#pragma unroll
+  for (int k = 0; k < N; k++) v[k] = wave_total(v[k]);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int k = 0; k < N; k++) sh[k][threadIdx.x >> 6] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; k++) {
+      float s = sh[k][0];
+#pragma unroll
+      for (int w = 1; w < W; w++) s += sh[k][w];
+      v[k] = s;
+    }
+  }
+}
+
+template <typename T, int TPR, int NV, bool EDGE>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
+  constexpr int V = bn_v<T>(), RPB = TPR > 256 ? 1 : 256 / TPR;
+  __shared__ float sh[2][1][16];
+  const int x = threadIdx.x % TPR;
+  const long long row = flat_block() * RPB + threadIdx.x / TPR;
+  if (row >= a.rows) return;  // whole wavefronts, whole rows
+  VecU<T, V> vx[NV], vz[NV], vr[NV];
+  float ss[1] = {0.f};
+#pragma unroll
+  for (int m = 0; m < NV; m++) {
+    const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+    vx[m] = bn_ld<T>(a.x, row, a.lx, at, true);
+    vz[m] = bn_ld<T>(a.z, row, a.lz, at, a.z != nullptr);
+    vr[m] = bn_ld<T>(a.res, row, a.lres, at, a.res != nullptr);
+  }
+  VecU<T, V> vw[NV], vs[NV], vn[NV];
+#pragma unroll
+  for (int m = 0; m < NV; m++) {
+    const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+    vw[m] = bn_ld<T>(a.w, 0, 0, at, a.w != nullptr);
+    vs[m] = bn_ld<T>(a.scale, 0, 0, at, a.scale != nullptr);
+    vn[m] = bn_ld<T>(a.wn, 0, 0, at, a.y && a.wn);
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const float v = vx[m].f(i);
+      ss[0] = !EDGE || i >= at.dup ? fmaf(v, v, ss[0]) : ss[0];
+    }
+  }
+  row_sums<TPR, 1>(ss, sh[0]);
+  const float rstd = 1.f / sqrtf(ss[0] / (float)a.n + a.eps);
+  const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
+  ss[0] = 0.f;
+  float t[NV][V];
+#pragma unroll
+  for (int m = 0; m < NV; m++) {
+    const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const float u = vx[m].f(i) * rstd * ((a.w ? vw[m].f(i) : 1.f) * (a.scale ? vs[m].f(i) : 1.f)) * act_v(gate, vz[m].f(i));
+      t[m][i] = to_storage<T>(a.res ? vr[m].f(i) + u : u);
+      ss[0] = !EDGE || i >= at.dup ? fmaf(t[m][i], t[m][i], ss[0]) : ss[0];
+    }
+    if (at.c >= 0) stu<T, V>((T *)a.t + row * a.lt + at.c, t[m], V);
+  }
+  if (!a.y) return;
+  row_sums<TPR, 1>(ss, sh[1]);
+  const float rstd2 = 1.f / sqrtf(ss[0] / (float)a.n + a.eps);
+#pragma unroll
+  for (int m = 0; m < NV; m++) {
+    const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+#pragma unroll
+    for (int i = 0; i < V; i++) t[m][i] *= rstd2 * (a.wn ? vn[m].f(i) : 1.f);
+    if (at.c >= 0) stu<T, V>((T *)a.y + row * a.ly + at.c, t[m], V);
+  }
+}
+
+// The adjoint on rows in registers.  One round of sums for a row: with
+// F = w scale act(z) x, sum(e x) = sum(dt F) + rstd2 (sum(w_next dy F) - k2 sum(t F)),
+// k2 = rstd2^2 mean(w_next dy t).  Blocks walk rows with a stride of the grid and
+// keep their columns' sums in registers.  Rows of more than 512 threads are loaded
+// again, from cache, once their sums are known: there are no registers for them.
+template <typename T, int TPR, int NV, bool EDGE>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 || TPR > 512 ? 4 : 2) void k_bn_adj(BnArgs a) {
+  constexpr int V = bn_v<T>(), RPB = TPR > 256 ? 1 : 256 / TPR, NT = TPR > 256 ? TPR : 256;
+  constexpr bool AGAIN = TPR > 512;
+  __shared__ float sh[2][6][16];
+  const int x = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
+  float q[NV][V], qn[NV][V];
+  VecU<T, V> vw[NV], vs[NV], vn[NV];
+  auto weights = [&](int m) __attribute__((always_inline)) {
+    const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+    vw[m] = bn_ld<T>(a.w, 0, 0, at, a.w != nullptr);
+    vs[m] = bn_ld<T>(a.scale, 0, 0, at, a.scale != nullptr);
+    vn[m] = bn_ld<T>(a.wn, 0, 0, at, a.wn != nullptr);
+  };
+  auto F = [&](int m, int i) __attribute__((always_inline)) {
+    return (a.w ? vw[m].f(i) : 1.f) * (a.scale ? vs[m].f(i) : 1.f);
+  };
+  auto wn = [&](int m, int i) __attribute__((always_inline)) { return a.wn ? vn[m].f(i) : 1.f; };
+#pragma unroll
+  for (int m = 0; m < NV; m++) {
+    if constexpr (!AGAIN) weights(m);
+#pragma unroll
+    for (int i = 0; i < V; i++) q[m][i] = qn[m][i] = 0.f;
+  }
+  int par = 0;
+  for (long long row = (long long)blockIdx.x * RPB + sub; row < a.rows; row += (long long)gridDim.x * RPB) {
+    VecU<T, V> vx[NV], vz[NV], vt[NV], vd[NV], vy[NV];
+    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    auto load = [&](int m) __attribute__((always_inline)) {
+      const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+      vx[m] = bn_ld<T>(a.x, row, a.lx, at, true);
+      vz[m] = bn_ld<T>(a.z, row, a.lz, at, a.z != nullptr);
+      vt[m] = bn_ld<T>(a.t, row, a.lt, at, a.dy != nullptr);
+      vy[m] = bn_ld<T>(a.dy, row, a.ldy, at, a.dy != nullptr);
+      vd[m] = bn_ld<T>(a.dt, row, a.ldt, at, a.dt != nullptr);
+    };
+    if constexpr (!AGAIN)
+#pragma unroll
+      for (int m = 0; m < NV; m++) load(m);
+#pragma unroll
+    for (int m = 0; m < NV; m++) {
+      const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+      if constexpr (AGAIN) {
+        asm volatile("" ::: "memory");  // (one vector's loads at a time)
+        weights(m);
+        load(m);
+      } else {  // (as they were stored: unpacked they would take twice the registers)
+        asm volatile("" : "+v"(vw[m].v), "+v"(vs[m].v), "+v"(vn[m].v));
+      }
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        if (EDGE && i < at.dup) continue;
+        const float xx = vx[m].f(i), t = vt[m].f(i), e = wn(m, i) * vy[m].f(i);
+        const float f = F(m, i) * act_v(gate, vz[m].f(i)) * xx;
+        s[0] = fmaf(xx, xx, s[0]);
+        s[1] = fmaf(vd[m].f(i), f, s[1]);
+        s[2] = fmaf(t, t, s[2]);
+        s[3] = fmaf(e, t, s[3]);
+        s[4] = fmaf(e, f, s[4]);
+        s[5] = fmaf(t, f, s[5]);
+      }
+    }
+    row_sums<TPR, 6>(s, sh[par]);
+    par ^= 1;  // the next row's sums go to the other half
+    const float n = (float)a.n, rstd1 = 1.f / sqrtf(s[0] / n + a.eps);
+    const float rstd2 = a.dy ? 1.f / sqrtf(s[2] / n + a.eps) : 0.f;  // without dy: t and dy are zeros
+    const float k2 = s[3] / n * rstd2 * rstd2, k1 = (s[1] + rstd2 * (s[4] - k2 * s[5])) / n * rstd1 * rstd1;
+#pragma unroll
+    for (int m = 0; m < NV; m++) {
+      const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+      float ox[V], oz[V], og[V];
+      if constexpr (AGAIN) {
+        asm volatile("" ::: "memory");  // (one vector's loads at a time)
+        weights(m);
+        load(m);
+      } else {
+        asm volatile("" : "+v"(vx[m].v), "+v"(vz[m].v), "+v"(vt[m].v), "+v"(vd[m].v), "+v"(vy[m].v));
+        asm volatile("" : "+v"(vw[m].v), "+v"(vs[m].v), "+v"(vn[m].v));
+      }
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        const float xh = vx[m].f(i) * rstd1, t = vt[m].f(i), dy = vy[m].f(i), f = F(m, i);
+        const Act act = act_vd(gate, vz[m].f(i));
+        const float g = fmaf(rstd2, fmaf(-t, k2, wn(m, i) * dy), vd[m].f(i));
+        qn[m][i] = fmaf(dy, t * rstd2, qn[m][i]);
+        q[m][i] = fmaf(g * act.v, xh, q[m][i]);
+        og[i] = g;
+        oz[i] = g * f * xh * act.d;
+        ox[i] = rstd1 * fmaf(-vx[m].f(i), k1, g * f * act.v);
+      }
+      if (at.c >= 0) {
+        if (a.dres) stu<T, V>((T *)a.dres + row * a.ldres + at.c, og, V);
+        if (a.dz) stu<T, V>((T *)a.dz + row * a.ldz + at.c, oz, V);
+        if (a.dx) stu<T, V>((T *)a.dx + row * a.ldx + at.c, ox, V);
+      }
+    }
+  }
+  if (!a.part) return;
+  float *pp = a.part + blockIdx.x * 2LL * a.n;
+  if constexpr (RPB == 1) {
+#pragma unroll
+    for (int m = 0; m < NV; m++) {
+      const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+      if (at.c >= 0) {  // (elements that two threads hold have the same sums)
+        stu<float, 4>(pp + at.c, q[m], 4);
+        stu<float, 4>(pp + a.n + at.c, qn[m], 4);
+        if constexpr (V == 8) {
+          stu<float, 4>(pp + at.c + 4, q[m] + 4, 4);
+          stu<float, 4>(pp + a.n + at.c + 4, qn[m] + 4, 4);
+        }
+      }
+    }
+  } else {  // join the block's rows
+    __shared__ float red[RPB][NV * V * TPR];
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      __syncthreads();
+#pragma unroll
+      for (int m = 0; m < NV; m++) {
+        const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+#pragma unroll
+        for (int i = 0; i < V; i++)
+          if (at.c >= 0 && i >= at.dup) red[sub][at.c + i] = k ? qn[m][i] : q[m][i];
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.n; c += NT) {
+        float v = red[0][c];
+#pragma unroll
+        for (int m = 1; m < RPB; m++) v += red[m][c];
+        pp[(long long)k * a.n + c] = v;
+      }
+    }
+  }
+}
+
 // Long rows: a block reads its row again for each pass.
 template <typename T>
 __global__ __launch_bounds__(256) void k_bn_long(BnArgs a) {
@@ -59,6 +308,7 @@ __global__ __launch_bounds__(256) void k_bn_long(BnArgs a) {
   if (row >= a.rows) return;
   const T *xp = (const T *)a.x + row * a.lx, *zp = (const T *)a.z + row * a.lz, *rp = (const T *)a.res + row * a.lres;
   T *tp = (T *)a.t + row * a.lt;
+  const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
   float ss = 0.f;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     const float v = ldf(xp, c);
@@ -68,7 +318,7 @@ __global__ __launch_bounds__(256) void k_bn_long(BnArgs a) {
   ss = 0.f;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     float u = ldf(xp, c) * rstd * (at1<T>(a.w, c) * at1<T>(a.scale, c));
-    if (a.z) u *= bn_act(a.gate, ldf(zp, c)).v;
+    if (a.z) u *= act_v(gate, ldf(zp, c));
     const float t = to_storage<T>(a.res ? ldf(rp, c) + u : u);
     stf(tp, c, t);
     ss = fmaf(t, t, ss);
@@ -124,11 +374,12 @@ __global__ __launch_bounds__(256) void k_bn_adj_cols(BnArgs a, int slices) {
   if (c >= a.n) return;
   const long long per = (a.rows + slices - 1) / slices, r0 = blockIdx.y * per;
   const long long r1 = r0 + per < a.rows ? r0 + per : a.rows;
+  const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
   float q = 0.f, wn = 0.f;
   for (long long r = r0; r < r1; r++) {
     const BnRow s{a.stat[r * 3], a.stat[r * 3 + 1], a.stat[r * 3 + 2]};
     const float xh = ldf((const T *)a.x + r * a.lx, c) * s.rstd1;
-    const float act = a.z ? bn_act(a.gate, ldf((const T *)a.z + r * a.lz, c)).v : 1.f;
+    const float act = a.z ? act_v(gate, ldf((const T *)a.z + r * a.lz, c)) : 1.f;
     q = fmaf(bn_gt<T>(a, s, r, c) * act, xh, q);
     if (a.dy)
       wn = fmaf(ldf((const T *)a.dy + r * a.ldy, c), ldf((const T *)a.t + r * a.lt, c) * s.rstd2, wn);
@@ -143,31 +394,101 @@ __global__ __launch_bounds__(256) void k_bn_adj_long(BnArgs a) {
   if (row >= a.rows) return;
   const BnRow s{a.stat[row * 3], a.stat[row * 3 + 1], a.stat[row * 3 + 2]};
   const T *xp = (const T *)a.x + row * a.lx, *zp = (const T *)a.z + row * a.lz;
+  const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
   float dot = 0.f;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     float e = bn_gt<T>(a, s, row, c) * (at1<T>(a.w, c) * at1<T>(a.scale, c));
-    if (a.z) e *= bn_act(a.gate, ldf(zp, c)).v;
+    if (a.z) e *= act_v(gate, ldf(zp, c));
     dot = fmaf(e, ldf(xp, c), dot);
   }
   const float k1 = block_sum(dot, sh) / (float)a.n * s.rstd1 * s.rstd1;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     const float gt = bn_gt<T>(a, s, row, c), ws = at1<T>(a.w, c) * at1<T>(a.scale, c), x = ldf(xp, c);
-    const Act act = a.z ? bn_act(a.gate, ldf(zp, c)) : Act{1.f, 0.f};
+    const Act act = act_vd(gate, a.z ? ldf(zp, c) : 0.f);
     if (a.dres) stf((T *)a.dres + row * a.ldres, c, gt);
     if (a.dz) stf((T *)a.dz + row * a.ldz, c, gt * ws * (x * s.rstd1) * act.d);
     if (a.dx) stf((T *)a.dx + row * a.ldx, c, s.rstd1 * fmaf(-x, k1, gt * ws * act.v));
   }
 }
 
-// The weights' gradients from the sums of the columns: q [n] becomes dw and dscale.
+// The weights' gradients from the partials [P][2][n], in 64 bits in a fixed
+// order: 32 columns by 32 slices of the partials a block.
 template <typename T>
-__global__ __launch_bounds__(256) void k_bn_weights(const float *q, const void *w, const void *scale, int n, float *dw,
-                                                    float *dscale) {
-  const int c = (int)blockIdx.x * 256 + threadIdx.x;
-  if (c >= n) return;
-  const float v = q[c];
-  if (dw) dw[c] = v * at1<T>(scale, c);
-  if (dscale) dscale[c] = v * at1<T>(w, c);
+__global__ __launch_bounds__(1024) void k_bn_sums(const float *__restrict__ part, int P, int n, const void *w,
+                                                  const void *scale, float *dw, float *dscale, float *dwn) {
+  __shared__ double sh[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, k = blockIdx.y, c = (int)blockIdx.x * 32 + x;
+  if (k ? !dwn : !dw && !dscale) return;
+  double s = 0;
+  if (c < n)
+    for (int p0 = y; p0 < P; p0 += 256) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; q++) v[q] = p0 + 32 * q < P ? part[((p0 + 32LL * q) * 2 + k) * n + c] : 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; q++) s += (double)v[q];
+    }
+  sh[y][x] = s;
+  for (int h = 16; h >= 1; h >>= 1) {
+    __syncthreads();
+    if (y < h) sh[y][x] += sh[y + h][x];
+  }
+  if (y != 0 || c >= n) return;
+  const float v = (float)sh[0][x];
+  if (k) {
+    dwn[c] = v;
+  } else {
+    if (dw) dw[c] = v * at1<T>(scale, c);
+    if (dscale) dscale[c] = v * at1<T>(w, c);
+  }
+}
+
+// Threads and vectors of a row of q vectors; 0 threads: the row is read again
+// for each pass.  The adjoint holds five inputs and two sums, so at most two
+// vectors a thread.
+struct BnGeom {
+  int tpr, nv;
+};
+static BnGeom bn_geom(int n, int V, bool adj) {
+  if (n < V) return {0, 0};
+  const int q = (n + V - 1) / V;
+  if (q <= 64) return {64, 1};
+  if (q <= 128) return {64, 2};
+  if (q <= 256) return {256, 1};
+  if (q <= 512) return {256, 2};
+  if (q <= 1024) return adj ? BnGeom{512, 2} : BnGeom{256, 4};
+  if (q <= 2048) return adj ? BnGeom{1024, 2} : BnGeom{512, 4};
+  return {0, 0};
+}
+
+// (FOR_ADJ: the geometry is the adjoint's or the forward's alone; -1: both's)
+template <typename T, int TPR, int NV, int FOR_ADJ = -1>
+void bn_go(const BnArgs &a, bool adj, unsigned blocks, hipStream_t s) {
+  constexpr int NT = TPR > 256 ? TPR : 256;
+  const bool edge = a.n % bn_v<T>() != 0;
+  const dim3 rows = flat_grid((a.rows + NT / TPR - 1) / (NT / TPR));
+  if constexpr (FOR_ADJ != 0)
+    if (adj) {
+      if (edge) k_bn_adj<T, TPR, NV, true><<<blocks, NT, 0, s>>>(a);
+      else k_bn_adj<T, TPR, NV, false><<<blocks, NT, 0, s>>>(a);
+    }
+  if constexpr (FOR_ADJ != 1)
+    if (!adj) {
+      if (edge) k_bn<T, TPR, NV, true><<<rows, NT, 0, s>>>(a);
+      else k_bn<T, TPR, NV, false><<<rows, NT, 0, s>>>(a);
+    }
+}
+template <typename T>
+hipError_t bn_launch(const BnArgs &a, const BnGeom &g, bool adj, unsigned blocks, hipStream_t s) {
+  if (g.tpr == 64 && g.nv == 1) bn_go<T, 64, 1>(a, adj, blocks, s);
+  else if (g.tpr == 64) bn_go<T, 64, 2>(a, adj, blocks, s);
+  else if (g.tpr == 256 && g.nv == 1) bn_go<T, 256, 1>(a, adj, blocks, s);
+  else if (g.tpr == 256 && g.nv == 2) bn_go<T, 256, 2>(a, adj, blocks, s);
+  else if (g.tpr == 256) bn_go<T, 256, 4, false>(a, adj, blocks, s);
+  else if (g.tpr == 1024) bn_go<T, 1024, 2, true>(a, adj, blocks, s);
+  else if (adj) bn_go<T, 512, 2, true>(a, adj, blocks, s);
+  else bn_go<T, 512, 4, false>(a, adj, blocks, s);
+  return hipGetLastError();
 }
 
 }  // namespace pr
@@ -210,16 +531,24 @@ int bn_fill(const pr_block_norm_problem *p, const pr_rows *x, const pr_rows *z, 
 }
 
 struct BnPlan {
-  size_t off_part, off_q, bytes;
+  BnGeom g;
+  size_t off_part, bytes;
   int parts;
 };
 BnPlan bn_plan(const pr_block_norm_problem *p) {
   BnPlan pl;
-  pl.parts = BN_SLICES;
-  size_t o = align256((size_t)p->rows * 12);
-  pl.off_part = o; o = align256(o + (size_t)pl.parts * 2 * p->n * 4);
-  pl.off_q = o; o = align256(o + (size_t)p->n * 4);
-  pl.bytes = o;
+  pl.g = bn_geom(p->n, p->dtype == PR_BF16 ? 8 : 4, true);
+  size_t o = 0;
+  if (pl.g.tpr) {  // a few rows a block, so that the partials are few
+    const long long rpb = pl.g.tpr > 256 ? 1 : 256 / pl.g.tpr, b = (p->rows + rpb - 1) / rpb;
+    const long long most = pl.g.tpr > 256 ? 1024 * 256 / pl.g.tpr : 1024;
+    pl.parts = (int)(b < most ? b : most);
+  } else {
+    pl.parts = BN_SLICES;
+    o = align256((size_t)p->rows * 12);
+  }
+  pl.off_part = o;
+  pl.bytes = align256(o + (size_t)pl.parts * 2 * p->n * 4);
   return pl;
 }
 
@@ -240,6 +569,11 @@ int pararnn_block_norm(const pr_block_norm_problem *p, const pr_rows *x, const p
   if (has(residual)) { a.res = residual->p; a.lres = residual->ld; }
   if (has(y)) { a.y = y->p; a.ly = y->ld; }
   hipStream_t s = (hipStream_t)stream;
+  const BnGeom g = bn_geom(p->n, p->dtype == PR_BF16 ? 8 : 4, false);
+  if (g.tpr) {
+    HIPCHK(p->dtype == PR_BF16 ? bn_launch<uint16_t>(a, g, false, 0, s) : bn_launch<float>(a, g, false, 0, s));
+    return PR_OK;
+  }
   const dim3 grid = flat_grid(p->rows);
   if (p->dtype == PR_BF16) k_bn_long<uint16_t><<<grid, 256, 0, s>>>(a);
   else k_bn_long<float><<<grid, 256, 0, s>>>(a);
@@ -275,33 +609,36 @@ int pararnn_block_norm_adjoint(const pr_block_norm_problem *p, const pr_rows *x,
   if (has(dy)) { a.dy = dy->p; a.ldy = dy->ld; }
   a.dx = gr->x.p; a.ldx = gr->x.ld; a.dz = gr->z.p; a.ldz = gr->z.ld; a.dres = gr->res.p; a.ldres = gr->res.ld;
   char *ws = (char *)workspace;
-  a.stat = (float *)ws;
-  a.part = (float *)(ws + pl.off_part);
-  float *q = (float *)(ws + pl.off_q);
-  hipStream_t s = (hipStream_t)stream;
-  const dim3 grid = flat_grid(p->rows), cols((unsigned)((p->n + 255) / 256), (unsigned)pl.parts);
   const bool bf = p->dtype == PR_BF16, sums = gr->w || gr->scale || gr->w_next;
-  if (bf) k_bn_adj_stat<uint16_t><<<grid, 256, 0, s>>>(a);
-  else k_bn_adj_stat<float><<<grid, 256, 0, s>>>(a);
+  float *part = (float *)(ws + pl.off_part);
+  hipStream_t s = (hipStream_t)stream;
+  if (pl.g.tpr) {
+    a.part = sums ? part : nullptr;
+    HIPCHK(bf ? bn_launch<uint16_t>(a, pl.g, true, (unsigned)pl.parts, s)
+              : bn_launch<float>(a, pl.g, true, (unsigned)pl.parts, s));
+  } else {
+    a.stat = (float *)ws;
+    a.part = part;
+    const dim3 grid = flat_grid(p->rows), cols((unsigned)((p->n + 255) / 256), (unsigned)pl.parts);
+    if (bf) k_bn_adj_stat<uint16_t><<<grid, 256, 0, s>>>(a);
+    else k_bn_adj_stat<float><<<grid, 256, 0, s>>>(a);
+    HIPCHK(hipGetLastError());
+    if (sums) {  // before the rows' gradients, of which dres may stand over dt
+      if (bf) k_bn_adj_cols<uint16_t><<<cols, 256, 0, s>>>(a, pl.parts);
+      else k_bn_adj_cols<float><<<cols, 256, 0, s>>>(a, pl.parts);
+      HIPCHK(hipGetLastError());
+    }
+    if (a.dx || a.dz || a.dres) {
+      if (bf) k_bn_adj_long<uint16_t><<<grid, 256, 0, s>>>(a);
+      else k_bn_adj_long<float><<<grid, 256, 0, s>>>(a);
+      HIPCHK(hipGetLastError());
+    }
+  }
+  if (!sums) return PR_OK;
+  const dim3 grid((unsigned)((p->n + 31) / 32), 2);
+  if (bf) k_bn_sums<uint16_t><<<grid, 1024, 0, s>>>(part, pl.parts, p->n, w, scale, gr->w, gr->scale, gr->w_next);
+  else k_bn_sums<float><<<grid, 1024, 0, s>>>(part, pl.parts, p->n, w, scale, gr->w, gr->scale, gr->w_next);
   HIPCHK(hipGetLastError());
-  if (sums) {  // before the rows' gradients, of which dres may stand over dt
-    if (bf) k_bn_adj_cols<uint16_t><<<cols, 256, 0, s>>>(a, pl.parts);
-    else k_bn_adj_cols<float><<<cols, 256, 0, s>>>(a, pl.parts);
-    HIPCHK(hipGetLastError());
-  }
-  if (a.dx || a.dz || a.dres) {
-    if (bf) k_bn_adj_long<uint16_t><<<grid, 256, 0, s>>>(a);
-    else k_bn_adj_long<float><<<grid, 256, 0, s>>>(a);
-    HIPCHK(hipGetLastError());
-  }
-  if (gr->w || gr->scale) {
-    HIPCHK(launch_part_sum(a.part, pl.parts, 2LL * p->n, p->n, q, s));
-    const unsigned nb = (unsigned)((p->n + 255) / 256);
-    if (bf) k_bn_weights<uint16_t><<<nb, 256, 0, s>>>(q, w, scale, p->n, gr->w, gr->scale);
-    else k_bn_weights<float><<<nb, 256, 0, s>>>(q, w, scale, p->n, gr->w, gr->scale);
-    HIPCHK(hipGetLastError());
-  }
-  if (gr->w_next) HIPCHK(launch_part_sum(a.part + p->n, pl.parts, 2LL * p->n, p->n, gr->w_next, s));
   return PR_OK;
 }
 
