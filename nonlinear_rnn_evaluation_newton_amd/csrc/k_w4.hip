@@ -13,30 +13,242 @@ struct W4Args {
   void *out;
   long long ldx, ldq, ldo;
   int M, N, K, group, G;  // G: groups of a row
+  float rgroup;           // 32 / group
 };
 
-// One wavefront for each row of weights and eight rows of x.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4v __attribute__((ext_vector_type(4)));
+constexpr int W4_CH = 128;  // columns of a wavefront's step: 16 bytes of 4-bit numbers a lane
+constexpr int W4_WAVES = 8;
+
+// Operands of v_mfma_f32_16x16x32_bf16 for 8 adjacent columns k0..k7 of a lane, in
+// the order k0 k4, k1 k5, k2 k6, k3 k7: both operands have the same, and a product's
+// terms may come in any.
+__device__ inline bf16x8 words(unsigned a, unsigned b, unsigned c, unsigned d) {
+  return __builtin_bit_cast(bf16x8, u32x4v{a, b, c, d});
+}
+// 16 + q for the eight numbers of a word: q in the upper four bits of a bf16 with
+// the exponent of 16, two numbers an operation.  The 16 (and the zero point) are
+// taken off by the sums of x, which the matrix unit makes from an operand of ones.
+__device__ inline bf16x8 w4_operand(unsigned w) {
+  constexpr unsigned M = 0x00780078u, E = 0x41804180u;
+  return words(((w << 3) & M) | E, ((w >> 1) & M) | E, ((w >> 5) & M) | E, ((w >> 9) & M) | E);
+}
+__device__ inline unsigned halves(unsigned lo, unsigned hi, bool upper) {  // their lower or upper 16 bits side by side
+  return __builtin_amdgcn_perm(hi, lo, upper ? 0x07060302u : 0x05040100u);
+}
+// Eight columns of x as operands: bf16 rows give one, fp32 ones three whose sum is
+// x, eight bits each.
 template <typename T>
-__global__ __launch_bounds__(256) void k_w4_plain(W4Args a) {
-  const int n = (int)blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63, m0 = (int)blockIdx.y * 8;
-  if (n >= a.N) return;
-  const uint8_t *qp = a.q + n * a.ldq;
-  float acc[8] = {};
-  for (int k = lane; k < a.K; k += 64) {
-    const int g = k / a.group;
-    const float s = ldf((const T *)a.scale, (long long)n * a.G + g);
-    const float z = a.zero ? ldf((const T *)a.zero, (long long)n * a.G + g) : 8.f;
-    const float w = ((float)((qp[k >> 1] >> (4 * (k & 1))) & 15) - z) * s;
+struct XOps;
+template <>
+struct XOps<uint16_t> {
+  static constexpr int N = 1;
+  bf16x8 o[1];
+  __device__ void set(const VecU<uint16_t, 8> &x) {
+    o[0] = words(halves(x.v.x, x.v.z, false), halves(x.v.x, x.v.z, true), halves(x.v.y, x.v.w, false),
+                 halves(x.v.y, x.v.w, true));
+  }
+};
+template <>
+struct XOps<float> {
+  static constexpr int N = 3;
+  bf16x8 o[3];
+  __device__ void set(const VecU<float, 8> &x) {
+    unsigned p[3][4];
 #pragma unroll
-    for (int i = 0; i < 8; i++)
-      if (m0 + i < a.M) acc[i] = fmaf(w, ldf((const T *)a.x + (m0 + i) * a.ldx, k), acc[i]);
+    for (int k = 0; k < 4; k++) {
+      float a = x.e[k], b = x.e[k + 4];
+#pragma unroll
+      for (int s = 0; s < 3; s++) {
+        p[s][k] = halves(__float_as_uint(a), __float_as_uint(b), true);
+        a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+        b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 3; s++) o[s] = words(p[s][0], p[s][1], p[s][2], p[s][3]);
+  }
+};
+
+// What a step of 128 columns reads.
+template <typename T, int MT, int NT>
+struct W4Step {
+  u32x4v w[NT];         // 32 numbers of one row of weights: words of 8
+  VecU<T, 8> x[MT][4];  // columns 32 j + 8 q .. of one row of x
+  float s[NT][4], z[NT][4];
+};
+
+// MT x NT tiles of 16 rows of x by 16 columns of the output; eight wavefronts share
+// K in steps of 128 and join in shared memory.  ONE: a step lies in one group.
+template <typename T, int MT, int NT, bool ONE>
+__global__ __launch_bounds__(64 * W4_WAVES) void k_w4_rows(W4Args a) {
+  __shared__ float red[W4_WAVES][NT * 256];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, q = lane >> 4;
+  const int nb = (a.N + 16 * NT - 1) / (16 * NT);
+  const int n0 = (int)(blockIdx.x % nb) * 16 * NT, m0 = (int)(blockIdx.x / nb) * 16 * MT;
+  // rows past the end read the last one; their results are not stored
+  const uint8_t *wp[NT];
+  const T *xp[MT], *sp[NT], *zp[NT];
+#pragma unroll
+  for (int j = 0; j < NT; j++) {
+    const int n = n0 + j * 16 + c < a.N ? n0 + j * 16 + c : a.N - 1;
+    wp[j] = a.q + n * a.ldq + q * 16;
+    sp[j] = (const T *)a.scale + (long long)n * a.G;
+    zp[j] = (const T *)a.zero + (long long)n * a.G;
   }
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const float v = wave_total(acc[i]);
-    if (lane == 0 && m0 + i < a.M)
-      stf((T *)a.out + (m0 + i) * a.ldo, n, v + (a.bias ? ldf((const T *)a.bias, n) : 0.f));
+  for (int i = 0; i < MT; i++) {
+    const int m = m0 + i * 16 + c < a.M ? m0 + i * 16 + c : a.M - 1;
+    xp[i] = (const T *)a.x + m * a.ldx + q * 8;
   }
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; i++)
+#pragma unroll
+    for (int j = 0; j < NT; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // the group of the 32 columns from k on (k / 32 below 2^19: the product is off by
+  // less than the half that separates it from the next number)
+  auto group = [&](int k) { return (int)(((float)(k >> 5) + 0.5f) * a.rgroup); };
+  auto load = [&](W4Step<T, MT, NT> &s, int kb) __attribute__((always_inline)) {
+    const bool full = kb + W4_CH <= a.K;
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      if (full) {
+        s.w[j] = reinterpret_cast<const Packed<uint8_t, 16> *>(wp[j] + (kb >> 1))->v;
+      } else {  // bytes past the row's end are not read
+        const int left = (a.K + 1) / 2 - (kb >> 1) - q * 16;
+        VecU<uint8_t, 16> b = ldu<uint8_t, 16>(wp[j] + (kb >> 1), left);
+        s.w[j] = b.v;
+      }
+#pragma unroll
+      for (int u = 0; u < (ONE ? 1 : 4); u++) {
+        int g = group(kb + 32 * u);
+        if (!full) g = g < a.G ? g : a.G - 1;
+        s.s[j][u] = ldf(sp[j], g);
+        s.z[j][u] = a.zero ? ldf(zp[j], g) : 8.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const T *p = xp[i] + kb + 32 * u;
+        if (full) s.x[i][u].v = reinterpret_cast<const Packed<T, 8> *>(p)->v;
+        else s.x[i][u] = ldu<T, 8>(p, a.K - kb - 32 * u - 8 * q);  // zeros past the end
+      }
+  };
+  const bf16x8 ones = words(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+  const f32x4 nil = {0.f, 0.f, 0.f, 0.f};
+  auto product = [&](W4Step<T, MT, NT> &s) __attribute__((always_inline)) {
+    // lane q's word j holds columns 32 q + 8 j ..; the matrix product of 32 columns
+    // wants 32 j + 8 q ..: a transposition of 4 x 4 words between the lanes' rows
+    bf16x8 b[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const auto e = __builtin_amdgcn_permlane32_swap(s.w[j][0], s.w[j][2], false, false);
+      const auto f = __builtin_amdgcn_permlane32_swap(s.w[j][1], s.w[j][3], false, false);
+      const auto g = __builtin_amdgcn_permlane16_swap(e[0], f[0], false, false);
+      const auto h = __builtin_amdgcn_permlane16_swap(e[1], f[1], false, false);
+      b[j][0] = w4_operand(g[0]);
+      b[j][1] = w4_operand(g[1]);
+      b[j][2] = w4_operand(h[0]);
+      b[j][3] = w4_operand(h[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+      f32x4 xs = nil, d[NT];
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        XOps<T> x;
+        x.set(s.x[i][u]);
+        if (!ONE || u == 0) {
+          xs = nil;
+#pragma unroll
+          for (int j = 0; j < NT; j++) d[j] = nil;
+        }
+#pragma unroll
+        for (int o = 0; o < XOps<T>::N; o++) {
+          xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.o[o], ones, xs, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < NT; j++) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.o[o], b[j][u], d[j], 0, 0, 0);
+        }
+        if (!ONE || u == 3) {
+#pragma unroll
+          for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+              acc[i][j][r] = fmaf(s.s[j][ONE ? 0 : u], fmaf(-16.f - s.z[j][ONE ? 0 : u], xs[r], d[j][r]), acc[i][j][r]);
+        }
+      }
+    }
+  };
+  constexpr int STEP = W4_CH * W4_WAVES, U = MT * NT == 1 && sizeof(T) == 2 ? 4 : MT * NT <= 4 && sizeof(T) == 2 ? 2 : 1;
+  int kb = wave * W4_CH;
+  for (; kb + (U - 1) * STEP < a.K; kb += U * STEP) {
+    W4Step<T, MT, NT> s[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) load(s[u], kb + u * STEP);
+#pragma unroll
+    for (int u = 0; u < U; u++) product(s[u]);
+  }
+  if constexpr (U > 1)
+    for (; kb < a.K; kb += STEP) {
+      W4Step<T, MT, NT> s;
+      load(s, kb);
+      product(s);
+    }
+#pragma unroll
+  for (int i = 0; i < MT; i++) {
+    if (i) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) red[wave][(q * 4 + r) * 16 * NT + j * 16 + c] = acc[i][j][r];
+    __syncthreads();
+    for (int e = threadIdx.x; e < NT * 256; e += 64 * W4_WAVES) {
+      const int m = m0 + i * 16 + e / (16 * NT), n = n0 + e % (16 * NT);
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < W4_WAVES; w++) v += red[w][e];
+      if (m < a.M && n < a.N) stf((T *)a.out + m * a.ldo, n, a.bias ? v + ldf((const T *)a.bias, n) : v);
+    }
+  }
+}
+
+// Tiles of a block: columns side by side where there are blocks enough for all CUs
+// without, since every block reads all of x.  At most 4 x 2 tiles of bf16 rows and
+// 2 x 2 of fp32 ones, whose operands take three times the registers.
+struct W4Geom {
+  int mt, nt;
+};
+static W4Geom w4_geom(int dtype, int M, int N) {
+  W4Geom g;
+  g.mt = M <= 16 ? 1 : M <= 32 || dtype != PR_BF16 ? 2 : 4;
+  g.nt = N >= 16384 && g.mt == 1 ? 4 : N >= 8192 ? 2 : 1;
+  return g;
+}
+template <typename T, int MT, int NT>
+void w4_go(const W4Args &a, unsigned blocks, hipStream_t s) {
+  if (a.group % W4_CH == 0) k_w4_rows<T, MT, NT, true><<<blocks, 64 * W4_WAVES, 0, s>>>(a);
+  else k_w4_rows<T, MT, NT, false><<<blocks, 64 * W4_WAVES, 0, s>>>(a);
+}
+template <typename T>
+hipError_t w4_launch(const W4Args &a, const W4Geom &g, unsigned blocks, hipStream_t s) {
+  if (g.mt == 1) {
+    if (g.nt == 1) w4_go<T, 1, 1>(a, blocks, s);
+    else if (g.nt == 2) w4_go<T, 1, 2>(a, blocks, s);
+    else w4_go<T, 1, 4>(a, blocks, s);
+  } else if (g.mt == 2) {
+    if (g.nt == 1) w4_go<T, 2, 1>(a, blocks, s);
+    else w4_go<T, 2, 2>(a, blocks, s);
+  } else if constexpr (sizeof(T) == 2) {
+    if (g.nt == 1) w4_go<T, 4, 1>(a, blocks, s);
+    else w4_go<T, 4, 2>(a, blocks, s);
+  }
+  return hipGetLastError();
 }
 
 struct W4QuantArgs {
@@ -192,12 +404,13 @@ int pararnn_gemm_w4(int dtype, int M, int N, int K, int group, const void *x, lo
   W4Args a{};
   a.x = x; a.q = q; a.scale = scale; a.zero = zero; a.bias = bias; a.out = out;
   a.ldx = ldx; a.ldq = ldq; a.ldo = ldo; a.M = M; a.N = N; a.K = K; a.group = group; a.G = w4_groups(K, group);
-  const dim3 grid((unsigned)((N + 3) / 4), (unsigned)((M + 7) / 8));
-  if ((double)grid.x * grid.y * 256 >= 4294967296.0) return fail(PR_EUNSUPPORTED, "problem too large: %d x %d results", M, N);
-  if (grid.y > 65535) return fail(PR_EUNSUPPORTED, "M = %d", M);
-  if (dtype == PR_BF16) k_w4_plain<uint16_t><<<grid, 256, 0, (hipStream_t)stream>>>(a);
-  else k_w4_plain<float><<<grid, 256, 0, (hipStream_t)stream>>>(a);
-  HIPCHK(hipGetLastError());
+  a.rgroup = 32.f / (float)group;
+  const W4Geom g = w4_geom(dtype, M, N);
+  const long long blocks = (long long)((N + 16 * g.nt - 1) / (16 * g.nt)) * ((M + 16 * g.mt - 1) / (16 * g.mt));
+  // a launch has 2^32 threads at most, 512 a block
+  if (blocks >= (1 << 23)) return fail(PR_EUNSUPPORTED, "problem too large: %d x %d results", M, N);
+  hipStream_t s = (hipStream_t)stream;
+  HIPCHK(dtype == PR_BF16 ? w4_launch<uint16_t>(a, g, (unsigned)blocks, s) : w4_launch<float>(a, g, (unsigned)blocks, s));
   return PR_OK;
 }
 
