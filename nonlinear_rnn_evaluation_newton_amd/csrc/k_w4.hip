@@ -14,13 +14,17 @@ struct W4Args {
   long long ldx, ldq, ldo;
   int M, N, K, group, G;  // G: groups of a row
   float rgroup;           // 32 / group
+  int slice;              // columns of a wavefront
 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4v __attribute__((ext_vector_type(4)));
 constexpr int W4_CH = 128;  // columns of a wavefront's step: 16 bytes of 4-bit numbers a lane
-constexpr int W4_WAVES = 8;
+#ifndef W8
+#define W8 8
+#define W44 4
+#endif
 
 // Operands of v_mfma_f32_16x16x32_bf16 for 8 adjacent columns k0..k7 of a lane, in
 // the order k0 k4, k1 k5, k2 k6, k3 k7: both operands have the same, and a product's
@@ -72,19 +76,43 @@ struct XOps<float> {
   }
 };
 
-// What a step of 128 columns reads.
-template <typename T, int MT, int NT>
-struct W4Step {
-  u32x4v w[NT];         // 32 numbers of one row of weights: words of 8
-  VecU<T, 8> x[MT][4];  // columns 32 j + 8 q .. of one row of x
-  float s[NT][4], z[NT][4];
+// The scales (or zero points) of one row of weights from a group on: 16 bytes at a
+// time, since a row's lie in one or two lines that would not stay in the cache from
+// step to step.
+template <typename T>
+struct GroupWindow {
+  static constexpr int N = 16 / (int)sizeof(T);
+  u32x4v v;
+  __device__ void load(const T *p, int left) { v = ldu<T, N>(p, left).v; }
+  __device__ float get(int i) const {
+    VecU<T, N> e;
+    e.v = v;
+    return e.f(i);
+  }
+  template <int GROUPS>
+  __device__ void drop() {
+    constexpr int B = GROUPS * (int)sizeof(T);
+    if constexpr (B == 2) {
+      v[0] = __builtin_amdgcn_alignbit(v[1], v[0], 16);
+      v[1] = __builtin_amdgcn_alignbit(v[2], v[1], 16);
+      v[2] = __builtin_amdgcn_alignbit(v[3], v[2], 16);
+      v[3] >>= 16;
+    } else if constexpr (B == 4) {
+      v = u32x4v{v[1], v[2], v[3], 0u};
+    } else if constexpr (B == 8) {
+      v = u32x4v{v[2], v[3], 0u, 0u};
+    }
+  }
 };
 
-// MT x NT tiles of 16 rows of x by 16 columns of the output; eight wavefronts share
-// K in steps of 128 and join in shared memory.  ONE: a step lies in one group.
-template <typename T, int MT, int NT, bool ONE>
-__global__ __launch_bounds__(64 * W4_WAVES) void k_w4_rows(W4Args a) {
-  __shared__ float red[W4_WAVES][NT * 256];
+// MT x NT tiles of 16 rows of x by 16 columns of the output; WV wavefronts take
+// slices of K, 256 columns (a line of a row of weights) at a time, and join in
+// shared memory.  GM: groups in 128 columns, 1 (also where a group is several times
+// 128), 2 or 4, or 0 where groups end anywhere between 32 columns.
+template <typename T, int MT, int NT, int GM, int WV>
+__global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
+  constexpr int NG = GM ? GM : 4;
+  __shared__ float red[WV][NT * 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;
   const int nb = (a.N + 16 * NT - 1) / (16 * NT);
@@ -109,97 +137,147 @@ __global__ __launch_bounds__(64 * W4_WAVES) void k_w4_rows(W4Args a) {
   for (int i = 0; i < MT; i++)
 #pragma unroll
     for (int j = 0; j < NT; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int k0 = wave * a.slice, k1 = a.K - k0 < a.slice ? a.K : k0 + a.slice;
   // the group of the 32 columns from k on (k / 32 below 2^19: the product is off by
   // less than the half that separates it from the next number)
   auto group = [&](int k) { return (int)(((float)(k >> 5) + 0.5f) * a.rgroup); };
-  auto load = [&](W4Step<T, MT, NT> &s, int kb) __attribute__((always_inline)) {
-    const bool full = kb + W4_CH <= a.K;
+  auto load_w = [&](u32x4v (&w)[NT][2], int kb) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < NT; j++) {
-      if (full) {
-        s.w[j] = reinterpret_cast<const Packed<uint8_t, 16> *>(wp[j] + (kb >> 1))->v;
-      } else {  // bytes past the row's end are not read
-        const int left = (a.K + 1) / 2 - (kb >> 1) - q * 16;
-        VecU<uint8_t, 16> b = ldu<uint8_t, 16>(wp[j] + (kb >> 1), left);
-        s.w[j] = b.v;
-      }
+    for (int u = 0; u < 2; u++)
 #pragma unroll
-      for (int u = 0; u < (ONE ? 1 : 4); u++) {
-        int g = group(kb + 32 * u);
-        if (!full) g = g < a.G ? g : a.G - 1;
-        s.s[j][u] = ldf(sp[j], g);
-        s.z[j][u] = a.zero ? ldf(zp[j], g) : 8.f;
+      for (int j = 0; j < NT; j++) {
+        const int k = kb + W4_CH * u;
+        if (k + W4_CH <= a.K) w[j][u] = reinterpret_cast<const Packed<uint8_t, 16> *>(wp[j] + (k >> 1))->v;
+        else w[j][u] = ldu<uint8_t, 16>(wp[j] + (k >> 1), (a.K + 1) / 2 - (k >> 1) - q * 16).v;  // not past the row's end
       }
-    }
+  };
+  auto load_x = [&](VecU<T, 8> (&x)[MT][4], int kb) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < MT; i++)
 #pragma unroll
       for (int u = 0; u < 4; u++) {
         const T *p = xp[i] + kb + 32 * u;
-        if (full) s.x[i][u].v = reinterpret_cast<const Packed<T, 8> *>(p)->v;
-        else s.x[i][u] = ldu<T, 8>(p, a.K - kb - 32 * u - 8 * q);  // zeros past the end
+        if (kb + W4_CH <= a.K) x[i][u].v = reinterpret_cast<const Packed<T, 8> *>(p)->v;
+        else x[i][u] = ldu<T, 8>(p, a.K - kb - 32 * u - 8 * q);  // zeros past the end
       }
   };
   const bf16x8 ones = words(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
   const f32x4 nil = {0.f, 0.f, 0.f, 0.f};
-  auto product = [&](W4Step<T, MT, NT> &s) __attribute__((always_inline)) {
-    // lane q's word j holds columns 32 q + 8 j ..; the matrix product of 32 columns
-    // wants 32 j + 8 q ..: a transposition of 4 x 4 words between the lanes' rows
-    bf16x8 b[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; j++) {
-      const auto e = __builtin_amdgcn_permlane32_swap(s.w[j][0], s.w[j][2], false, false);
-      const auto f = __builtin_amdgcn_permlane32_swap(s.w[j][1], s.w[j][3], false, false);
-      const auto g = __builtin_amdgcn_permlane16_swap(e[0], f[0], false, false);
-      const auto h = __builtin_amdgcn_permlane16_swap(e[1], f[1], false, false);
-      b[j][0] = w4_operand(g[0]);
-      b[j][1] = w4_operand(g[1]);
-      b[j][2] = w4_operand(h[0]);
-      b[j][3] = w4_operand(h[1]);
-    }
-#pragma unroll
-    for (int i = 0; i < MT; i++) {
-      f32x4 xs = nil, d[NT];
+  // scales and zero points: from the window, or for each 32 columns
+  GroupWindow<T> gs[NT], gz[NT];
+  int have = 0, g0 = group(k0);                      // groups left in the window, the next one's number
+  const int per = GM == 1 ? a.group / W4_CH : 1;     // steps of a group
+  int stay = GM == 1 ? per - (k0 / W4_CH) % per : 1;  // steps left in this one
+  auto step = [&](const u32x4v (&w)[NT][2], int half, const VecU<T, 8> (&xv)[MT][4], int kb) __attribute__((always_inline)) {
+    float sc[NT][NG], zr[NT][NG];
+    if constexpr (GM == 0) {
 #pragma unroll
       for (int u = 0; u < 4; u++) {
-        XOps<T> x;
-        x.set(s.x[i][u]);
-        if (!ONE || u == 0) {
-          xs = nil;
+        const int g = min(group(kb + 32 * u), a.G - 1);
 #pragma unroll
-          for (int j = 0; j < NT; j++) d[j] = nil;
+        for (int j = 0; j < NT; j++) {
+          sc[j][u] = ldf(sp[j], g);
+          zr[j][u] = a.zero ? ldf(zp[j], g) : 8.f;
+        }
+      }
+    } else {
+      if (have == 0) {
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+          gs[j].load(sp[j] + g0, a.G - g0);
+          if (a.zero) gz[j].load(zp[j] + g0, a.G - g0);
+        }
+        have = GroupWindow<T>::N;
+        g0 += have;
+      }
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int u = 0; u < NG; u++) {
+          sc[j][u] = gs[j].get(u);
+          zr[j][u] = a.zero ? gz[j].get(u) : 8.f;
+        }
+      if (--stay == 0) {
+        stay = per;
+        have -= NG;
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+          gs[j].template drop<NG>();
+          if (a.zero) gz[j].template drop<NG>();
+        }
+      }
+    }
+    // lane q's word j holds columns 32 q + 8 j ..; the matrix product of 32 columns
+    // wants 32 j + 8 q ..: a transposition of 4 x 4 words between the lanes' rows
+    unsigned b[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const u32x4v v = w[j][half];
+      const auto e = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+      const auto f = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+      const auto g = __builtin_amdgcn_permlane16_swap(e[0], f[0], false, false);
+      const auto h = __builtin_amdgcn_permlane16_swap(e[1], f[1], false, false);
+      b[j][0] = g[0];
+      b[j][1] = g[1];
+      b[j][2] = h[0];
+      b[j][3] = h[1];
+    }
+    f32x4 xs[MT], d[MT][NT];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      bf16x8 bw[NT];
+#pragma unroll
+      for (int j = 0; j < NT; j++) bw[j] = w4_operand(b[j][u]);
+#pragma unroll
+      for (int i = 0; i < MT; i++) {
+        XOps<T> x;
+        x.set(xv[i][u]);
+        if (u % (4 / NG) == 0) {
+          xs[i] = nil;
+#pragma unroll
+          for (int j = 0; j < NT; j++) d[i][j] = nil;
         }
 #pragma unroll
         for (int o = 0; o < XOps<T>::N; o++) {
-          xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.o[o], ones, xs, 0, 0, 0);
+          xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.o[o], ones, xs[i], 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < NT; j++) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.o[o], b[j][u], d[j], 0, 0, 0);
+          for (int j = 0; j < NT; j++)
+            d[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.o[o], bw[j], d[i][j], 0, 0, 0);
         }
-        if (!ONE || u == 3) {
+        if (u % (4 / NG) == 4 / NG - 1) {
 #pragma unroll
           for (int j = 0; j < NT; j++)
 #pragma unroll
             for (int r = 0; r < 4; r++)
-              acc[i][j][r] = fmaf(s.s[j][ONE ? 0 : u], fmaf(-16.f - s.z[j][ONE ? 0 : u], xs[r], d[j][r]), acc[i][j][r]);
+              acc[i][j][r] = fmaf(sc[j][u * NG / 4], fmaf(-16.f - zr[j][u * NG / 4], xs[i][r], d[i][j][r]), acc[i][j][r]);
         }
       }
     }
   };
-  constexpr int STEP = W4_CH * W4_WAVES, U = MT * NT == 1 && sizeof(T) == 2 ? 4 : MT * NT <= 4 && sizeof(T) == 2 ? 2 : 1;
-  int kb = wave * W4_CH;
-  for (; kb + (U - 1) * STEP < a.K; kb += U * STEP) {
-    W4Step<T, MT, NT> s[U];
-#pragma unroll
-    for (int u = 0; u < U; u++) load(s[u], kb + u * STEP);
-#pragma unroll
-    for (int u = 0; u < U; u++) product(s[u]);
+  // the next 256 columns' weights in flight during a pair of steps, and where there
+  // are registers the next step's x
+  constexpr bool AHEAD = MT * NT * sizeof(T) <= 4;
+  u32x4v w0[NT][2], w1[NT][2];
+  VecU<T, 8> x0[MT][4], x1[MT][4];
+  auto pair = [&](const u32x4v (&w)[NT][2], u32x4v (&next)[NT][2], int kb) __attribute__((always_inline)) {
+    if (kb + 2 * W4_CH < k1) load_w(next, kb + 2 * W4_CH);
+    if (!AHEAD) load_x(x0, kb);
+    else if (kb + W4_CH < k1) load_x(x1, kb + W4_CH);
+    step(w, 0, x0, kb);
+    if (kb + W4_CH >= k1) return;
+    if (!AHEAD) load_x(x0, kb + W4_CH);
+    else if (kb + 2 * W4_CH < k1) load_x(x0, kb + 2 * W4_CH);
+    step(w, 1, AHEAD ? x1 : x0, kb + W4_CH);
+  };
+  if (k0 < k1) {
+    load_w(w0, k0);
+    if (AHEAD) load_x(x0, k0);
   }
-  if constexpr (U > 1)
-    for (; kb < a.K; kb += STEP) {
-      W4Step<T, MT, NT> s;
-      load(s, kb);
-      product(s);
-    }
+  for (int kb = k0; kb < k1; kb += 4 * W4_CH) {
+    pair(w0, w1, kb);
+    if (kb + 2 * W4_CH >= k1) break;
+    pair(w1, w0, kb + 2 * W4_CH);
+  }
 #pragma unroll
   for (int i = 0; i < MT; i++) {
     if (i) __syncthreads();
@@ -208,11 +286,11 @@ __global__ __launch_bounds__(64 * W4_WAVES) void k_w4_rows(W4Args a) {
 #pragma unroll
       for (int r = 0; r < 4; r++) red[wave][(q * 4 + r) * 16 * NT + j * 16 + c] = acc[i][j][r];
     __syncthreads();
-    for (int e = threadIdx.x; e < NT * 256; e += 64 * W4_WAVES) {
+    for (int e = threadIdx.x; e < NT * 256; e += 64 * WV) {
       const int m = m0 + i * 16 + e / (16 * NT), n = n0 + e % (16 * NT);
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < W4_WAVES; w++) v += red[w][e];
+      for (int w = 0; w < WV; w++) v += red[w][e];
       if (m < a.M && n < a.N) stf((T *)a.out + m * a.ldo, n, a.bias ? v + ldf((const T *)a.bias, n) : v);
     }
   }
@@ -228,15 +306,23 @@ static W4Geom w4_geom(int dtype, int M, int N) {
   W4Geom g;
   g.mt = M <= 16 ? 1 : M <= 32 || dtype != PR_BF16 ? 2 : 4;
   g.nt = N >= 16384 && g.mt == 1 ? 4 : N >= 8192 ? 2 : 1;
+#ifdef NTF
+  g.nt = NTF; if (g.mt > 1 && g.nt == 4) g.nt = 2;
+#endif
   return g;
 }
 template <typename T, int MT, int NT>
-void w4_go(const W4Args &a, unsigned blocks, hipStream_t s) {
-  if (a.group % W4_CH == 0) k_w4_rows<T, MT, NT, true><<<blocks, 64 * W4_WAVES, 0, s>>>(a);
-  else k_w4_rows<T, MT, NT, false><<<blocks, 64 * W4_WAVES, 0, s>>>(a);
+void w4_go(W4Args &a, unsigned blocks, hipStream_t s) {
+  constexpr int WV = NT == 4 ? W44 : W8, NT_ = 64 * WV;
+  const int steps = (a.K + W4_CH - 1) / W4_CH;
+  a.slice = (steps + WV - 1) / WV * W4_CH;
+  if (a.group % W4_CH == 0) k_w4_rows<T, MT, NT, 1, WV><<<blocks, NT_, 0, s>>>(a);
+  else if (a.group == 64) k_w4_rows<T, MT, NT, 2, WV><<<blocks, NT_, 0, s>>>(a);
+  else if (a.group == 32) k_w4_rows<T, MT, NT, 4, WV><<<blocks, NT_, 0, s>>>(a);
+  else k_w4_rows<T, MT, NT, 0, WV><<<blocks, NT_, 0, s>>>(a);
 }
 template <typename T>
-hipError_t w4_launch(const W4Args &a, const W4Geom &g, unsigned blocks, hipStream_t s) {
+hipError_t w4_launch(W4Args &a, const W4Geom &g, unsigned blocks, hipStream_t s) {
   if (g.mt == 1) {
     if (g.nt == 1) w4_go<T, 1, 1>(a, blocks, s);
     else if (g.nt == 2) w4_go<T, 1, 2>(a, blocks, s);
