@@ -21,10 +21,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4v __attribute__((ext_vector_type(4)));
 constexpr int W4_CH = 128;  // columns of a wavefront's step: 16 bytes of 4-bit numbers a lane
-#ifndef W8
-#define W8 8
-#define W44 4
-#endif
 
 // Operands of v_mfma_f32_16x16x32_bf16 for 8 adjacent columns k0..k7 of a lane, in
 // the order k0 k4, k1 k5, k2 k6, k3 k7: both operands have the same, and a product's
@@ -306,14 +302,11 @@ static W4Geom w4_geom(int dtype, int M, int N) {
   W4Geom g;
   g.mt = M <= 16 ? 1 : M <= 32 || dtype != PR_BF16 ? 2 : 4;
   g.nt = N >= 16384 && g.mt == 1 ? 4 : N >= 8192 ? 2 : 1;
-#ifdef NTF
-  g.nt = NTF; if (g.mt > 1 && g.nt == 4) g.nt = 2;
-#endif
   return g;
 }
 template <typename T, int MT, int NT>
 void w4_go(W4Args &a, unsigned blocks, hipStream_t s) {
-  constexpr int WV = NT == 4 ? W44 : W8, NT_ = 64 * WV;
+  constexpr int WV = NT == 4 ? 4 : 8, NT_ = 64 * WV;
   const int steps = (a.K + W4_CH - 1) / W4_CH;
   a.slice = (steps + WV - 1) / WV * W4_CH;
   if (a.group % W4_CH == 0) k_w4_rows<T, MT, NT, 1, WV><<<blocks, NT_, 0, s>>>(a);
@@ -344,10 +337,23 @@ struct W4QuantArgs {
   int N, K, group, G;
 };
 
-// y / s to the nearest, ties to even; s > 0 and finite
-__device__ inline float w4_round(float y, float s) { return rintf(__fdiv_rn(y, s)); }
+// y / s to the nearest, ties to even, for s > 0 and finite.  With inv the rounded
+// reciprocal, the product's exact remainder times inv corrects it, three operations
+// for a division's dozen; scales near the ends of the range are divided by.
+struct Divisor {
+  float s, inv;
+  bool plain;
+  __device__ explicit Divisor(float v) : s(v), inv(__fdiv_rn(1.f, v)), plain(v > 1e-30f && v < 1e30f) {}
+  __device__ float round(float y) const {
+    if (!plain) return rintf(__fdiv_rn(y, s));
+    const float q = y * inv;
+    return rintf(fmaf(fmaf(-q, s, y), inv, q));
+  }
+};
 
-// L lanes (a power of two) for each group, eight columns each at a time.
+// L lanes (a power of two) for each group, eight columns each, which stay in
+// registers between the extremes and the rounding; groups of more than 8 L columns
+// (L = 64) are read again.
 template <typename T, int L>
 __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a) {
   const long long id = flat_block() * (256 / L) + threadIdx.x / L;  // row and group
@@ -355,20 +361,23 @@ __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a) {
   const bool on = id < (long long)a.N * a.G;
   const int g = on ? (int)(id % a.G) : 0;
   const long long n = on ? id / a.G : 0;
-  const int k0 = g * a.group, k1 = on ? (a.K - k0 < a.group ? a.K : k0 + a.group) : k0;
+  const int k0 = g * a.group, k1 = on ? (a.K - k0 < a.group ? a.K : k0 + a.group) : k0, first = k0 + lane * 8;
   const T *wp = (const T *)a.w + n * a.ldw;
+  const VecU<T, 8> own = ldu<T, 8>(wp + first, k1 - first);
   // the largest of max(w, 0) and of max(-w, 0), compared by their bits: a NaN wins
   unsigned hi = 0, lo = 0;
-  for (int k = k0 + lane * 8; k < k1; k += L * 8) {
-    const VecU<T, 8> v = ldu<T, 8>(wp + k, k1 - k);
+  auto extremes = [&](const VecU<T, 8> &v) {
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       const float f = v.f(i);
-      const unsigned bits = __float_as_uint(fabsf(f));
-      if (f > 0.f || f != f) hi = max(hi, bits);
-      else lo = max(lo, bits);
+      const unsigned bits = __float_as_uint(fabsf(f)), up = f > 0.f || f != f ? bits : 0u;
+      hi = max(hi, up);
+      lo = max(lo, bits ^ up);
     }
-  }
+  };
+  extremes(own);
+  if constexpr (L == 64)
+    for (int k = first + L * 8; k < k1; k += L * 8) extremes(ldu<T, 8>(wp + k, k1 - k));
 #pragma unroll
   for (int o = L / 2; o >= 1; o >>= 1) {
     hi = max(hi, (unsigned)__shfl_xor((int)hi, o, 64));
@@ -378,20 +387,20 @@ __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a) {
   T st;
   stf(&st, 0, a.zero ? (fh + fl) * (1.f / 15.f) : __uint_as_float(max(hi, lo)) * (1.f / 7.f));
   const float s = ldf(&st, 0);
-  const bool plain = s > 0.f && s < __builtin_inff();
+  const bool some = s > 0.f && s < __builtin_inff();
+  const Divisor by(some ? s : 1.f);
   float z = 8.f;
-  if (a.zero) z = plain ? fminf(fmaxf(w4_round(fl, s), 0.f), 15.f) : s == 0.f ? 0.f : 8.f;
+  if (a.zero) z = some ? fminf(fmaxf(by.round(fl), 0.f), 15.f) : s == 0.f ? 0.f : 8.f;
   if (on && lane == 0) {
     ((T *)a.scale)[id] = st;
     if (a.zero) stf((T *)a.zero, id, z);
   }
-  for (int k = k0 + lane * 8; k < k1; k += L * 8) {
+  auto store = [&](int k, const VecU<T, 8> &v) {
     const int c = k1 - k;
-    const VecU<T, 8> v = ldu<T, 8>(wp + k, c);
     unsigned word = 0;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const float f = plain ? w4_round(v.f(i), s) + z : z;
+      const float f = some ? by.round(v.f(i)) + z : z;
       word |= (unsigned)(int)fminf(fmaxf(f, 0.f), 15.f) << (4 * i);
     }
     uint8_t *qp = a.q + n * a.ldq + (k >> 1);
@@ -402,7 +411,10 @@ __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a) {
       for (int i = 0; i < 4; i++)
         if (2 * i < c) qp[i] = (uint8_t)(word >> (8 * i));
     }
-  }
+  };
+  if (first < k1) store(first, own);
+  if constexpr (L == 64)
+    for (int k = first + L * 8; k < k1; k += L * 8) store(k, ldu<T, 8>(wp + k, k1 - k));
 }
 
 // Eight columns a thread.
