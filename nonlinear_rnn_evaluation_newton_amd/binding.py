@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -94,13 +95,6 @@ class GatedProblem(C.Structure):
 class GatedInputs(C.Structure):
     _fields_ = [("x", View), ("r", View), ("i", View), ("decay", C.c_void_p), ("r_bias", C.c_void_p),
                 ("i_bias", C.c_void_p), ("h0", C.c_void_p), ("lengths", C.c_void_p)]
-
-
-class _GatedInputsFlat(C.Structure):
-    """The same layout without nested structures, which take longer to fill."""
-    _fields_ = [(a + "_" + f, c) for a in ("x", "r", "i")
-                for f, c in (("p", C.c_void_p), ("sb", C.c_longlong), ("st", C.c_longlong))] + [
-        (a, C.c_void_p) for a in ("decay", "r_bias", "i_bias", "h0", "lengths")]
 
 
 class GatedGrads(C.Structure):
@@ -645,9 +639,51 @@ def gemm_i8(a, a_scale, w, w_scale, out, workspace, bias=None, check: bool = Tru
 # ---------------------------------------------------------------------------
 # operators of a gated recurrent block
 # ---------------------------------------------------------------------------
+# Their structures are packed as bytes, in the C layout: single tokens' calls are
+# bound by the work done here, and a ctypes structure takes several times as long.
+_PACK_VIEW, _PACK_ROWS = struct.Struct("qqq").pack, struct.Struct("qq").pack
+_PACK_GATED, _PACK_GATED_IN = struct.Struct("iiii").pack, struct.Struct("14q").pack
+_PACK_GATED_GRADS, _PACK_BLOCK_NORM = struct.Struct("13q").pack, struct.Struct("iiqfi").pack
+_PACK_BLOCK_NORM_GRADS = struct.Struct("9q").pack
+
+
+def _strided(where, name, t, shape, dtype):
+    """The address and the strides of t, whose last axis must be adjacent."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or _several_gpus:
+        _need(where, name, t, shape, dtype)
+    s = t.stride()
+    if s[-1] != 1:
+        _strides(where, name, t, shape, 1)
+    return t.data_ptr(), s
+
+
+def _address(where, name, t, shape, dtype):
+    """The address of t, all of whose axes must be contiguous; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or _several_gpus or not t.is_contiguous():
+        return _dense(where, name, t, shape, dtype)
+    return t.data_ptr()
+
+
+def _seq(where, name, t, shape, dtype):
+    """The fields of a pr_view of t [B, T, channels] or, for single tokens, [B, channels]."""
+    if t is None:
+        return 0, 0, 0
+    p, s = _strided(where, name, t, shape, dtype)
+    return p, s[0], s[1] if len(s) == 3 else 0
+
+
+def _row2(where, name, t, shape, dtype):
+    """The fields of a pr_rows of t."""
+    if t is None:
+        return 0, 0
+    p, s = _strided(where, name, t, shape, dtype)
+    return p, s[0]
+
+
 def gated_workspace_bytes(dtype, B: int, T: int, D: int, with_adjoint: bool = True) -> int:
-    return lib().pararnn_gated_workspace_bytes(C.byref(GatedProblem(_dtype_code(dtype, "gated"), B, T, D)),
-                                               int(with_adjoint))
+    return lib().pararnn_gated_workspace_bytes(_PACK_GATED(_dtype_code(dtype, "gated"), B, T, D), int(with_adjoint))
 
 
 def gated_states_shape(B: int, T: int, D: int):
@@ -662,12 +698,12 @@ def _gated(where, axes, x, r, i, decay, r_bias, i_bias, h0, lengths):
     if len(shape) != axes:
         raise ValueError(f"{where}: x must be [B, {'T, ' if axes == 3 else ''}channels], got {tuple(shape)}")
     B, D = shape[0], shape[-1]
-    pb = GatedProblem(_dtype_code(st, where), B, shape[1] if axes == 3 else 1, D)
-    return pb, _GatedInputsFlat(
-        *_flat(where, "x", x, shape, st), *_flat(where, "r", r, shape, st), *_flat(where, "i", i, shape, st),
-        _dense(where, "decay", decay, (D,), f32), _dense(where, "r_bias", r_bias, (D,), f32),
-        _dense(where, "i_bias", i_bias, (D,), f32), _dense(where, "h0", h0, (B, D), f32),
-        _dense(where, "lengths", lengths, (B,), torch.int32))
+    ch = (D,)
+    return shape, st, _PACK_GATED(_dtype_code(st, where), B, shape[1] if axes == 3 else 1, D), _PACK_GATED_IN(
+        *_seq(where, "x", x, shape, st), *_seq(where, "r", r, shape, st), *_seq(where, "i", i, shape, st),
+        _address(where, "decay", decay, ch, f32), _address(where, "r_bias", r_bias, ch, f32),
+        _address(where, "i_bias", i_bias, ch, f32), _address(where, "h0", h0, (B, D), f32),
+        _address(where, "lengths", lengths, (B,), torch.int32))
 
 
 def gated_scan(x, r, i, decay, y, workspace, r_bias=None, i_bias=None, h0=None, h_last=None, states=None, lengths=None,
@@ -675,11 +711,11 @@ def gated_scan(x, r, i, decay, y, workspace, r_bias=None, i_bias=None, h0=None, 
     """pararnn_gated_scan: the gated recurrence of x [B, T, channels] with gates r and i into y."""
     import torch
     n, f32 = "gated_scan", torch.float32
-    pb, inp = _gated(n, 3, x, r, i, decay, r_bias, i_bias, h0, lengths)
+    shape, t, pb, inp = _gated(n, 3, x, r, i, decay, r_bias, i_bias, h0, lengths)
+    B, T, D = shape
     st = lib().pararnn_gated_scan(
-        C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, x.shape, x.dtype)),
-        _dense(n, "h_last", h_last, (pb.B, pb.D), f32),
-        _dense(n, "states", states, gated_states_shape(pb.B, pb.T, pb.D), f32), *_ws(n, workspace), _stream_of(x))
+        pb, inp, _PACK_VIEW(*_seq(n, "y", y, shape, t)), _address(n, "h_last", h_last, (B, D), f32),
+        _address(n, "states", states, gated_states_shape(B, T, D), f32), *_ws(n, workspace), _stream_of(x))
     return _done(st, "pararnn_gated_scan", check)
 
 
@@ -688,15 +724,17 @@ def gated_scan_adjoint(x, r, i, decay, states, dy, workspace, r_bias=None, i_bia
                        check: bool = True) -> int:
     """pararnn_gated_adjoint: gradients of gated_scan from the states it saved; any output may be None."""
     import torch
-    n, f32, shape, t = "gated_scan_adjoint", torch.float32, x.shape, x.dtype
-    pb, inp = _gated(n, 3, x, r, i, decay, r_bias, i_bias, None, lengths)
-    B, D = pb.B, pb.D
-    gr = GatedGrads(_view(n, "dx", dx, shape, t), _view(n, "dr", dr, shape, t), _view(n, "di", di, shape, t),
-                    _dense(n, "ddecay", ddecay, (D,), f32), _dense(n, "dr_bias", dr_bias, (D,), f32),
-                    _dense(n, "di_bias", di_bias, (D,), f32), _dense(n, "dh0", dh0, (B, D), f32))
+    n, f32 = "gated_scan_adjoint", torch.float32
+    shape, t, pb, inp = _gated(n, 3, x, r, i, decay, r_bias, i_bias, None, lengths)
+    B, T, D = shape
+    ch = (D,)
+    gr = _PACK_GATED_GRADS(
+        *_seq(n, "dx", dx, shape, t), *_seq(n, "dr", dr, shape, t), *_seq(n, "di", di, shape, t),
+        _address(n, "ddecay", ddecay, ch, f32), _address(n, "dr_bias", dr_bias, ch, f32),
+        _address(n, "di_bias", di_bias, ch, f32), _address(n, "dh0", dh0, (B, D), f32))
     st = lib().pararnn_gated_adjoint(
-        C.byref(pb), C.byref(inp), _dense(n, "states", states, gated_states_shape(B, pb.T, D), f32),
-        C.byref(_view(n, "dy", dy, shape, t)), _dense(n, "dh_last", dh_last, (B, D), f32), C.byref(gr),
+        pb, inp, _address(n, "states", states, gated_states_shape(B, T, D), f32),
+        _PACK_VIEW(*_seq(n, "dy", dy, shape, t)), _address(n, "dh_last", dh_last, (B, D), f32), gr,
         *_ws(n, workspace), _stream_of(x))
     return _done(st, "pararnn_gated_adjoint", check)
 
@@ -705,39 +743,43 @@ def gated_step(x, r, i, decay, state, y, r_bias=None, i_bias=None, slots=None, c
     """pararnn_gated_step: one token x [B, channels] per sequence on the fp32 pool state [slots, channels]."""
     import torch
     n = "gated_step"
-    pb, inp = _gated(n, 2, x, r, i, decay, r_bias, i_bias, None, None)
+    shape, t, pb, inp = _gated(n, 2, x, r, i, decay, r_bias, i_bias, None, None)
     pool = state.shape[0]
-    st = lib().pararnn_gated_step(C.byref(pb), C.byref(inp), C.byref(_view(n, "y", y, x.shape, x.dtype)),
-                                  _dense(n, "state", state, (pool, pb.D), torch.float32), pool,
-                                  _dense(n, "slots", slots, (pb.B,), torch.int32), _stream_of(x))
+    st = lib().pararnn_gated_step(pb, inp, _PACK_VIEW(*_seq(n, "y", y, shape, t)),
+                                  _address(n, "state", state, (pool, shape[1]), torch.float32), pool,
+                                  _address(n, "slots", slots, (shape[0],), torch.int32), _stream_of(x))
     return _done(st, "pararnn_gated_step", check)
 
 
-def _gate_code(where, z, gate):
+def _block_norm(where, x, z, gate, eps):
+    """The shape and type of the rows x and the packed problem."""
+    lib()
+    shape, dt = x.shape, x.dtype
+    if len(shape) != 2:
+        raise ValueError(f"{where}: x must be [rows, n], got {tuple(shape)}")
     if gate not in GATES:
         raise ValueError(f"{where}: gate must be one of {sorted(GATES)}, got {gate!r}")
-    return GATES[gate] if z is not None else 0
+    return shape, dt, _PACK_BLOCK_NORM(_dtype_code(dt, where), shape[1], shape[0], eps, GATES[gate] if z is not None else 0)
 
 
 def block_norm(x, w, t, z=None, gate: str = "silu", scale=None, residual=None, y=None, w_next=None, eps: float = 1e-5,
                check: bool = True) -> int:
     """pararnn_block_norm of x [rows, n]: t = residual + norm(x) w scale act(z) and, where y is given, y = norm(t) w_next."""
-    lib()
-    shape, dt, where = x.shape, x.dtype, "block_norm"
-    rows, n = shape
-    pb = BlockNormProblem(_dtype_code(dt, where), n, rows, eps, _gate_code(where, z, gate))
+    n = "block_norm"
+    shape, dt, pb = _block_norm(n, x, z, gate, eps)
+    ch = (shape[1],)
     st = lib().pararnn_block_norm(
-        C.byref(pb), _rows(where, "x", x, shape, dt), _rows(where, "z", z, shape, dt),
-        _rows(where, "residual", residual, shape, dt), _dense(where, "w", w, (n,), dt),
-        _dense(where, "scale", scale, (n,), dt), _dense(where, "w_next", w_next, (n,), dt),
-        _rows(where, "t", t, shape, dt), _rows(where, "y", y, shape, dt), _stream_of(x))
+        pb, _PACK_ROWS(*_row2(n, "x", x, shape, dt)), None if z is None else _PACK_ROWS(*_row2(n, "z", z, shape, dt)),
+        None if residual is None else _PACK_ROWS(*_row2(n, "residual", residual, shape, dt)),
+        _address(n, "w", w, ch, dt), _address(n, "scale", scale, ch, dt), _address(n, "w_next", w_next, ch, dt),
+        _PACK_ROWS(*_row2(n, "t", t, shape, dt)), None if y is None else _PACK_ROWS(*_row2(n, "y", y, shape, dt)),
+        _stream_of(x))
     return _done(st, "pararnn_block_norm", check)
 
 
 def block_norm_workspace_bytes(dtype, rows: int, n: int) -> int:
     """Workspace of block_norm_adjoint for rows stored in the torch type dtype."""
-    pb = BlockNormProblem(_dtype_code(dtype, "block_norm"), n, rows, 0.0, 0)
-    return lib().pararnn_block_norm_workspace_bytes(C.byref(pb))
+    return lib().pararnn_block_norm_workspace_bytes(_PACK_BLOCK_NORM(_dtype_code(dtype, "block_norm"), n, rows, 0.0, 0))
 
 
 def block_norm_adjoint(x, w, dx, workspace, z=None, gate: str = "silu", scale=None, w_next=None, t=None, dt=None,
@@ -745,21 +787,17 @@ def block_norm_adjoint(x, w, dx, workspace, z=None, gate: str = "silu", scale=No
                        check: bool = True) -> int:
     """pararnn_block_norm_adjoint: gradients of block_norm at x, z and the stored t from dt and dy; any output may be None."""
     import torch
-    lib()
-    shape, st, where, f32 = x.shape, x.dtype, "block_norm_adjoint", torch.float32
-    rows, n = shape
-    pb = BlockNormProblem(_dtype_code(st, where), n, rows, eps, _gate_code(where, z, gate))
-
-    def out(name, v):
-        return Rows(None, 0) if v is None else Rows(_need(where, name, v, shape, st), v.stride(0))
-
-    gr = BlockNormGrads(out("dx", dx), out("dz", dz), out("dres", dres), _dense(where, "dw", dw, (n,), f32),
-                        _dense(where, "dscale", dscale, (n,), f32), _dense(where, "dw_next", dw_next, (n,), f32))
+    n, f32 = "block_norm_adjoint", torch.float32
+    shape, st, pb = _block_norm(n, x, z, gate, eps)
+    ch = (shape[1],)
+    gr = _PACK_BLOCK_NORM_GRADS(*_row2(n, "dx", dx, shape, st), *_row2(n, "dz", dz, shape, st),
+                                *_row2(n, "dres", dres, shape, st), _address(n, "dw", dw, ch, f32),
+                                _address(n, "dscale", dscale, ch, f32), _address(n, "dw_next", dw_next, ch, f32))
     rc = lib().pararnn_block_norm_adjoint(
-        C.byref(pb), _rows(where, "x", x, shape, st), _rows(where, "z", z, shape, st), _dense(where, "w", w, (n,), st),
-        _dense(where, "scale", scale, (n,), st), _dense(where, "w_next", w_next, (n,), st),
-        _rows(where, "t", t, shape, st), _rows(where, "dt", dt, shape, st), _rows(where, "dy", dy, shape, st),
-        C.byref(gr), *_ws(where, workspace), _stream_of(x))
+        pb, _PACK_ROWS(*_row2(n, "x", x, shape, st)), _PACK_ROWS(*_row2(n, "z", z, shape, st)),
+        _address(n, "w", w, ch, st), _address(n, "scale", scale, ch, st), _address(n, "w_next", w_next, ch, st),
+        _PACK_ROWS(*_row2(n, "t", t, shape, st)), _PACK_ROWS(*_row2(n, "dt", dt, shape, st)),
+        _PACK_ROWS(*_row2(n, "dy", dy, shape, st)), gr, *_ws(n, workspace), _stream_of(x))
     return _done(rc, "pararnn_block_norm_adjoint", check)
 
 
@@ -769,8 +807,8 @@ def _w4(where, q, scale, zero, N, K, group, dt):
     if group < 1:
         raise ValueError(f"{where}: groups must have at least one column, got {group}")
     shape = (N, -(-K // group))
-    return (_need(where, "q", q, (N, (K + 1) // 2), torch.uint8), q.stride(0),
-            _dense(where, "scale", scale, shape, dt), _dense(where, "zero", zero, shape, dt))
+    return (*_row2(where, "q", q, (N, (K + 1) // 2), torch.uint8), _address(where, "scale", scale, shape, dt),
+            _address(where, "zero", zero, shape, dt))
 
 
 def gemm_w4(x, q, scale, out, group: int, zero=None, bias=None, check: bool = True) -> int:
@@ -778,9 +816,9 @@ def gemm_w4(x, q, scale, out, group: int, zero=None, bias=None, check: bool = Tr
     n, dt = "gemm_w4", x.dtype
     lib()
     (M, K), N = x.shape, q.shape[0]
-    st = lib().pararnn_gemm_w4(_dtype_code(dt, n), M, N, K, group, _need(n, "x", x, (M, K), dt), x.stride(0),
-                               *_w4(n, q, scale, zero, N, K, group, dt), _dense(n, "bias", bias, (N,), dt),
-                               _need(n, "out", out, (M, N), dt), out.stride(0), _stream_of(x))
+    st = lib().pararnn_gemm_w4(_dtype_code(dt, n), M, N, K, group, *_row2(n, "x", x, (M, K), dt),
+                               *_w4(n, q, scale, zero, N, K, group, dt), _address(n, "bias", bias, (N,), dt),
+                               *_row2(n, "out", out, (M, N), dt), _stream_of(x))
     return _done(st, "pararnn_gemm_w4", check)
 
 
@@ -789,7 +827,7 @@ def quant_w4(w, q, scale, group: int, zero=None, check: bool = True) -> int:
     n, dt = "quant_w4", w.dtype
     lib()
     N, K = w.shape
-    st = lib().pararnn_quant_w4(_dtype_code(dt, n), N, K, group, _need(n, "w", w, (N, K), dt), w.stride(0),
+    st = lib().pararnn_quant_w4(_dtype_code(dt, n), N, K, group, *_row2(n, "w", w, (N, K), dt),
                                 *_w4(n, q, scale, zero, N, K, group, dt), _stream_of(w))
     return _done(st, "pararnn_quant_w4", check)
 
@@ -800,7 +838,7 @@ def dequant_w4(q, scale, w, group: int, zero=None, check: bool = True) -> int:
     lib()
     N, K = w.shape
     st = lib().pararnn_dequant_w4(_dtype_code(dt, n), N, K, group, *_w4(n, q, scale, zero, N, K, group, dt),
-                                  _need(n, "w", w, (N, K), dt), w.stride(0), _stream_of(w))
+                                  *_row2(n, "w", w, (N, K), dt), _stream_of(w))
     return _done(st, "pararnn_dequant_w4", check)
 
 

@@ -579,24 +579,24 @@ __global__ __launch_bounds__(64 * NW, WPS) void k_gated_adj(GatedArgs a, GatedCh
 }
 
 // ddecay, dr_bias and di_bias from the tiles' partials [P][3][D], in 64 bits in a
-// fixed order: 32 columns by 32 slices of the partials a block.
+// fixed order: 16 columns by 64 slices of the partials a block.
 __global__ __launch_bounds__(1024) void k_gated_sums(const float *__restrict__ part, int P, int D, float *o0, float *o1,
                                                      float *o2) {
-  __shared__ double sh[32][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, k = blockIdx.y, d = (int)blockIdx.x * 32 + x;
+  __shared__ double sh[64][17];
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4, k = blockIdx.y, d = (int)blockIdx.x * 16 + x;
   float *o = k == 0 ? o0 : k == 1 ? o1 : o2;
   if (!o) return;
   double s = 0;
   if (d < D)
-    for (int p0 = y; p0 < P; p0 += 256) {
+    for (int p0 = y; p0 < P; p0 += 512) {
       float v[8];
 #pragma unroll
-      for (int q = 0; q < 8; q++) v[q] = p0 + 32 * q < P ? part[((p0 + 32LL * q) * 3 + k) * D + d] : 0.f;
+      for (int q = 0; q < 8; q++) v[q] = p0 + 64 * q < P ? part[((p0 + 64LL * q) * 3 + k) * D + d] : 0.f;
 #pragma unroll
       for (int q = 0; q < 8; q++) s += (double)v[q];
     }
   sh[y][x] = s;
-  for (int h = 16; h >= 1; h >>= 1) {
+  for (int h = 32; h >= 1; h >>= 1) {
     __syncthreads();
     if (y < h) sh[y][x] += sh[y + h][x];
   }
@@ -810,7 +810,7 @@ int pararnn_gated_adjoint(const pr_gated_problem *p, const pr_gated_inputs *in, 
   else k_gated_adj<float, 2, 8, 4><<<grid, 64 * pl.waves, 0, s>>>(a, ch);
   HIPCHK(hipGetLastError());
   if (!sums) return PR_OK;
-  k_gated_sums<<<dim3((unsigned)((p->D + 31) / 32), 3), 1024, 0, s>>>(a.part, p->B * pl.tiles, p->D, gr->decay,
+  k_gated_sums<<<dim3((unsigned)((p->D + 15) / 16), 3), 1024, 0, s>>>(a.part, p->B * pl.tiles, p->D, gr->decay,
                                                                       gr->r_bias, gr->i_bias);
   HIPCHK(hipGetLastError());
   return PR_OK;

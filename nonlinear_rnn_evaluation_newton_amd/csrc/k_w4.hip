@@ -28,13 +28,6 @@ constexpr int W4_CH = 128;  // columns of a wavefront's step: 16 bytes of 4-bit 
 __device__ inline bf16x8 words(unsigned a, unsigned b, unsigned c, unsigned d) {
   return __builtin_bit_cast(bf16x8, u32x4v{a, b, c, d});
 }
-// 16 + q for the eight numbers of a word: q in the upper four bits of a bf16 with
-// the exponent of 16, two numbers an operation.  The 16 (and the zero point) are
-// taken off by the sums of x, which the matrix unit makes from an operand of ones.
-__device__ inline bf16x8 w4_operand(unsigned w) {
-  constexpr unsigned M = 0x00780078u, E = 0x41804180u;
-  return words(((w << 3) & M) | E, ((w >> 1) & M) | E, ((w >> 5) & M) | E, ((w >> 9) & M) | E);
-}
 __device__ inline unsigned halves(unsigned lo, unsigned hi, bool upper) {  // their lower or upper 16 bits side by side
   return __builtin_amdgcn_perm(hi, lo, upper ? 0x07060302u : 0x05040100u);
 }
@@ -45,6 +38,15 @@ struct XOps;
 template <>
 struct XOps<uint16_t> {
   static constexpr int N = 1;
+  // The weights' operand for the eight numbers of a word: 16 + q, q in the upper four
+  // bits of a bf16 with the exponent of 16, two numbers an operation.  The 16 and the
+  // zero point are taken off by the sums of x, which the matrix unit makes from an
+  // operand of ones.
+  static constexpr float OFFSET = 16.f;
+  static __device__ bf16x8 weights(unsigned w) {
+    constexpr unsigned M = 0x00780078u, E = 0x41804180u;
+    return words(((w << 3) & M) | E, ((w >> 1) & M) | E, ((w >> 5) & M) | E, ((w >> 9) & M) | E);
+  }
   bf16x8 o[1];
   __device__ void set(const VecU<uint16_t, 8> &x) {
     o[0] = words(halves(x.v.x, x.v.z, false), halves(x.v.x, x.v.z, true), halves(x.v.y, x.v.w, false),
@@ -54,6 +56,19 @@ struct XOps<uint16_t> {
 template <>
 struct XOps<float> {
   static constexpr int N = 3;
+  // q - 8, so that sums of 24 bits lose nothing to an offset: 16 + q as fp32 less 24.
+  // The sums of x are needed for other zero points than 8 only.
+  static constexpr float OFFSET = -8.f;
+  static __device__ bf16x8 weights(unsigned w) {
+    unsigned p[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const float a = __uint_as_float(((w << (19 - 4 * k)) & 0x00780000u) | 0x41800000u) - 24.f;
+      const float b = __uint_as_float(((4 * k <= 3 ? w << (3 - 4 * k) : w >> (4 * k - 3)) & 0x00780000u) | 0x41800000u) - 24.f;
+      p[k] = halves(__float_as_uint(a), __float_as_uint(b), true);
+    }
+    return words(p[0], p[1], p[2], p[3]);
+  }
   bf16x8 o[3];
   __device__ void set(const VecU<float, 8> &x) {
     unsigned p[3][4];
@@ -105,14 +120,16 @@ struct GroupWindow {
 // slices of K, 256 columns (a line of a row of weights) at a time, and join in
 // shared memory.  GM: groups in 128 columns, 1 (also where a group is several times
 // 128), 2 or 4, or 0 where groups end anywhere between 32 columns.
-template <typename T, int MT, int NT, int GM, int WV>
+template <typename T, int MT, int NT, int GM, int WV, bool ZERO>
 __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
   constexpr int NG = GM ? GM : 4;
+  constexpr bool SUMS = ZERO || XOps<T>::OFFSET != -8.f;
   __shared__ float red[WV][NT * 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;
-  const int nb = (a.N + 16 * NT - 1) / (16 * NT);
-  const int n0 = (int)(blockIdx.x % nb) * 16 * NT, m0 = (int)(blockIdx.x / nb) * 16 * MT;
+  // (blocks side by side share weights: they are read from memory once)
+  const int mb = (a.M + 16 * MT - 1) / (16 * MT);
+  const int n0 = (int)(blockIdx.x / mb) * 16 * NT, m0 = (int)(blockIdx.x % mb) * 16 * MT;
   // rows past the end read the last one; their results are not stored
   const uint8_t *wp[NT];
   const T *xp[MT], *sp[NT], *zp[NT];
@@ -173,7 +190,7 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
 #pragma unroll
         for (int j = 0; j < NT; j++) {
           sc[j][u] = ldf(sp[j], g);
-          zr[j][u] = a.zero ? ldf(zp[j], g) : 8.f;
+          zr[j][u] = ZERO ? ldf(zp[j], g) : 8.f;
         }
       }
     } else {
@@ -181,7 +198,7 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
 #pragma unroll
         for (int j = 0; j < NT; j++) {
           gs[j].load(sp[j] + g0, a.G - g0);
-          if (a.zero) gz[j].load(zp[j] + g0, a.G - g0);
+          if (ZERO) gz[j].load(zp[j] + g0, a.G - g0);
         }
         have = GroupWindow<T>::N;
         g0 += have;
@@ -191,7 +208,7 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
 #pragma unroll
         for (int u = 0; u < NG; u++) {
           sc[j][u] = gs[j].get(u);
-          zr[j][u] = a.zero ? gz[j].get(u) : 8.f;
+          zr[j][u] = ZERO ? gz[j].get(u) : 8.f;
         }
       if (--stay == 0) {
         stay = per;
@@ -199,7 +216,7 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
 #pragma unroll
         for (int j = 0; j < NT; j++) {
           gs[j].template drop<NG>();
-          if (a.zero) gz[j].template drop<NG>();
+          if (ZERO) gz[j].template drop<NG>();
         }
       }
     }
@@ -223,7 +240,7 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
     for (int u = 0; u < 4; u++) {
       bf16x8 bw[NT];
 #pragma unroll
-      for (int j = 0; j < NT; j++) bw[j] = w4_operand(b[j][u]);
+      for (int j = 0; j < NT; j++) bw[j] = XOps<T>::weights(b[j][u]);
 #pragma unroll
       for (int i = 0; i < MT; i++) {
         XOps<T> x;
@@ -235,7 +252,7 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
         }
 #pragma unroll
         for (int o = 0; o < XOps<T>::N; o++) {
-          xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.o[o], ones, xs[i], 0, 0, 0);
+          if (SUMS) xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.o[o], ones, xs[i], 0, 0, 0);
 #pragma unroll
           for (int j = 0; j < NT; j++)
             d[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.o[o], bw[j], d[i][j], 0, 0, 0);
@@ -245,7 +262,7 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
           for (int j = 0; j < NT; j++)
 #pragma unroll
             for (int r = 0; r < 4; r++)
-              acc[i][j][r] = fmaf(sc[j][u * NG / 4], fmaf(-16.f - zr[j][u * NG / 4], xs[i][r], d[i][j][r]), acc[i][j][r]);
+              acc[i][j][r] = fmaf(sc[j][u * NG / 4], SUMS ? fmaf(-XOps<T>::OFFSET - zr[j][u * NG / 4], xs[i][r], d[i][j][r]) : d[i][j][r], acc[i][j][r]);
         }
       }
     }
@@ -292,40 +309,40 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
   }
 }
 
-// Tiles of a block: columns side by side where there are blocks enough for all CUs
-// without, since every block reads all of x.  At most 4 x 2 tiles of bf16 rows and
-// 2 x 2 of fp32 ones, whose operands take three times the registers.
+// Tiles of a block.  A step of a tile of columns reads 1 KB of weights, one of a
+// tile of bf16 rows 4 KB of x (from the L2, which holds it): columns side by side
+// share x, as long as there are blocks for all CUs, and where there are many, two
+// tiles of rows share weights.
 struct W4Geom {
   int mt, nt;
 };
 static W4Geom w4_geom(int dtype, int M, int N) {
-  W4Geom g;
-  g.mt = M <= 16 ? 1 : M <= 32 || dtype != PR_BF16 ? 2 : 4;
-  g.nt = N >= 16384 && g.mt == 1 ? 4 : N >= 8192 ? 2 : 1;
-  return g;
+  const long long rows = (M + 15) / 16, cols = (N + 15) / 16, tiles = rows * cols;
+  if (rows > 1 && tiles >= 8 * 256 && dtype == PR_BF16) return {2, 4};
+  if (rows > 1 && tiles >= 4 * 256 && tiles < 8 * 256) return {2, 2};
+  return {1, tiles >= 4 * 256 ? 4 : tiles >= 2 * 256 ? 2 : 1};
 }
-template <typename T, int MT, int NT>
-void w4_go(W4Args &a, unsigned blocks, hipStream_t s) {
-  constexpr int WV = NT == 4 ? 4 : 8, NT_ = 64 * WV;
+template <typename T, int MT, int NT, bool ZERO, int WV>
+void w4_groups(W4Args &a, unsigned blocks, hipStream_t s) {
   const int steps = (a.K + W4_CH - 1) / W4_CH;
   a.slice = (steps + WV - 1) / WV * W4_CH;
-  if (a.group % W4_CH == 0) k_w4_rows<T, MT, NT, 1, WV><<<blocks, NT_, 0, s>>>(a);
-  else if (a.group == 64) k_w4_rows<T, MT, NT, 2, WV><<<blocks, NT_, 0, s>>>(a);
-  else if (a.group == 32) k_w4_rows<T, MT, NT, 4, WV><<<blocks, NT_, 0, s>>>(a);
-  else k_w4_rows<T, MT, NT, 0, WV><<<blocks, NT_, 0, s>>>(a);
+  if (a.group % W4_CH == 0) k_w4_rows<T, MT, NT, 1, WV, ZERO><<<blocks, 64 * WV, 0, s>>>(a);
+  else if (a.group == 64) k_w4_rows<T, MT, NT, 2, WV, ZERO><<<blocks, 64 * WV, 0, s>>>(a);
+  else if (a.group == 32) k_w4_rows<T, MT, NT, 4, WV, ZERO><<<blocks, 64 * WV, 0, s>>>(a);
+  else k_w4_rows<T, MT, NT, 0, WV, ZERO><<<blocks, 64 * WV, 0, s>>>(a);
 }
-template <typename T>
+template <typename T, bool ZERO>
 hipError_t w4_launch(W4Args &a, const W4Geom &g, unsigned blocks, hipStream_t s) {
-  if (g.mt == 1) {
-    if (g.nt == 1) w4_go<T, 1, 1>(a, blocks, s);
-    else if (g.nt == 2) w4_go<T, 1, 2>(a, blocks, s);
-    else w4_go<T, 1, 4>(a, blocks, s);
-  } else if (g.mt == 2) {
-    if (g.nt == 1) w4_go<T, 2, 1>(a, blocks, s);
-    else w4_go<T, 2, 2>(a, blocks, s);
-  } else if constexpr (sizeof(T) == 2) {
-    if (g.nt == 1) w4_go<T, 4, 1>(a, blocks, s);
-    else w4_go<T, 4, 2>(a, blocks, s);
+  if (g.mt == 2) {
+    if constexpr (sizeof(T) == 2)
+      if (g.nt == 4) w4_groups<T, 2, 4, ZERO, 4>(a, blocks, s);
+    if (g.nt == 2) w4_groups<T, 2, 2, ZERO, 8>(a, blocks, s);
+  } else if (g.nt == 4) {
+    w4_groups<T, 1, 4, ZERO, 4>(a, blocks, s);
+  } else if (g.nt == 2) {
+    w4_groups<T, 1, 2, ZERO, 8>(a, blocks, s);
+  } else {
+    w4_groups<T, 1, 1, ZERO, 8>(a, blocks, s);
   }
   return hipGetLastError();
 }
@@ -481,7 +498,7 @@ int w4_check(int dtype, int M, int N, int K, int group) {
   return PR_OK;
 }
 
-int w4_groups(int K, int group) { return (int)(((long long)K + group - 1) / group); }
+int w4_group_count(int K, int group) { return (int)(((long long)K + group - 1) / group); }
 
 }  // namespace
 
@@ -501,14 +518,16 @@ int pararnn_gemm_w4(int dtype, int M, int N, int K, int group, const void *x, lo
     return fail(PR_EINVAL, "row strides %lld, %lld, %lld are below K = %d, (K + 1) / 2, N = %d", ldx, ldq, ldo, K, N);
   W4Args a{};
   a.x = x; a.q = q; a.scale = scale; a.zero = zero; a.bias = bias; a.out = out;
-  a.ldx = ldx; a.ldq = ldq; a.ldo = ldo; a.M = M; a.N = N; a.K = K; a.group = group; a.G = w4_groups(K, group);
+  a.ldx = ldx; a.ldq = ldq; a.ldo = ldo; a.M = M; a.N = N; a.K = K; a.group = group; a.G = w4_group_count(K, group);
   a.rgroup = 32.f / (float)group;
   const W4Geom g = w4_geom(dtype, M, N);
   const long long blocks = (long long)((N + 16 * g.nt - 1) / (16 * g.nt)) * ((M + 16 * g.mt - 1) / (16 * g.mt));
   // a launch has 2^32 threads at most, 512 a block
   if (blocks >= (1 << 23)) return fail(PR_EUNSUPPORTED, "problem too large: %d x %d results", M, N);
   hipStream_t s = (hipStream_t)stream;
-  HIPCHK(dtype == PR_BF16 ? w4_launch<uint16_t>(a, g, (unsigned)blocks, s) : w4_launch<float>(a, g, (unsigned)blocks, s));
+  const unsigned nb = (unsigned)blocks;
+  if (dtype == PR_BF16) HIPCHK((zero ? w4_launch<uint16_t, true>(a, g, nb, s) : w4_launch<uint16_t, false>(a, g, nb, s)));
+  else HIPCHK((zero ? w4_launch<float, true>(a, g, nb, s) : w4_launch<float, false>(a, g, nb, s)));
   return PR_OK;
 }
 
@@ -520,7 +539,7 @@ int pararnn_quant_w4(int dtype, int N, int K, int group, const void *w, long lon
   if (!w || !q || !scale) return fail(PR_EINVAL, "w, q and scale are required");
   if (N == 1) { ldw = K; ldq = (K + 1) / 2; }
   if (ldq < (K + 1) / 2) return fail(PR_EINVAL, "row stride %lld is below (K + 1) / 2 = %d", ldq, (K + 1) / 2);
-  W4QuantArgs a{(void *)w, scale, zero, q, ldw, ldq, N, K, group, w4_groups(K, group)};
+  W4QuantArgs a{(void *)w, scale, zero, q, ldw, ldq, N, K, group, w4_group_count(K, group)};
   HIPCHK(dtype == PR_BF16 ? w4_quant_go<uint16_t>(a, (hipStream_t)stream) : w4_quant_go<float>(a, (hipStream_t)stream));
   return PR_OK;
 }
@@ -534,7 +553,7 @@ int pararnn_dequant_w4(int dtype, int N, int K, int group, const unsigned char *
   if (N == 1) { ldw = K; ldq = (K + 1) / 2; }
   if (ldw < K || ldq < (K + 1) / 2)
     return fail(PR_EINVAL, "row strides %lld, %lld are below K = %d, (K + 1) / 2", ldw, ldq, K);
-  W4QuantArgs a{w, (void *)scale, (void *)zero, (uint8_t *)q, ldw, ldq, N, K, group, w4_groups(K, group)};
+  W4QuantArgs a{w, (void *)scale, (void *)zero, (uint8_t *)q, ldw, ldq, N, K, group, w4_group_count(K, group)};
   const int per = (K + 7) / 8;
   const dim3 grid = flat_grid(((long long)N * per + 255) / 256);
   if (dtype == PR_BF16) k_w4_dequant<uint16_t><<<grid, 256, 0, (hipStream_t)stream>>>(a, per);

@@ -135,6 +135,18 @@ def test_four_bit_arguments():
     assert quant(w=None) == bd.PR_EINVAL and dequant(w=None) == bd.PR_EINVAL and dequant(ldw=99) == bd.PR_EINVAL
 
 
+def test_packed_structures_have_the_header_layout():
+    """The binding packs these as bytes; ctypes lays the same fields out by the C rules."""
+    view, rows = [7, 8, 9], [5, 6]
+    for cls, pack, v in ((bd.GatedProblem, bd._PACK_GATED, [1, 2, 3, 4]), (bd.View, bd._PACK_VIEW, view),
+                         (bd.Rows, bd._PACK_ROWS, rows), (bd.BlockNormProblem, bd._PACK_BLOCK_NORM, [1, 2, 3, 0.5, 4])):
+        assert pack(*v) == bytes(cls(*v)), cls
+    V3, R2 = bd.View(*view), bd.Rows(*rows)
+    assert bd._PACK_GATED_IN(*view * 3, 1, 2, 3, 4, 5) == bytes(bd.GatedInputs(V3, V3, V3, 1, 2, 3, 4, 5))
+    assert bd._PACK_GATED_GRADS(*view * 3, 1, 2, 3, 4) == bytes(bd.GatedGrads(V3, V3, V3, 1, 2, 3, 4))
+    assert bd._PACK_BLOCK_NORM_GRADS(*rows * 3, 1, 2, 3) == bytes(bd.BlockNormGrads(R2, R2, R2, 1, 2, 3))
+
+
 def test_binding_refuses_what_the_library_cannot_see():
     x, z = torch.zeros(2, 8, 16), torch.zeros(2, 16)
     f16, ws = torch.zeros(16), torch.empty(1 << 10, dtype=torch.uint8)

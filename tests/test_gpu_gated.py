@@ -321,7 +321,11 @@ PRODUCTS = [  # M, N, K, group, bytes around the rows of q, columns around x
     (17, 50, 1001, 64, (0, 0), (1, 0)), (31, 16, 2048, 128, (0, 0), (0, 0)), (32, 100, 513, 96, (2, 3), (0, 0)),
     (33, 7, 700, 128, (0, 0), (0, 0)), (64, 130, 1500, 160, (0, 0), (0, 2)), (65, 20, 300, 32, (0, 0), (0, 0)),
     (150, 35, 260, 64, (0, 0), (0, 0)), (5, 300, 4096, 4096, (0, 0), (0, 0)), (1, 2000, 640, 1 << 20, (0, 0), (0, 0)),
-    (4, 19, 9000, 256, (5, 0), (3, 3))]
+    (4, 19, 9000, 256, (5, 0), (3, 3)),
+    # two and four tiles of columns, two of rows by two and by four; long rows with every number of groups in 128 columns
+    (3, 8201, 130, 32, (0, 0), (0, 0)), (16, 16400, 260, 64, (0, 0), (0, 0)), (33, 8300, 300, 128, (0, 0), (0, 0)),
+    (20, 16390, 270, 64, (0, 0), (0, 0)), (40, 16400, 513, 32, (0, 0), (0, 0)), (2, 40, 5000, 64, (0, 0), (0, 0)),
+    (2, 40, 5003, 32, (0, 0), (0, 0)), (2, 40, 7000, 384, (0, 0), (0, 0))]
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
