@@ -354,24 +354,23 @@ struct W4QuantArgs {
   int N, K, group, G;
 };
 
-// y / s to the nearest, ties to even, for s > 0 and finite.  With inv the rounded
-// reciprocal, the product's exact remainder times inv corrects it, three operations
-// for a division's dozen; scales near the ends of the range are divided by.
+// y / s, correctly rounded, for s > 0 and finite.  With inv the rounded reciprocal,
+// the product's exact remainder times inv corrects it, three operations for a
+// division's dozen; scales near the ends of the range are divided by.
 struct Divisor {
   float s, inv;
   bool plain;
   __device__ explicit Divisor(float v) : s(v), inv(__fdiv_rn(1.f, v)), plain(v > 1e-30f && v < 1e30f) {}
-  __device__ float round(float y) const {
-    if (!plain) return rintf(__fdiv_rn(y, s));
+  __device__ float of(float y) const {
     const float q = y * inv;
-    return rintf(fmaf(fmaf(-q, s, y), inv, q));
+    return plain ? fmaf(fmaf(-q, s, y), inv, q) : __fdiv_rn(y, s);
   }
 };
 
 // L lanes (a power of two) for each group, eight columns each, which stay in
 // registers between the extremes and the rounding; groups of more than 8 L columns
 // (L = 64) are read again.
-template <typename T, int L>
+template <typename T, int L, bool ZERO>
 __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a) {
   const long long id = flat_block() * (256 / L) + threadIdx.x / L;  // row and group
   const int lane = threadIdx.x % L;
@@ -387,9 +386,9 @@ __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       const float f = v.f(i);
-      const unsigned bits = __float_as_uint(fabsf(f)), up = f > 0.f || f != f ? bits : 0u;
+      const unsigned bits = __float_as_uint(fabsf(f)), up = !ZERO || f > 0.f || f != f ? bits : 0u;
       hi = max(hi, up);
-      lo = max(lo, bits ^ up);
+      if (ZERO) lo = max(lo, bits ^ up);
     }
   };
   extremes(own);
@@ -398,27 +397,30 @@ __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a) {
 #pragma unroll
   for (int o = L / 2; o >= 1; o >>= 1) {
     hi = max(hi, (unsigned)__shfl_xor((int)hi, o, 64));
-    lo = max(lo, (unsigned)__shfl_xor((int)lo, o, 64));
+    if (ZERO) lo = max(lo, (unsigned)__shfl_xor((int)lo, o, 64));
   }
   const float fh = __uint_as_float(hi), fl = __uint_as_float(lo);
   T st;
-  stf(&st, 0, a.zero ? (fh + fl) * (1.f / 15.f) : __uint_as_float(max(hi, lo)) * (1.f / 7.f));
+  stf(&st, 0, ZERO ? (fh + fl) * (1.f / 15.f) : fh * (1.f / 7.f));
   const float s = ldf(&st, 0);
   const bool some = s > 0.f && s < __builtin_inff();
   const Divisor by(some ? s : 1.f);
   float z = 8.f;
-  if (a.zero) z = some ? fminf(fmaxf(by.round(fl), 0.f), 15.f) : s == 0.f ? 0.f : 8.f;
+  if (ZERO) z = some ? fminf(fmaxf(rintf(by.of(fl)), 0.f), 15.f) : s == 0.f ? 0.f : 8.f;
   if (on && lane == 0) {
     ((T *)a.scale)[id] = st;
-    if (a.zero) stf((T *)a.zero, id, z);
+    if (ZERO) stf((T *)a.zero, id, z);
   }
   auto store = [&](int k, const VecU<T, 8> &v) {
     const int c = k1 - k;
-    unsigned word = 0;
+    // held to the range, then rounded by the sum with 1.5 2^23, whose bits are a
+    // constant plus the number; constants and the zero point come off the whole word
+    unsigned word = ((unsigned)(int)z - 0x4b400000u) * 0x11111111u;
+    const float low = -z, high = 15.f - z;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const float f = some ? by.round(v.f(i)) + z : z;
-      word |= (unsigned)(int)fminf(fmaxf(f, 0.f), 15.f) << (4 * i);
+      const float f = some ? __builtin_amdgcn_fmed3f(by.of(v.f(i)), low, high) : 0.f;
+      word += __float_as_uint(f + 12582912.f) << (4 * i);
     }
     uint8_t *qp = a.q + n * a.ldq + (k >> 1);
     if (c >= 8) {
@@ -463,7 +465,9 @@ hipError_t w4_quant_go(const W4QuantArgs &a, hipStream_t s) {
   const long long groups = (long long)a.N * a.G;
 #define PR_Q(L)                                                                    \
   {                                                                                \
-    k_w4_quant<T, L><<<flat_grid((groups * L + 255) / 256), 256, 0, s>>>(a);       \
+    const dim3 grid = flat_grid((groups * L + 255) / 256);                         \
+    if (a.zero) k_w4_quant<T, L, true><<<grid, 256, 0, s>>>(a);                    \
+    else k_w4_quant<T, L, false><<<grid, 256, 0, s>>>(a);                          \
     return hipGetLastError();                                                      \
   }
   if (a.group <= 32) PR_Q(4)
