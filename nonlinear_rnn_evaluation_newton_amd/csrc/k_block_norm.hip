@@ -162,19 +162,20 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
 // The adjoint on rows in registers.  One round of sums for a row: with
 // F = w scale act(z) x, sum(e x) = sum(dt F) + rstd2 (sum(w_next dy F) - k2 sum(t F)),
 // k2 = rstd2^2 mean(w_next dy t).  Blocks walk rows with a stride of the grid and
-// keep their columns' sums in registers.  Rows of more than 512 threads are loaded
-// again, from cache, once their sums are known: there are no registers for them.
+// keep their columns' sums in registers.  Rows of more than two vectors a thread are
+// loaded again, from cache, once their sums are known: there are no registers for them.
 template <typename T, int TPR, int NV, bool EDGE>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 || TPR > 512 ? 4 : 2) void k_bn_adj(BnArgs a) {
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_adj(BnArgs a) {
   constexpr int V = bn_v<T>(), RPB = TPR > 256 ? 1 : 256 / TPR, NT = TPR > 256 ? TPR : 256;
-  constexpr bool AGAIN = TPR > 512;
+  constexpr bool AGAIN = NV > 2;
   __shared__ float sh[2][6][16];
   const int x = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  int xr = x;
   const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
   float q[NV][V], qn[NV][V];
   VecU<T, V> vw[NV], vs[NV], vn[NV];
   auto weights = [&](int m) __attribute__((always_inline)) {
-    const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+    const BnAt at = bn_at<T, TPR, EDGE>(xr, m, a.n);
     vw[m] = bn_ld<T>(a.w, 0, 0, at, a.w != nullptr);
     vs[m] = bn_ld<T>(a.scale, 0, 0, at, a.scale != nullptr);
     vn[m] = bn_ld<T>(a.wn, 0, 0, at, a.wn != nullptr);
@@ -194,7 +195,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 || TPR > 512 ? 4 : 2
     VecU<T, V> vx[NV], vz[NV], vt[NV], vd[NV], vy[NV];
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     auto load = [&](int m) __attribute__((always_inline)) {
-      const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+      const BnAt at = bn_at<T, TPR, EDGE>(xr, m, a.n);
       vx[m] = bn_ld<T>(a.x, row, a.lx, at, true);
       vz[m] = bn_ld<T>(a.z, row, a.lz, at, a.z != nullptr);
       vt[m] = bn_ld<T>(a.t, row, a.lt, at, a.dy != nullptr);
@@ -206,9 +207,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 || TPR > 512 ? 4 : 2
       for (int m = 0; m < NV; m++) load(m);
 #pragma unroll
     for (int m = 0; m < NV; m++) {
-      const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+      const BnAt at = bn_at<T, TPR, EDGE>(xr, m, a.n);
       if constexpr (AGAIN) {
-        asm volatile("" ::: "memory");  // (one vector's loads at a time)
+        asm volatile("" : "+v"(xr) : : "memory");  // (one vector's loads at a time)
         weights(m);
         load(m);
       } else {  // (as they were stored: unpacked they would take twice the registers)
@@ -234,10 +235,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 || TPR > 512 ? 4 : 2
     const float k2 = s[3] / n * rstd2 * rstd2, k1 = (s[1] + rstd2 * (s[4] - k2 * s[5])) / n * rstd1 * rstd1;
 #pragma unroll
     for (int m = 0; m < NV; m++) {
-      const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
+      const BnAt at = bn_at<T, TPR, EDGE>(xr, m, a.n);
       float ox[V], oz[V], og[V];
       if constexpr (AGAIN) {
-        asm volatile("" ::: "memory");  // (one vector's loads at a time)
+        asm volatile("" : "+v"(xr) : : "memory");  // (one vector's loads at a time)
         weights(m);
         load(m);
       } else {
@@ -412,24 +413,24 @@ __global__ __launch_bounds__(256) void k_bn_adj_long(BnArgs a) {
 }
 
 // The weights' gradients from the partials [P][2][n], in 64 bits in a fixed
-// order: 32 columns by 32 slices of the partials a block.
+// order: 16 columns by 64 slices of the partials a block.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_bn_sums(const float *__restrict__ part, int P, int n, const void *w,
                                                   const void *scale, float *dw, float *dscale, float *dwn) {
-  __shared__ double sh[32][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, k = blockIdx.y, c = (int)blockIdx.x * 32 + x;
+  __shared__ double sh[64][17];
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4, k = blockIdx.y, c = (int)blockIdx.x * 16 + x;
   if (k ? !dwn : !dw && !dscale) return;
   double s = 0;
   if (c < n)
-    for (int p0 = y; p0 < P; p0 += 256) {
+    for (int p0 = y; p0 < P; p0 += 512) {
       float v[8];
 #pragma unroll
-      for (int q = 0; q < 8; q++) v[q] = p0 + 32 * q < P ? part[((p0 + 32LL * q) * 2 + k) * n + c] : 0.f;
+      for (int q = 0; q < 8; q++) v[q] = p0 + 64 * q < P ? part[((p0 + 64LL * q) * 2 + k) * n + c] : 0.f;
 #pragma unroll
       for (int q = 0; q < 8; q++) s += (double)v[q];
     }
   sh[y][x] = s;
-  for (int h = 16; h >= 1; h >>= 1) {
+  for (int h = 32; h >= 1; h >>= 1) {
     __syncthreads();
     if (y < h) sh[y][x] += sh[y + h][x];
   }
@@ -444,8 +445,8 @@ __global__ __launch_bounds__(1024) void k_bn_sums(const float *__restrict__ part
 }
 
 // Threads and vectors of a row of q vectors; 0 threads: the row is read again
-// for each pass.  The adjoint holds five inputs and two sums, so at most two
-// vectors a thread.
+// for each pass.  The adjoint holds five inputs and two sums: two vectors a thread
+// stay in registers, and four of fp32 rows or three of bf16 ones are loaded twice.
 struct BnGeom {
   int tpr, nv;
 };
@@ -457,7 +458,8 @@ static BnGeom bn_geom(int n, int V, bool adj) {
   if (q <= 256) return {256, 1};
   if (q <= 512) return {256, 2};
   if (q <= 1024) return adj ? BnGeom{512, 2} : BnGeom{256, 4};
-  if (q <= 2048) return adj ? BnGeom{1024, 2} : BnGeom{512, 4};
+  if (adj && V == 8) return q <= 1536 ? BnGeom{512, 3} : BnGeom{0, 0};
+  if (q <= 2048) return {512, 4};
   return {0, 0};
 }
 
@@ -485,9 +487,9 @@ hipError_t bn_launch(const BnArgs &a, const BnGeom &g, bool adj, unsigned blocks
   else if (g.tpr == 256 && g.nv == 1) bn_go<T, 256, 1>(a, adj, blocks, s);
   else if (g.tpr == 256 && g.nv == 2) bn_go<T, 256, 2>(a, adj, blocks, s);
   else if (g.tpr == 256) bn_go<T, 256, 4, false>(a, adj, blocks, s);
-  else if (g.tpr == 1024) bn_go<T, 1024, 2, true>(a, adj, blocks, s);
-  else if (adj) bn_go<T, 512, 2, true>(a, adj, blocks, s);
-  else bn_go<T, 512, 4, false>(a, adj, blocks, s);
+  else if (g.nv == 2) bn_go<T, 512, 2, true>(a, adj, blocks, s);
+  else if (!adj) bn_go<T, 512, 4, false>(a, adj, blocks, s);
+  else bn_go<T, 512, sizeof(T) == 2 ? 3 : 4, true>(a, adj, blocks, s);
   return hipGetLastError();
 }
 
@@ -635,7 +637,7 @@ int pararnn_block_norm_adjoint(const pr_block_norm_problem *p, const pr_rows *x,
     }
   }
   if (!sums) return PR_OK;
-  const dim3 grid((unsigned)((p->n + 31) / 32), 2);
+  const dim3 grid((unsigned)((p->n + 15) / 16), 2);
   if (bf) k_bn_sums<uint16_t><<<grid, 1024, 0, s>>>(part, pl.parts, p->n, w, scale, gr->w, gr->scale, gr->w_next);
   else k_bn_sums<float><<<grid, 1024, 0, s>>>(part, pl.parts, p->n, w, scale, gr->w, gr->scale, gr->w_next);
   HIPCHK(hipGetLastError());

@@ -316,11 +316,13 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
 struct W4Geom {
   int mt, nt;
 };
-static W4Geom w4_geom(int dtype, int M, int N) {
+static W4Geom w4_geom(int dtype, int M, int N, bool zero) {
   const long long rows = (M + 15) / 16, cols = (N + 15) / 16, tiles = rows * cols;
-  if (rows > 1 && tiles >= 8 * 256 && dtype == PR_BF16) return {2, 4};
+  const bool bf = dtype == PR_BF16;
   if (rows > 1 && tiles >= 4 * 256 && tiles < 8 * 256) return {2, 2};
-  return {1, tiles >= 4 * 256 ? 4 : tiles >= 2 * 256 ? 2 : 1};
+  // (zero points take the registers of 2 x 4 tiles, and of 1 x 4 with fp32 rows)
+  if (rows > 1 && tiles >= 8 * 256 && bf && !zero) return {2, 4};
+  return {1, tiles >= 4 * 256 && (bf || !zero) ? 4 : tiles >= 2 * 256 ? 2 : 1};
 }
 template <typename T, int MT, int NT, bool ZERO, int WV>
 void w4_groups(W4Args &a, unsigned blocks, hipStream_t s) {
@@ -334,11 +336,11 @@ void w4_groups(W4Args &a, unsigned blocks, hipStream_t s) {
 template <typename T, bool ZERO>
 hipError_t w4_launch(W4Args &a, const W4Geom &g, unsigned blocks, hipStream_t s) {
   if (g.mt == 2) {
-    if constexpr (sizeof(T) == 2)
+    if constexpr (sizeof(T) == 2 && !ZERO)
       if (g.nt == 4) w4_groups<T, 2, 4, ZERO, 4>(a, blocks, s);
     if (g.nt == 2) w4_groups<T, 2, 2, ZERO, 8>(a, blocks, s);
   } else if (g.nt == 4) {
-    w4_groups<T, 1, 4, ZERO, 4>(a, blocks, s);
+    if constexpr (sizeof(T) == 2 || !ZERO) w4_groups<T, 1, 4, ZERO, 4>(a, blocks, s);
   } else if (g.nt == 2) {
     w4_groups<T, 1, 2, ZERO, 8>(a, blocks, s);
   } else {
@@ -524,7 +526,7 @@ int pararnn_gemm_w4(int dtype, int M, int N, int K, int group, const void *x, lo
   a.x = x; a.q = q; a.scale = scale; a.zero = zero; a.bias = bias; a.out = out;
   a.ldx = ldx; a.ldq = ldq; a.ldo = ldo; a.M = M; a.N = N; a.K = K; a.group = group; a.G = w4_group_count(K, group);
   a.rgroup = 32.f / (float)group;
-  const W4Geom g = w4_geom(dtype, M, N);
+  const W4Geom g = w4_geom(dtype, M, N, zero != nullptr);
   const long long blocks = (long long)((N + 16 * g.nt - 1) / (16 * g.nt)) * ((M + 16 * g.mt - 1) / (16 * g.mt));
   // a launch has 2^32 threads at most, 512 a block
   if (blocks >= (1 << 23)) return fail(PR_EUNSUPPORTED, "problem too large: %d x %d results", M, N);
