@@ -473,6 +473,10 @@ int pararnn_gemm_i8(int dtype, int M, int N, int K, const signed char *a, long l
  *   h_last  [B, D] or NULL: the state after the last step (may be h0)
  *   states  NULL, or [B, ceil(T / 64), D] fp32: the state that enters every
  *           64th step, for the adjoint (not written from a sequence's length on)
+ * A tile of steps waits for the tiles before it, which are handed out in order:
+ * they run already, whatever else keeps the device busy, so nothing has to be
+ * resident together.  (Such a wait is bounded all the same, by 2^16 polls without
+ * an answer; past it the states are NaN.)
  */
 #define PR_GATED_STATE_STEPS 64
 typedef struct {
@@ -550,8 +554,9 @@ int pararnn_block_norm_adjoint(const pr_block_norm_problem *p, const pr_rows *x,
  *   scale, zero [N, ceil(K / group)] in the storage dtype; zero NULL (= 8)
  */
 /* out[m][n] = sum_k x[m][k] w[n][k] + bias[n] for few rows x (decoding
- * batches; any number is computed, 64 at a time).  x [M, K], out [M, N] with row
- * strides, bias [N] or NULL, all in `dtype`.  Products are exact, sums in fp32. */
+ * batches; any number is computed).  x [M, K], out [M, N] with row strides, bias
+ * [N] or NULL, all in `dtype`.  Products are exact, sums in fp32, of x times up to
+ * 31: x is finite and below 1e36 (a row with an infinity or a NaN gives NaN).    */
 int pararnn_gemm_w4(int dtype, int M, int N, int K, int group, const void *x, long long ldx, const unsigned char *q,
                     long long ldq, const void *scale, const void *zero, const void *bias, void *out, long long ldo,
                     void *stream);

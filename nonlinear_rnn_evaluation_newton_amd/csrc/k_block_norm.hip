@@ -62,7 +62,8 @@ __device__ inline float block_sum(float v, float *sh) {
 // Rows that stay in registers: TPR threads a row, NV vectors of V elements (16
 // bytes) a thread.  EDGE: n is no multiple of V, and a row's last vector is its
 // last V elements, of which the first `dup` belong to the vector before: they are
-// left out of the sums, and written twice with the same values.
+// left out of the sums, and not written (a result may stand where an input did
+// that the other thread has still to read).
 template <typename T>
 constexpr int bn_v() { return 16 / (int)sizeof(T); }
 struct BnAt {
@@ -72,13 +73,25 @@ template <typename T, int TPR, bool EDGE>
 __device__ inline BnAt bn_at(int x, int m, int n) {
   constexpr int V = bn_v<T>();
   const int c = (x + m * TPR) * V;
-  if (c >= n) return BnAt{-1, V};
+  if (c >= n) return BnAt{-1, EDGE ? V : 0};
   if (EDGE && c > n - V) return BnAt{n - V, c - (n - V)};
   return BnAt{c, 0};
 }
 template <typename T>
 __device__ inline VecU<T, bn_v<T>()> bn_ld(const void *p, long long row, long long ld, const BnAt &at, bool there) {
   return ldu<T, bn_v<T>()>((const T *)p + row * ld + at.c, there && at.c >= 0 ? bn_v<T>() : 0);
+}
+template <typename T, bool EDGE>
+__device__ inline void bn_st(void *p, long long row, long long ld, const BnAt &at, const float *f) {
+  constexpr int V = bn_v<T>();
+  T *o = (T *)p + row * ld + at.c;
+  if (!EDGE || at.dup == 0) {
+    if (at.c >= 0) stu<T, V>(o, f, V);
+  } else {
+#pragma unroll
+    for (int i = 1; i < V; i++)
+      if (i >= at.dup) stf(o, i, f[i]);
+  }
 }
 // N sums over the threads of a row, the same in all of them, in a fixed order;
 // rows of several wavefronts use one half of sh for each call, in turn.
@@ -145,7 +158,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
       t[m][i] = to_storage<T>(a.res ? vr[m].f(i) + u : u);
       ss[0] = !EDGE || i >= at.dup ? fmaf(t[m][i], t[m][i], ss[0]) : ss[0];
     }
-    if (at.c >= 0) stu<T, V>((T *)a.t + row * a.lt + at.c, t[m], V);
+    bn_st<T, EDGE>(a.t, row, a.lt, at, t[m]);
   }
   if (!a.y) return;
   row_sums<TPR, 1>(ss, sh[1]);
@@ -155,7 +168,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
     const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
 #pragma unroll
     for (int i = 0; i < V; i++) t[m][i] *= rstd2 * (a.wn ? vn[m].f(i) : 1.f);
-    if (at.c >= 0) stu<T, V>((T *)a.y + row * a.ly + at.c, t[m], V);
+    bn_st<T, EDGE>(a.y, row, a.ly, at, t[m]);
   }
 }
 
@@ -256,11 +269,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
         oz[i] = g * f * xh * act.d;
         ox[i] = rstd1 * fmaf(-vx[m].f(i), k1, g * f * act.v);
       }
-      if (at.c >= 0) {
-        if (a.dres) stu<T, V>((T *)a.dres + row * a.ldres + at.c, og, V);
-        if (a.dz) stu<T, V>((T *)a.dz + row * a.ldz + at.c, oz, V);
-        if (a.dx) stu<T, V>((T *)a.dx + row * a.ldx + at.c, ox, V);
-      }
+      if (a.dres) bn_st<T, EDGE>(a.dres, row, a.ldres, at, og);
+      if (a.dz) bn_st<T, EDGE>(a.dz, row, a.ldz, at, oz);
+      if (a.dx) bn_st<T, EDGE>(a.dx, row, a.ldx, at, ox);
     }
   }
   if (!a.part) return;
@@ -269,14 +280,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
 #pragma unroll
     for (int m = 0; m < NV; m++) {
       const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
-      if (at.c >= 0) {  // (elements that two threads hold have the same sums)
-        stu<float, 4>(pp + at.c, q[m], 4);
-        stu<float, 4>(pp + a.n + at.c, qn[m], 4);
-        if constexpr (V == 8) {
-          stu<float, 4>(pp + at.c + 4, q[m] + 4, 4);
-          stu<float, 4>(pp + a.n + at.c + 4, qn[m] + 4, 4);
+#pragma unroll
+      for (int i = 0; i < V; i += 4)
+        if (at.c >= 0 && at.dup == 0) {
+          stu<float, 4>(pp + at.c + i, q[m] + i, 4);
+          stu<float, 4>(pp + a.n + at.c + i, qn[m] + i, 4);
         }
-      }
+      if (EDGE && at.c >= 0 && at.dup > 0)
+#pragma unroll
+        for (int i = 1; i < V; i++)
+          if (i >= at.dup) {
+            pp[at.c + i] = q[m][i];
+            pp[a.n + at.c + i] = qn[m][i];
+          }
     }
   } else {  // join the block's rows
     __shared__ float red[RPB][NV * V * TPR];

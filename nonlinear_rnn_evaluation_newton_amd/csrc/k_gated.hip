@@ -688,7 +688,8 @@ int gated_plan(const pr_gated_problem *p, bool adj, GatedPlan *pl) {
   pl->tiles = (p->T + pl->tt - 1) / pl->tt;
   pl->cb = (p->D + G_CH - 1) / G_CH;
   pl->cols = (long long)p->B * pl->cb;
-  if ((double)pl->cols * pl->tiles * 64 > 1e12) return fail(PR_EUNSUPPORTED, "problem too large");
+  if ((double)pl->cols * pl->tiles * 64 > 1e12 || (double)p->B * pl->tiles >= 2147483648.0)
+    return fail(PR_EUNSUPPORTED, "problem too large: %lld columns of %d tiles", pl->cols, pl->tiles);
   size_t o = 0;
   const size_t words = (size_t)pl->cols * 64 * 8, supers = (pl->tiles + G_SUPER - 1) / G_SUPER;
   if (pl->tiles > 1) {

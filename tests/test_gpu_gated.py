@@ -287,6 +287,32 @@ def test_block_norm(dtype, rows, n, gate):
     near(dx, R.block_norm_grads(x, w, z, gate, None, wn, t.cpu(), None, dy)["dx"], TOL, "dx")
 
 
+@pytest.mark.parametrize("dtype,n", [(BF, 513), (BF, 2049), (BF, 4099), (BF, 8193), (BF, 8199), (BF, 8705), (F, 257),
+                                     (F, 1025), (F, 4097), (F, 4099), (F, 4353), (F, 6146), (BF, 12297), (F, 8193)])
+def test_block_norm_in_place_at_row_ends(dtype, n):
+    """The last vector of a row overlaps the one before: where it lies in another
+    wavefront, or is taken later, a result over its input must not reach it."""
+    g, rows = gen(n), 5
+    x, z, res, dt, dy = (rnd(g, rows, n, dtype=dtype).cuda() for _ in range(5))
+    w, scale, wn = (rnd(g, n, dtype=dtype).cuda() for _ in range(3))
+    parts = dict(z=z, scale=scale, w_next=wn)
+    ws = work(bd.block_norm_workspace_bytes(dtype, rows, n))
+    t, y = nan(rows, n, dtype=dtype), nan(rows, n, dtype=dtype)
+    bd.block_norm(x, w, t, residual=res, y=y, **parts)
+    near(t, R.block_norm(x.cpu(), w.cpu(), z.cpu(), "silu", scale.cpu(), res.cpu()), TOL, "t")
+    r = R.block_norm_grads(x.cpu(), w.cpu(), z.cpu(), "silu", scale.cpu(), wn.cpu(), t.cpu(), dt.cpu(), dy.cpu())
+    for k in range(3):
+        same = res.clone()
+        bd.block_norm(x, w, same, residual=same, y=y, **parts)
+        assert torch.equal(same, t)
+        same = dt.clone()
+        o = dict(dx=nan(rows, n, dtype=dtype), dz=nan(rows, n, dtype=dtype), dw=nan(n), dscale=nan(n), dw_next=nan(n))
+        bd.block_norm_adjoint(x, w, workspace=ws, t=t, dt=same, dy=dy, dres=same, **parts, **o)
+        near(same, r["dres"], TOL, "dres")
+        for key, v in o.items():
+            near(v, r[key], SUM_TOL if v.dim() == 1 else TOL, key)
+
+
 def test_block_norm_zero_rows_and_far_gates():
     """A row of zeros, and gates beyond the exponential's range."""
     inf = float("inf")
