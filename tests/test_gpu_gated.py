@@ -492,3 +492,139 @@ def test_run_of_all_on_another_stream_and_in_a_graph():
         got = results()
         for key in want:
             assert torch.equal(want[key], got[key]), (k, key)
+
+
+# ---------------------------------------------------------------------------
+# far offsets, many tiles, many rows
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("B,T,D,ragged", [(1, 20000, 66, False), (3, 3000, 5, True), (9, 1100, 515, True)])
+def test_gated_many_tiles(dtype, B, T, D, ragged):
+    """Sequences of several hundred tiles, and many columns of tiles at once;
+    calls that repeat give the same bits, however the tiles met."""
+    g = gen(T + D)
+    p = gated_problem(g, dtype, B, T, D)
+    n = None
+    if ragged:
+        n = torch.randint(0, T + 1, (B,), generator=g).int()
+        n[0], n[-1] = T, 1
+    h0, dh, dy = rnd(g, B, D), rnd(g, B, D), rnd(g, B, T, D, dtype=dtype)
+    dev = {k: v.cuda() for k, v in p.items()}
+    main, kw = (dev["x"], dev["r"], dev["i"], dev["decay"]), dict(r_bias=dev["r_bias"], i_bias=dev["i_bias"],
+                                                                  lengths=None if n is None else n.cuda())
+    ws = work(bd.gated_workspace_bytes(dtype, B, T, D))
+    ry, rh = R.gated(**p, h0=h0, lengths=n)
+    r = R.gated_grads(**p, dy=dy, h0=h0, lengths=n, dh_last=dh)
+    first = None
+    for _ in range(4):
+        o = dict(y=nan(B, T, D, dtype=dtype), h=nan(B, D), dx=nan(B, T, D, dtype=dtype), dr=nan(B, T, D, dtype=dtype),
+                 di=nan(B, T, D, dtype=dtype), ddecay=nan(D), dr_bias=nan(D), di_bias=nan(D), dh0=nan(B, D))
+        states = nan(*bd.gated_states_shape(B, T, D))
+        bd.gated_scan(*main, o["y"], ws, h0=h0.cuda(), h_last=o["h"], states=states, **kw)
+        bd.gated_scan_adjoint(*main, states, dy.cuda(), ws, dh_last=dh.cuda(), **kw,
+                              **{k: v for k, v in o.items() if k not in ("y", "h")})
+        if first is None:
+            first = o
+            near(o["y"], ry, TOL, "y")
+            near(o["h"], rh, TOL, "h")
+            for k in ("dx", "dr", "di", "ddecay", "dr_bias", "di_bias", "dh0"):
+                near(o[k], r[k], SUM_TOL if o[k].dim() == 1 else TOL, k)
+        for k, v in o.items():
+            assert torch.equal(v, first[k]), k
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_gated_of_far_steps(dtype):
+    """Time strides whose products with the steps pass 2^32 bytes."""
+    g = gen(8)
+    B, T, D, st = 1, 1300, 37, 1 << 21 if dtype == BF else 1 << 20
+    p = gated_problem(g, dtype, B, T, D)
+    base = torch.empty(T * st, dtype=dtype, device="cuda")
+    far = {}
+    for k, at in (("x", 0), ("r", 1000), ("i", 2001), ("y", 3000), ("dx", 4001)):
+        far[k] = base.as_strided((B, T, D), (T * st, st, 1), at)
+        far[k].copy_(p[k].cuda() if k in p else torch.full((B, T, D), float("nan"), dtype=dtype, device="cuda"))
+    dev = {k: p[k].cuda() for k in ("decay", "r_bias", "i_bias")}
+    ws, states = work(bd.gated_workspace_bytes(dtype, B, T, D)), nan(*bd.gated_states_shape(B, T, D))
+    kw = dict(r_bias=dev["r_bias"], i_bias=dev["i_bias"])
+    bd.gated_scan(far["x"], far["r"], far["i"], dev["decay"], far["y"], ws, states=states, **kw)
+    near(far["y"].contiguous(), R.gated(**p)[0], TOL, "y")
+    dy = rnd(g, B, T, D, dtype=dtype)
+    bd.gated_scan_adjoint(far["x"], far["r"], far["i"], dev["decay"], states, dy.cuda(), ws, dx=far["dx"], **kw)
+    near(far["dx"].contiguous(), R.gated_grads(**p, dy=dy)["dx"], TOL, "dx")
+
+
+def test_gated_step_on_a_large_pool():
+    """States past 2^32 bytes of the pool."""
+    g = gen(9)
+    B, D, pool = 3, 1001, 1_200_000
+    p = gated_problem(g, F, B, 1, D)
+    dev = {k: v.cuda() for k, v in p.items()}
+    state, st = torch.empty(pool, D, device="cuda"), rnd(g, B, D)
+    at = torch.tensor([pool - 1, 0, pool - 2])
+    state[at.cuda()] = st.cuda()
+    y = nan(B, D)
+    bd.gated_step(dev["x"][:, 0], dev["r"][:, 0], dev["i"][:, 0], dev["decay"], state, y, r_bias=dev["r_bias"],
+                  i_bias=dev["i_bias"], slots=at.int().cuda())
+    ry, rh = R.gated(**p, h0=st)
+    near(y, ry[:, 0], TOL, "y")
+    near(state[at.cuda()], rh, TOL, "state")
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("n", [5, 300, 2051, 20000])
+def test_block_norm_of_far_rows(dtype, n):
+    """Rows that lie more than 2^32 bytes apart."""
+    g, rows, ld = gen(n), 3, (1 << 31) + 40 if dtype == BF else (1 << 30) + 24
+    base = torch.empty(ld * (rows - 1) + 8 * n, dtype=dtype, device="cuda")
+    names = ("x", "z", "res", "dt", "dy")
+    v = {k: rnd(g, rows, n, dtype=dtype) for k in names}
+    far = {k: base.as_strided((rows, n), (ld, 1), i * n) for i, k in enumerate(names + ("t", "y", "dx"))}
+    for k in far:
+        far[k].copy_(v[k].cuda() if k in v else torch.full((rows, n), float("nan"), dtype=dtype, device="cuda"))
+    bd.block_norm(far["x"], None, far["t"], z=far["z"], residual=far["res"], y=far["y"])
+    near(far["t"].contiguous(), R.block_norm(v["x"], None, v["z"], "silu", None, v["res"]), TOL, "t")
+    near(far["y"].contiguous(), R.norm_next(far["t"].cpu()), TOL, "y")
+    ws = work(bd.block_norm_workspace_bytes(dtype, rows, n))
+    bd.block_norm_adjoint(far["x"], None, far["dx"], ws, z=far["z"], t=far["t"], dt=far["dt"], dy=far["dy"])
+    r = R.block_norm_grads(v["x"], None, v["z"], "silu", None, None, far["t"].cpu(), v["dt"], v["dy"])
+    near(far["dx"].contiguous(), r["dx"], TOL, "dx")
+
+
+@pytest.mark.parametrize("n", [3, 8])
+def test_block_norm_of_very_many_rows(n):
+    """More rows than one grid dimension has blocks for: the first and the last ones."""
+    rows = (1 << 24) + 300
+    x = torch.randn(rows, n, device="cuda", dtype=BF)
+    t, y = torch.full_like(x, float("nan")), torch.full_like(x, float("nan"))
+    bd.block_norm(x, None, t, y=y)
+    dx = torch.full_like(x, float("nan"))
+    bd.block_norm_adjoint(x, None, dx, work(bd.block_norm_workspace_bytes(BF, rows, n)), dt=t)
+    for s in (slice(0, 400), slice(rows - 400, rows)):
+        near(t[s], R.block_norm(x[s].cpu()), TOL, "t")
+        near(y[s], R.norm_next(t[s].cpu()), TOL, "y")
+        near(dx[s], R.block_norm_grads(x[s].cpu(), dt=t[s].cpu())["dx"], TOL, "dx")
+    assert not torch.isnan(t).any() and not torch.isnan(dx).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_four_bits_of_far_rows(dtype):
+    """Packed rows and rows of weights past 2^32 bytes; very many rows of x."""
+    g, N, K, ld = gen(3), 40, 131, 120_000_000
+    w = rnd(g, N, K, dtype=dtype)
+    base = torch.empty(N * ld, dtype=torch.uint8, device="cuda")
+    q = base.as_strided((N, (K + 1) // 2), (ld, 1), 7)
+    scale = nan(N, 5, dtype=dtype)
+    bd.quant_w4(w.cuda(), q, scale, 32)
+    rq, rs, _ = R.quant(w, 32)
+    assert torch.equal(R.unpack(q.cpu(), K), rq) and torch.equal(scale.cpu(), rs)
+    x, out = rnd(g, 70000, K, dtype=dtype), nan(70000, N, dtype=dtype)
+    bd.gemm_w4(x.cuda(), q, scale, out, 32)
+    ws = R.weights(q.cpu(), rs, K, 32)
+    ref = x.double() @ ws.t()
+    room = 4 * K ** 0.5 * 2.0 ** -24 * (x.double().abs() @ (31 * rs.double().repeat_interleave(32, 1)[:, :K]).t())
+    room = room + (2.0 ** -8 if dtype == BF else 2.0 ** -24) * ref.abs()
+    assert bool(((out.double().cpu() - ref).abs() <= room).all())
+    back = torch.empty(N * ld // 2, dtype=dtype, device="cuda").as_strided((N, K), (ld // 2, 1), 3)
+    bd.dequant_w4(q, scale, back, 32)
+    assert torch.equal(back.cpu(), R.weights(q.cpu(), rs, K, 32, to=F).to(dtype))
