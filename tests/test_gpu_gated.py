@@ -628,3 +628,114 @@ def test_four_bits_of_far_rows(dtype):
     back = torch.empty(N * ld // 2, dtype=dtype, device="cuda").as_strided((N, K), (ld // 2, 1), 3)
     bd.dequant_w4(q, scale, back, 32)
     assert torch.equal(back.cpu(), R.weights(q.cpu(), rs, K, 32, to=F).to(dtype))
+
+
+# ---------------------------------------------------------------------------
+# the operators as a model calls them
+# ---------------------------------------------------------------------------
+def example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "gated_block.py")
+    spec = importlib.util.spec_from_file_location("gated_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    return ex
+
+
+def plain_model(first, blocks, s, c):
+    """The example's forward pass in elementary operations (any type, any device)."""
+    def norm(v, w):
+        return v / torch.sqrt((v * v).mean(-1, keepdim=True) + 1e-5) * w
+
+    y = norm(s, first)
+    for w in blocks:
+        x, r, i, z = (y @ w["inp"].t()).split(c, -1)
+        v = w["decay"] * torch.sigmoid(r + w["r_bias"])
+        a, u = torch.exp(-v), torch.sqrt(-torch.expm1(-2 * v)) * torch.sigmoid(i + w["i_bias"]) * x
+        h, hs = torch.zeros_like(u[:, 0]), []
+        for t in range(s.shape[1]):
+            h = a[:, t] * h + u[:, t]
+            hs.append(h)
+        o = (norm(torch.stack(hs, 1), w["norm"]) * z * torch.sigmoid(z)) @ w["out"].t()
+        s = s + norm(o, w["post"]) * w["scale"]
+        y = norm(s, w["after"])
+    return y
+
+
+def test_example_gradients():
+    """The example's model in fp32: output and gradients of all weights against
+    torch's autograd in 64 bits.  The products and the scans are off by 5e-5 at
+    most; each of the five norms behind them passes an error on at no more than
+    about twice its size: 32 x 5e-5, compared to 2e-3 of the largest value."""
+    ex = example()
+    model = ex.Model(dim=48, width=80, dtype=F, seed=4)
+    s = torch.randn(2, 150, 48, generator=gen(5))
+    dy = torch.randn(2, 150, 48, generator=gen(6))
+    y = model.forward(s.cuda())
+    y.backward(dy.cuda())
+    first, blocks = model.first.detach().double().cpu().requires_grad_(), [
+        {k: v.detach().double().cpu().requires_grad_() for k, v in b.items()} for b in model.blocks]
+    ref = plain_model(first, blocks, s.double(), 80)
+    ref.backward(dy.double())
+    near(y.detach(), ref.detach(), 2e-3, "y")
+    near(model.first.grad, first.grad, 2e-3, "first")
+    for mine, theirs in zip(model.blocks, blocks):
+        for k in mine:
+            near(mine[k].grad, theirs[k].grad, 2e-3, k)
+
+
+def test_example_runs():
+    """A few training steps have finite losses; single tokens continue a prompt as
+    the whole sequence does.  A prompt's products take the weights rounded to
+    bf16 (2^-9 each), and a dozen values on the way are rounded to bf16 in both:
+    20 roundings of 2^-9 of the largest output."""
+    ex = example()
+    model = ex.Model(dim=64, width=96, seed=3)
+    losses = ex.train(model, steps=3)
+    assert all(v == v and v < 1e3 for v in losses), losses
+    got, whole = ex.serve(model)
+    assert torch.isfinite(got).all()
+    assert float((got.float() - whole.float()).abs().max()) <= 20 * 2.0 ** -9 * float(whole.float().abs().max())
+
+
+def test_two_streams_at_once():
+    """Scans on two streams, each with its workspace, at the same time: the same bits as alone."""
+    g, dt, B, T, D = gen(31), BF, 2, 6000, 192
+    sets = []
+    for _ in range(2):
+        p = {k: v.cuda() for k, v in gated_problem(g, dt, B, T, D).items()}
+        sets.append(dict(p=p, dy=rnd(g, B, T, D, dtype=dt).cuda(), ws=work(bd.gated_workspace_bytes(dt, B, T, D)),
+                         states=nan(*bd.gated_states_shape(B, T, D))))
+
+    def run(s, y, dx):
+        p, kw = s["p"], dict(r_bias=s["p"]["r_bias"], i_bias=s["p"]["i_bias"])
+        bd.gated_scan(p["x"], p["r"], p["i"], p["decay"], y, s["ws"], states=s["states"], **kw)
+        bd.gated_scan_adjoint(p["x"], p["r"], p["i"], p["decay"], s["states"], s["dy"], s["ws"], dx=dx, **kw)
+
+    alone = [(nan(B, T, D, dtype=dt), nan(B, T, D, dtype=dt)) for _ in sets]
+    for s, (y, dx) in zip(sets, alone):
+        run(s, y, dx)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    together = [(nan(B, T, D, dtype=dt), nan(B, T, D, dtype=dt)) for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (y, dx), st in zip(sets, together, streams):
+            with torch.cuda.stream(st):
+                run(s, y, dx)
+    torch.cuda.synchronize()
+    for one, two in zip(alone, together):
+        assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+
+
+def test_host_workspace_is_refused():
+    """Every call that takes a workspace refuses one in host memory before it launches anything."""
+    z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    host, x, d = torch.empty(1 << 20, dtype=torch.uint8), z(2, 32, 16), z(16)
+    states, rows = z(*bd.gated_states_shape(2, 32, 16)), z(64, 16)
+    for name, call in (("gated_scan", lambda: bd.gated_scan(x, x, x, d, z(2, 32, 16), host)),
+                       ("gated_scan_adjoint", lambda: bd.gated_scan_adjoint(x, x, x, d, states, x, host, dx=z(2, 32, 16))),
+                       ("block_norm_adjoint", lambda: bd.block_norm_adjoint(rows, None, z(64, 16), host, dt=rows))):
+        with pytest.raises(ValueError, match=name + ": the workspace must be on the GPU"):
+            call()
