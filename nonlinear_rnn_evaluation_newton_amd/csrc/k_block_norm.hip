@@ -22,23 +22,19 @@ struct BnArgs {
   float eps;
 };
 
-// act(z) and its derivative.  The gate's kind is the same for a whole launch:
-// selects, so that no branch stands between the loads of a row.
+// act(z) and its derivative from p = sigm(z): both are a factor, z or a number,
+// of p and of p (1 - p), plus p times a number.  The gate's kind is the same for a
+// whole launch: one select, so that no branch stands between the loads of a row.
 struct Gate {
-  bool there, silu;
+  bool silu;
+  float k, c;  // act = (silu ? z : k) p; without a gate z is 0 and act = 2 sigm(0)
+  __device__ Gate(const void *z, int kind) : silu(z && kind == PR_GATE_SILU), k(z ? 1.f : 2.f), c(silu ? 1.f : 0.f) {}
 };
-struct Act {
-  float v, d;
-};
-__device__ inline float act_v(const Gate &g, float z) {
-  const float p = fsigm(z);
-  return g.there ? (g.silu ? z * p : p) : 1.f;
+__device__ inline float act_of(const Gate &g, float z, float p) { return (g.silu ? z : g.k) * p; }
+__device__ inline float act_d(const Gate &g, float z, float p) {
+  return fmaf(g.silu ? z : g.k, p * (1.f - p), g.c * p);
 }
-__device__ inline Act act_vd(const Gate &g, float z) {
-  const float p = fsigm(z), s = p * (1.f - p);
-  if (!g.there) return Act{1.f, 0.f};
-  return g.silu ? Act{z * p, fmaf(z, s, p)} : Act{p, s};
-}
+__device__ inline float act_v(const Gate &g, float z) { return act_of(g, z, fsigm(z)); }
 template <typename T>
 __device__ inline float to_storage(float v) {
   T t;
@@ -146,7 +142,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
   }
   row_sums<TPR, 1>(ss, sh[0]);
   const float rstd = 1.f / sqrtf(ss[0] / (float)a.n + a.eps);
-  const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
+  const Gate gate(a.z, a.gate);
   ss[0] = 0.f;
   float t[NV][V];
 #pragma unroll
@@ -175,8 +171,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
 // The adjoint on rows in registers.  One round of sums for a row: with
 // F = w scale act(z) x, sum(e x) = sum(dt F) + rstd2 (sum(w_next dy F) - k2 sum(t F)),
 // k2 = rstd2^2 mean(w_next dy t).  Blocks walk rows with a stride of the grid and
-// keep their columns' sums in registers.  Rows of more than two vectors a thread are
-// loaded again, from cache, once their sums are known: there are no registers for them.
+// keep their columns' sums in registers, and where a row is at most two vectors a
+// thread its weights in fp32 and each gate's sigmoid too.  Longer rows are loaded
+// again, from cache, once their sums are known: there are no registers for them.
 template <typename T, int TPR, int NV, bool EDGE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_adj(BnArgs a) {
   constexpr int V = bn_v<T>(), RPB = TPR > 256 ? 1 : 256 / TPR, NT = TPR > 256 ? TPR : 256;
@@ -184,19 +181,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
   __shared__ float sh[2][6][16];
   const int x = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   int xr = x;
-  const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
+  const Gate gate(a.z, a.gate);
   float q[NV][V], qn[NV][V];
-  VecU<T, V> vw[NV], vs[NV], vn[NV];
+  float F[NV][V], wn[NV][V];  // w scale, w_next
   auto weights = [&](int m) __attribute__((always_inline)) {
     const BnAt at = bn_at<T, TPR, EDGE>(xr, m, a.n);
-    vw[m] = bn_ld<T>(a.w, 0, 0, at, a.w != nullptr);
-    vs[m] = bn_ld<T>(a.scale, 0, 0, at, a.scale != nullptr);
-    vn[m] = bn_ld<T>(a.wn, 0, 0, at, a.wn != nullptr);
+    const VecU<T, V> vw = bn_ld<T>(a.w, 0, 0, at, a.w != nullptr), vs = bn_ld<T>(a.scale, 0, 0, at, a.scale != nullptr),
+                     vn = bn_ld<T>(a.wn, 0, 0, at, a.wn != nullptr);
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      F[m][i] = (a.w ? vw.f(i) : 1.f) * (a.scale ? vs.f(i) : 1.f);
+      wn[m][i] = a.wn ? vn.f(i) : 1.f;
+    }
   };
-  auto F = [&](int m, int i) __attribute__((always_inline)) {
-    return (a.w ? vw[m].f(i) : 1.f) * (a.scale ? vs[m].f(i) : 1.f);
-  };
-  auto wn = [&](int m, int i) __attribute__((always_inline)) { return a.wn ? vn[m].f(i) : 1.f; };
 #pragma unroll
   for (int m = 0; m < NV; m++) {
     if constexpr (!AGAIN) weights(m);
@@ -206,6 +203,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
   int par = 0;
   for (long long row = (long long)blockIdx.x * RPB + sub; row < a.rows; row += (long long)gridDim.x * RPB) {
     VecU<T, V> vx[NV], vz[NV], vt[NV], vd[NV], vy[NV];
+    float pz[AGAIN ? 1 : NV][V];
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     auto load = [&](int m) __attribute__((always_inline)) {
       const BnAt at = bn_at<T, TPR, EDGE>(xr, m, a.n);
@@ -225,14 +223,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
         asm volatile("" : "+v"(xr) : : "memory");  // (one vector's loads at a time)
         weights(m);
         load(m);
-      } else {  // (as they were stored: unpacked they would take twice the registers)
-        asm volatile("" : "+v"(vw[m].v), "+v"(vs[m].v), "+v"(vn[m].v));
       }
 #pragma unroll
       for (int i = 0; i < V; i++) {
+        const float p = fsigm(vz[m].f(i));
+        if constexpr (!AGAIN) pz[m][i] = p;
         if (EDGE && i < at.dup) continue;
-        const float xx = vx[m].f(i), t = vt[m].f(i), e = wn(m, i) * vy[m].f(i);
-        const float f = F(m, i) * act_v(gate, vz[m].f(i)) * xx;
+        const float xx = vx[m].f(i), t = vt[m].f(i), e = wn[m][i] * vy[m].f(i);
+        const float f = F[m][i] * act_of(gate, vz[m].f(i), p) * xx;
         s[0] = fmaf(xx, xx, s[0]);
         s[1] = fmaf(vd[m].f(i), f, s[1]);
         s[2] = fmaf(t, t, s[2]);
@@ -254,20 +252,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
         asm volatile("" : "+v"(xr) : : "memory");  // (one vector's loads at a time)
         weights(m);
         load(m);
-      } else {
+      } else {  // (as they were stored: unpacked they would take twice the registers)
         asm volatile("" : "+v"(vx[m].v), "+v"(vz[m].v), "+v"(vt[m].v), "+v"(vd[m].v), "+v"(vy[m].v));
-        asm volatile("" : "+v"(vw[m].v), "+v"(vs[m].v), "+v"(vn[m].v));
       }
 #pragma unroll
       for (int i = 0; i < V; i++) {
-        const float xh = vx[m].f(i) * rstd1, t = vt[m].f(i), dy = vy[m].f(i), f = F(m, i);
-        const Act act = act_vd(gate, vz[m].f(i));
-        const float g = fmaf(rstd2, fmaf(-t, k2, wn(m, i) * dy), vd[m].f(i));
+        const float x_ = vx[m].f(i), xh = x_ * rstd1, t = vt[m].f(i), dy = vy[m].f(i), z = vz[m].f(i);
+        const float p = AGAIN ? fsigm(z) : pz[AGAIN ? 0 : m][i], act = act_of(gate, z, p);
+        const float g = fmaf(rstd2, fmaf(-t, k2, wn[m][i] * dy), vd[m].f(i)), gf = g * F[m][i];
         qn[m][i] = fmaf(dy, t * rstd2, qn[m][i]);
-        q[m][i] = fmaf(g * act.v, xh, q[m][i]);
+        q[m][i] = fmaf(g * act, xh, q[m][i]);
         og[i] = g;
-        oz[i] = g * f * xh * act.d;
-        ox[i] = rstd1 * fmaf(-vx[m].f(i), k1, g * f * act.v);
+        oz[i] = gf * xh * act_d(gate, z, p);
+        ox[i] = rstd1 * fmaf(-x_, k1, gf * act);
       }
       if (a.dres) bn_st<T, EDGE>(a.dres, row, a.ldres, at, og);
       if (a.dz) bn_st<T, EDGE>(a.dz, row, a.ldz, at, oz);
@@ -325,7 +322,7 @@ __global__ __launch_bounds__(256) void k_bn_long(BnArgs a) {
   if (row >= a.rows) return;
   const T *xp = (const T *)a.x + row * a.lx, *zp = (const T *)a.z + row * a.lz, *rp = (const T *)a.res + row * a.lres;
   T *tp = (T *)a.t + row * a.lt;
-  const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
+  const Gate gate(a.z, a.gate);
   float ss = 0.f;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     const float v = ldf(xp, c);
@@ -391,7 +388,7 @@ __global__ __launch_bounds__(256) void k_bn_adj_cols(BnArgs a, int slices) {
   if (c >= a.n) return;
   const long long per = (a.rows + slices - 1) / slices, r0 = blockIdx.y * per;
   const long long r1 = r0 + per < a.rows ? r0 + per : a.rows;
-  const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
+  const Gate gate(a.z, a.gate);
   float q = 0.f, wn = 0.f;
   for (long long r = r0; r < r1; r++) {
     const BnRow s{a.stat[r * 3], a.stat[r * 3 + 1], a.stat[r * 3 + 2]};
@@ -411,7 +408,7 @@ __global__ __launch_bounds__(256) void k_bn_adj_long(BnArgs a) {
   if (row >= a.rows) return;
   const BnRow s{a.stat[row * 3], a.stat[row * 3 + 1], a.stat[row * 3 + 2]};
   const T *xp = (const T *)a.x + row * a.lx, *zp = (const T *)a.z + row * a.lz;
-  const Gate gate{a.z != nullptr, a.gate == PR_GATE_SILU};
+  const Gate gate(a.z, a.gate);
   float dot = 0.f;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     float e = bn_gt<T>(a, s, row, c) * (at1<T>(a.w, c) * at1<T>(a.scale, c));
@@ -421,10 +418,10 @@ __global__ __launch_bounds__(256) void k_bn_adj_long(BnArgs a) {
   const float k1 = block_sum(dot, sh) / (float)a.n * s.rstd1 * s.rstd1;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     const float gt = bn_gt<T>(a, s, row, c), ws = at1<T>(a.w, c) * at1<T>(a.scale, c), x = ldf(xp, c);
-    const Act act = act_vd(gate, a.z ? ldf(zp, c) : 0.f);
+    const float z = a.z ? ldf(zp, c) : 0.f, p = fsigm(z);
     if (a.dres) stf((T *)a.dres + row * a.ldres, c, gt);
-    if (a.dz) stf((T *)a.dz + row * a.ldz, c, gt * ws * (x * s.rstd1) * act.d);
-    if (a.dx) stf((T *)a.dx + row * a.ldx, c, s.rstd1 * fmaf(-x, k1, gt * ws * act.v));
+    if (a.dz) stf((T *)a.dz + row * a.ldz, c, gt * ws * (x * s.rstd1) * act_d(gate, z, p));
+    if (a.dx) stf((T *)a.dx + row * a.ldx, c, s.rstd1 * fmaf(-x, k1, gt * ws * act_of(gate, z, p)));
   }
 }
 
@@ -557,9 +554,13 @@ BnPlan bn_plan(const pr_block_norm_problem *p) {
   BnPlan pl;
   pl.g = bn_geom(p->n, p->dtype == PR_BF16 ? 8 : 4, true);
   size_t o = 0;
-  if (pl.g.tpr) {  // a few rows a block, so that the partials are few
+  if (pl.g.tpr) {
+    // as many blocks as run at once on 256 CUs, each with its share of the rows: with
+    // more, the last ones run on a device that is half empty, and there are more
+    // partials.  (Wavefronts a SIMD by the kernels' registers, 2 to 4.)
     const long long rpb = pl.g.tpr > 256 ? 1 : 256 / pl.g.tpr, b = (p->rows + rpb - 1) / rpb;
-    const long long most = pl.g.tpr > 256 ? 1024 * 256 / pl.g.tpr : 1024;
+    const int per_simd = (p->dtype == PR_BF16 ? 2 : 3) + (pl.g.nv == 1 ? 1 : 0);
+    const long long most = 256 * (pl.g.tpr > 256 ? 1 : per_simd);
     pl.parts = (int)(b < most ? b : most);
   } else {
     pl.parts = BN_SLICES;
