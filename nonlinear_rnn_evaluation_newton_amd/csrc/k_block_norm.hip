@@ -5,6 +5,13 @@
 //   e = gt w scale act(z),  dx = rstd1 (e - x^ mean(e x^)),
 //   dz = gt w scale x^ act'(z),  q = sum over rows of gt act(z) x^,
 //   dw = scale q,  dscale = w q,  dw_next = sum over rows of dy t^
+//
+// Bound by memory: every array is read or written once while a row stays in
+// registers, 16 bytes a thread and access.  Between a block's two norms nothing goes
+// through memory but t.  Squares and dot products are summed in fp32, the weights'
+// gradients over the rows in fp32 within a block and in fp64 over the blocks.
+// Measured, 16384 x 2048, bf16, with gate and residual: forward 59 us for 336 MB (in
+// part from the last-level cache); @ADJ@
 #include "pararnn.h"
 #include "ssm.h"
 #include "vec.h"
@@ -82,7 +89,7 @@ __device__ inline void bn_st(void *p, long long row, long long ld, const BnAt &a
   constexpr int V = bn_v<T>();
   T *o = (T *)p + row * ld + at.c;
   if (!EDGE || at.dup == 0) {
-    if (at.c >= 0) stu<T, V>(o, f, V);
+    if (at.c >= 0) stu_nt<T, V>(o, f, V);
   } else {
 #pragma unroll
     for (int i = 1; i < V; i++)
@@ -314,7 +321,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
   }
 }
 
-// Long rows: a block reads its row again for each pass.
+// Long rows (more than 16384 values of bf16 or 8192 of fp32; the adjoint's of bf16 more
+// than 12288) and rows shorter than a vector: a block reads its row again, from
+// cache, for each pass, element by element.
 template <typename T>
 __global__ __launch_bounds__(256) void k_bn_long(BnArgs a) {
   __shared__ float sh[2][4];

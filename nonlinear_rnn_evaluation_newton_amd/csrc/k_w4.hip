@@ -116,6 +116,16 @@ struct GroupWindow {
   }
 };
 
+// For one token or a decoding batch the weights' bytes are the floor; what they cost
+// on the way is what bounds the kernel: two operations for two numbers, a transposition
+// and the scales' for each group.  Few rows leave the matrix unit nearly idle (5% at 16
+// rows), so its 16 rows are no waste, and it takes over the sums of x besides.  The
+// scale multiplies a group's sum once and not each weight.
+// Measured (bf16): one token, 4096 x 4096, groups of 128: 6.3 us, of which a launch with
+// its first loads is 3 to 4; 16 x 32768 x 4096, groups of 64 with zero points: 28 us for 77
+// MB (2.7 TB/s; vector instructions in 45% of the cycles of two wavefronts a SIMD, whose
+// registers are full; twice the wavefronts by two tiles of columns take 40); without
+// zero points, groups of 128: 25; 64 rows: 85.
 // MT x NT tiles of 16 rows of x by 16 columns of the output; WV wavefronts take
 // slices of K, 256 columns (a line of a row of weights) at a time, and join in
 // shared memory.  GM: groups in 128 columns, 1 (also where a group is several times
@@ -372,6 +382,9 @@ struct Divisor {
   }
 };
 
+// Bound by memory: 8192 x 4096 in bf16 to groups of 128 takes 21 us (84 MB, 3.9 TB/s;
+// the reciprocal, the maximum over lanes and the rounding stand between a group's one
+// load and one store), and back 15.8 (5.3 TB/s).
 // L lanes (a power of two) for each group, eight columns each, which stay in
 // registers between the extremes and the rounding; groups of more than 8 L columns
 // (L = 64) are read again.

@@ -115,5 +115,22 @@ __device__ inline void stu(T *p, const float *f, int n) {
       if (i < n) p[i] = r.e[i];
   }
 }
+// The same for outputs that the call does not read again: stored non-temporally, they
+// leave the caches to its inputs (a block's norms and their gradients, 16384 x 2048 in
+// bf16: 177 to 166 us; the gated scan's training, 2 x 2048 x 2048: 64 to 54 us).
+template <typename T, int V>
+__device__ inline void stu_nt(T *p, const float *f, int n) {
+  VecU<T, V> r;
+#pragma unroll
+  for (int i = 0; i < V; i++) stf(r.e, i, f[i]);
+  typedef typename WordsOf<sizeof(T) * V>::type W __attribute__((aligned(sizeof(T))));
+  if (n >= V) {
+    __builtin_nontemporal_store(r.v, reinterpret_cast<W *>(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V - 1; i++)
+      if (i < n) p[i] = r.e[i];
+  }
+}
 
 }  // namespace pr
