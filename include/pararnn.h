@@ -465,7 +465,7 @@ int pararnn_gemm_i8(int dtype, int M, int N, int K, const signed char *a, long l
  *   r_t = sigm(rg_t + r_bias), i_t = sigm(ig_t + i_bias)
  *   a_t = exp(-decay r_t)
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t,  y_t = h_t
- * decay >= 0 and finite; where 1 - a_t^2 is 0 (a decay of 0, a closed gate)
+ * 0 <= decay <= 1e38; where 1 - a_t^2 is 0 (a decay of 0, a closed gate)
  * the input's term and its gradients are 0.
  *   x, r, i [B, T, D] (r, i: the gates rg, ig before the sigmoid), y   storage dtype
  *   decay [D], r_bias [D] or NULL, i_bias [D] or NULL                  fp32
@@ -564,8 +564,8 @@ int pararnn_gemm_w4(int dtype, int M, int N, int K, int group, const void *x, lo
  * (as a product with 1/7, rounded to storage), q = w / scale to the nearest,
  * ties to even, plus 8; with it: scale = (hi - lo) / 15 for lo = min(w, 0), hi =
  * max(w, 0), zero = -lo / scale, to the nearest and held to 0..15.  q is held to
- * 0..15.  A group of zeros has scale 0; one with an infinity or a NaN has that
- * as its scale, and q is its zero (8 where not asked for).                   */
+ * 0..15.  A group of zeros has scale 0; one with an infinity or a NaN, or whose
+ * hi - lo passes the type, has that (an infinity) as its scale; q and zero are 8. */
 int pararnn_quant_w4(int dtype, int N, int K, int group, const void *w, long long ldw, unsigned char *q, long long ldq,
                      void *scale, void *zero, void *stream);
 /* The values that q stands for, w [N, K] with row stride ldw in `dtype`. */

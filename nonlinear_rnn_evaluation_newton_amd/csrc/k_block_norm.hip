@@ -10,8 +10,11 @@
 // registers, 16 bytes a thread and access.  Between a block's two norms nothing goes
 // through memory but t.  Squares and dot products are summed in fp32, the weights'
 // gradients over the rows in fp32 within a block and in fp64 over the blocks.
-// Measured, 16384 x 2048, bf16, with gate and residual: forward 59 us for 336 MB (in
-// part from the last-level cache); @ADJ@
+// Measured, 16384 x 2048, bf16, with gate and residual: forward 56 us for 336 MB (in
+// part from the last-level cache; vector instructions in 77% of the cycles), adjoint 100
+// us for 540 MB (5.4 TB/s, 76%), the weights' sums 8; the same in fp32 on 8192 rows 159
+// together.  Instructions count as much as bytes here: with a division by n and a square
+// root for each sum, and row addresses in vector registers, the three took 166.
 #include "pararnn.h"
 #include "ssm.h"
 #include "vec.h"
@@ -26,8 +29,16 @@ struct BnArgs {
   long long lx, lz, lres, lt, ly, ldt, ldy, ldx, ldz, ldres;  // row strides
   long long rows;
   int n, gate;
-  float eps;
+  float eps, rn;  // rn = 1 / n
 };
+
+// 1 / sqrt(mean + eps) by the hardware's instruction, which is good to the last place
+// but takes no denormals.
+__device__ inline float rstd_of(float sum, const BnArgs &a) {
+  const float v = fmaf(sum, a.rn, a.eps);
+  const bool small = v < 0x1p-96f;
+  return __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v) * (small ? 0x1p32f : 1.f);
+}
 
 // act(z) and its derivative from p = sigm(z): both are a factor, z or a number,
 // of p and of p (1 - p), plus p times a number.  The gate's kind is the same for a
@@ -123,7 +134,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
   constexpr int V = bn_v<T>(), RPB = TPR > 256 ? 1 : 256 / TPR;
   __shared__ float sh[2][1][16];
   const int x = threadIdx.x % TPR;
-  const long long row = flat_block() * RPB + threadIdx.x / TPR;
+  const long long row = flat_block() * RPB + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
   if (row >= a.rows) return;  // whole wavefronts, whole rows
   VecU<T, V> vx[NV], vz[NV], vr[NV];
   float ss[1] = {0.f};
@@ -148,7 +159,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
     }
   }
   row_sums<TPR, 1>(ss, sh[0]);
-  const float rstd = 1.f / sqrtf(ss[0] / (float)a.n + a.eps);
+  const float rstd = rstd_of(ss[0], a);
   const Gate gate(a.z, a.gate);
   ss[0] = 0.f;
   float t[NV][V];
@@ -165,7 +176,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
   }
   if (!a.y) return;
   row_sums<TPR, 1>(ss, sh[1]);
-  const float rstd2 = 1.f / sqrtf(ss[0] / (float)a.n + a.eps);
+  const float rstd2 = rstd_of(ss[0], a);
 #pragma unroll
   for (int m = 0; m < NV; m++) {
     const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
@@ -186,7 +197,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
   constexpr int V = bn_v<T>(), RPB = TPR > 256 ? 1 : 256 / TPR, NT = TPR > 256 ? TPR : 256;
   constexpr bool AGAIN = NV > 2;
   __shared__ float sh[2][6][16];
-  const int x = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int x = threadIdx.x % TPR, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
   int xr = x;
   const Gate gate(a.z, a.gate);
   float q[NV][V], qn[NV][V];
@@ -248,9 +259,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
     }
     row_sums<TPR, 6>(s, sh[par]);
     par ^= 1;  // the next row's sums go to the other half
-    const float n = (float)a.n, rstd1 = 1.f / sqrtf(s[0] / n + a.eps);
-    const float rstd2 = a.dy ? 1.f / sqrtf(s[2] / n + a.eps) : 0.f;  // without dy: t and dy are zeros
-    const float k2 = s[3] / n * rstd2 * rstd2, k1 = (s[1] + rstd2 * (s[4] - k2 * s[5])) / n * rstd1 * rstd1;
+    const float rstd1 = rstd_of(s[0], a), rstd2 = a.dy ? rstd_of(s[2], a) : 0.f;  // without dy: t and dy are zeros
+    const float k2 = s[3] * a.rn * rstd2 * rstd2, k1 = (s[1] + rstd2 * (s[4] - k2 * s[5])) * a.rn * rstd1 * rstd1;
 #pragma unroll
     for (int m = 0; m < NV; m++) {
       const BnAt at = bn_at<T, TPR, EDGE>(xr, m, a.n);
@@ -337,7 +347,7 @@ __global__ __launch_bounds__(256) void k_bn_long(BnArgs a) {
     const float v = ldf(xp, c);
     ss = fmaf(v, v, ss);
   }
-  const float rstd = 1.f / sqrtf(block_sum(ss, sh[0]) / (float)a.n + a.eps);
+  const float rstd = rstd_of(block_sum(ss, sh[0]), a);
   ss = 0.f;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     float u = ldf(xp, c) * rstd * (at1<T>(a.w, c) * at1<T>(a.scale, c));
@@ -347,7 +357,7 @@ __global__ __launch_bounds__(256) void k_bn_long(BnArgs a) {
     ss = fmaf(t, t, ss);
   }
   if (!a.y) return;
-  const float rstd2 = 1.f / sqrtf(block_sum(ss, sh[1]) / (float)a.n + a.eps);
+  const float rstd2 = rstd_of(block_sum(ss, sh[1]), a);
   for (int c = threadIdx.x; c < a.n; c += 256)
     stf((T *)a.y + row * a.ly, c, ldf(tp, c) * rstd2 * at1<T>(a.wn, c));
 }
@@ -384,10 +394,10 @@ __global__ __launch_bounds__(256) void k_bn_adj_stat(BnArgs a) {
   dot = block_sum(dot, sh[2]);
   if (threadIdx.x == 0) {
     float *o = a.stat + row * 3;
-    const float n = (float)a.n, rstd2 = 1.f / sqrtf(st / n + a.eps);
-    o[0] = 1.f / sqrtf(ss / n + a.eps);
+    const float rstd2 = rstd_of(st, a);
+    o[0] = rstd_of(ss, a);
     o[1] = rstd2;
-    o[2] = dot / n * rstd2 * rstd2;
+    o[2] = dot * a.rn * rstd2 * rstd2;
   }
 }
 // q and dw_next: a block sums one slice of the rows for 256 columns
@@ -424,7 +434,7 @@ __global__ __launch_bounds__(256) void k_bn_adj_long(BnArgs a) {
     if (a.z) e *= act_v(gate, ldf(zp, c));
     dot = fmaf(e, ldf(xp, c), dot);
   }
-  const float k1 = block_sum(dot, sh) / (float)a.n * s.rstd1 * s.rstd1;
+  const float k1 = block_sum(dot, sh) * a.rn * s.rstd1 * s.rstd1;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     const float gt = bn_gt<T>(a, s, row, c), ws = at1<T>(a.w, c) * at1<T>(a.scale, c), x = ldf(xp, c);
     const float z = a.z ? ldf(zp, c) : 0.f, p = fsigm(z);
@@ -550,7 +560,7 @@ int bn_fill(const pr_block_norm_problem *p, const pr_rows *x, const pr_rows *z, 
     a->z = z->p; a->lz = z->ld;
   }
   a->w = w; a->scale = scale; a->wn = wn;
-  a->rows = p->rows; a->n = p->n; a->gate = p->gate; a->eps = p->eps;
+  a->rows = p->rows; a->n = p->n; a->gate = p->gate; a->eps = p->eps; a->rn = 1.f / (float)p->n;
   return PR_OK;
 }
 
