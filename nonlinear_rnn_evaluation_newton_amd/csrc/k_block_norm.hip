@@ -12,7 +12,7 @@
 // gradients over the rows in fp32 within a block and in fp64 over the blocks.
 // Measured, 16384 x 2048, bf16, with gate and residual: forward 56 us for 336 MB (in
 // part from the last-level cache; vector instructions in 77% of the cycles), adjoint 100
-// us for 540 MB (5.4 TB/s, 76%), the weights' sums 8; the same in fp32 on 8192 rows 159
+// us for 550 MB (5.5 TB/s, 76%), the weights' sums 8; the same in fp32 on 8192 rows 159
 // together.  Instructions count as much as bytes here: with a division by n and a square
 // root for each sum, and row addresses in vector registers, the three took 166.
 #include "pararnn.h"

@@ -14,11 +14,11 @@
 // the three inputs twice.  The adjoint reads x, r and i
 // again and makes the gates and states anew: storing a, m and both gates in fp32 would
 // move 32 bytes a step and channel to save 4.
-// Measured: 8 x 4096 x 2048, bf16, forward with saved states 121 us for 550 MB (4.5
-// TB/s, vector instructions in 62% of the cycles), adjoint 253 us for 976 MB (3.9 TB/s,
+// Measured: 8 x 4096 x 2048, bf16, forward with saved states 125 us for 550 MB (4.4
+// TB/s, vector instructions in 62% of the cycles), adjoint 260 us for 976 MB (3.8 TB/s,
 // 61%; three outputs and four inputs share the memory's reads and writes), the sums of
 // decay's and the biases' gradients 8, the chains' clearing 5 each; 1 x 32768 x 256,
-// fp32, 34 us (3.9 TB/s: 2048 tiles, of which each waits for those before it).
+// fp32, 35 us (3.9 TB/s: 2048 tiles, of which each waits for those before it).
 #include <type_traits>
 
 #include "pararnn.h"
