@@ -66,8 +66,8 @@ __device__ inline GateVals gate_vals(float rg, float ig, const GateConsts<T> &c)
     o.i = frcp(1.f + __builtin_amdgcn_exp2f(fmaf(ig, -LOG2E, c.ib)));
     o.a = __builtin_amdgcn_exp2f(c.nd * o.r);
   } else {
-    o.r = frcp(1.f + exp_acc(-(rg + c.rb)));
-    o.i = frcp(1.f + exp_acc(-(ig + c.ib)));
+    o.r = frcp(1.f + exp_any(-(rg + c.rb)));
+    o.i = frcp(1.f + exp_any(-(ig + c.ib)));
     o.a = exp_acc(c.nd * o.r);
   }
   // 1 - e^-w for w = 2 v: the difference where little is lost, else its series.

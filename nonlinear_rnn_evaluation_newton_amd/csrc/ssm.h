@@ -76,6 +76,17 @@ __device__ inline float exp_acc(float x) {
   return fabsf(x) < 128.f ? fmaf(e, r * 0.6931471805599453f, e) : e;
 }
 
+// The same for any x.  From 88.7 on e^x is infinite, and its product with a negative
+// r would make it a NaN: past 88 the plain result stands (off by 4e-6 up to there).
+__device__ inline float exp_any(float x) {
+  const float L = 1.44269502162933349609f, Ll = 1.92596299112661746887e-8f;
+  const float p = x * L;
+  float r = fmaf(x, L, -p);
+  r = fmaf(x, Ll, r);
+  const float e = __builtin_amdgcn_exp2f(p);
+  return fabsf(x + 20.f) < 108.f ? fmaf(e, r * 0.6931471805599453f, e) : e;
+}
+
 // log(1 + e) for 0 <= e <= 1: the logarithm of the rounded sum u, and what its
 // rounding left out, e - (u - 1), over u.  That quotient is taken without the
 // division: where u is not near 1 the term is below 2^-24 of the result.

@@ -1,0 +1,57 @@
+"""The gated block's operators at the ends of their ranges: far gates, large
+values, long memories, exact operands, long sums.  Every tolerance counts
+roundings: U = 2^-24 is half a step of fp32 relative to the value, and the
+device's exponential, root and reciprocal are good to one step, 2 U."""
+import pytest
+import torch
+
+import gated_reference as R
+from nonlinear_rnn_evaluation_newton_amd import binding as bd
+from test_gpu_gated import BF, F, example, gated_problem, gen, nan, near, rnd, work
+
+pytestmark = pytest.mark.gpu
+TOL = 5e-5  # of an output's largest value, for arithmetic in 32 bits over up to 250 steps
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    bd.lib()
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_gates_past_the_exponentials_range(dtype):
+    """Gates whose e^-x passes fp32 (x below -88.7) and its logarithm's sum, from the
+    gate itself and from the bias: closed gates, with finite outputs and gradients."""
+    g = gen(40)
+    B, T = 1, 70
+    far = torch.linspace(-131, -86, 181)
+    D = 2 * far.numel()
+    p = gated_problem(g, dtype, B, T, D)
+    p["r_bias"].zero_(), p["i_bias"].zero_()
+    for k, some in (("r", slice(0, far.numel())), ("i", slice(far.numel(), D))):
+        p[k][:, ::2, some] = far.to(dtype)
+        p[k][:, 1::2, some] += far.to(dtype) / 2
+        p[k + "_bias"][some][::2] = far[::2] / 2
+        p[k][:, ::2, some][..., ::2] = far[::2].to(dtype) / 2  # every other channel: half from the bias
+    dy = rnd(g, B, T, D, dtype=dtype)
+    dev = {k: v.cuda() for k, v in p.items()}
+    main, kw = (dev["x"], dev["r"], dev["i"], dev["decay"]), dict(r_bias=dev["r_bias"], i_bias=dev["i_bias"])
+    ws = work(bd.gated_workspace_bytes(dtype, B, T, D))
+    y, states = nan(B, T, D, dtype=dtype), nan(*bd.gated_states_shape(B, T, D))
+    bd.gated_scan(*main, y, ws, states=states, **kw)
+    near(y, R.gated(**p)[0], TOL, "y")
+    o = dict(dx=nan(B, T, D, dtype=dtype), dr=nan(B, T, D, dtype=dtype), di=nan(B, T, D, dtype=dtype))
+    bd.gated_scan_adjoint(*main, states, dy.cuda(), ws, **kw, **o)
+    r = R.gated_grads(**p, dy=dy)
+    for k, v in o.items():
+        near(v, r[k], TOL, k)
+    for t in (0, 1):
+        state, h0 = rnd(g, B, D), nan(B, D, dtype=dtype)
+        pool = state.cuda()
+        bd.gated_step(*(v[:, t] for v in main[:3]), dev["decay"], pool, h0, **kw)
+        one = {k: v[:, t:t + 1] if v.dim() == 3 else v for k, v in p.items()}
+        near(pool, R.gated(**one, h0=state)[1], TOL, "state")
