@@ -22,6 +22,11 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4v __attribute__((ext_vector_type(4)));
 constexpr int W4_CH = 128;  // columns of a wavefront's step: 16 bytes of 4-bit numbers a lane
 
+// Weights are multiplied as sixteenths, exact powers of two away from their values: up
+// to 128 columns are summed before their scale comes in, and of rows below 1e36 such a
+// sum, of at most two for each, stays below fp32's largest.  The result is multiplied by 16.
+constexpr float W4_UNIT = 16.f;
+
 // Operands of v_mfma_f32_16x16x32_bf16 for 8 adjacent columns k0..k7 of a lane, in
 // the order k0 k4, k1 k5, k2 k6, k3 k7: both operands have the same, and a product's
 // terms may come in any.
@@ -38,13 +43,13 @@ struct XOps;
 template <>
 struct XOps<uint16_t> {
   static constexpr int N = 1;
-  // The weights' operand for the eight numbers of a word: 16 + q, q in the upper four
-  // bits of a bf16 with the exponent of 16, two numbers an operation.  The 16 and the
+  // The weights' operand for the eight numbers of a word: 1 + q / 16, q in the upper
+  // four bits of a bf16 with the exponent of 1, two numbers an operation.  The 1 and the
   // zero point are taken off by the sums of x, which the matrix unit makes from an
   // operand of ones.
-  static constexpr float OFFSET = 16.f;
+  static constexpr float OFFSET = 1.f;
   static __device__ bf16x8 weights(unsigned w) {
-    constexpr unsigned M = 0x00780078u, E = 0x41804180u;
+    constexpr unsigned M = 0x00780078u, E = 0x3f803f80u;
     return words(((w << 3) & M) | E, ((w >> 1) & M) | E, ((w >> 5) & M) | E, ((w >> 9) & M) | E);
   }
   bf16x8 o[1];
@@ -56,15 +61,15 @@ struct XOps<uint16_t> {
 template <>
 struct XOps<float> {
   static constexpr int N = 3;
-  // q - 8, so that sums of 24 bits lose nothing to an offset: 16 + q as fp32 less 24.
-  // The sums of x are needed for other zero points than 8 only.
-  static constexpr float OFFSET = -8.f;
+  // (q - 8) / 16, so that sums of 24 bits lose nothing to an offset: 1 + q / 16 as fp32
+  // less 1.5.  The sums of x are needed for other zero points than 8 only.
+  static constexpr float OFFSET = -0.5f;
   static __device__ bf16x8 weights(unsigned w) {
     unsigned p[4];
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-      const float a = __uint_as_float(((w << (19 - 4 * k)) & 0x00780000u) | 0x41800000u) - 24.f;
-      const float b = __uint_as_float(((4 * k <= 3 ? w << (3 - 4 * k) : w >> (4 * k - 3)) & 0x00780000u) | 0x41800000u) - 24.f;
+      const float a = __uint_as_float(((w << (19 - 4 * k)) & 0x00780000u) | 0x3f800000u) - 1.5f;
+      const float b = __uint_as_float(((4 * k <= 3 ? w << (3 - 4 * k) : w >> (4 * k - 3)) & 0x00780000u) | 0x3f800000u) - 1.5f;
       p[k] = halves(__float_as_uint(a), __float_as_uint(b), true);
     }
     return words(p[0], p[1], p[2], p[3]);
@@ -133,7 +138,7 @@ struct GroupWindow {
 template <typename T, int MT, int NT, int GM, int WV, bool ZERO>
 __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
   constexpr int NG = GM ? GM : 4;
-  constexpr bool SUMS = ZERO || XOps<T>::OFFSET != -8.f;
+  constexpr bool SUMS = ZERO || XOps<T>::OFFSET != -8.f / W4_UNIT;
   __shared__ float red[WV][NT * 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;
@@ -272,7 +277,7 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
           for (int j = 0; j < NT; j++)
 #pragma unroll
             for (int r = 0; r < 4; r++)
-              acc[i][j][r] = fmaf(sc[j][u * NG / 4], SUMS ? fmaf(-XOps<T>::OFFSET - zr[j][u * NG / 4], xs[i][r], d[i][j][r]) : d[i][j][r], acc[i][j][r]);
+              acc[i][j][r] = fmaf(sc[j][u * NG / 4], SUMS ? fmaf(fmaf(zr[j][u * NG / 4], -1.f / W4_UNIT, -XOps<T>::OFFSET), xs[i][r], d[i][j][r]) : d[i][j][r], acc[i][j][r]);
         }
       }
     }
@@ -314,7 +319,8 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_rows(W4Args a) {
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < WV; w++) v += red[w][e];
-      if (m < a.M && n < a.N) stf((T *)a.out + m * a.ldo, n, a.bias ? v + ldf((const T *)a.bias, n) : v);
+      if (m < a.M && n < a.N)
+        stf((T *)a.out + m * a.ldo, n, a.bias ? fmaf(v, W4_UNIT, ldf((const T *)a.bias, n)) : v * W4_UNIT);
     }
   }
 }

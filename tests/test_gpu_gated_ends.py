@@ -55,3 +55,38 @@ def test_gates_past_the_exponentials_range(dtype):
         bd.gated_step(*(v[:, t] for v in main[:3]), dev["decay"], pool, h0, **kw)
         one = {k: v[:, t:t + 1] if v.dim() == 3 else v for k, v in p.items()}
         near(pool, R.gated(**one, h0=state)[1], TOL, "state")
+
+
+# ---------------------------------------------------------------------------
+PRODUCT_SIZES = [  # M, N, K, group: one, two and four tiles of columns, one and two of rows, every number of groups in 128 columns
+    (1, 40, 300, 128), (3, 33, 1001, 64), (17, 50, 700, 32), (5, 20, 513, 96), (3, 8201, 130, 32), (16, 16400, 260, 64),
+    (33, 8300, 300, 128), (40, 16400, 513, 32)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("zero", [True, False])
+@pytest.mark.parametrize("case", PRODUCT_SIZES)
+def test_product_of_large_rows(dtype, zero, case):
+    """Rows up to 1e36, of one sign and of both, by the largest and the smallest
+    numbers: sums of K terms of up to 31 steps, each sum rounded K times at most."""
+    M, N, K, group = case
+    print("large rows", dtype, zero, case, flush=True)
+    g = gen(M + N + K)
+    G = -(-K // group)
+    scale = (2.0 ** -20 * (torch.rand(N, G, generator=g) + 0.5)).to(dtype)
+    z = torch.randint(0, 16, (N, G), generator=g).to(dtype) if zero else None
+    q = torch.randint(0, 256, (N, (K + 1) // 2), generator=g, dtype=torch.uint8)
+    q[0::3], q[1::3] = 255, 0
+    top = torch.tensor(0.99e36).to(dtype)
+    x = torch.where(torch.rand(M, K, generator=g) < 0.5, top, -top)
+    x[0] = top
+    if M > 1:
+        x[1] = -top
+    out = nan(M, N, dtype=dtype)
+    bd.gemm_w4(x.cuda(), q.cuda(), scale.cuda(), out, group, zero=None if z is None else z.cuda())
+    ref = x.double() @ R.weights(q, scale, K, group, z).t()
+    got = out.double().cpu()
+    assert torch.isfinite(got).all(), torch.nonzero(~torch.isfinite(got))[:4].tolist()
+    steps = scale.double().repeat_interleave(group, 1)[:, :K]
+    room = 4 * K ** 0.5 * U * (x.double().abs() @ (31 * steps).t()) + (2.0 ** -8 if dtype == BF else U) * ref.abs()
+    assert bool(((got - ref).abs() <= room).all()), float(((got - ref).abs() / room).max())
