@@ -90,3 +90,26 @@ def test_product_of_large_rows(dtype, zero, case):
     steps = scale.double().repeat_interleave(group, 1)[:, :K]
     room = 4 * K ** 0.5 * U * (x.double().abs() @ (31 * steps).t()) + (2.0 ** -8 if dtype == BF else U) * ref.abs()
     assert bool(((got - ref).abs() <= room).all()), float(((got - ref).abs() / room).max())
+
+
+@pytest.mark.parametrize("zero", [True, False])
+@pytest.mark.parametrize("case", PRODUCT_SIZES)
+def test_product_has_every_bit_of_fp32_rows(zero, case):
+    """One column with a weight other than 0 for each output: the result is x times
+    a power of two, bit for bit.  All 24 bits of x are random: two operands of eight
+    bits instead of three would miss nearly every one."""
+    M, N, K, group = case
+    g = gen(M + N + K + 1)
+    G = -(-K // group)
+    bits = torch.randint(1 << 23, 1 << 24, (M, K), generator=g).float()
+    x = bits * 2.0 ** torch.randint(-40, 10, (M, K), generator=g).float()
+    col, up = torch.randint(0, K, (N,), generator=g), torch.rand(N, generator=g) < 0.5
+    q = torch.full((N, K + K % 2), 8, dtype=torch.uint8)
+    step = torch.where(up, 4, -2)  # q - 8
+    q[torch.arange(N), col] = (8 + step).to(torch.uint8)
+    power = torch.randint(-3, 4, (N, G), generator=g).float()
+    scale = 2.0 ** power
+    out = nan(M, N)
+    bd.gemm_w4(x.cuda(), (q[:, ::2] | q[:, 1::2] << 4).cuda(), scale.cuda(), out, group,
+               zero=torch.full((N, G), 8.0, device="cuda") if zero else None)
+    assert torch.equal(out.cpu(), x[:, col] * (step.float() * scale[torch.arange(N), col // group]))
