@@ -40,10 +40,10 @@ struct GatedArgs {
   int cb, tiles, tt, nst;    // columns of channels a sequence, tiles a column, steps a tile, saved states a sequence
 };
 
-// What a step's gates give: both gates, and a = e^-v and m = sqrt(1 - a^2) for
-// v = decay r.
+// What a step's gates give: both gates, and a = e^-v, its logarithm l (SHORT: to base
+// 2) and m = sqrt(1 - a^2) for v = decay r.
 struct GateVals {
-  float r, i, a, m;
+  float r, i, a, l, m;
 };
 constexpr float LOG2E = 1.4426950408889634f;
 // A channel's constants.  Rows stored in 8 significant bits take plain products
@@ -64,11 +64,13 @@ __device__ inline GateVals gate_vals(float rg, float ig, const GateConsts<T> &c)
   if constexpr (GateConsts<T>::SHORT) {
     o.r = frcp(1.f + __builtin_amdgcn_exp2f(fmaf(rg, -LOG2E, c.rb)));
     o.i = frcp(1.f + __builtin_amdgcn_exp2f(fmaf(ig, -LOG2E, c.ib)));
-    o.a = __builtin_amdgcn_exp2f(c.nd * o.r);
+    o.l = c.nd * o.r;
+    o.a = __builtin_amdgcn_exp2f(o.l);
   } else {
     o.r = frcp(1.f + exp_any(-(rg + c.rb)));
     o.i = frcp(1.f + exp_any(-(ig + c.ib)));
-    o.a = exp_acc(c.nd * o.r);
+    o.l = c.nd * o.r;
+    o.a = exp_acc(o.l);
   }
   // 1 - e^-w for w = 2 v: the difference where little is lost, else its series.
   // SHORT: up to w^4, the first term left out is below w^4 / 120 of it, 1.3e-7 at
@@ -88,6 +90,24 @@ __device__ inline GateVals gate_vals(float rg, float ig, const GateConsts<T> &c)
   return o;
 }
 
+// A sequence of steps multiplies the state by e^(sum of their l).  Near 1 a factor in
+// fp32 is off by a part of 1 - a that may be large, the same at every step of a steady
+// gate, and a product of thousands of them by thousands of times that (1e-3 of a state
+// kept over 24000 steps); the sum keeps what a factor loses.  So longer runs of steps
+// go by their sum, to base 2.
+__device__ inline float decay_of(float l2) { return __builtin_amdgcn_exp2f(l2); }
+// A h + b for A = e^-v, without the factor's rounding: near 1 by what it takes off,
+// 1 - e^-v, whose series is that of m^2.  (An infinite state stays one.)
+__device__ inline float decayed(float A, float v, float h, float b) {
+  float s = fmaf(v, -1.f / 24.f, 1.f / 6.f);
+  s = fmaf(v, s, -0.5f);
+  s = fmaf(v, s, 1.f);
+  const float e = v < 0.0625f ? v * s : 1.f - A, near = h + fmaf(-e, h, b);
+  return A > 0.5f && near == near ? near : fmaf(A, h, b);
+}
+constexpr float LN2 = 0.6931471805599453f;
+__device__ inline float decayed(float l2, float h, float b) { return decayed(decay_of(l2), l2 * -LN2, h, b); }
+
 // ---------------------------------------------------------------------------
 // tiles
 // ---------------------------------------------------------------------------
@@ -100,12 +120,12 @@ constexpr int G_CH = 64;
 constexpr int G_SUPER = 8;  // tiles of a super tile
 
 // State between the tiles of a column.  A tile publishes what it does to a
-// state, h -> A h + B; the last of 8 publishes the same of all 8, and, once it
+// state, h -> 2^L h + B; the last of 8 publishes the same of all 8, and, once it
 // is known, the state that leaves them.  A tile's state is the one that enters
 // its super tile, taken through the tiles before it in order, and that one is
 // the first state, taken through the super tiles in order: the same products and
 // sums whatever was published when it looked, so results repeat bit by bit.
-//   Words of 64 bits, A or 0 above B or the state; all ones: not there yet.  The
+//   Words of 64 bits, L or 0 above B or the state; all ones: not there yet.  The
 // word is read and written whole, so nothing has to be ordered around it.
 //   Tiles of a column are handed out in order by a counter: a tile waits only for
 // blocks that already run, whatever else runs on the device.
@@ -115,19 +135,19 @@ struct GatedChain {
   long long cols;
 };
 constexpr unsigned G_NONE = 0xffffffffu;
-__device__ inline unsigned long long chain_word(float A, float B) {
-  const unsigned h = __float_as_uint(A);
+__device__ inline unsigned long long chain_word(float L, float B) {
+  const unsigned h = __float_as_uint(L);
   return ((unsigned long long)(h == G_NONE ? 0x7fc00000u : h) << 32) | __float_as_uint(B);
 }
 __device__ inline bool chain_there(unsigned long long w) { return (unsigned)(w >> 32) != G_NONE; }
-__device__ inline float chain_A(unsigned long long w) { return __uint_as_float((unsigned)(w >> 32)); }
+__device__ inline float chain_L(unsigned long long w) { return __uint_as_float((unsigned)(w >> 32)); }
 __device__ inline float chain_B(unsigned long long w) { return __uint_as_float((unsigned)w); }
 
 // The state that enters tile j (j-th in the order of the chain) of column c,
-// for one channel a lane, after the tile's own A, B were published; `first`: the
+// for one channel a lane, after the tile's own L, B were published; `first`: the
 // column's first state, read by tile 0 alone.  A wait that sees nothing for
 // PR_SPIN_LIMIT polls gives up with a NaN.
-__device__ inline float chain_enter(const GatedChain &ch, long long c, int j, int tiles, float A, float B, float first) {
+__device__ inline float chain_enter(const GatedChain &ch, long long c, int j, int tiles, float L, float B, float first) {
   const unsigned lane = threadIdx.x & 63;
   const int s = j / G_SUPER, q = j % G_SUPER;
   const long long step = ch.cols * 64;
@@ -154,19 +174,19 @@ __device__ inline float chain_enter(const GatedChain &ch, long long c, int j, in
     if (++polls > PR_SPIN_LIMIT) return __builtin_nanf("");
     __builtin_amdgcn_s_sleep(1);
   }
-  float SA = A, SB = B;
+  float SL = L, SB = B;
   const bool closes = q == G_SUPER - 1 && j + 1 < tiles;
   if (closes) {
-    SA = chain_A(w[0]);
+    SL = chain_L(w[0]);
     SB = chain_B(w[0]);
 #pragma unroll
     for (int i = 1; i < G_SUPER - 1; i++) {
-      SB = fmaf(chain_A(w[i]), SB, chain_B(w[i]));
-      SA *= chain_A(w[i]);
+      SB = fmaf(decay_of(chain_L(w[i])), SB, chain_B(w[i]));
+      SL += chain_L(w[i]);
     }
-    SB = fmaf(A, SB, B);
-    SA *= A;
-    st_agent64(sagg, chain_word(SA, SB));
+    SB = fmaf(decay_of(L), SB, B);
+    SL += L;
+    st_agent64(sagg, chain_word(SL, SB));
   }
   // the state that enters the super tile: there, or from one of the 4 before it
   float h;
@@ -197,7 +217,7 @@ __device__ inline float chain_enter(const GatedChain &ch, long long c, int j, in
 #pragma unroll
     for (int i = W - 1; i >= 0; i--) {
       if (i == from) v = chain_B(pre[i]);
-      if (i <= from) v = fmaf(chain_A(ag[i]), v, chain_B(ag[i]));
+      if (i <= from) v = decayed(chain_L(ag[i]), v, chain_B(ag[i]));
     }
     if (!ok) {
       ok = from >= 0;
@@ -208,10 +228,10 @@ __device__ inline float chain_enter(const GatedChain &ch, long long c, int j, in
     __builtin_amdgcn_s_sleep(1);
     p = ld_agent64(spre);
   }
-  if (closes) st_agent64(spre + step, chain_word(0.f, fmaf(SA, h, SB)));
+  if (closes) st_agent64(spre + step, chain_word(0.f, decayed(SL, h, SB)));
 #pragma unroll
   for (int i = 0; i < G_SUPER - 1; i++)
-    if (i < q) h = fmaf(chain_A(w[i]), h, chain_B(w[i]));
+    if (i < q) h = fmaf(decay_of(chain_L(w[i])), h, chain_B(w[i]));
   return h;
 }
 
@@ -322,7 +342,8 @@ __device__ inline bool gated_tile(const GatedArgs &a, const GatedChain &ch, int 
 
 template <typename T, int K, int NW, int WPS>
 __global__ __launch_bounds__(64 * NW, WPS) void k_gated_fwd(GatedArgs a, GatedChain ch) {
-  __shared__ float lA[4 * NW * G_CH], lB[4 * NW * G_CH];
+  // of each row of steps: its factor, its sum B (then its first state), its factor's logarithm
+  __shared__ __attribute__((aligned(16))) float lA[4 * NW * G_CH], lB[4 * NW * G_CH], lL[4 * NW * G_CH];
   __shared__ int sh;
   long long c;
   int tile;
@@ -348,7 +369,7 @@ __global__ __launch_bounds__(64 * NW, WPS) void k_gated_fwd(GatedArgs a, GatedCh
   }
   auto body = [&](auto full) __attribute__((always_inline)) {
     constexpr bool FULL = decltype(full)::value;
-    float ga[K][4], gb[K][4], A[4], B[4];
+    float ga[K][4], gb[K][4], L[4], B[4];
     {
       const TileOf in[3] = {tile_of<T>(a.r, b, p.t0), tile_of<T>(a.i, b, p.t0), tile_of<T>(a.x, b, p.t0)};
       VecU<T, 4> raw[3][K];
@@ -362,29 +383,32 @@ __global__ __launch_bounds__(64 * NW, WPS) void k_gated_fwd(GatedArgs a, GatedCh
           const GateVals g = gate_vals<T>(raw[0][k].f(v), raw[1][k].f(v), cs.c[v]);
           ga[k][v] = on ? g.a : 1.f;
           gb[k][v] = on ? g.m * g.i * raw[2][k].f(v) : 0.f;
-          A[v] = k ? A[v] * ga[k][v] : ga[k][v];
+          L[v] = (k ? L[v] : 0.f) + (on ? g.l : 0.f);
           B[v] = k ? fmaf(ga[k][v], B[v], gb[k][v]) : gb[k][v];
         }
         __builtin_amdgcn_sched_barrier(0);  // one step's temporaries at a time
       }
+#pragma unroll
+      for (int v = 0; v < 4; v++) L[v] *= GateConsts<T>::SHORT ? 1.f : LOG2E;
     }
     const int at = (w * 4 + (lane >> 4)) * G_CH + (lane & 15) * 4;
-    *reinterpret_cast<float4 *>(lA + at) = make_float4(A[0], A[1], A[2], A[3]);
+    *reinterpret_cast<float4 *>(lA + at) =
+        make_float4(decay_of(L[0]), decay_of(L[1]), decay_of(L[2]), decay_of(L[3]));
     *reinterpret_cast<float4 *>(lB + at) = make_float4(B[0], B[1], B[2], B[3]);
+    *reinterpret_cast<float4 *>(lL + at) = make_float4(L[0], L[1], L[2], L[3]);
     lds_barrier();
     if (w == 0) {
       const int rows = nw * 4;
       float h = first;
       if (live > 1) {
-        float tA = lA[lane], tB = lB[lane];
+        float tL = lL[lane], tB = lB[lane];
 #pragma unroll 3
         for (int q = 1; q < rows; q++) {
-          const float qa = lA[q * G_CH + lane];
-          tB = fmaf(qa, tB, lB[q * G_CH + lane]);
-          tA *= qa;
+          tB = fmaf(lA[q * G_CH + lane], tB, lB[q * G_CH + lane]);
+          tL += lL[q * G_CH + lane];
         }
-        if (tile + 1 < live) st_agent64(ch.agg + (tile * ch.cols + c) * 64 + (unsigned)lane, chain_word(tA, tB));
-        h = chain_enter(ch, c, tile, live, tA, tB, first);
+        if (tile + 1 < live) st_agent64(ch.agg + (tile * ch.cols + c) * 64 + (unsigned)lane, chain_word(tL, tB));
+        h = chain_enter(ch, c, tile, live, tL, tB, first);
       }
 #pragma unroll 4
       for (int q = 0; q < rows; q++) {
@@ -421,7 +445,7 @@ __global__ __launch_bounds__(64 * NW, WPS) void k_gated_fwd(GatedArgs a, GatedCh
 // forwards.  The tile's states are made again from the saved one.
 template <typename T, int K, int NW, int WPS>
 __global__ __launch_bounds__(64 * NW, WPS) void k_gated_adj(GatedArgs a, GatedChain ch) {
-  __shared__ float lds[3][4 * NW * G_CH];
+  __shared__ __attribute__((aligned(16))) float lds[3][4 * NW * G_CH], lL[4 * NW * G_CH];
   __shared__ float4 lcv[K][64 * NW];  // dv = g cv
   __shared__ int sh;
   float *lA = lds[0], *lF = lds[1], *lR = lds[2];
@@ -461,7 +485,7 @@ __global__ __launch_bounds__(64 * NW, WPS) void k_gated_adj(GatedArgs a, GatedCh
   float sums[3][4] = {};
   auto body = [&](auto full) __attribute__((always_inline)) {
     constexpr bool FULL = decltype(full)::value;
-    float ga[K][4], gm[K][4], gr[K][4], gi[K][4], A[4], F[4];
+    float ga[K][4], gm[K][4], gr[K][4], gi[K][4], L[4], F[4];
     VecU<T, 4> x[K], gy[K];
     {
       const TileOf in[4] = {tile_of<T>(a.r, b, p.t0), tile_of<T>(a.i, b, p.t0), tile_of<T>(a.x, b, p.t0),
@@ -486,11 +510,13 @@ __global__ __launch_bounds__(64 * NW, WPS) void k_gated_adj(GatedArgs a, GatedCh
           gr[k][v] = on ? g.r : 0.f;
           gi[k][v] = on ? g.i : 0.f;
           const float bb = gm[k][v] * gi[k][v] * x[k].f(v);
-          A[v] = k ? A[v] * ga[k][v] : ga[k][v];
+          L[v] = (k ? L[v] : 0.f) + (on ? g.l : 0.f);
           F[v] = k ? fmaf(ga[k][v], F[v], bb) : bb;
         }
         __builtin_amdgcn_sched_barrier(0);  // one step's temporaries at a time
       }
+#pragma unroll
+      for (int v = 0; v < 4; v++) L[v] *= GateConsts<T>::SHORT ? 1.f : LOG2E;
     }
     float R[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -500,7 +526,9 @@ __global__ __launch_bounds__(64 * NW, WPS) void k_gated_adj(GatedArgs a, GatedCh
     // (the inputs stay as they were stored: unpacked they would take twice the registers)
 #pragma unroll
     for (int k = 0; k < K; k++) asm volatile("" : "+v"(x[k].v), "+v"(gy[k].v));
-    *reinterpret_cast<float4 *>(lA + at) = make_float4(A[0], A[1], A[2], A[3]);
+    *reinterpret_cast<float4 *>(lA + at) =
+        make_float4(decay_of(L[0]), decay_of(L[1]), decay_of(L[2]), decay_of(L[3]));
+    *reinterpret_cast<float4 *>(lL + at) = make_float4(L[0], L[1], L[2], L[3]);
     *reinterpret_cast<float4 *>(lF + at) = make_float4(F[0], F[1], F[2], F[3]);
     *reinterpret_cast<float4 *>(lR + at) = make_float4(R[0], R[1], R[2], R[3]);
     lds_barrier();
@@ -516,15 +544,14 @@ __global__ __launch_bounds__(64 * NW, WPS) void k_gated_adj(GatedArgs a, GatedCh
     if (w == 0) {
       float mu = first;
       if (live > 1) {
-        float tA = lA[(rows - 1) * G_CH + lane], tB = lR[(rows - 1) * G_CH + lane];
+        float tL = lL[(rows - 1) * G_CH + lane], tB = lR[(rows - 1) * G_CH + lane];
 #pragma unroll 3
         for (int q = rows - 2; q >= 0; q--) {
-          const float qa = lA[q * G_CH + lane];
-          tB = fmaf(qa, tB, lR[q * G_CH + lane]);
-          tA *= qa;
+          tB = fmaf(lA[q * G_CH + lane], tB, lR[q * G_CH + lane]);
+          tL += lL[q * G_CH + lane];
         }
-        if (j + 1 < live) st_agent64(ch.agg + (j * ch.cols + c) * 64 + (unsigned)lane, chain_word(tA, tB));
-        mu = chain_enter(ch, c, j, live, tA, tB, first);
+        if (j + 1 < live) st_agent64(ch.agg + (j * ch.cols + c) * 64 + (unsigned)lane, chain_word(tL, tB));
+        mu = chain_enter(ch, c, j, live, tL, tB, first);
       }
 #pragma unroll 4
       for (int q = rows - 1; q >= 0; q--) {
@@ -648,7 +675,7 @@ __global__ __launch_bounds__(256) void k_gated_step(GatedStepArgs a) {
 #pragma unroll
     for (int k = 0; k < V; k++) {
       const GateVals g = gate_vals<T>(r.f(k), i.f(k), cs.c[k]);
-      o[k] = fmaf(g.a, h.f(k), g.m * g.i * x.f(k));
+      o[k] = decayed(g.a, GateConsts<T>::SHORT ? g.l * -LN2 : -g.l, h.f(k), g.m * g.i * x.f(k));
     }
     stu<float, V>(hp, o, n);
   }

@@ -113,3 +113,74 @@ def test_product_has_every_bit_of_fp32_rows(zero, case):
     bd.gemm_w4(x.cuda(), (q[:, ::2] | q[:, 1::2] << 4).cuda(), scale.cuda(), out, group,
                zero=torch.full((N, G), 8.0, device="cuda") if zero else None)
     assert torch.equal(out.cpu(), x[:, col] * (step.float() * scale[torch.arange(N), col // group]))
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_long_memories(dtype):
+    """Channels that remember most of a long sequence (a decay of 0.008 behind nearly
+    closed gates, inputs of one sign).  States and their gradients are within 256 U of
+    the largest: their decay is the sum of v over 1024 steps at a time, known to
+    some 40 U of itself with the gates' far exponents (0.37 of that in e^-V), the input's
+    factor to 20 U; inside those 1024 steps a value passes at most 30 factors of 2 U, and
+    the 24 pieces of 1024 steps round it once each, without a factor's error."""
+    g = gen(50)
+    B, T = 1, 24601
+    gate = torch.tensor([-3.0, -6.0, -9.0, -12.0]).repeat(9)
+    D = gate.numel()
+    p = dict(x=(1 + 0.5 * rnd(g, B, T, D)).to(dtype), r=rnd(g, B, T, D, std=0.1).to(dtype), i=rnd(g, B, T, D, dtype=dtype),
+             decay=0.008 * (1 + 0.2 * torch.rand(D, generator=g)), r_bias=gate, i_bias=rnd(g, D))
+    p["r"][..., ::2] = 0  # every other channel has a constant gate
+    h0, dh, dy = 100 * rnd(g, B, D), 10 * rnd(g, B, D), (0.5 + rnd(g, B, T, D)).to(dtype)
+    dev = {k: v.cuda() for k, v in p.items()}
+    main, kw = (dev["x"], dev["r"], dev["i"], dev["decay"]), dict(r_bias=dev["r_bias"], i_bias=dev["i_bias"])
+    ws = work(bd.gated_workspace_bytes(dtype, B, T, D))
+    y, hl, states = nan(B, T, D, dtype=dtype), nan(B, D), nan(*bd.gated_states_shape(B, T, D))
+    bd.gated_scan(*main, y, ws, h0=h0.cuda(), h_last=hl, states=states, **kw)
+    ry, rh, hs = R.gated(**p, h0=h0, keep=True)
+
+    def close(got, ref, k, dim):  # each channel by its own largest value
+        off = (got.double().cpu() - ref).abs() - (2.0 ** -8 * ref.abs() if got.dtype == BF else 0)
+        off = (off / ref.abs().amax(dim, keepdim=True)).max()
+        assert float(off) <= 256 * U, (k, float(off) / U)
+
+    close(hl, rh, "h", 0)
+    close(states, torch.stack(hs[:-1][::bd.GATED_STATE_STEPS], 1), "states", (0, 1))
+    close(y, ry, "y", (0, 1))
+    o = dict(dx=nan(B, T, D, dtype=dtype), dr=nan(B, T, D, dtype=dtype), di=nan(B, T, D, dtype=dtype), dh0=nan(B, D),
+             ddecay=nan(D))
+    bd.gated_scan_adjoint(*main, states, dy.cuda(), ws, dh_last=dh.cuda(), **kw, **o)
+    r = R.gated_grads(**p, dy=dy, h0=h0, dh_last=dh)
+    for k in ("dx", "di", "dh0"):
+        close(o[k], r[k], k, 0 if k == "dh0" else (0, 1))
+    # g a^2 / m i x and g a h are each off by twice that of their own size; the sum over
+    # the steps by that of the sum of the sizes
+    gr, gi, a, m = R._gates(p["r"], p["i"], p["decay"], p["r_bias"], p["i_bias"])
+    grad = (r["dx"] / (m * gi)).abs()  # |g|
+    size = grad * (a * a / m * gi * p["x"].double().abs() + a * torch.stack(hs[:-1], 1).abs())
+    part = p["decay"].double() * gr * (1 - gr)
+    off = (o["dr"].double().cpu() - r["dr"]).abs() - (2.0 ** -8 * r["dr"].abs() if dtype == BF else 0)
+    assert float((off / (size * part).amax((0, 1))).max()) <= 512 * U
+    off = (o["ddecay"].double().cpu() - r["ddecay"]).abs() / (size * gr).sum((0, 1))
+    assert float(off.max()) <= 512 * U, float(off.max()) / U
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_long_memories_by_single_tokens(dtype):
+    """The same with a step for each token: the state is rounded to fp32 at each, by U of
+    it at most, to either side: 4 sqrt(T) U, beside the 60 U of decay and input."""
+    g = gen(51)
+    B, T = 1, 20000
+    gate = torch.tensor([-3.0, -6.0, -9.0]).repeat(12)
+    D = gate.numel()
+    p = dict(x=(1 + 0.5 * rnd(g, B, T, D)).to(dtype), r=torch.zeros(B, T, D, dtype=dtype), i=rnd(g, B, T, D, dtype=dtype),
+             decay=0.008 * (1 + 0.2 * torch.rand(D, generator=g)), r_bias=gate, i_bias=rnd(g, D))
+    h0 = 100 * rnd(g, B, D)
+    dev = {k: v.cuda() for k, v in p.items()}
+    state, y = h0.cuda(), nan(B, D, dtype=dtype)
+    for t in range(T):
+        bd.gated_step(dev["x"][:, t], dev["r"][:, t], dev["i"][:, t], dev["decay"], state, y, r_bias=dev["r_bias"],
+                      i_bias=dev["i_bias"])
+    _, rh, hs = R.gated(**p, h0=h0, keep=True)
+    off = (state.double().cpu() - rh).abs() / torch.stack(hs).abs().amax((0, 1))
+    assert float(off.max()) <= (4 * T ** 0.5 + 60) * U, float(off.max()) / U
