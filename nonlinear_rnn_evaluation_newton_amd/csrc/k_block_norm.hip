@@ -29,15 +29,24 @@ struct BnArgs {
   long long lx, lz, lres, lt, ly, ldt, ldy, ldx, ldz, ldres;  // row strides
   long long rows;
   int n, gate;
-  float eps, rn;  // rn = 1 / n
+  float eps, nf, rn;  // n and 1 / n
 };
 
-// 1 / sqrt(mean + eps) by the hardware's instruction, which is good to the last place
-// but takes no denormals.
+// sum / n to the nearest: the product with the rounded 1 / n, corrected by its exact
+// remainder.  (An infinite sum has none.)
+__device__ inline float mean_of(float sum, const BnArgs &a) {
+  const float q = sum * a.rn, c = fmaf(fmaf(-q, a.nf, sum), a.rn, q);
+  return c == c ? c : q;
+}
+// 1 / sqrt(mean + eps) to the nearest (but for values next to a tie): the hardware's
+// instruction, good to one place, with one Newton step on its exact remainder.  It takes
+// no denormals, and of 0 and infinity its own answer stands.
 __device__ inline float rstd_of(float sum, const BnArgs &a) {
-  const float v = fmaf(sum, a.rn, a.eps);
-  const bool small = v < 0x1p-96f;
-  return __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v) * (small ? 0x1p32f : 1.f);
+  const float v0 = mean_of(sum, a) + a.eps;
+  const bool small = v0 < 0x1p-96f;
+  const float v = small ? v0 * 0x1p64f : v0, y = __builtin_amdgcn_rsqf(v);
+  const float h = v * y, l = fmaf(v, y, -h), e = fmaf(-l, y, fmaf(-h, y, 1.f)), c = fmaf(0.5f * y, e, y);
+  return (c == c ? c : y) * (small ? 0x1p32f : 1.f);
 }
 
 // act(z) and its derivative from p = sigm(z): both are a factor, z or a number,
@@ -260,7 +269,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
     row_sums<TPR, 6>(s, sh[par]);
     par ^= 1;  // the next row's sums go to the other half
     const float rstd1 = rstd_of(s[0], a), rstd2 = a.dy ? rstd_of(s[2], a) : 0.f;  // without dy: t and dy are zeros
-    const float k2 = s[3] * a.rn * rstd2 * rstd2, k1 = (s[1] + rstd2 * (s[4] - k2 * s[5])) * a.rn * rstd1 * rstd1;
+    const float k2 = mean_of(s[3], a) * rstd2 * rstd2;
+    const float k1 = mean_of(s[1] + rstd2 * (s[4] - k2 * s[5]), a) * rstd1 * rstd1;
 #pragma unroll
     for (int m = 0; m < NV; m++) {
       const BnAt at = bn_at<T, TPR, EDGE>(xr, m, a.n);
@@ -397,7 +407,7 @@ __global__ __launch_bounds__(256) void k_bn_adj_stat(BnArgs a) {
     const float rstd2 = rstd_of(st, a);
     o[0] = rstd_of(ss, a);
     o[1] = rstd2;
-    o[2] = dot * a.rn * rstd2 * rstd2;
+    o[2] = mean_of(dot, a) * rstd2 * rstd2;
   }
 }
 // q and dw_next: a block sums one slice of the rows for 256 columns
@@ -434,7 +444,7 @@ __global__ __launch_bounds__(256) void k_bn_adj_long(BnArgs a) {
     if (a.z) e *= act_v(gate, ldf(zp, c));
     dot = fmaf(e, ldf(xp, c), dot);
   }
-  const float k1 = block_sum(dot, sh) * a.rn * s.rstd1 * s.rstd1;
+  const float k1 = mean_of(block_sum(dot, sh), a) * s.rstd1 * s.rstd1;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     const float gt = bn_gt<T>(a, s, row, c), ws = at1<T>(a.w, c) * at1<T>(a.scale, c), x = ldf(xp, c);
     const float z = a.z ? ldf(zp, c) : 0.f, p = fsigm(z);
@@ -560,7 +570,7 @@ int bn_fill(const pr_block_norm_problem *p, const pr_rows *x, const pr_rows *z, 
     a->z = z->p; a->lz = z->ld;
   }
   a->w = w; a->scale = scale; a->wn = wn;
-  a->rows = p->rows; a->n = p->n; a->gate = p->gate; a->eps = p->eps; a->rn = 1.f / (float)p->n;
+  a->rows = p->rows; a->n = p->n; a->gate = p->gate; a->eps = p->eps; a->nf = (float)p->n; a->rn = 1.f / a->nf;
   return PR_OK;
 }
 

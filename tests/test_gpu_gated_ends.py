@@ -184,3 +184,34 @@ def test_long_memories_by_single_tokens(dtype):
     _, rh, hs = R.gated(**p, h0=h0, keep=True)
     off = (state.double().cpu() - rh).abs() / torch.stack(hs).abs().amax((0, 1))
     assert float(off.max()) <= (4 * T ** 0.5 + 60) * U, float(off.max()) / U
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("n", [1, 3, 7, 64, 100, 257, 700, 1111, 2049, 5003, 9001, 20001])
+def test_block_norm_factor(n):
+    """Rows of powers of two without eps: the sum of squares is exact (below 2^24), the
+    mean's rounding (U) counts half under the root, the factor is rounded once (U, and a
+    hundredth for what its making leaves), and its product with a power of two is exact."""
+    g, rows = gen(n), max(4, min(4000, 2_000_000 // n))
+    x = 2.0 ** torch.randint(0, 4, (rows, n), generator=g).float() * torch.where(torch.rand(rows, n, generator=g) < 0.5, 1, -1)
+    t, y = nan(rows, n), nan(rows, n)
+    bd.block_norm(x.cuda(), None, t, y=y, eps=0.0)
+    ref = R.block_norm(x, eps=0.0)
+    off = ((t.double().cpu() - ref).abs() / ref.abs()).max()
+    assert float(off) <= 1.51 * U, float(off) / U
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -70, 2.0 ** -20, 2.0 ** 20, 2.0 ** 55])
+def test_block_norm_factor_of_far_rows(scale):
+    """The same where the mean is denormal or near fp32's largest; and rows whose squares
+    pass it, whose factor is 0, and rows of zeros with an eps."""
+    x = torch.full((4, 40), scale)
+    x[:, ::2] *= 2
+    t = nan(4, 40)
+    bd.block_norm(x.cuda(), None, t, eps=0.0)
+    ref = R.block_norm(x, eps=0.0)
+    assert float(((t.double().cpu() - ref).abs() / ref).max()) <= (1.51 * U if scale > 2.0 ** -60 else 2.0 ** -9)
+    bd.block_norm(torch.full((4, 40), 1e30, device="cuda"), None, t)
+    assert bool((t == 0).all())
+    bd.block_norm(torch.zeros(4, 40, device="cuda"), None, t)
+    assert bool((t == 0).all())
