@@ -49,6 +49,12 @@ __device__ inline float rstd_of(float sum, const BnArgs &a) {
   return (c == c ? c : y) * (small ? 0x1p32f : 1.f);
 }
 
+// sigm(z).  A plain product as the exponential's argument is off by |z| 2^-24 of the
+// result: far below a step of rows stored in 8 significant bits, but not of fp32 ones.
+template <typename T>
+__device__ inline float sigm_of(float z) {
+  return sizeof(T) == 2 ? fsigm(z) : frcp(1.f + exp_any(-z));
+}
 // act(z) and its derivative from p = sigm(z): both are a factor, z or a number,
 // of p and of p (1 - p), plus p times a number.  The gate's kind is the same for a
 // whole launch: one select, so that no branch stands between the loads of a row.
@@ -61,7 +67,8 @@ __device__ inline float act_of(const Gate &g, float z, float p) { return (g.silu
 __device__ inline float act_d(const Gate &g, float z, float p) {
   return fmaf(g.silu ? z : g.k, p * (1.f - p), g.c * p);
 }
-__device__ inline float act_v(const Gate &g, float z) { return act_of(g, z, fsigm(z)); }
+template <typename T>
+__device__ inline float act_v(const Gate &g, float z) { return act_of(g, z, sigm_of<T>(z)); }
 template <typename T>
 __device__ inline float to_storage(float v) {
   T t;
@@ -177,7 +184,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
     const BnAt at = bn_at<T, TPR, EDGE>(x, m, a.n);
 #pragma unroll
     for (int i = 0; i < V; i++) {
-      const float u = vx[m].f(i) * rstd * ((a.w ? vw[m].f(i) : 1.f) * (a.scale ? vs[m].f(i) : 1.f)) * act_v(gate, vz[m].f(i));
+      const float u = vx[m].f(i) * rstd * ((a.w ? vw[m].f(i) : 1.f) * (a.scale ? vs[m].f(i) : 1.f)) * act_v<T>(gate, vz[m].f(i));
       t[m][i] = to_storage<T>(a.res ? vr[m].f(i) + u : u);
       ss[0] = !EDGE || i >= at.dup ? fmaf(t[m][i], t[m][i], ss[0]) : ss[0];
     }
@@ -253,7 +260,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
       }
 #pragma unroll
       for (int i = 0; i < V; i++) {
-        const float p = fsigm(vz[m].f(i));
+        const float p = sigm_of<T>(vz[m].f(i));
         if constexpr (!AGAIN) pz[m][i] = p;
         if (EDGE && i < at.dup) continue;
         const float xx = vx[m].f(i), t = vt[m].f(i), e = wn[m][i] * vy[m].f(i);
@@ -285,7 +292,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
 #pragma unroll
       for (int i = 0; i < V; i++) {
         const float x_ = vx[m].f(i), xh = x_ * rstd1, t = vt[m].f(i), dy = vy[m].f(i), z = vz[m].f(i);
-        const float p = AGAIN ? fsigm(z) : pz[AGAIN ? 0 : m][i], act = act_of(gate, z, p);
+        const float p = AGAIN ? sigm_of<T>(z) : pz[AGAIN ? 0 : m][i], act = act_of(gate, z, p);
         const float g = fmaf(rstd2, fmaf(-t, k2, wn[m][i] * dy), vd[m].f(i)), gf = g * F[m][i];
         qn[m][i] = fmaf(dy, t * rstd2, qn[m][i]);
         q[m][i] = fmaf(g * act, xh, q[m][i]);
@@ -361,7 +368,7 @@ __global__ __launch_bounds__(256) void k_bn_long(BnArgs a) {
   ss = 0.f;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     float u = ldf(xp, c) * rstd * (at1<T>(a.w, c) * at1<T>(a.scale, c));
-    if (a.z) u *= act_v(gate, ldf(zp, c));
+    if (a.z) u *= act_v<T>(gate, ldf(zp, c));
     const float t = to_storage<T>(a.res ? ldf(rp, c) + u : u);
     stf(tp, c, t);
     ss = fmaf(t, t, ss);
@@ -422,7 +429,7 @@ __global__ __launch_bounds__(256) void k_bn_adj_cols(BnArgs a, int slices) {
   for (long long r = r0; r < r1; r++) {
     const BnRow s{a.stat[r * 3], a.stat[r * 3 + 1], a.stat[r * 3 + 2]};
     const float xh = ldf((const T *)a.x + r * a.lx, c) * s.rstd1;
-    const float act = a.z ? act_v(gate, ldf((const T *)a.z + r * a.lz, c)) : 1.f;
+    const float act = a.z ? act_v<T>(gate, ldf((const T *)a.z + r * a.lz, c)) : 1.f;
     q = fmaf(bn_gt<T>(a, s, r, c) * act, xh, q);
     if (a.dy)
       wn = fmaf(ldf((const T *)a.dy + r * a.ldy, c), ldf((const T *)a.t + r * a.lt, c) * s.rstd2, wn);
@@ -441,13 +448,13 @@ __global__ __launch_bounds__(256) void k_bn_adj_long(BnArgs a) {
   float dot = 0.f;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     float e = bn_gt<T>(a, s, row, c) * (at1<T>(a.w, c) * at1<T>(a.scale, c));
-    if (a.z) e *= act_v(gate, ldf(zp, c));
+    if (a.z) e *= act_v<T>(gate, ldf(zp, c));
     dot = fmaf(e, ldf(xp, c), dot);
   }
   const float k1 = mean_of(block_sum(dot, sh), a) * s.rstd1 * s.rstd1;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     const float gt = bn_gt<T>(a, s, row, c), ws = at1<T>(a.w, c) * at1<T>(a.scale, c), x = ldf(xp, c);
-    const float z = a.z ? ldf(zp, c) : 0.f, p = fsigm(z);
+    const float z = a.z ? ldf(zp, c) : 0.f, p = sigm_of<T>(z);
     if (a.dres) stf((T *)a.dres + row * a.ldres, c, gt);
     if (a.dz) stf((T *)a.dz + row * a.ldz, c, gt * ws * (x * s.rstd1) * act_d(gate, z, p));
     if (a.dx) stf((T *)a.dx + row * a.ldx, c, s.rstd1 * fmaf(-x, k1, gt * ws * act_of(gate, z, p)));

@@ -76,15 +76,12 @@ __device__ inline float exp_acc(float x) {
   return fabsf(x) < 128.f ? fmaf(e, r * 0.6931471805599453f, e) : e;
 }
 
-// The same for any x.  From 88.7 on e^x is infinite, and its product with a negative
-// r would make it a NaN: past 88 the plain result stands (off by 4e-6 up to there).
+// The same for any x: what the product's rounding left out, k = x - p ln 2, multiplies
+// e where that is finite and k small; else (an infinite e, x or p) e is the answer.
 __device__ inline float exp_any(float x) {
-  const float L = 1.44269502162933349609f, Ll = 1.92596299112661746887e-8f;
-  const float p = x * L;
-  float r = fmaf(x, L, -p);
-  r = fmaf(x, Ll, r);
-  const float e = __builtin_amdgcn_exp2f(p);
-  return fabsf(x + 20.f) < 108.f ? fmaf(e, r * 0.6931471805599453f, e) : e;
+  const float p = x * 1.44269502162933349609f, e = __builtin_amdgcn_exp2f(p);
+  const float k = fmaf(p, 1.90465429995776804525e-9f, fmaf(p, -0.693147182464599609375f, x));
+  return fmaf(__builtin_amdgcn_fmed3f(e, 0.f, 3.4028234664e38f), __builtin_amdgcn_fmed3f(k, -1.f, 1.f), e);
 }
 
 // log(1 + e) for 0 <= e <= 1: the logarithm of the rounded sum u, and what its

@@ -215,3 +215,24 @@ def test_block_norm_factor_of_far_rows(scale):
     assert bool((t == 0).all())
     bd.block_norm(torch.zeros(4, 40, device="cuda"), None, t)
     assert bool((t == 0).all())
+
+
+@pytest.mark.parametrize("n", [3, 80, 1111, 9001])
+@pytest.mark.parametrize("gate", ["silu", "sigmoid"])
+def test_block_norm_gates_in_fp32(n, gate):
+    """Rows of ones, whose factor is 1: t is the gate itself.  e^-z: one step of the
+    exponential and two roundings (4 U), the sum (U), the reciprocal (2 U) and the
+    product with z (U): 8 U of the value.  Its derivative is a sum of two such terms,
+    p and z p (1 - p), where 1 - p is off by the 7 U of p: 12 U of their sizes with
+    the products, and 8 U |z| p more for 1 - p."""
+    z = torch.linspace(-86, 86, n * 5).view(5, n)
+    x, t = torch.ones(5, n), nan(5, n)
+    bd.block_norm(x.cuda(), None, t, z=z.cuda(), gate=gate, eps=0.0)
+    ref, p = R.act(z, gate), torch.sigmoid(z.double())
+    assert float(((t.double().cpu() - ref[0]).abs() / ref[0].abs().clamp(min=1e-300)).nan_to_num(0).max()) <= 8 * U
+    dz = nan(5, n)
+    bd.block_norm_adjoint(x.cuda(), None, None, work(bd.block_norm_workspace_bytes(F, 5, n)), z=z.cuda(), gate=gate,
+                          dt=torch.ones(5, n, device="cuda"), dz=dz, eps=0.0)
+    size = p * (1 - p) if gate == "sigmoid" else p + z.double().abs() * p * (1 - p)
+    room = 12 * U * size + 8 * U * p * (1 if gate == "sigmoid" else z.double().abs())
+    assert bool(((dz.double().cpu() - ref[1]).abs() <= room).all())
