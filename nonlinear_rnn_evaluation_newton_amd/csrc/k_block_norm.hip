@@ -348,6 +348,24 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? 3 : 2) void k_bn_a
   }
 }
 
+// N sums over a row's n elements, a thread's share of them: in fp32 over 256 elements
+// at a time, which 64 bits join.  (One fp32 sum of a long row's squares drops the small
+// ones as it grows: the gradients of 2^26 elements were off by 5e-5 to 3e-4.)
+template <int N, typename F>
+__device__ inline void long_sums(int n, float (&out)[N], F add) {
+  constexpr int PIECE = 256 * 256;
+  double total[N] = {};
+  for (int c0 = threadIdx.x; c0 < n; c0 += PIECE) {
+    const int c1 = n - c0 < PIECE ? n : c0 + PIECE;
+    float s[N] = {};
+    for (int c = c0; c < c1; c += 256) add(c, s);
+#pragma unroll
+    for (int k = 0; k < N; k++) total[k] += (double)s[k];
+  }
+#pragma unroll
+  for (int k = 0; k < N; k++) out[k] = (float)total[k];
+}
+
 // Long rows (more than 16384 values of bf16 or 8192 of fp32; the adjoint's of bf16 more
 // than 12288) and rows shorter than a vector: a block reads its row again, from
 // cache, for each pass, element by element.
@@ -359,22 +377,21 @@ __global__ __launch_bounds__(256) void k_bn_long(BnArgs a) {
   const T *xp = (const T *)a.x + row * a.lx, *zp = (const T *)a.z + row * a.lz, *rp = (const T *)a.res + row * a.lres;
   T *tp = (T *)a.t + row * a.lt;
   const Gate gate(a.z, a.gate);
-  float ss = 0.f;
-  for (int c = threadIdx.x; c < a.n; c += 256) {
+  float ss[1];
+  long_sums(a.n, ss, [&](int c, float (&s)[1]) {
     const float v = ldf(xp, c);
-    ss = fmaf(v, v, ss);
-  }
-  const float rstd = rstd_of(block_sum(ss, sh[0]), a);
-  ss = 0.f;
-  for (int c = threadIdx.x; c < a.n; c += 256) {
+    s[0] = fmaf(v, v, s[0]);
+  });
+  const float rstd = rstd_of(block_sum(ss[0], sh[0]), a);
+  long_sums(a.n, ss, [&](int c, float (&s)[1]) {
     float u = ldf(xp, c) * rstd * (at1<T>(a.w, c) * at1<T>(a.scale, c));
     if (a.z) u *= act_v<T>(gate, ldf(zp, c));
     const float t = to_storage<T>(a.res ? ldf(rp, c) + u : u);
     stf(tp, c, t);
-    ss = fmaf(t, t, ss);
-  }
+    s[0] = fmaf(t, t, s[0]);
+  });
   if (!a.y) return;
-  const float rstd2 = rstd_of(block_sum(ss, sh[1]), a);
+  const float rstd2 = rstd_of(block_sum(ss[0], sh[1]), a);
   for (int c = threadIdx.x; c < a.n; c += 256)
     stf((T *)a.y + row * a.ly, c, ldf(tp, c) * rstd2 * at1<T>(a.wn, c));
 }
@@ -396,19 +413,17 @@ __global__ __launch_bounds__(256) void k_bn_adj_stat(BnArgs a) {
   __shared__ float sh[3][4];
   const long long row = flat_block();
   if (row >= a.rows) return;
-  float ss = 0.f, st = 0.f, dot = 0.f;
-  for (int c = threadIdx.x; c < a.n; c += 256) {
+  float sums[3];
+  long_sums(a.n, sums, [&](int c, float (&s)[3]) {
     const float v = ldf((const T *)a.x + row * a.lx, c);
-    ss = fmaf(v, v, ss);
+    s[0] = fmaf(v, v, s[0]);
     if (a.dy) {
       const float t = ldf((const T *)a.t + row * a.lt, c);
-      st = fmaf(t, t, st);
-      dot = fmaf(at1<T>(a.wn, c) * ldf((const T *)a.dy + row * a.ldy, c), t, dot);
+      s[1] = fmaf(t, t, s[1]);
+      s[2] = fmaf(at1<T>(a.wn, c) * ldf((const T *)a.dy + row * a.ldy, c), t, s[2]);
     }
-  }
-  ss = block_sum(ss, sh[0]);
-  st = block_sum(st, sh[1]);
-  dot = block_sum(dot, sh[2]);
+  });
+  const float ss = block_sum(sums[0], sh[0]), st = block_sum(sums[1], sh[1]), dot = block_sum(sums[2], sh[2]);
   if (threadIdx.x == 0) {
     float *o = a.stat + row * 3;
     const float rstd2 = rstd_of(st, a);
@@ -445,13 +460,13 @@ __global__ __launch_bounds__(256) void k_bn_adj_long(BnArgs a) {
   const BnRow s{a.stat[row * 3], a.stat[row * 3 + 1], a.stat[row * 3 + 2]};
   const T *xp = (const T *)a.x + row * a.lx, *zp = (const T *)a.z + row * a.lz;
   const Gate gate(a.z, a.gate);
-  float dot = 0.f;
-  for (int c = threadIdx.x; c < a.n; c += 256) {
+  float dot[1];
+  long_sums(a.n, dot, [&](int c, float (&v)[1]) {
     float e = bn_gt<T>(a, s, row, c) * (at1<T>(a.w, c) * at1<T>(a.scale, c));
     if (a.z) e *= act_v<T>(gate, ldf(zp, c));
-    dot = fmaf(e, ldf(xp, c), dot);
-  }
-  const float k1 = mean_of(block_sum(dot, sh), a) * s.rstd1 * s.rstd1;
+    v[0] = fmaf(e, ldf(xp, c), v[0]);
+  });
+  const float k1 = mean_of(block_sum(dot[0], sh), a) * s.rstd1 * s.rstd1;
   for (int c = threadIdx.x; c < a.n; c += 256) {
     const float gt = bn_gt<T>(a, s, row, c), ws = at1<T>(a.w, c) * at1<T>(a.scale, c), x = ldf(xp, c);
     const float z = a.z ? ldf(zp, c) : 0.f, p = sigm_of<T>(z);

@@ -236,3 +236,21 @@ def test_block_norm_gates_in_fp32(n, gate):
     size = p * (1 - p) if gate == "sigmoid" else p + z.double().abs() * p * (1 - p)
     room = 12 * U * size + 8 * U * p * (1 if gate == "sigmoid" else z.double().abs())
     assert bool(((dz.double().cpu() - ref[1]).abs() <= room).all())
+
+
+def test_block_norm_sums_of_long_rows():
+    """A row of 2^25 values: its squares are added 256 at a time in fp32 (256 U at most,
+    half of it under the root), then in 64 bits; a gradient takes three such sums."""
+    n = (1 << 25) + 40
+    g = torch.Generator(device="cuda").manual_seed(71)
+    x, dt, dy = (torch.randn(1, n, generator=g, device="cuda") for _ in range(3))
+    t, y, dx = (torch.full_like(x, float("nan")) for _ in range(3))
+    bd.block_norm(x, None, t, y=y)
+    ref = R.block_norm(x)
+    assert bool(((t.double() - ref).abs() <= 130 * U * ref.abs()).all())
+    ref = R.norm_next(t)
+    assert bool(((y.double() - ref).abs() <= 130 * U * ref.abs()).all())
+    dt += x  # a gradient along the row, which the norm takes off
+    bd.block_norm_adjoint(x, None, dx, work(bd.block_norm_workspace_bytes(F, 1, n)), t=t, dt=dt, dy=dy)
+    ref = R.block_norm_grads(x, t=t, dt=dt, dy=dy)["dx"]
+    assert float((dx.double() - ref).abs().max()) <= 520 * U * float(ref.abs().max())
