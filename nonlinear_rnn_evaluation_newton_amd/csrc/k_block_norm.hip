@@ -482,7 +482,8 @@ template <typename T>
 __global__ __launch_bounds__(1024) void k_bn_sums(const float *__restrict__ part, int P, int n, const void *w,
                                                   const void *scale, float *dw, float *dscale, float *dwn) {
   __shared__ double sh[64][17];
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4, k = blockIdx.y, c = (int)blockIdx.x * 16 + x;
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4, k = blockIdx.z;
+  const long long c = flat_block() * 16 + x;
   if (k ? !dwn : !dw && !dscale) return;
   double s = 0;
   if (c < n)
@@ -614,7 +615,7 @@ BnPlan bn_plan(const pr_block_norm_problem *p) {
     const long long most = 256 * (pl.g.tpr > 256 ? 1 : per_simd);
     pl.parts = (int)(b < most ? b : most);
   } else {
-    pl.parts = BN_SLICES;
+    pl.parts = (int)(p->rows < BN_SLICES ? p->rows : BN_SLICES);
     o = align256((size_t)p->rows * 12);
   }
   pl.off_part = o;
@@ -705,7 +706,8 @@ int pararnn_block_norm_adjoint(const pr_block_norm_problem *p, const pr_rows *x,
     }
   }
   if (!sums) return PR_OK;
-  const dim3 grid((unsigned)((p->n + 15) / 16), 2);
+  dim3 grid = flat_grid(((long long)p->n + 15) / 16);
+  grid.z = 2;
   if (bf) k_bn_sums<uint16_t><<<grid, 1024, 0, s>>>(part, pl.parts, p->n, w, scale, gr->w, gr->scale, gr->w_next);
   else k_bn_sums<float><<<grid, 1024, 0, s>>>(part, pl.parts, p->n, w, scale, gr->w, gr->scale, gr->w_next);
   HIPCHK(hipGetLastError());

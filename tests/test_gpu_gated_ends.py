@@ -254,3 +254,22 @@ def test_block_norm_sums_of_long_rows():
     bd.block_norm_adjoint(x, None, dx, work(bd.block_norm_workspace_bytes(F, 1, n)), t=t, dt=dt, dy=dy)
     ref = R.block_norm_grads(x, t=t, dt=dt, dy=dy)["dx"]
     assert float((dx.double() - ref).abs().max()) <= 520 * U * float(ref.abs().max())
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_block_norm_of_very_long_rows(dtype):
+    """More columns than one grid dimension has threads for in the weights' sums."""
+    rows, n = 2, (1 << 26) + 40
+    g = torch.Generator(device="cuda").manual_seed(70)
+    x, res, dt, dy = (torch.randn(rows, n, generator=g, device="cuda", dtype=dtype) for _ in range(4))
+    w, wn = (1 + 0.1 * torch.randn(n, generator=g, device="cuda", dtype=dtype) for _ in range(2))
+    t, y = (torch.full_like(x, float("nan")) for _ in range(2))
+    bd.block_norm(x, w, t, residual=res, y=y, w_next=wn)
+    o = dict(dx=torch.full_like(x, float("nan")), dw=nan(n), dscale=nan(n), dw_next=nan(n))
+    bd.block_norm_adjoint(x, w, workspace=work(bd.block_norm_workspace_bytes(dtype, rows, n)), t=t, dt=dt, dy=dy,
+                          w_next=wn, **o)
+    r = R.block_norm_grads(x, w, w_next=wn, t=t, dt=dt, dy=dy)
+    r.update(t=R.block_norm(x, w, residual=res), y=R.norm_next(t, wn))
+    for k, v in dict(o, t=t, y=y).items():
+        off = (v.double() - r[k]).abs() - (2.0 ** -8 * r[k].abs() if v.dtype == BF else 0)
+        assert float(off.max()) <= TOL * max(1.0, float(r[k].abs().max())), k
