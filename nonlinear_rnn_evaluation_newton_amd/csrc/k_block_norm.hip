@@ -435,9 +435,10 @@ __global__ __launch_bounds__(256) void k_bn_adj_stat(BnArgs a) {
 // q and dw_next: a block sums one slice of the rows for 256 columns
 template <typename T>
 __global__ __launch_bounds__(256) void k_bn_adj_cols(BnArgs a, int slices) {
-  const int c = (int)blockIdx.x * 256 + threadIdx.x;
-  if (c >= a.n) return;
-  const long long per = (a.rows + slices - 1) / slices, r0 = blockIdx.y * per;
+  const int cb = (a.n + 255) / 256, c = (int)(flat_block() % cb) * 256 + threadIdx.x;
+  const long long slice = flat_block() / cb;
+  if (slice >= slices || c >= a.n) return;
+  const long long per = (a.rows + slices - 1) / slices, r0 = slice * per;
   const long long r1 = r0 + per < a.rows ? r0 + per : a.rows;
   const Gate gate(a.z, a.gate);
   float q = 0.f, wn = 0.f;
@@ -449,8 +450,8 @@ __global__ __launch_bounds__(256) void k_bn_adj_cols(BnArgs a, int slices) {
     if (a.dy)
       wn = fmaf(ldf((const T *)a.dy + r * a.ldy, c), ldf((const T *)a.t + r * a.lt, c) * s.rstd2, wn);
   }
-  a.part[(blockIdx.y * 2LL) * a.n + c] = q;
-  a.part[(blockIdx.y * 2LL + 1) * a.n + c] = wn;
+  a.part[slice * 2 * a.n + c] = q;
+  a.part[(slice * 2 + 1) * a.n + c] = wn;
 }
 template <typename T>
 __global__ __launch_bounds__(256) void k_bn_adj_long(BnArgs a) {
@@ -571,6 +572,10 @@ namespace {
   } while (0)
 
 constexpr int BN_SLICES = 64;  // slices of the rows in the columns' sums of long rows
+// The most rows that a thread adds in fp32, 2^-25 of the sum lost at each: more rows are
+// more partials, which 64 bits add (from 32768 long rows on, from 131072 wide ones, from
+// a million short ones).
+constexpr int BN_ROWS = 512;
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 bool has(const pr_rows *r) { return r && r->p; }
@@ -613,9 +618,11 @@ BnPlan bn_plan(const pr_block_norm_problem *p) {
     const long long rpb = pl.g.tpr > 256 ? 1 : 256 / pl.g.tpr, b = (p->rows + rpb - 1) / rpb;
     const int per_simd = (p->dtype == PR_BF16 ? 2 : 3) + (pl.g.nv == 1 ? 1 : 0);
     const long long most = 256 * (pl.g.tpr > 256 ? 1 : per_simd);
-    pl.parts = (int)(b < most ? b : most);
+    const long long least = (b + BN_ROWS - 1) / BN_ROWS;
+    pl.parts = (int)(b < most ? b : least < most ? most : least);
   } else {
-    pl.parts = (int)(p->rows < BN_SLICES ? p->rows : BN_SLICES);
+    const long long least = (p->rows + BN_ROWS - 1) / BN_ROWS;
+    pl.parts = (int)(p->rows < BN_SLICES ? p->rows : least < BN_SLICES ? BN_SLICES : least);
     o = align256((size_t)p->rows * 12);
   }
   pl.off_part = o;
@@ -690,7 +697,7 @@ int pararnn_block_norm_adjoint(const pr_block_norm_problem *p, const pr_rows *x,
   } else {
     a.stat = (float *)ws;
     a.part = part;
-    const dim3 grid = flat_grid(p->rows), cols((unsigned)((p->n + 255) / 256), (unsigned)pl.parts);
+    const dim3 grid = flat_grid(p->rows), cols = flat_grid(((long long)p->n + 255) / 256 * pl.parts);
     if (bf) k_bn_adj_stat<uint16_t><<<grid, 256, 0, s>>>(a);
     else k_bn_adj_stat<float><<<grid, 256, 0, s>>>(a);
     HIPCHK(hipGetLastError());

@@ -273,3 +273,25 @@ def test_block_norm_of_very_long_rows(dtype):
     for k, v in dict(o, t=t, y=y).items():
         off = (v.double() - r[k]).abs() - (2.0 ** -8 * r[k].abs() if v.dtype == BF else 0)
         assert float(off.max()) <= TOL * max(1.0, float(r[k].abs().max())), k
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("n", [3, 12, 300])
+def test_block_norm_weights_gradients_of_very_many_rows(dtype, n):
+    """2^26 equal rows (of stride 0): every addition of a sum rounds to the same side
+    while the sum's exponent stays.  512 of them in fp32 lose 256 U at most, as the sum
+    grows from nothing; a term itself has some 12 roundings."""
+    g, rows = gen(80 + n), 1 << 26
+    x, dt, dy, t = (1 + torch.rand(1, n, generator=g).to(dtype) for _ in range(4))
+    w, scale, wn = (1 + torch.rand(n, generator=g).to(dtype) for _ in range(3))
+    wide = lambda v: v.cuda().expand(rows, n)  # noqa: E731
+    o = dict(dw=nan(n), dscale=nan(n), dw_next=nan(n))
+    bd.block_norm_adjoint(wide(x), w.cuda(), None, work(bd.block_norm_workspace_bytes(dtype, rows, n)), scale=scale.cuda(),
+                          w_next=wn.cuda(), t=wide(t), dt=wide(dt), dy=wide(dy), **o)
+    r = R.block_norm_grads(x, w, scale=scale, w_next=wn, t=t, dt=dt, dy=dy)
+    # (of the gradient at t the norm takes off what lies along t: the size of dt is left of it and more)
+    size = x.double() * R._rstd(x.double(), 1e-5) * (dt.double() + 2 * dy.double() * wn.double() * R._rstd(t.double(), 1e-5))
+    for k, f in (("dw", scale), ("dscale", w), ("dw_next", None)):
+        top = r[k].abs() if f is None else (size * f.double())[0]
+        off = ((o[k].double().cpu() - rows * r[k]).abs() / (rows * top)).max()
+        assert float(off) <= 270 * U, (k, float(off) / U)
