@@ -92,9 +92,13 @@ class Join(torch.autograd.Function):
 
 
 def rows(z):
-    """[.., n] as [rows, n] in place: slices of a wider projection keep its row stride."""
-    return z.reshape(-1, z.shape[-1]) if z.dim() == 2 else z.as_strided((z.shape[0] * z.shape[1], z.shape[2]), (z.stride(1), 1),
-                                                                        z.storage_offset())
+    """[.., n] as [rows, n]: in place where the rows lie at one stride, as slices of a wider projection do."""
+    n = z.shape[-1]
+    if z.dim() == 2 and z.stride(1) == 1:
+        return z
+    if z.dim() == 3 and z.stride(2) == 1 and z.stride(0) == z.shape[1] * z.stride(1):
+        return z.as_strided((z.shape[0] * z.shape[1], n), (z.stride(1), 1), z.storage_offset())
+    return z.reshape(-1, n).contiguous()
 
 
 class Model:

@@ -295,3 +295,15 @@ def test_block_norm_weights_gradients_of_very_many_rows(dtype, n):
         top = r[k].abs() if f is None else (size * f.double())[0]
         off = ((o[k].double().cpu() - rows * r[k]).abs() / (rows * top)).max()
         assert float(off) <= 270 * U, (k, float(off) / U)
+
+
+# ---------------------------------------------------------------------------
+def test_example_rows_of_any_view():
+    """Gates that are views cut in time or transposed keep their rows."""
+    ex = example()
+    g = gen(60)
+    x, w = rnd(g, 3, 5, 24).cuda(), rnd(g, 24).cuda()
+    whole = rnd(g, 3, 9, 48).cuda()
+    for z in (whole[:, 2:7, 3:27], whole[:, :5, :24].contiguous(), whole.transpose(1, 2)[:, :5, :9].repeat(1, 1, 3)[..., :24],
+              rnd(g, 5, 3, 24).cuda().transpose(0, 1)):
+        near(ex.Norm.apply(x, w, z).view(15, 24), R.block_norm(x.view(15, 24).cpu(), w.cpu(), z.reshape(15, 24).cpu()), TOL, "t")
