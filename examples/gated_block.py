@@ -210,6 +210,9 @@ def train(model, steps=8, B=2, T=96, lr=2e-3, seed=1):
         optimizer.zero_grad()
         loss.backward()
         optimizer.step()
+        with torch.no_grad():
+            for w in model.blocks:
+                w["decay"].clamp_(min=1e-4)  # below 0 the recurrence is not defined
         losses.append(float(loss.detach()))
     return losses
 

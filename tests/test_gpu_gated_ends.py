@@ -307,3 +307,13 @@ def test_example_rows_of_any_view():
     for z in (whole[:, 2:7, 3:27], whole[:, :5, :24].contiguous(), whole.transpose(1, 2)[:, :5, :9].repeat(1, 1, 3)[..., :24],
               rnd(g, 5, 3, 24).cuda().transpose(0, 1)):
         near(ex.Norm.apply(x, w, z).view(15, 24), R.block_norm(x.view(15, 24).cpu(), w.cpu(), z.reshape(15, 24).cpu()), TOL, "t")
+
+
+def test_example_keeps_its_decays():
+    """Large steps do not take a decay below 0, where the recurrence is not defined."""
+    ex = example()
+    model = ex.Model(dim=32, width=64, blocks=1, seed=5)
+    losses = ex.train(model, steps=40, lr=0.1)
+    assert all(v == v for v in losses), losses
+    for b in model.blocks:
+        assert float(b["decay"].detach().min()) > 0
