@@ -16,6 +16,7 @@ import sys
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from nonlinear_rnn_evaluation_newton_amd import binding as bd  # noqa: E402
@@ -41,6 +42,7 @@ class Scan(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, r, i, decay, r_bias, i_bias, states = ctx.saved_tensors
         new = lambda t: like(t, *t.shape)  # noqa: E731
@@ -60,6 +62,7 @@ class Norm(torch.autograd.Function):
         return t
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dt):
         x, w, z = ctx.saved_tensors
         n, count = x.shape[-1], x.numel() // x.shape[-1]
@@ -79,6 +82,7 @@ class Join(torch.autograd.Function):
         return t, y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dt, dy):
         x, w, scale, w_next, t = ctx.saved_tensors
         n, count = x.shape[-1], x.numel() // x.shape[-1]

@@ -317,3 +317,13 @@ def test_example_keeps_its_decays():
     assert all(v == v for v in losses), losses
     for b in model.blocks:
         assert float(b["decay"].detach().min()) > 0
+
+
+def test_example_does_not_differentiate_twice():
+    """The operators have no second derivatives: asking for one is an error, not a zero."""
+    ex = example()
+    model = ex.Model(dim=16, width=32, blocks=1, dtype=F)
+    s = torch.randn(1, 20, 16, device="cuda", requires_grad=True)
+    first, = torch.autograd.grad(model.forward(s).square().sum(), s, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        first.sum().backward()
