@@ -465,8 +465,9 @@ int pararnn_gemm_i8(int dtype, int M, int N, int K, const signed char *a, long l
  *   r_t = sigm(rg_t + r_bias), i_t = sigm(ig_t + i_bias)
  *   a_t = exp(-decay r_t)
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t,  y_t = h_t
- * 0 <= decay <= 1e38; where 1 - a_t^2 is 0 (a decay of 0, a closed gate)
- * the input's term and its gradients are 0.
+ * 0 <= decay <= 1e38; where 1 - a_t^2 is 0 (a decay of 0, a closed gate), or
+ * below 2^-126, the input's term and its gradients are 0.  From an infinite or
+ * NaN input on its channel's states are infinite or NaN.
  *   x, r, i [B, T, D] (r, i: the gates rg, ig before the sigmoid), y   storage dtype
  *   decay [D], r_bias [D] or NULL, i_bias [D] or NULL                  fp32
  *   h0 [B, D] or NULL (= 0)                                            fp32
@@ -502,7 +503,7 @@ int pararnn_gated_adjoint(const pr_gated_problem *p, const pr_gated_inputs *in, 
                           const float *dh_last, const pr_gated_grads *grads, void *workspace, size_t ws_bytes,
                           void *stream);
 /* One token for each of B sequences (p->T, h0 and lengths are not used, T may
- * be 0; row strides sb): state [nslots, D] fp32 is updated in place.        */
+ * be 0; row strides sb; B up to 65535): state [nslots, D] fp32 is updated in place. */
 int pararnn_gated_step(const pr_gated_problem *p, const pr_gated_inputs *in, const pr_view *y, float *state, int nslots,
                        const int *slots, void *stream);
 

@@ -97,7 +97,7 @@ __device__ inline GateVals gate_vals(float rg, float ig, const GateConsts<T> &c)
 // go by their sum, to base 2.
 __device__ inline float decay_of(float l2) { return __builtin_amdgcn_exp2f(l2); }
 // A h + b for A = e^-v, without the factor's rounding: near 1 by what it takes off,
-// 1 - e^-v, whose series is that of m^2.  (An infinite state stays one.)
+// 1 - e^-v, whose series is that of m^2.  (An infinite state takes the product.)
 __device__ inline float decayed(float A, float v, float h, float b) {
   float s = fmaf(v, -1.f / 24.f, 1.f / 6.f);
   s = fmaf(v, s, -0.5f);

@@ -327,3 +327,68 @@ def test_example_does_not_differentiate_twice():
     first, = torch.autograd.grad(model.forward(s).square().sum(), s, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         first.sum().backward()
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_decays_of_any_size(dtype):
+    """Decays from 0 to 1e38 over many tiles, each channel held to its own largest value:
+    a state that is only kept, one that hardly fades, one that is gone at once.  A decay
+    of 1e-38 leaves 1 - a^2 below 2^-126 at some steps, whose inputs' terms (1e-19 of x)
+    may be 0: its outputs are finite and its state is the first one."""
+    g = gen(90)
+    B, T = 2, 1500
+    each = torch.tensor([0.0, 1e-38, 1e-30, 1e-12, 1e-7, 1e-5, 1e-3, 0.03, 0.0624, 0.126, 1.0, 20.0, 80.0, 150.0, 1e10, 1e38])
+    D = each.numel() * 5
+    p = gated_problem(g, dtype, B, T, D)
+    p["decay"] = each.repeat(5)
+    h0, dh, dy = rnd(g, B, D), rnd(g, B, D), rnd(g, B, T, D, dtype=dtype)
+    dev = {k: v.cuda() for k, v in p.items()}
+    main, kw = (dev["x"], dev["r"], dev["i"], dev["decay"]), dict(r_bias=dev["r_bias"], i_bias=dev["i_bias"])
+    ws = work(bd.gated_workspace_bytes(dtype, B, T, D))
+    o = dict(y=nan(B, T, D, dtype=dtype), h=nan(B, D), dx=nan(B, T, D, dtype=dtype), dr=nan(B, T, D, dtype=dtype),
+             di=nan(B, T, D, dtype=dtype), ddecay=nan(D), dh0=nan(B, D))
+    states = nan(*bd.gated_states_shape(B, T, D))
+    bd.gated_scan(*main, o["y"], ws, h0=h0.cuda(), h_last=o["h"], states=states, **kw)
+    bd.gated_scan_adjoint(*main, states, dy.cuda(), ws, dh_last=dh.cuda(), **kw,
+                          **{k: o[k] for k in ("dx", "dr", "di", "ddecay", "dh0")})
+    y, h, hs = R.gated(**p, h0=h0, keep=True)
+    r = R.gated_grads(**p, dy=dy, h0=h0, dh_last=dh)
+    r.update(y=y, h=h)
+    gr, gi, a, m = R._gates(p["r"], p["i"], p["decay"], p["r_bias"], p["i_bias"])
+    inv = torch.where(m > 0, 1 / m, torch.zeros((), dtype=R.F64))
+    grad = R.gated_grads(**{**p, "i": torch.full_like(p["i"], 1e4)}, dy=dy, h0=h0, dh_last=dh)["dx"] * inv  # g, where m > 0
+    # at a decay of 0, g is the sum of all that follows
+    grad = torch.where(m > 0, grad, (dy.double().flip(1).cumsum(1).flip(1) + dh.double()[:, None])).abs()
+    size = grad * (a * a * inv * gi * p["x"].double().abs() + a * torch.stack(hs[:-1], 1).abs())
+    size = dict(dr=(size * p["decay"].double() * gr * (1 - gr)).amax((0, 1)), ddecay=(size * gr).sum((0, 1)))
+    near(o["h"][:, 1::each.numel()], h0.double()[:, 1::each.numel()], TOL, "h")
+    for k, v in o.items():
+        assert torch.isfinite(v).all(), k
+        top = size[k] if k in size else r[k].abs().amax(tuple(range(v.dim() - 1)))
+        off = (v.double().cpu() - r[k]).abs() - (2.0 ** -8 * r[k].abs() if v.dtype == BF else 0)
+        room = TOL * top
+        if k == "dh0":  # a_0 = e^-v times the rest: v, of 16 roundings at most (two gates' terms, sigmoid, product), counts v times
+            room = room + 16 * U * p["decay"].double() * gr[:, 0].amax(0) * top
+        bad = off > room
+        bad[..., 1::each.numel()] = False  # (1e-38)
+        assert not bad.any(), (k, p["decay"][torch.nonzero(bad)[0, -1]], float((off / top).nan_to_num(0).max()))
+
+
+def test_infinite_inputs_stay_in_their_channel():
+    """From an infinite input on its channel's states are infinite or NaN (its tiles' factors
+    may be 0, and 0 times infinity is a NaN), by scan and by step, and no other's are."""
+    g = gen(91)
+    B, T, D = 1, 2500, 20
+    p = gated_problem(g, F, B, T, D)
+    p["x"][0, 700, 3], p["x"][0, 900, 7] = float("inf"), float("-inf")
+    dev = {k: v.cuda() for k, v in p.items()}
+    kw = dict(r_bias=dev["r_bias"], i_bias=dev["i_bias"])
+    y, h = nan(B, T, D), nan(B, D)
+    bd.gated_scan(dev["x"], dev["r"], dev["i"], dev["decay"], y, work(bd.gated_workspace_bytes(F, B, T, D)), h_last=h, **kw)
+    ref = R.gated(**p)[0]
+    assert torch.equal(torch.isfinite(y).cpu(), torch.isfinite(ref))
+    near(y[..., 8:], ref[..., 8:], TOL, "y")
+    one = nan(B, D)
+    bd.gated_step(*(dev[k][:, 0] for k in ("x", "r", "i")), dev["decay"], h, one, **kw)
+    assert torch.equal(torch.isfinite(one).cpu(), torch.isfinite(ref[:, -1]))
