@@ -45,22 +45,20 @@ struct GatedArgs {
 struct GateVals {
   float r, i, a, l, m;
 };
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // A channel's constants.  Rows stored in 8 significant bits take plain products
 // for the exponentials' arguments, with the constants folded in; fp32 ones carry
 // the products in two words.
 template <typename T>
 struct GateConsts {
   static constexpr bool SHORT = sizeof(T) == 2;
-  float rb, ib, nd, d2;  // SHORT: the biases and the decay times -log2 e; d2 = 2 decay
+  float rb, ib, nd;  // nd = -decay; SHORT: the biases and the decay times -log2 e
   __device__ GateConsts(float decay, float r_bias, float i_bias)
-      : rb(SHORT ? -LOG2E * r_bias : r_bias), ib(SHORT ? -LOG2E * i_bias : i_bias), nd(SHORT ? -LOG2E * decay : -decay),
-        d2(decay + decay) {}
+      : rb(SHORT ? -LOG2E * r_bias : r_bias), ib(SHORT ? -LOG2E * i_bias : i_bias), nd(SHORT ? -LOG2E * decay : -decay) {}
 };
 template <typename T>
 __device__ inline GateVals gate_vals(float rg, float ig, const GateConsts<T> &c) {
   GateVals o;
-  const float w0 = c.d2;
   if constexpr (GateConsts<T>::SHORT) {
     o.r = frcp(1.f + __builtin_amdgcn_exp2f(fmaf(rg, -LOG2E, c.rb)));
     o.i = frcp(1.f + __builtin_amdgcn_exp2f(fmaf(ig, -LOG2E, c.ib)));
@@ -75,7 +73,7 @@ __device__ inline GateVals gate_vals(float rg, float ig, const GateConsts<T> &c)
   // 1 - e^-w for w = 2 v: the difference where little is lost, else its series.
   // SHORT: up to w^4, the first term left out is below w^4 / 120 of it, 1.3e-7 at
   // w = 1/16, where the difference has lost 4 bits; else up to w^6, 5e-8 at 1/4.
-  const float w = w0 * o.r;
+  const float w = o.l * (GateConsts<T>::SHORT ? -2.f * LN2 : -2.f);
   float s;
   if constexpr (GateConsts<T>::SHORT) {
     s = fmaf(w, -1.f / 24.f, 1.f / 6.f);
@@ -105,7 +103,6 @@ __device__ inline float decayed(float A, float v, float h, float b) {
   const float e = v < 0.0625f ? v * s : 1.f - A, near = h + fmaf(-e, h, b);
   return A > 0.5f && near == near ? near : fmaf(A, h, b);
 }
-constexpr float LN2 = 0.6931471805599453f;
 __device__ inline float decayed(float l2, float h, float b) { return decayed(decay_of(l2), l2 * -LN2, h, b); }
 
 // ---------------------------------------------------------------------------
