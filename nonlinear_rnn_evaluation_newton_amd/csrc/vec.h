@@ -73,8 +73,6 @@ struct WordsOf<16> { typedef unsigned type __attribute__((ext_vector_type(4))); 
 template <>
 struct WordsOf<8> { typedef unsigned type __attribute__((ext_vector_type(2))); };
 template <>
-struct WordsOf<2> { typedef unsigned short type; };
-template <>
 struct WordsOf<4> { typedef unsigned type; };
 template <typename T, int V>
 struct __attribute__((packed, aligned(sizeof(T)))) Packed {
