@@ -161,6 +161,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_bn(BnArgs a) {
     vz[m] = bn_ld<T>(a.z, row, a.lz, at, a.z != nullptr);
     vr[m] = bn_ld<T>(a.res, row, a.lres, at, a.res != nullptr);
   }
+  // (read while the row is on its way: the compiler would put these loads behind it)
+  asm volatile("" : "+s"(a.eps), "+s"(a.nf), "+s"(a.rn), "+s"(a.gate), "+s"(a.lt), "+s"(a.ly));
   VecU<T, V> vw[NV], vs[NV], vn[NV];
 #pragma unroll
   for (int m = 0; m < NV; m++) {
@@ -612,9 +614,11 @@ BnPlan bn_plan(const pr_block_norm_problem *p) {
   pl.g = bn_geom(p->n, p->dtype == PR_BF16 ? 8 : 4, true);
   size_t o = 0;
   if (pl.g.tpr) {
-    // as many blocks as run at once on 256 CUs, each with its share of the rows: with
-    // more, the last ones run on a device that is half empty, and there are more
-    // partials.  (Wavefronts a SIMD by the kernels' registers, 2 to 4.)
+    // as many blocks of bf16 rows as run at once on 256 CUs (by the kernels' registers 3
+    // wavefronts a SIMD with one vector, 2 with more), each with its share of the rows:
+    // with more, the last ones run on a device that is half empty, and there are more
+    // partials.  Of fp32 rows 4 and 3 where 5 and 4 would fit, which was not compared.
+    // (The workspace's size is asked for without a device too: a count of 256 CUs.)
     const long long rpb = pl.g.tpr > 256 ? 1 : 256 / pl.g.tpr, b = (p->rows + rpb - 1) / rpb;
     const int per_simd = (p->dtype == PR_BF16 ? 2 : 3) + (pl.g.nv == 1 ? 1 : 0);
     const long long most = 256 * (pl.g.tpr > 256 ? 1 : per_simd);
