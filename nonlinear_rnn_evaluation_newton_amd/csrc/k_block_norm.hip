@@ -10,11 +10,13 @@
 // registers, 16 bytes a thread and access.  Between a block's two norms nothing goes
 // through memory but t.  Squares and dot products are summed in fp32, the weights'
 // gradients over the rows in fp32 within a block and in fp64 over the blocks.
-// Measured, 16384 x 2048, bf16, with gate and residual: forward 56 us for 336 MB (in
-// part from the last-level cache; vector instructions in 77% of the cycles), adjoint 100
-// us for 550 MB (5.5 TB/s, 76%), the weights' sums 8; the same in fp32 on 8192 rows 159
-// together.  Instructions count as much as bytes here: with a division by n and a square
-// root for each sum, and row addresses in vector registers, the three took 166.
+// Measured, 16384 x 2048, bf16, with gate and residual: forward 57 us for 336 MB (in
+// part from the last-level cache; VALU issue 84% by the counters), adjoint 106 us for 550
+// MB (5.2 TB/s, 77%), the weights' sums 8; the same in fp32 on 8192 rows 160 together.
+// Instructions count as much as bytes here: with a division by n and a square root for
+// each sum, and row addresses in vector registers, a pass took 166 us for 161 to 163.
+// Widths that do not fill the threads take more: 20000 x 1111 with a gate 126 us (52 at
+// the rate of a copy), in fp32 143 (103); 4096 x 8192 with both 178 (130).
 #include "pararnn.h"
 #include "ssm.h"
 #include "vec.h"

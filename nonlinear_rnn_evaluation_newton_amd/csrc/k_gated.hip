@@ -15,10 +15,12 @@
 // again and makes the gates and states anew: storing a, m and both gates in fp32 would
 // move 32 bytes a step and channel to save 4.
 // Measured: 8 x 4096 x 2048, bf16, forward with saved states 125 us for 550 MB (4.4
-// TB/s, vector instructions in 62% of the cycles), adjoint 260 us for 976 MB (3.8 TB/s,
-// 61%; three outputs and four inputs share the memory's reads and writes), the sums of
-// decay's and the biases' gradients 8, the chains' clearing 5 each; 1 x 32768 x 256,
-// fp32, 35 us (3.9 TB/s: 2048 tiles, of which each waits for those before it).
+// TB/s, VALU issue 64% by the counters), adjoint 264 us for 976 MB (3.7 TB/s, 62%; three
+// outputs and four inputs share the memory's reads and writes, and at three wavefronts a
+// SIMD a tile's phases, load, gates, join, walk and store, do not fill each other's
+// gaps), the sums of decay's and the biases' gradients 8, the chains' clearing 5 to 6
+// each; 1 x 32768 x 256, fp32, 35 us (3.9 TB/s: 2048 tiles, of which each waits for
+// those before it); 4 x 4096 x 2048, fp32, training 306 us together.
 #include <type_traits>
 
 #include "pararnn.h"

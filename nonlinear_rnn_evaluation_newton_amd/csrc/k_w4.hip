@@ -126,11 +126,11 @@ struct GroupWindow {
 // and the scales' for each group.  Few rows leave the matrix unit nearly idle (5% at 16
 // rows), so its 16 rows are no waste, and it takes over the sums of x besides.  The
 // scale multiplies a group's sum once and not each weight.
-// Measured (bf16): one token, 4096 x 4096, groups of 128: 6.3 us, of which a launch with
-// its first loads is 3 to 4; 16 x 32768 x 4096, groups of 64 with zero points: 28 us for 77
-// MB (2.7 TB/s; vector instructions in 45% of the cycles of two wavefronts a SIMD, whose
-// registers are full; twice the wavefronts by two tiles of columns take 40); without
-// zero points, groups of 128: 25; 64 rows: 85.
+// Measured (bf16): one token, 4096 x 4096, groups of 128: 6.4 us, of which a launch with
+// its first loads is 3 to 4; one token on 32768 x 4096, with zero points: 23; 16 rows of it,
+// groups of 64: 28 us for 77 MB (2.7 TB/s; VALU issue 47% by the counters at two wavefronts
+// a SIMD, whose registers are full; twice the wavefronts by two tiles of columns take 40);
+// without zero points, groups of 128: 25; 64 rows, which unpack every weight four times: 83 to 86.
 // MT x NT tiles of 16 rows of x by 16 columns of the output; WV wavefronts take
 // slices of K, 256 columns (a line of a row of weights) at a time, and join in
 // shared memory.  GM: groups in 128 columns, 1 (also where a group is several times
@@ -336,8 +336,8 @@ static W4Geom w4_geom(int dtype, int M, int N, bool zero) {
   const long long rows = (M + 15) / 16, cols = (N + 15) / 16, tiles = rows * cols;
   const bool bf = dtype == PR_BF16;
   // (fp32 rows with zero points, which one tile of rows takes two tiles of columns
-  // only: 64 x 32768 x 4096 in 175 us against 217; without zero points, and in bf16,
-  // four columns are faster: 135 against 156, 85 against 116)
+  // only: 64 x 32768 x 4096 in 173 us against 206; without zero points, and in bf16,
+  // four columns are faster: 127 against 157, 86 against 117)
   if (rows > 1 && tiles >= 4 * 256 && (tiles < 8 * 256 || (!bf && zero))) return {2, 2};
   // (zero points take the registers of 2 x 4 tiles, and of 1 x 4 with fp32 rows)
   if (rows > 1 && tiles >= 8 * 256 && bf && !zero) return {2, 4};
