@@ -392,3 +392,65 @@ def test_infinite_inputs_stay_in_their_channel():
     one = nan(B, D)
     bd.gated_step(*(dev[k][:, 0] for k in ("x", "r", "i")), dev["decay"], h, one, **kw)
     assert torch.equal(torch.isfinite(one).cpu(), torch.isfinite(ref[:, -1]))
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_two_million_steps(dtype):
+    """A chain of thousands of tiles of 8, against the recurrence by doubling in 64 bits:
+    256 U as for long memories, and 4096 roundings to either side beside them, 4 x 64 U."""
+    B, T, D = 1, 2 ** 21 + 77, 6
+    g = torch.Generator(device="cuda").manual_seed(95)
+    x, r, i, dy = (torch.randn(B, T, D, generator=g, device="cuda").add_(0.5).to(dtype) for _ in range(4))
+    decay = torch.tensor([1e-5, 1e-3, 0.008, 0.05, 0.3, 2.0], device="cuda")
+    rb = torch.tensor([-2.0, -6.0, -9.0, -3.0, 0.0, 1.0], device="cuda")
+    ws = work(bd.gated_workspace_bytes(dtype, B, T, D))
+    y, dx = (torch.full_like(x, float("nan")) for _ in range(2))
+    h, dh0, states = nan(B, D), nan(B, D), nan(*bd.gated_states_shape(B, T, D))
+    bd.gated_scan(x, r, i, decay, y, ws, r_bias=rb, h_last=h, states=states)
+    bd.gated_scan_adjoint(x, r, i, decay, states, dy, ws, r_bias=rb, dx=dx, dh0=dh0)
+    gi, v = torch.sigmoid(i.double()), decay.double() * torch.sigmoid(r.double() + rb.double())
+    m = torch.sqrt(-torch.expm1(-2 * v))
+
+    def recurrence(a, b):  # along axis 1
+        a, s = a.clone(), 1
+        while s < T:
+            b = torch.cat([b[:, :s], b[:, s:] + a[:, s:] * b[:, :-s]], 1)
+            a = torch.cat([a[:, :s], a[:, s:] * a[:, :-s]], 1)
+            s *= 2
+        return b
+
+    ry = recurrence(torch.exp(-v), m * gi * x.double())
+    later = torch.cat([torch.exp(-v)[:, 1:], torch.zeros(B, 1, D, dtype=R.F64, device="cuda")], 1)
+    rg = recurrence(later.flip(1), dy.double().flip(1)).flip(1)
+    for k, got, ref in (("h", h, ry[:, -1]), ("states", states[:, 1:], ry[:, 63::64][:, :states.shape[1] - 1]), ("y", y, ry),
+                        ("dx", dx, rg * m * gi), ("dh0", dh0, rg[:, 0] * torch.exp(-v[:, 0]))):
+        dims = tuple(range(got.dim() - 1))
+        off = (got.double() - ref).abs() - (2.0 ** -8 * ref.abs() if got.dtype == BF else 0)
+        off = off.amax(dims) / (ry if k in ("h", "states") else ref if k != "dh0" else rg).abs().amax((0, 1) if k != "dx" else dims)
+        assert float(off.max()) <= 512 * U, (k, (off / U).tolist())
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("zero", [True, False])
+@pytest.mark.parametrize("group", [32, 64, 1024])
+def test_four_bits_of_every_size(dtype, zero, group):
+    """Groups from fp32's denormals to its largest values, and values that lie between two
+    numbers: the 4-bit form is the definition's, bit for bit."""
+    g, N, K = gen(group), 260, 1030
+    size = 2.0 ** torch.linspace(-147, 126, N, dtype=R.F64)[:, None]
+    w = (torch.randn(N, K, generator=g).clamp(-1.9, 1.9).double() * size).to(dtype)
+    half = (torch.randint(-15, 16, (N, K), generator=g) * 0.5).double() * size.clamp(2.0 ** -140, 2.0 ** 120)
+    w[::2] = half.to(dtype)[::2]  # a group's scale is a power of two over 7 or 15: ties and what lies next to them
+    rq, rs, rz = R.quant(w, group, zero)
+    q = torch.zeros(N, (K + 1) // 2, dtype=torch.uint8, device="cuda")
+    G = -(-K // group)
+    scale, z, back = nan(N, G, dtype=dtype), nan(N, G, dtype=dtype) if zero else None, nan(N, K, dtype=dtype)
+    bd.quant_w4(w.cuda(), q, scale, group, zero=z)
+    assert torch.equal(scale.cpu(), rs), torch.nonzero(scale.cpu() != rs)[:5].tolist()
+    assert not zero or torch.equal(z.cpu(), rz), torch.nonzero(z.cpu() != rz)[:5].tolist()
+    live = (rs.float() > 0).repeat_interleave(group, 1)[:, :K]  # a scale that rounds to 0 stands for zeros, whatever q is
+    bad = (R.unpack(q.cpu(), K) != rq) & live
+    assert not bad.any(), (int(bad.sum()), torch.nonzero(bad)[:5].tolist())
+    bd.dequant_w4(q, scale, back, group, zero=z)
+    assert torch.equal(back.cpu(), R.weights(q.cpu(), rs, K, group, rz if zero else None, to=F).to(dtype))
