@@ -558,7 +558,7 @@ int pararnn_block_norm_adjoint(const pr_block_norm_problem *p, const pr_rows *x,
  * batches; any number is computed).  x [M, K], out [M, N] with row strides, bias
  * [N] or NULL, all in `dtype`.  Products are exact, sums in fp32, of x times up to
  * 31 sixteenths before the scale: x is finite and at most 1e36 (a row with an
- * infinity or a NaN gives NaN).                                                  */
+ * infinity or a NaN gives NaN); of fp32 rows what lies below 2^-133 is dropped.   */
 int pararnn_gemm_w4(int dtype, int M, int N, int K, int group, const void *x, long long ldx, const unsigned char *q,
                     long long ldq, const void *scale, const void *zero, const void *bias, void *out, long long ldo,
                     void *stream);

@@ -454,3 +454,16 @@ def test_four_bits_of_every_size(dtype, zero, group):
     assert not bad.any(), (int(bad.sum()), torch.nonzero(bad)[:5].tolist())
     bd.dequant_w4(q, scale, back, group, zero=z)
     assert torch.equal(back.cpu(), R.weights(q.cpu(), rs, K, group, rz if zero else None, to=F).to(dtype))
+
+
+def test_product_of_tiny_fp32_rows():
+    """From 2^-109 on every bit of x counts; below it what lies above 2^-133 does."""
+    g, N, K, M = gen(97), 64, 128, 60
+    x = (torch.randint(1 << 23, 1 << 24, (M, K), generator=g).double() * 2.0 ** (-23 - 140 + torch.arange(M)[:, None])).float()
+    col = torch.randint(0, K, (N,), generator=g)
+    q = torch.full((N, K), 8, dtype=torch.uint8)
+    q[torch.arange(N), col] = 12
+    out = nan(M, N)
+    bd.gemm_w4(x.cuda(), (q[:, ::2] | q[:, 1::2] << 4).cuda(), torch.full((N, 4), 2.0 ** 60, device="cuda"), out, 32)
+    off = (out.double().cpu() - x[:, col].double() * 2.0 ** 62).abs()
+    assert float(off[31:].max()) == 0 and float(off.max()) <= 2.0 ** (62 - 133)
